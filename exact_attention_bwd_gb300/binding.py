@@ -31,7 +31,8 @@ FA_DTYPE_E4M3 = 1
 FA_DTYPE_F16 = 2
 
 EXPORTS = ("fa_fwd", "fa_bwd", "fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_read_device_status",
-           "fa_status_string", "fa_profile_enable", "fa_profile_read", "fa_version", "fa_fwd_noalloc")
+           "fa_status_string", "fa_profile_enable", "fa_profile_read", "fa_version", "fa_fwd_noalloc",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_page_plan")
 
 FA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -51,6 +52,26 @@ class FaParams(ctypes.Structure):
         ("v_descale", ctypes.c_void_p), ("seqused_q", ctypes.c_void_p),
         ("wait_limit_ns", ctypes.c_ulonglong),
     ]
+
+
+class FaRopeParams(ctypes.Structure):
+    """Mirror of ``fa_rope_params``."""
+    _fields_ = [
+        ("T", ctypes.c_int), ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int),
+        ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("seq_len", ctypes.c_int), ("max_pos", ctypes.c_int),
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("weight_f32", ctypes.c_int),
+        ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong),
+        ("dq_stride", ctypes.c_longlong), ("dk_stride", ctypes.c_longlong),
+        ("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("num_slots", ctypes.c_longlong), ("status", ctypes.c_void_p),
+    ]
+
+
+class FaPagePlanParams(ctypes.Structure):
+    """Mirror of ``fa_page_plan_params``."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_blocks_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int), ("n_free", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -104,6 +125,15 @@ def load(build_if_missing: bool = True):
         lib.fa_profile_read.restype = ctypes.c_int
         lib.fa_fwd_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp]
         lib.fa_fwd_noalloc.restype = ctypes.c_int
+        R, L = ctypes.POINTER(FaRopeParams), ctypes.POINTER(FaPagePlanParams)
+        lib.fa_qk_norm_rope.argtypes = [R] + [vp] * 8
+        lib.fa_qk_norm_rope.restype = ctypes.c_int
+        lib.fa_qk_norm_rope_bwd.argtypes = [R] + [vp] * 9 + [sz, vp]
+        lib.fa_qk_norm_rope_bwd.restype = ctypes.c_int
+        lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [R]
+        lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+        lib.fa_page_plan.argtypes = [L] + [vp] * 12
+        lib.fa_page_plan.restype = ctypes.c_int
         lib.fa_version.argtypes = []
         lib.fa_version.restype = ctypes.c_char_p
         _lib = lib
@@ -135,6 +165,26 @@ def fa_fwd_workspace_size(params: FaParams) -> int:
 
 def fa_bwd_workspace_size(params: FaParams) -> int:
     return int(load().fa_bwd_workspace_size(ctypes.byref(params)))
+
+
+def fa_qk_norm_rope(params: FaRopeParams, q, k, v, q_out, k_out, k_cache, v_cache, stream) -> int:
+    return load().fa_qk_norm_rope(ctypes.byref(params), q, k, v, q_out, k_out, k_cache, v_cache, stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_size(params: FaRopeParams) -> int:
+    return int(load().fa_qk_norm_rope_bwd_workspace_size(ctypes.byref(params)))
+
+
+def fa_qk_norm_rope_bwd(params: FaRopeParams, q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, workspace_bytes,
+                        stream) -> int:
+    return load().fa_qk_norm_rope_bwd(ctypes.byref(params), q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace,
+                                      workspace_bytes, stream)
+
+
+def fa_page_plan(params: FaPagePlanParams, cached, fresh, free_pages, free_head, block_table, cu_seqlens_q, seqused_k,
+                 positions, slots, free_head_out, status, stream) -> int:
+    return load().fa_page_plan(ctypes.byref(params), cached, fresh, free_pages, free_head, block_table, cu_seqlens_q,
+                               seqused_k, positions, slots, free_head_out, status, stream)
 
 
 def fa_read_device_status(workspace, stream) -> int:
@@ -169,14 +219,18 @@ def _ptr(t):
 
 def make_params(q, k, *, causal=False, window=(-1, -1), softmax_scale=None, sinks=None, cu_q=None,
                 cu_k=None, flags=0, seqused_k=None, block_table=None, s_kv=None, dtype=None, q_descale=None,
-                k_descale=None, v_descale=None, seqused_q=None, wait_limit_ns=0) -> FaParams:
+                k_descale=None, v_descale=None, seqused_q=None, wait_limit_ns=0, max_seqlen_q=0) -> FaParams:
     """fa_params from tensor shapes: [B,S,H,D] dense or [T,H,D] packed (with cu_q / cu_k).
 
     With a block_table ([B, max_blocks_per_seq] int32), k is a page pool
-    [num_pages, page_size, h_kv, d] and s_kv (the logical cache length) must be given.
+    [num_pages, page_size, h_kv, d] and s_kv (the logical cache length) must be given; q is
+    dense, or packed with cu_q (then seqused_k must be given, and cu_k not).
     seqused_q / seqused_k: int32 [B] queries / keys used per sequence, or None."""
     if block_table is not None:
-        B, s_q, h_q, d = q.shape
+        if cu_q is not None:
+            (s_q, h_q, d), B = q.shape, cu_q.numel() - 1
+        else:
+            B, s_q, h_q, d = q.shape
         num_pages, page_size, h_kv, _ = k.shape
         if s_kv is None:
             raise ValueError("a paged cache needs the logical cache length s_kv")
@@ -195,7 +249,7 @@ def make_params(q, k, *, causal=False, window=(-1, -1), softmax_scale=None, sink
     p.sinks = None if sinks is None else sinks.data_ptr()
     p.cu_seqlens_q = None if cu_q is None else cu_q.data_ptr()
     p.cu_seqlens_k = None if cu_k is None else cu_k.data_ptr()
-    p.max_seqlen_q = p.max_seqlen_k = 0
+    p.max_seqlen_q, p.max_seqlen_k = int(max_seqlen_q), 0
     p.flags = flags
     p.seqused_k = None if seqused_k is None else seqused_k.data_ptr()
     p.seqused_q = None if seqused_q is None else seqused_q.data_ptr()
@@ -270,8 +324,11 @@ def _kv_shape(p, k, cu_q, block_table):
 
 def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks=None, cu_q=None, cu_k=None,
             flags=0, out=None, lse=None, workspace=None, seqused_k=None, block_table=None, s_kv=None,
-            descale=None, seqused_q=None, wait_limit_ns=0):
+            descale=None, seqused_q=None, wait_limit_ns=0, max_seqlen_q=0):
     """Runs fa_fwd on torch CUDA tensors; returns (o, lse, workspace).
+
+    Packed queries over a paged cache: q [T, h_q, d] with cu_q, seqused_k, block_table and s_kv
+    (no cu_k); max_seqlen_q is the most new tokens of a sequence, if the caller knows it.
 
     q, k, v are all bfloat16, all float16, or all uint8 = e4m3 bytes (FA_DTYPE_E4M3);
     descale = (q, k, v) fp32 [B * h_kv] factors or None (all 1).  The output has the
@@ -287,7 +344,7 @@ def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks
     p = make_params(q, k, causal=causal, window=window, softmax_scale=softmax_scale, sinks=sinks, cu_q=cu_q,
                     cu_k=cu_k, flags=flags, seqused_k=seqused_k, block_table=block_table, s_kv=s_kv,
                     dtype=_type_code(q.dtype), q_descale=dq_, k_descale=dk_, v_descale=dv_,
-                    seqused_q=seqused_q, wait_limit_ns=wait_limit_ns)
+                    seqused_q=seqused_q, wait_limit_ns=wait_limit_ns, max_seqlen_q=max_seqlen_q)
     lse_shape = (p.B, p.h_q, p.s_q) if cu_q is None else (p.h_q, p.s_q)
     _check_tensors(q, [("k", k, None, _kv_shape(p, k, cu_q, block_table)), ("v", v, None, k.shape),
                        ("out", out, torch.bfloat16 if fp8 else q.dtype, q.shape), ("lse", lse, torch.float32, lse_shape),
@@ -354,6 +411,208 @@ def backward(q, k, v, o, lse, dout, *, causal=False, window=(-1, -1), softmax_sc
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd")
     return dq, dk, dv, dsinks, workspace
+
+
+def _on_device(t, call, *args, **kw):
+    """call(*args, **kw) with t's device current (the library launches on the current device)."""
+    import torch
+    with torch.cuda.device(t.device):
+        return call(*args, **kw)
+
+
+def _elsewhere(t):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("torch tensors are wanted")
+    if t.device.type != "cuda":
+        raise ValueError(f"the tensors must be CUDA tensors; the first is on {t.device}")
+    return t.device.index != torch.cuda.current_device()
+
+
+def _check_vector(name, t, like, dtype, n):
+    if t is None:
+        return
+    if t.device != like.device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {like.device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements; it has {t.numel()}")
+
+
+def _rows(name, t, like=None):
+    """(tokens, heads, d, elements from token to token) of [T, h, d] or [B, S, h, d] rows, whose
+    heads are contiguous and whose tokens lie at one stride (a slice of a fused projection)."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [T, h, d] or [B, S, h, d]")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} must have the type and device of q")
+    shape, st = t.shape, t.stride()
+    h, d = shape[-2:]
+    if t.numel() and (st[-1] != 1 or (h > 1 and st[-2] != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    T, step = shape[-3], st[-3]
+    if len(shape) == 4:
+        if shape[0] > 1 and T > 1 and st[0] != T * step:
+            raise ValueError(f"{name}: the tokens must lie at one stride")
+        if T == 1:
+            step = st[0]
+        T *= shape[0]
+    return T, h, d, step if T > 1 else h * d
+
+
+def _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status):
+    import torch
+    T, h_q, d, q_stride = _rows("q", q)
+    Tk, h_kv, dk, k_stride = _rows("k", k, q)
+    code = _type_code(q.dtype)
+    if code is None or code == FA_DTYPE_E4M3:
+        raise TypeError(f"q and k must be bfloat16 or float16; q is {q.dtype}")
+    if Tk != T or dk != d or k.shape[:-2] != q.shape[:-2]:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must have the same tokens and head dimension")
+    p = FaRopeParams()
+    p.T, p.h_q, p.h_kv, p.d, p.eps, p.dtype, p.interleaved = T, h_q, h_kv, d, eps, code, 1 if interleaved else 0
+    p.q_stride, p.k_stride, p.v_stride = q_stride, k_stride, h_kv * d
+    p.dq_stride, p.dk_stride = h_q * d, h_kv * d
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        max_pos, half = cos.shape
+        _check_vector("cos", cos, q, torch.float32, max_pos * half)
+        _check_vector("sin", sin, q, torch.float32, max_pos * half)
+        p.cos, p.sin, p.max_pos, p.rot_dim = cos.data_ptr(), sin.data_ptr(), max_pos, 2 * half
+    wt = q_weight if q_weight is not None else k_weight
+    if wt is not None:
+        if wt.dtype not in (q.dtype, torch.float32):
+            raise TypeError(f"the weights must be {q.dtype} or float32; they are {wt.dtype}")
+        p.weight_f32 = 1 if wt.dtype == torch.float32 else 0
+        _check_vector("q_weight", q_weight, q, wt.dtype, d)
+        _check_vector("k_weight", k_weight, q, wt.dtype, d)
+        p.q_weight = None if q_weight is None else q_weight.data_ptr()
+        p.k_weight = None if k_weight is None else k_weight.data_ptr()
+    if positions is not None:
+        _check_vector("positions", positions, q, torch.int32, T)
+        p.positions = positions.data_ptr()
+    p.seq_len = int(seq_len) if seq_len is not None else max(1, q.shape[1] if q.dim() == 4 else T)
+    if status is not None:
+        _check_vector("status", status, q, torch.int32, 1)
+        p.status = status.data_ptr()
+    return p
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6, interleaved=False,
+                 v=None, k_cache=None, v_cache=None, slots=None, out=None, status=None):
+    """Runs fa_qk_norm_rope on torch CUDA tensors; returns (q_out, k_out).
+
+    q [T, h_q, d] and k [T, h_kv, d] (or [B, S, h, d]) may be slices of a fused projection;
+    q_weight, k_weight [d] (or None: ones) have their type or are fp32; cos, sin are fp32
+    [max_pos, rot_dim / 2] (or None: no rotation); positions int32 [T], by default the token's
+    place in its sequence of seq_len (S, or T).  With v, k_cache, v_cache ([num_pages, page_size,
+    h_kv, d]) and slots (int32 [T]) keys and values go to the paged cache, and k_out is None
+    unless out = (q_out, k_out) gives one.  status: int32 [1] or None."""
+    import torch
+    if _elsewhere(q):
+        return _on_device(q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions=positions, seq_len=seq_len, eps=eps,
+                          interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status)
+    p = _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    append = v is not None or k_cache is not None or v_cache is not None or slots is not None
+    if append:
+        if v is None or k_cache is None or v_cache is None or slots is None:
+            raise ValueError("an append takes v, k_cache, v_cache and slots together")
+        if v.shape != k.shape:
+            raise ValueError(f"v must have k's shape {tuple(k.shape)}; it has {tuple(v.shape)}")
+        p.v_stride = _rows("v", v, q)[3]
+        for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if c.dim() != 4 or c.shape != k_cache.shape or c.shape[2:] != k.shape[-2:]:
+                raise ValueError(f"{name} must be [num_pages, page_size, {p.h_kv}, {p.d}]; it has {tuple(c.shape)}")
+            _check_vector(name, c, q, q.dtype, c.numel())
+        _check_vector("slots", slots, q, torch.int32, p.T)
+        p.slots, p.num_slots = slots.data_ptr(), k_cache.shape[0] * k_cache.shape[1]
+    q_out, k_out = out if out is not None else (None, None)
+    _check_vector("q_out", q_out, q, q.dtype, q.numel())
+    _check_vector("k_out", k_out, q, q.dtype, k.numel())
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and not append:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    rc = fa_qk_norm_rope(p, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), q_out.data_ptr(),
+                         None if k_out is None else k_out.data_ptr(), None if k_cache is None else k_cache.data_ptr(),
+                         None if v_cache is None else v_cache.data_ptr(), _stream())
+    if rc != FA_OK:
+        raise FaError(rc, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6,
+                          interleaved=False, grads=None, workspace=None, status=None):
+    """Runs fa_qk_norm_rope_bwd on torch CUDA tensors; returns (dq, dk, dq_weight, dk_weight).
+
+    q, k and the arguments behind dk_out are those of qk_norm_rope; dq_out, dk_out (contiguous)
+    are the gradients of its outputs.  grads: (dq, dk, dq_weight, dk_weight) to write, dq and dk at
+    any token stride (slices of a fused projection's gradient); the weights' are fp32 [d]."""
+    import torch
+    if _elsewhere(q):
+        return _on_device(q, qk_norm_rope_backward, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions=positions,
+                          seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status)
+    p = _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    for name, g, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        if g.shape != x.shape:
+            raise ValueError(f"{name} must have shape {tuple(x.shape)}; it has {tuple(g.shape)}")
+        _check_vector(name, g, q, q.dtype, x.numel())
+    if grads is None:
+        dq, dk = torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        dwq, dwk = torch.empty(2, p.d, dtype=torch.float32, device=q.device).unbind()
+    else:
+        dq, dk, dwq, dwk = grads
+        for name, g, x in (("dq", dq, q), ("dk", dk, k)):
+            if g.shape != x.shape:
+                raise ValueError(f"{name} must have shape {tuple(x.shape)}; it has {tuple(g.shape)}")
+        p.dq_stride, p.dk_stride = _rows("dq", dq, q)[3], _rows("dk", dk, q)[3]
+        _check_vector("dq_weight", dwq, q, torch.float32, p.d)
+        _check_vector("dk_weight", dwk, q, torch.float32, p.d)
+    nbytes = fa_qk_norm_rope_bwd_workspace_size(p)
+    if nbytes == 0:
+        raise FaError(FA_ERR_UNSUPPORTED, "fa_qk_norm_rope_bwd_workspace_size")
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    else:
+        _check_vector("workspace", workspace, q, torch.uint8, workspace.numel())
+    rc = fa_qk_norm_rope_bwd(p, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                             dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream())
+    if rc != FA_OK:
+        raise FaError(rc, "fa_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, tokens, free_head=None, out=None, status=None):
+    """Runs fa_page_plan on int32 torch CUDA tensors; returns (cu_seqlens_q, seqused_k, positions,
+    slots, free_head_out) and writes the new pages' entries into block_table [B, max_blocks].
+
+    cached, fresh: [B] tokens in the cache and new ones; free_pages: pages to take from, from
+    index free_head ([1], None: 0) on; tokens: rows of the packed batch (positions and slots are
+    -1 behind the last new token).  out: the five results' tensors to write, status: [1] or None."""
+    import torch
+    if _elsewhere(cached):
+        return _on_device(cached, page_plan, cached, fresh, block_table, free_pages, page_size=page_size, num_pages=num_pages,
+                          tokens=tokens, free_head=free_head, out=out, status=status)
+    B, i32 = cached.numel(), torch.int32
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks_per_seq]")
+    blocks, n_free = block_table.shape[1], free_pages.numel()
+    for name, t, n in (("cached", cached, B), ("fresh", fresh, B), ("block_table", block_table, B * blocks),
+                       ("free_pages", free_pages, n_free), ("free_head", free_head, 1), ("status", status, 1)):
+        _check_vector(name, t, cached, i32, n)
+    sizes = (B + 1, B, tokens, tokens, 1)
+    if out is None:
+        out = torch.empty(2 * (B + tokens + 1), dtype=i32, device=cached.device).split(sizes)
+    else:
+        for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"), out, sizes):
+            _check_vector(name, t, cached, i32, n)
+    p = FaPagePlanParams(B, tokens, page_size, blocks, num_pages, n_free)
+    rc = fa_page_plan(p, cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(),
+                      None if free_head is None else free_head.data_ptr(), block_table.data_ptr(),
+                      *(t.data_ptr() for t in out), None if status is None else status.data_ptr(), _stream())
+    if rc != FA_OK:
+        raise FaError(rc, "fa_page_plan")
+    return tuple(out)
 
 
 def device_status(workspace) -> int:

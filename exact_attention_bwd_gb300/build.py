@@ -24,7 +24,8 @@ LIB = os.path.join(HERE, "libfa_gb300.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 TRACE_LIB = os.path.join(HERE, "libfa_gb300_trace.so")
 TRACE_BUILD_DIR = os.path.join(HERE, "_build_trace")
-SOURCES = ["api.cu", "fwd.cu", "fwd256.cu", "fwd_e4m3.cu", "bwd.cu", "decode.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "fwd.cu", "fwd256.cu", "fwd_e4m3.cu", "bwd.cu", "decode.cu", "noalloc.cu",
+           "paged.cu", "rope.cu", "page_plan.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 f"-I{INCLUDE}"]

@@ -89,8 +89,10 @@ bool encode_u8_4d(CUtensorMap* m, const void* base, const cuuint64_t dims[4], co
 // ------------------------------------------------------------------------------------------
 // profiling hooks
 // ------------------------------------------------------------------------------------------
-const char* const kKernelNames[] = {"fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post"};
-enum KernelId { kFwd = 0, kDecode, kCombine, kBwdPre, kBwdMain, kBwdPost, kNumKernels };
+const char* const kKernelNames[] = {"fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post", "paged_prep", "paged_few",
+                                    "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan"};
+enum KernelId { kFwd = 0, kDecode, kCombine, kBwdPre, kBwdMain, kBwdPost, kPagedPrep, kPagedFew, kPagedMerge, kNormRope,
+                kNormRopeBwd, kPagePlan, kNumKernels };
 
 struct Profiler {
     std::mutex mu;
@@ -135,7 +137,8 @@ fa_status normalise(const fa_params* in, Problem& p) {
     const fa_params& a = *in;
     if (a.B < 0 || a.s_q < 0 || a.s_kv < 0 || a.h_q <= 0 || a.h_kv <= 0 || a.d <= 0) return FA_ERR_INVALID_ARG;
     if (a.h_q % a.h_kv != 0) return FA_ERR_INVALID_ARG;
-    if ((a.cu_seqlens_q == nullptr) != (a.cu_seqlens_k == nullptr)) return FA_ERR_INVALID_ARG;
+    // packed queries come with packed keys, or (cu_seqlens_k absent) with a paged cache
+    if ((a.cu_seqlens_q == nullptr) != (a.cu_seqlens_k == nullptr) && !(a.cu_seqlens_q && a.block_table)) return FA_ERR_INVALID_ARG;
     if (a.window_left < -1 || a.window_right < -1) return FA_ERR_INVALID_ARG;
     if (a.d % 8 != 0 || a.d > 256) return FA_ERR_UNSUPPORTED;
     if (a.dtype != FA_DTYPE_BF16 && a.dtype != FA_DTYPE_F16 && a.dtype != FA_DTYPE_E4M3) return FA_ERR_INVALID_ARG;
@@ -166,13 +169,15 @@ fa_status normalise(const fa_params* in, Problem& p) {
     }
     p.dtype = a.dtype;
     p.wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNsDefault;
-    // KV-cache forms: a per-sequence used length, and a paged cache (dense q only)
+    // KV-cache forms: a per-sequence used length, and a paged cache
     p.seqused_q = a.seqused_q;
     p.seqused_k = a.seqused_k;
     p.block_table = a.block_table;
     if (a.block_table) {
-        if (p.cu_q) return FA_ERR_UNSUPPORTED;
-        if (a.page_size <= 0 || a.page_size % 128 != 0 || a.max_blocks_per_seq <= 0 || a.num_pages <= 0)
+        const bool packed = p.cu_q != nullptr;  // packed queries over a paged cache
+        if (packed && (p.cu_k || p.dtype == FA_DTYPE_E4M3)) return FA_ERR_UNSUPPORTED;
+        if (packed && !p.seqused_k) return FA_ERR_INVALID_ARG;
+        if (a.page_size <= 0 || a.page_size % (packed ? 16 : 128) != 0 || a.max_blocks_per_seq <= 0 || a.num_pages <= 0)
             return FA_ERR_INVALID_ARG;
         if ((long)a.max_blocks_per_seq * a.page_size < (long)a.s_kv) return FA_ERR_INVALID_ARG;
         p.page_size = a.page_size;
@@ -348,6 +353,123 @@ fa_status plan_fwd(const Problem& p, unsigned flags, FwdPlan& pl) {
 }
 
 // ------------------------------------------------------------------------------------------
+// packed queries over a paged cache
+// ------------------------------------------------------------------------------------------
+fa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+bool paged_packed(const Problem& p) { return p.block_table && p.cu_q; }
+
+struct PagedPlan {
+    bool empty = true;
+    int ctas = 0, few_rows = 0;
+    size_t off_pre = 0, off_o = 0, off_ml = 0, ws_bytes = kStatusBytes;
+};
+
+fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
+    pl = PagedPlan();
+    if (!supported_d(p.d)) return FA_ERR_UNSUPPORTED;
+    if (p.B == 0 || p.T_q == 0) return FA_OK;
+    pl.empty = false;
+    pl.ctas = sm_count();
+    const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
+    const long rows = longest * p.G;
+    pl.few_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    pl.off_pre = kStatusBytes;
+    pl.off_o = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
+    pl.off_ml = pl.off_o + align256((size_t)2 * pl.ctas * pl.few_rows * p.d * 4);
+    pl.ws_bytes = pl.off_ml + align256((size_t)2 * pl.ctas * pl.few_rows * 8);
+    return FA_OK;
+}
+
+fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const void* k, const void* v, void* o, float* lse,
+                    void* workspace, size_t ws_bytes, cudaStream_t st) {
+    PagedPlan pl;
+    fa_status rc = plan_paged(p, in, pl);
+    if (rc != FA_OK) return rc;
+    if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    if (ws_bytes < pl.ws_bytes) return FA_ERR_WORKSPACE;
+    int* status = reinterpret_cast<int*>(workspace);
+    if (pl.empty) return cuda_status(cudaMemsetAsync(status, 0, sizeof(int), st));
+    if (!q || !o || !k || !v || !aligned16(q) || !aligned16(o) || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    PagedArgs a{};
+    a.p = p;
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.o = reinterpret_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.num_pages = in.num_pages;
+    // the largest power of two that divides both the page and the key tile
+    a.box = p.page_size & -p.page_size;
+    if (a.box > kTileRows) a.box = kTileRows;
+    a.few_rows = pl.few_rows;
+    a.few_max = 0x7fffffffffffffffL;
+    a.many_rows = pl.few_rows;
+    a.no_split = (in.flags & FA_FLAG_NO_SPLIT) ? 1 : 0;
+    a.validate = (in.flags & FA_FLAG_VALIDATE_CU) ? 1 : 0;
+    a.pre = reinterpret_cast<long long*>(ws + pl.off_pre);
+    a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
+    a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+    a.status = status;
+    CUtensorMap tk, tv;
+    const bool f16 = p.dtype == FA_DTYPE_F16;
+    if (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16) ||
+        !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16))
+        return FA_ERR_CUDA;
+    cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
+    if (e == cudaSuccess) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
+    if (e == cudaSuccess) e = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, a.pre, pl.ctas, a.few_rows, st); });
+    return cuda_status(e);
+}
+
+// ------------------------------------------------------------------------------------------
+// norm and rotation of queries and keys
+// ------------------------------------------------------------------------------------------
+
+// Whether [a, a + na) and [b, b + nb) (bytes) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// Bytes from the first to the last element of T rows of `row` 16-bit values, `stride` apart.
+size_t span16(long T, long stride, long row) { return T > 0 ? ((size_t)(T - 1) * stride + row) * 2 : 0; }
+
+fa_status normalise_rope(const fa_rope_params* in, RopeArgs& a) {
+    if (!in) return FA_ERR_INVALID_ARG;
+    const fa_rope_params& x = *in;
+    if (x.T < 0 || x.h_q <= 0 || x.h_kv <= 0 || x.d <= 0 || x.rot_dim < 0 || x.rot_dim > x.d || !(x.eps >= 0.f)) return FA_ERR_INVALID_ARG;
+    if (x.dtype != FA_DTYPE_BF16 && x.dtype != FA_DTYPE_F16) return x.dtype == FA_DTYPE_E4M3 ? FA_ERR_UNSUPPORTED : FA_ERR_INVALID_ARG;
+    if (!supported_d(x.d) || x.rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+    // rows are read 16 bytes at a time
+    if (x.q_stride < (long long)x.h_q * x.d || x.k_stride < (long long)x.h_kv * x.d || x.q_stride % 8 || x.k_stride % 8)
+        return FA_ERR_INVALID_ARG;
+    if (x.rot_dim > 0 && (!x.cos || !x.sin || !aligned16(x.cos) || !aligned16(x.sin) || x.max_pos <= 0)) return FA_ERR_INVALID_ARG;
+    if (!aligned16(x.q_weight) || !aligned16(x.k_weight)) return FA_ERR_INVALID_ARG;
+    if (!x.positions && (x.seq_len <= 0 || (x.rot_dim > 0 && (x.seq_len < x.T ? x.seq_len : x.T) > x.max_pos))) return FA_ERR_INVALID_ARG;
+    a = RopeArgs{};
+    a.T = x.T;
+    a.h_q = x.h_q;
+    a.h_kv = x.h_kv;
+    a.d = x.d;
+    a.rot = x.rot_dim;
+    a.adjacent = x.interleaved ? 1 : 0;
+    a.seq_len = x.seq_len;
+    a.f16 = x.dtype == FA_DTYPE_F16 ? 1 : 0;
+    a.weight_f32 = x.weight_f32 ? 1 : 0;
+    a.max_pos = x.rot_dim > 0 ? x.max_pos : 0x7fffffff;
+    a.eps = x.eps;
+    a.q_stride = (long)x.q_stride;
+    a.k_stride = (long)x.k_stride;
+    a.positions = x.positions;
+    a.cos = x.cos;
+    a.sin = x.sin;
+    a.wq = x.q_weight;
+    a.wk = x.k_weight;
+    a.status = x.status;
+    return FA_OK;
+}
+
+// ------------------------------------------------------------------------------------------
 // backward plan
 // ------------------------------------------------------------------------------------------
 struct BwdPlan {
@@ -409,8 +531,6 @@ fa_status plan_bwd(const Problem& p, unsigned flags, BwdPlan& pl) {
     return FA_OK;
 }
 
-fa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
-
 __global__ void validate_cu_kernel(const int32_t* cu_q, const int32_t* cu_k, int n, int Tq, int Tk, int* status) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i > n) return;
@@ -456,6 +576,10 @@ const char* fa_status_string(fa_status s) {
 size_t fa_fwd_workspace_size(const fa_params* in) {
     Problem p;
     if (normalise(in, p) != FA_OK) return 0;
+    if (paged_packed(p)) {
+        PagedPlan pp;
+        return plan_paged(p, *in, pp) == FA_OK ? pp.ws_bytes : 0;
+    }
     FwdPlan pl;
     if (plan_fwd(p, in->flags, pl) != FA_OK) return 0;
     return pl.ws_bytes;
@@ -474,6 +598,7 @@ fa_status fa_fwd(const fa_params* in, const void* q, const void* k, const void* 
     Problem p;
     fa_status rc = normalise(in, p);
     if (rc != FA_OK) return rc;
+    if (paged_packed(p)) return paged_fwd(p, *in, q, k, v, o, lse, workspace, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
     FwdPlan pl;
     if ((rc = plan_fwd(p, in->flags, pl)) != FA_OK) return rc;
     if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
@@ -674,6 +799,126 @@ fa_status fa_bwd(const fa_params* in, const void* q, const void* k, const void* 
     if (e != cudaSuccess) return FA_ERR_CUDA;
     e = timed(kBwdPost, st, [&] { return launch_bwd_post(a, st); });
     return cuda_status(e);
+}
+
+fa_status fa_qk_norm_rope(const fa_rope_params* in, const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                          void* k_cache, void* v_cache, struct CUstream_st* stream) {
+    RopeArgs a;
+    fa_status rc = normalise_rope(in, a);
+    if (rc != FA_OK) return rc;
+    if (a.T == 0) return FA_OK;
+    const bool append = k_cache || v_cache || in->slots;
+    // an append needs all of its parts; without one there is no value to copy
+    if (append && (!k_cache || !v_cache || !in->slots || !v || in->num_slots <= 0)) return FA_ERR_INVALID_ARG;
+    if (!append && (v || !k_out)) return FA_ERR_INVALID_ARG;
+    if (append && (in->v_stride < (long long)a.h_kv * a.d || in->v_stride % 8)) return FA_ERR_INVALID_ARG;
+    if (!q || !k || !q_out) return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache))
+        return FA_ERR_INVALID_ARG;
+    const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;
+    // a row is read whole before it is written: an output may be its own input, in the same layout,
+    // and nothing else that the call touches
+    const size_t nq = span16(a.T, a.q_stride, wq), nk = span16(a.T, a.k_stride, wk), oq = span16(a.T, wq, wq), ok = span16(a.T, wk, wk);
+    const size_t nv = v ? span16(a.T, (long)in->v_stride, wk) : 0, nc = append ? (size_t)in->num_slots * wk * 2 : 0;
+    const bool own_q = q_out == q && a.q_stride == wq, own_k = k_out == k && a.k_stride == wk;
+    if ((!own_q && overlap(q_out, oq, q, nq)) || overlap(q_out, oq, k, nk) || overlap(q_out, oq, v, nv) || overlap(q_out, oq, k_out, ok) ||
+        overlap(k_out, ok, q, nq) || (!own_k && overlap(k_out, ok, k, nk)) || overlap(k_out, ok, v, nv))
+        return FA_ERR_INVALID_ARG;
+    for (const void* cache : {(const void*)k_cache, (const void*)v_cache})
+        if (overlap(cache, nc, q, nq) || overlap(cache, nc, k, nk) || overlap(cache, nc, v, nv) || overlap(cache, nc, q_out, oq) ||
+            overlap(cache, nc, k_out, ok))
+            return FA_ERR_INVALID_ARG;
+    if (overlap(k_cache, nc, v_cache, nc)) return FA_ERR_INVALID_ARG;
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.k = reinterpret_cast<const uint16_t*>(k);
+    a.v = reinterpret_cast<const uint16_t*>(v);
+    a.v_stride = (long)in->v_stride;
+    a.q_out = reinterpret_cast<uint16_t*>(q_out);
+    a.k_out = reinterpret_cast<uint16_t*>(k_out);
+    a.k_cache = reinterpret_cast<uint16_t*>(k_cache);
+    a.v_cache = reinterpret_cast<uint16_t*>(v_cache);
+    a.slots = in->slots;
+    a.num_slots = (long)in->num_slots;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, st); }));
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* in) {
+    RopeArgs a;
+    if (normalise_rope(in, a) != FA_OK) return 0;
+    const int ctas = norm_rope_bwd_ctas((long)a.T * a.h_q, a.d, sm_count());
+    return align256((size_t)2 * ctas * a.d * 4);
+}
+
+fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const void* k, const void* dq_out, const void* dk_out,
+                              void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes,
+                              struct CUstream_st* stream) {
+    RopeArgs a;
+    fa_status rc = normalise_rope(in, a);
+    if (rc != FA_OK) return rc;
+    const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;
+    if (in->dq_stride < wq || in->dk_stride < wk || in->dq_stride % 8 || in->dk_stride % 8) return FA_ERR_INVALID_ARG;
+    if (!dq_weight || !dk_weight || !workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    const int ctas = norm_rope_bwd_ctas((long)a.T * a.h_q, a.d, sm_count());
+    if (ws_bytes < align256((size_t)2 * ctas * a.d * 4)) return FA_ERR_WORKSPACE;
+    if (a.T > 0) {
+        if (!q || !k || !dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
+        if (!aligned16(q) || !aligned16(k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk))
+            return FA_ERR_INVALID_ARG;
+        // dq may be q or dq_out, dk may be k or dk_out, in the same layout (strided halves of one
+        // buffer interleave, so their spans say nothing: there, only the same start is looked at)
+        const size_t gq = span16(a.T, wq, wq), gk = span16(a.T, wk, wk);
+        const size_t oq = span16(a.T, (long)in->dq_stride, wq), ok = span16(a.T, (long)in->dk_stride, wk);
+        const bool same_q = dq == q && in->dq_stride == a.q_stride, same_k = dk == k && in->dk_stride == a.k_stride;
+        const bool same_gq = dq == dq_out && in->dq_stride == wq, same_gk = dk == dk_out && in->dk_stride == wk;
+        if ((!same_q && dq == q) || (!same_k && dk == k) || (!same_gq && overlap(dq, oq, dq_out, gq)) ||
+            (!same_gk && overlap(dk, ok, dk_out, gk)) || overlap(dq, oq, dk_out, gk) || overlap(dk, ok, dq_out, gq) || dq == dk)
+            return FA_ERR_INVALID_ARG;
+    }
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.k = reinterpret_cast<const uint16_t*>(k);
+    a.dq_out = reinterpret_cast<const uint16_t*>(dq_out);
+    a.dk_out = reinterpret_cast<const uint16_t*>(dk_out);
+    a.dq = reinterpret_cast<uint16_t*>(dq);
+    a.dk = reinterpret_cast<uint16_t*>(dk);
+    a.dq_stride = (long)in->dq_stride;
+    a.dk_stride = (long)in->dk_stride;
+    a.dwq = dq_weight;
+    a.dwk = dk_weight;
+    a.dw_part = reinterpret_cast<float*>(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(timed(kNormRopeBwd, st, [&] { return launch_norm_rope_bwd(a, ctas, st); }));
+}
+
+fa_status fa_page_plan(const fa_page_plan_params* in, const int32_t* cached, const int32_t* fresh, const int32_t* free_pages,
+                       const int32_t* free_head, int32_t* block_table, int32_t* cu_seqlens_q, int32_t* seqused_k,
+                       int32_t* positions, int32_t* slots, int32_t* free_head_out, int32_t* status, struct CUstream_st* stream) {
+    if (!in) return FA_ERR_INVALID_ARG;
+    const fa_page_plan_params& x = *in;
+    if (x.B < 0 || x.T < 0 || x.page_size <= 0 || x.max_blocks_per_seq <= 0 || x.num_pages <= 0 || x.n_free < 0) return FA_ERR_INVALID_ARG;
+    // positions and slots are 32-bit
+    if ((long long)x.max_blocks_per_seq * x.page_size > 0x7fffffffLL || (long long)x.num_pages * x.page_size > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    if (!cu_seqlens_q || !free_head_out || (x.B > 0 && (!cached || !fresh || !block_table || !seqused_k)) ||
+        (x.T > 0 && (!positions || !slots)) || (x.n_free > 0 && !free_pages))
+        return FA_ERR_INVALID_ARG;
+    // every CTA reads the lengths, the free list and its head while others write: no output may be one
+    const struct { const void* at; size_t n; } ins[] = {{cached, (size_t)x.B * 4}, {fresh, (size_t)x.B * 4},
+                                                        {free_pages, (size_t)x.n_free * 4}, {free_head, 4}};
+    const struct { const void* at; size_t n; } outs[] = {{block_table, (size_t)x.B * x.max_blocks_per_seq * 4},
+                                                         {cu_seqlens_q, ((size_t)x.B + 1) * 4}, {seqused_k, (size_t)x.B * 4},
+                                                         {positions, (size_t)x.T * 4}, {slots, (size_t)x.T * 4}, {free_head_out, 4}};
+    for (int i = 0; i < 6; ++i) {
+        for (const auto& y : ins)
+            if (overlap(outs[i].at, outs[i].n, y.at, y.n)) return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].at, outs[i].n, outs[j].at, outs[j].n)) return FA_ERR_INVALID_ARG;
+    }
+    PagePlanArgs a{x.B, x.T, x.page_size, x.max_blocks_per_seq, x.num_pages, x.n_free, cached, fresh, free_pages, free_head,
+                   block_table, cu_seqlens_q, seqused_k, positions, slots, free_head_out, status};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(timed(kPagePlan, st, [&] { return launch_page_plan(a, st); }));
 }
 
 fa_status fa_read_device_status(const void* workspace, struct CUstream_st* stream) {

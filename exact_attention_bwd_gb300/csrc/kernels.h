@@ -125,6 +125,54 @@ struct BwdArgs {
     unsigned long long* trace;  // trace builds only: the workspace's trace region (else null)
 };
 
+// ------------------------------------------------------------------------------------------
+// packed queries over a paged cache
+// ------------------------------------------------------------------------------------------
+struct PagedArgs {
+    Problem p;          // cu_q, seqused_k, block_table; T_q rows of q, s_kv the longest cache
+    const uint16_t* q;  // [T_q, h_q, d]
+    uint16_t* o;
+    float* lse;         // [h_q, T_q] or null
+    int num_pages;
+    int box;            // rows of one K / V copy: the part of a 128-key tile that lies in one page
+    int few_rows;       // rows of a row tile of the few-row kernel
+    long few_max;       // sequences of at most this many rows are its work
+    int many_rows;      // rows of a row tile of the tensor-core kernel, the others' work
+    int no_split;       // every item whole
+    int validate;       // check the offsets and lengths first
+    long long* pre;     // [2][B + 1] units before each sequence: few-row work, the rest
+    float* part_o;      // [2 CTAs][rows][d] un-normalised partial outputs
+    float2* part_ml;    // [2 CTAs][rows] reference maximum (log2 units) and sum
+    int* status;
+};
+
+// ------------------------------------------------------------------------------------------
+// around the attention: norm and rotation of queries and keys, the page plan
+// ------------------------------------------------------------------------------------------
+struct RopeArgs {
+    int T, h_q, h_kv, d, rot, adjacent, seq_len, f16, weight_f32, max_pos;
+    float eps;
+    long q_stride, k_stride, v_stride, dq_stride, dk_stride;  // elements between tokens
+    const int32_t* positions;  // [T] or null: t % seq_len
+    const float *cos, *sin;    // [max_pos, rot / 2]
+    const void *wq, *wk;       // [d] or null
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_out, *k_cache, *v_cache;
+    const int32_t* slots;
+    long num_slots;
+    const uint16_t *dq_out, *dk_out;
+    uint16_t *dq, *dk;
+    float *dwq, *dwk, *dw_part;
+    int* status;
+    int segments;              // warps per token
+};
+
+struct PagePlanArgs {
+    int B, T, page_size, max_blocks, num_pages, n_free;
+    const int32_t *cached, *fresh, *free_pages, *free_head;
+    int32_t *table, *cu, *used, *positions, *slots, *head_out, *status;
+};
+
 // host-side launchers (defined next to each kernel)
 cudaError_t launch_fwd(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        cudaStream_t st);
@@ -140,6 +188,13 @@ cudaError_t launch_bwd_pre(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_bwd_main(const BwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& tdo, cudaStream_t st);
 cudaError_t launch_bwd_post(const BwdArgs& a, cudaStream_t st);
+cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedArgs& a, const long long* pre, int ctas, int rows, cudaStream_t st);
+cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int ctas, cudaStream_t st);
+int norm_rope_bwd_ctas(long rows, int d, int sms);
+cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st);
 
 // Number of 16-byte-aligned KV tiles etc. shared by planner and kernels.
 constexpr int kTileRows = 128;

@@ -1,0 +1,786 @@
+// Attention of packed queries over a paged cache, few query rows per key/value head (decode,
+// verification of drafted tokens, short chunks), with its schedule and combine.
+//
+// With few rows the work is a stream over the cache, so the tensor cores take the keys as the
+// long side: S^T = K Q^T (128 keys x NR rows) and O^T = V^T P^T (d x NR rows), both with the
+// cache tile as the 128-row operand straight from the swizzled tile that TMA wrote, and NR = 16,
+// 32 or 64 columns.  A key is a TMEM lane, so each of 128 threads does the softmax of one key
+// for all rows: NR exponentials a tile and thread, a small part of the time its 128 keys take
+// to arrive.  The online softmax's reference maximum is only moved when some score passes it
+// by more than 2^8 (one vote per tile), so the cross-lane maxima are formed rarely.
+//
+// Warp roles (256 threads, one CTA per SM):
+//   warp 0       TMA producer: K and V tiles, page by page, through a ring of [128 keys] units
+//   warp 1       MMA issuer (one thread)
+//   warp 2       owns the TMEM allocation
+//   warp 3       scheduler: finds the CTA's pieces of work, stages each item's Q rows
+//   warps 4..7   softmax (thread = key) and epilogue (thread = column of O)
+#include "paged.cuh"
+
+namespace fa {
+namespace {
+
+// ------------------------------------------------------------------------------------------
+// schedule: the line of units
+// ------------------------------------------------------------------------------------------
+constexpr int kPrepThreads = 1024;
+
+__global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArgs a) {
+    __shared__ long long warp_sum[2][32];
+    __shared__ int bad_any;
+    const Problem& p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long run0 = 0, run1 = 0;
+    bool bad = false;
+    if (tid == 0) bad_any = 0;
+    __syncthreads();
+    for (int base = 0; base < p.B; base += kPrepThreads) {
+        const int b = base + tid;
+        long long w0 = 0, w1 = 0;
+        if (b < p.B) {
+            if (a.validate) {
+                bad = bad || (b == 0 && p.cu_q[0] != 0) || p.cu_q[b + 1] < p.cu_q[b] || p.cu_q[b + 1] > p.T_q ||
+                      p.seqused_k[b] < 0 || p.seqused_k[b] > p.s_kv;
+            }
+            const PagedSeq s = paged_seq(p, b);
+            const long rows = (long)s.nq * p.G;
+            if (rows > 0) {
+                const bool few = rows <= a.few_max;
+                const int step = few ? a.few_rows : a.many_rows;
+                long long w = 0;
+                for (long r = 0; r < rows; r += step) {
+                    int t0, t1;
+                    w += paged_tiles(p, s, r, step, t0, t1);
+                }
+                (few ? w0 : w1) = w * p.h_kv;
+            }
+        }
+        long long s0 = w0, s1 = w1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x0 = __shfl_up_sync(0xffffffffu, s0, o), x1 = __shfl_up_sync(0xffffffffu, s1, o);
+            if (lane >= o) {
+                s0 += x0;
+                s1 += x1;
+            }
+        }
+        if (lane == 31) {
+            warp_sum[0][warp] = s0;
+            warp_sum[1][warp] = s1;
+        }
+        __syncthreads();
+        long long b0 = run0, b1 = run1;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) {
+                b0 += warp_sum[0][w];
+                b1 += warp_sum[1][w];
+            }
+            run0 += warp_sum[0][w];
+            run1 += warp_sum[1][w];
+        }
+        if (b < p.B) {
+            a.pre[b + 1] = b0 + s0;
+            a.pre[p.B + 1 + b + 1] = b1 + s1;
+        }
+        __syncthreads();
+    }
+    if (bad) bad_any = 1;
+    __syncthreads();
+    if (tid == 0) {
+        a.pre[0] = 0;
+        a.pre[p.B + 1] = 0;
+        *a.status = bad_any ? kStatusDeviceCheck : kStatusOk;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// few-row kernel
+// ------------------------------------------------------------------------------------------
+constexpr int kThreadsFew = 256;
+constexpr int kItems = 4;
+constexpr int kSmemMax = 227 * 1024;
+
+constexpr int pow2_at_least(int x) { return x <= 32 ? 32 : x <= 64 ? 64 : x <= 128 ? 128 : x <= 256 ? 256 : 512; }
+
+template <int D, int NR>
+struct FewCfg {
+    static constexpr int UC = D == 256 ? 128 : D;      // columns of a ring unit
+    static constexpr int KU = D / UC;                  // units of a K (or V) tile
+    static constexpr int CHUNK = kKeyTile * 128;       // [128 keys][64 columns]
+    static constexpr int UNIT = kKeyTile * UC * 2;
+    static constexpr int Q_BYTES = NR * D * 2, P_BYTES = NR * kKeyTile * 2;
+    static constexpr int Q_BUFS = Q_BYTES <= 16384 ? 2 : 1;
+    static constexpr int FIT = (kSmemMax - 1024 - 4096 - Q_BUFS * Q_BYTES - 2 * P_BYTES) / UNIT;
+    // at d = 64 the ring is even (see slot_of)
+    static constexpr int RING = D == 64 ? (FIT > 12 ? 12 : FIT / 2 * 2) : (FIT > 6 ? 6 : FIT);
+    static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile and the next K have to fit");
+    static constexpr int OH = D > 128 ? 2 : 1;         // 128-lane accumulators of O^T
+    static constexpr int TMEM_COLS = pow2_at_least(2 * NR + OH * NR);
+    // Unit n of the stream: K and V tiles in turn.  At d = 64 the 128-row V^T operand takes the
+    // slot behind V's as its second 64 rows (their products, lanes 64 .. 127, are not read): K and V
+    // swap slots so that this is the K of the same tile, which is held until then.
+    __device__ static __forceinline__ int slot_of(uint32_t n) { return D == 64 ? (int)(n % RING) ^ 1 : (int)(n % RING); }
+};
+
+struct FewItem {
+    int end;
+    int b, q0, nq, nk, g;
+    int r0, rows;      // first row of the sequence's (position, head) rows, rows held
+    int t0, t1;        // key tiles
+    int lo, hi;        // keys that any row of the item may see
+    int part;          // partial slot, or -1: the item is whole
+};
+
+template <int D, int NR>
+struct __align__(1024) FewSmem {
+    using C = FewCfg<D, NR>;
+    uint8_t ring[C::RING][C::UNIT];
+    uint8_t q[C::Q_BUFS][C::Q_BYTES];
+    uint8_t p[2][C::P_BYTES];
+    float mref[NR], alpha[NR];  // reference maxima of the item's rows (log2 units), last change as a factor
+    float wmax[4][NR];
+    float lsum[4][NR];
+    uint64_t full[C::RING], empty[C::RING];
+    uint64_t q_full[C::Q_BUFS], q_empty[C::Q_BUFS];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain;
+    uint64_t item_full[kItems], item_empty[kItems];
+    FewItem item[kItems];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// NR consecutive fp32 TMEM columns of the warp's 32 lanes.
+template <int NR>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t* r) {
+    if constexpr (NR == 16) tmem_ld_32x32b_x16(addr, r);
+    else if constexpr (NR == 32) tmem_ld_32x32b_x32(addr, r);
+    else tmem_ld_32x32b_x64(addr, r);
+}
+template <int NR>
+__device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t* r) {
+    if constexpr (NR == 16) tmem_st_32x32b_x16(addr, r);
+    else if constexpr (NR == 32) tmem_st_32x32b_x32(addr, r);
+    else tmem_st_32x32b_x64(addr, r);
+}
+
+// Votes of the four softmax warps (named barrier 1): what one of them decides all decide, so no
+// warp is left waiting for another that gave up.
+__device__ __forceinline__ bool vote_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool vote_and(bool x) { return !vote_or(!x); }
+
+// Largest value over the warp, by the order of its bits as an integer.
+__device__ __forceinline__ float warp_max(float x) {
+    const int i = __float_as_int(x);
+    const int key = i >= 0 ? i : i ^ 0x7fffffff;
+    const int m = __reduce_max_sync(0xffffffffu, key);
+    return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreadsFew, 1)
+    paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    using C = FewCfg<D, NR>;
+    constexpr int RING = C::RING, KU = C::KU;
+    extern __shared__ uint8_t smem_raw[];
+    FewSmem<D, NR>& s = *reinterpret_cast<FewSmem<D, NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Problem& p = a.p;
+    const bool f16 = p.dtype == FA_DTYPE_F16;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (*reinterpret_cast<volatile int*>(a.status) != 0) return;
+    const long long W = a.pre[p.B];
+    const int n_ctas = paged_ctas(W, (int)gridDim.x), cta = blockIdx.x;
+    if (cta >= n_ctas) return;
+
+    Abort ab{&s.abort_flag, a.status, p.wait_ns};
+    if (tid == 0) {
+        s.abort_flag = 0;
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < C::Q_BUFS; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.pv_done[i], 1);
+        }
+        mbar_init(&s.o_free, 4);
+        mbar_init(&s.drain, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&s.item_full[i], 1);
+            mbar_init(&s.item_empty[i], 6);  // producer, MMA issuer, four softmax warps
+        }
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(&s.tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    constexpr uint32_t cS = 0, cO = 2 * NR;  // TMEM columns of the two S buffers and of O
+
+    if (warp == 0) {
+        // ================= TMA producer =================
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        const int boxes = kKeyTile / a.box;
+        uint32_t n = 0;  // units issued
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int slot = it % kItems;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (it / kItems) & 1, ab)))) break;
+            const int end = s.item[slot].end, b = s.item[slot].b, nk = s.item[slot].nk, g = s.item[slot].g;
+            const int t0 = s.item[slot].t0, t1 = s.item[slot].t1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[slot]);
+            if (end) break;
+            const int32_t* table = p.block_table + (long)b * p.max_blocks;
+            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used
+            // keys or for a table entry outside the pool.  The entry of the next tile is on its way
+            // while this one waits for its slots.
+            auto entry = [&](int t) {
+                const int j = t * kKeyTile + lane * a.box;
+                return lane < boxes && t < t1 && j < nk ? table[j / p.page_size] : a.num_pages;
+            };
+            int next = entry(t0);
+            for (int t = t0; ok && t < t1; ++t) {
+                int page = next;
+                next = entry(t + 1);
+                const int j = t * kKeyTile + lane * a.box, row = j % p.page_size;
+                if (lane < boxes && (unsigned)page >= (unsigned)a.num_pages) {
+                    if (j < nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    page = a.num_pages;
+                }
+#pragma unroll
+                for (int x = 0; x < 2 * KU; ++x, ++n) {
+                    const int sl = C::slot_of(n);
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.empty[sl], ((n / RING) & 1) ^ 1, ab)))) break;
+                    if (lane == 0) mbar_expect_tx(&s.full[sl], C::UNIT);
+                    __syncwarp();
+                    if (lane < boxes) {
+#pragma unroll
+                        for (int c = 0; c < C::UC / 64; ++c)
+                            tma_load_4d(&s.ring[sl][c * C::CHUNK + lane * a.box * 128], x < KU ? &tmk : &tmv, &s.full[sl],
+                                        (x % KU) * C::UC + c * 64, g, row, page);
+                    }
+                }
+            }
+        }
+        // every copy still in flight lands before the CTA may exit
+        for (uint32_t back = 1; back <= (uint32_t)RING && back <= n; ++back)
+            mbar_wait_quiet(&s.full[C::slot_of(n - back)], ((n - back) / RING) & 1);
+    } else if (warp == 1) {
+        // ================= MMA issuer =================
+        if (lane == 0) {
+            const uint32_t idS = idesc_16(128, NR, false, false, f16);
+            const uint32_t idO = idesc_16(128, NR, true, false, f16);
+            uint32_t gt = 0, qi = 0;  // tiles whose S was issued, items with keys
+            uint32_t gp = 0;          // tiles whose P V was issued
+            bool ok = true;
+            auto wait_unit = [&](uint32_t n) { return mbar_wait(&s.full[C::slot_of(n)], (n / RING) & 1, ab); };
+            auto issue_s = [&](uint32_t q_addr) {
+                for (int h = 0; h < KU; ++h) {
+                    const uint32_t n = 2 * KU * gt + h;
+                    if (!wait_unit(n)) return false;
+                    tc_fence_after();
+                    const int sl = C::slot_of(n);
+                    const uint64_t kd = sdesc_sw128(smem_u32(s.ring[sl]), 16, 1024);
+                    const uint64_t qd = sdesc_sw128(q_addr + h * (C::UC / 64) * NR * 128, 16, 1024);
+#pragma unroll
+                    for (int c = 0; c < C::UC / 64; ++c)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_ss(tmem + cS + NR * (gt & 1), kd + c * (C::CHUNK >> 4) + 2 * x, qd + c * (NR * 8) + 2 * x, idS,
+                                   h > 0 || c > 0 || x > 0 ? 1u : 0u);
+                    if (D != 64) tc_commit(&s.empty[sl]);
+                }
+                tc_commit(&s.s_full[gt & 1]);
+                ++gt;
+                return true;
+            };
+            for (int it = 0; ok; ++it) {
+                const int slot = it % kItems;
+                if (!(ok = mbar_wait(&s.item_full[slot], (it / kItems) & 1, ab))) break;
+                const int end = s.item[slot].end, nt = s.item[slot].t1 - s.item[slot].t0;
+                mbar_arrive(&s.item_empty[slot]);
+                if (end) break;
+                if (nt <= 0) continue;
+                const int qb = (int)(qi % C::Q_BUFS);
+                if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
+                tc_fence_after();
+                const uint32_t q_addr = smem_u32(s.q[qb]);
+                if (!(ok = issue_s(q_addr))) break;
+                for (int t = 0; t < nt; ++t, ++gp) {
+                    if (t + 1 < nt) {
+                        if (!(ok = issue_s(q_addr))) break;
+                    }
+                    if (t + 2 == nt || nt == 1) tc_commit(&s.q_empty[qb]);  // the item's last S is issued
+                    const int pb = gp & 1;
+                    if (!(ok = mbar_wait(&s.p_full[pb], (gp >> 1) & 1, ab))) break;
+                    // the previous item's O has been read
+                    if (t == 0 && qi > 0 && !(ok = mbar_wait(&s.o_free, (qi - 1) & 1, ab))) break;
+                    const uint64_t pd = sdesc_sw128(smem_u32(s.p[pb]), 16, 1024);
+                    auto issue_pv = [&](uint32_t o_col, uint32_t v_addr) {
+                        const uint64_t vd = sdesc_sw128(v_addr, C::CHUNK, 1024);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            mma_ss(tmem + o_col, vd + 128 * x, pd + (x / 4) * (NR * 8) + 2 * (x % 4), idO, t > 0 || x > 0 ? 1u : 0u);
+                    };
+                    for (int h = 0; h < KU; ++h) {
+                        const uint32_t n = 2 * KU * gp + KU + h;
+                        if (!(ok = wait_unit(n))) break;
+                        tc_fence_after();
+                        const int sl = C::slot_of(n);
+                        issue_pv(cO + NR * h, smem_u32(s.ring[sl]));
+                        // d = 192: columns 64 .. 191 again as the second accumulator
+                        if (D == 192) issue_pv(cO + NR, smem_u32(s.ring[sl]) + C::CHUNK);
+                        tc_commit(&s.empty[sl]);
+                    }
+                    if (!ok) break;
+                    if (D == 64) tc_commit(&s.empty[C::slot_of(2 * gp)]);
+                    tc_commit(&s.pv_done[pb]);
+                }
+                ++qi;
+            }
+            tc_commit(&s.drain);
+            mbar_wait_quiet(&s.drain, 0);
+        }
+    } else if (warp == 3) {
+        // ================= scheduler =================
+        long long u = (long long)cta * W / n_ctas;
+        const long long u_end = (long long)(cta + 1) * W / n_ctas;
+        int it = 0, b = -1;
+        uint32_t qi = 0;
+        bool ok = true;
+        PagedSeq sq{};
+        long long pb = 0, pe = 0;  // units before and up to the end of the sequence
+        while (ok && u < u_end) {
+            if (u >= pe) {
+                b = find_sequence(a.pre, p.B, u);
+                pb = a.pre[b];
+                pe = a.pre[b + 1];
+                sq = paged_seq(p, b);
+            }
+            const PagedUnit x = paged_unit(p, sq, NR, u - pb);
+            if (a.no_split && x.k > 0) {  // the item belongs to the CTA that holds its first unit
+                u += x.cost - x.k;
+                continue;
+            }
+            const int take = a.no_split ? x.cost : (int)min((long long)(x.cost - x.k), u_end - u);
+            const int t0 = x.t0 + x.k, t1 = min(t0 + take, x.t1);
+            const int r0 = x.rt * NR, rows = min(NR, sq.nq * p.G - r0);
+            const int slot = it % kItems;
+            if (it >= kItems && !(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_empty[slot], ((it / kItems) - 1) & 1, ab)))) break;
+            if (lane == 0) {
+                const Band bd{sq.nk - sq.nq, p.left, p.right, sq.nk};
+                FewItem& w = s.item[slot];
+                w.end = 0;
+                w.b = b;
+                w.q0 = sq.q0;
+                w.nq = sq.nq;
+                w.nk = sq.nk;
+                w.g = x.g;
+                w.r0 = r0;
+                w.rows = rows;
+                w.t0 = t0;
+                w.t1 = t1;
+                w.lo = bd.lo(r0 / p.G);
+                w.hi = bd.hi((r0 + rows - 1) / p.G);
+                w.part = take == x.cost ? -1 : 2 * cta + (x.k == 0 ? 1 : 0);
+                mbar_arrive(&s.item_full[slot]);
+            }
+            ++it;
+            u += take;
+            if (t1 <= t0) continue;
+            // Q rows of the item, in the 128-byte-swizzled layout the MMA reads; zeros past them
+            const int qb = (int)(qi % C::Q_BUFS);
+            if (qi >= (uint32_t)C::Q_BUFS &&
+                !(ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty[qb], ((qi / C::Q_BUFS) - 1) & 1, ab))))
+                break;
+            constexpr int UNITS = NR * D / 8;  // 16-byte units
+            constexpr int BATCH = 4;
+            static_assert(UNITS % (32 * BATCH) == 0, "whole batches of the warp");
+#pragma unroll 1
+            for (int y = 0; y < UNITS; y += 32 * BATCH) {
+                uint4 v[BATCH];
+#pragma unroll
+                for (int z = 0; z < BATCH; ++z) {
+                    const int e = y + 32 * z + lane, r = e / (D / 8), col = e % (D / 8);
+                    v[z] = make_uint4(0, 0, 0, 0);
+                    if (r < rows) {
+                        const int i = (r0 + r) / p.G, h = x.g * p.G + (r0 + r) - i * p.G;
+                        v[z] = *reinterpret_cast<const uint4*>(a.q + (((long)sq.q0 + i) * p.h_q + h) * D + 8 * col);
+                    }
+                }
+#pragma unroll
+                for (int z = 0; z < BATCH; ++z) {
+                    const int e = y + 32 * z + lane, r = e / (D / 8), col = e % (D / 8);
+                    *reinterpret_cast<uint4*>(&s.q[qb][(col >> 3) * NR * 128 + r * 128 + (((col ^ r) & 7) << 4)]) = v[z];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.q_full[qb]);
+            ++qi;
+        }
+        if (ok) {
+            const int slot = it % kItems;
+            if (it < kItems || __all_sync(0xffffffffu, mbar_wait(&s.item_empty[slot], ((it / kItems) - 1) & 1, ab))) {
+                if (lane == 0) {
+                    s.item[slot].end = 1;
+                    mbar_arrive(&s.item_full[slot]);
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ================= softmax: one thread per key =================
+        const int key = tid - 128, sub = warp & 3;
+        const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
+        const float c = p.scale_log2;
+        // byte offset of this key in row r of a P buffer: p_at[r & 7] + 128 r
+        uint32_t p_at[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            p_at[x] = (key >> 6) * (NR * 128) + (((((key & 63) >> 3) ^ x) & 7) << 4) + (key & 7) * 2;
+        uint32_t gt = 0;  // tiles done
+        bool ok = true;
+        for (int it = 0;; ++it) {
+            const int slot = it % kItems;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (it / kItems) & 1, ab)) && ok;
+            if (!vote_and(ok)) break;
+            if (s.item[slot].end) break;
+            const FewItem& w = s.item[slot];
+            const int t0 = w.t0, t1 = w.t1, off = w.nk - w.nq, nk = w.nk, lo = w.lo, hi = w.hi, r0 = w.r0;
+            // a tile inside [in_lo, in_hi] is seen by every row
+            const int in_lo = p.left >= 0 ? (r0 + w.rows - 1) / p.G + off - p.left : 0;
+            const int in_hi = p.right >= 0 ? min(nk - 1, r0 / p.G + off + p.right) : nk - 1;
+            float l[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            bool gave_up = false;
+            for (int t = t0; t < t1; ++t, ++gt) {
+                const int buf = gt & 1, j0 = t * kKeyTile, j = j0 + key;
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (gt >> 1) & 1, ab)) && ok;
+                tc_fence_after();
+                uint32_t sr[NR];
+                tmem_ld_cols<NR>(tmem + lane_base + cS + NR * buf, sr);
+                const bool edge = j0 < in_lo || j0 + kKeyTile - 1 > in_hi;
+                if (edge) {
+                    // rows that see key j: positions j - off - right <= i <= j - off + left
+                    int ra = 0, rb = NR - 1;
+                    if (p.right >= 0) ra = (int)max(min(((long)j - off - p.right) * p.G - r0, (long)NR), 0l);
+                    if (p.left >= 0) rb = (int)min(max(((long)j - off + p.left + 1) * p.G - 1 - r0, -1l), (long)NR);
+                    if (j >= nk) ra = NR;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (r < ra || r > rb) sr[r] = __float_as_uint(-INFINITY);
+                    // values at keys that no row sees may be anything (unused rows of a page): 0 * NaN
+                    // would reach every row, so they are cleared
+                    bool there = true;
+#pragma unroll
+                    for (int h = 0; h < KU; ++h) {
+                        const uint32_t n = 2 * KU * gt + KU + h;
+                        const int sl = C::slot_of(n);
+                        there = mbar_wait(&s.full[sl], (n / RING) & 1, ab) && there;
+                        if (there && (j < lo || j > hi)) {
+#pragma unroll
+                            for (int x = 0; x < C::UC / 64; ++x)
+#pragma unroll
+                                for (int y = 0; y < 8; ++y)
+                                    *reinterpret_cast<uint4*>(&s.ring[sl][x * C::CHUNK + key * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, there) && ok;
+                }
+                bool over = t == t0;  // the item's first tile sets the references
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float x = __uint_as_float(sr[r]) * c;
+                    sr[r] = __float_as_uint(x);
+                    over = over || x > s.mref[r] + 8.f;
+                }
+                if (vote_or(over || !ok)) {
+                    if (!vote_and(ok)) {
+                        gave_up = true;
+                        break;
+                    }
+                    // some score passes its row's reference by more than 2^8: the references move to the
+                    // maxima so far, sums and O follow
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const float x = warp_max(__uint_as_float(sr[r]));
+                        if (lane == 0) s.wmax[sub][r] = x;
+                    }
+                    vote_or(false);  // all four warps' maxima are in
+                    if (key < NR) {
+                        const float x = fmaxf(fmaxf(s.wmax[0][key], s.wmax[1][key]), fmaxf(s.wmax[2][key], s.wmax[3][key]));
+                        const float m = t == t0 ? -INFINITY : s.mref[key], mn = fmaxf(m, x);
+                        s.alpha[key] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
+                        s.mref[key] = mn;
+                    }
+                    if (t > t0) {  // O holds P V of the tile before
+                        ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, ab)) && ok;
+                        tc_fence_after();
+                    }
+                    vote_or(false);  // the new references are in
+                    if (t > t0) {
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) l[r] *= s.alpha[r];
+#pragma unroll
+                        for (int h = 0; h < C::OH; ++h) {
+                            uint32_t o[NR];
+                            tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s.alpha[r]);
+                            tmem_st_cols<NR>(tmem + lane_base + cO + NR * h, o);
+                        }
+                    }
+                }
+                // P^T of this key: 16-bit (the MMA's operand type), the sums from the unrounded values
+                if (gt >= 2) {  // the buffer's last P V has completed
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf], ((gt - 2) >> 1) & 1, ab)) && ok;
+                }
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float m = s.mref[r];
+                    const float e = ex2(__uint_as_float(sr[r]) - (m == -INFINITY ? 0.f : m));
+                    l[r] += e;
+                    *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[r & 7] + 128 * r]) = f16 ? round16<true>(e) : round16<false>(e);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[buf]);
+            }
+            if (gave_up) break;
+            // ---------------- epilogue ----------------
+            const bool has_o = t1 > t0;
+            if (has_o) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab)) && ok;
+                tc_fence_after();
+            }
+            // row sums over the keys: the lanes, then the four warps
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float x = l[r];
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane == 0) s.lsum[sub][r] = x;
+            }
+            if (!vote_and(ok)) break;
+            const int rows = w.rows, part = w.part, g = w.g, q0 = w.q0;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = (s.lsum[0][r] + s.lsum[1][r]) + (s.lsum[2][r] + s.lsum[3][r]);
+            if (part >= 0) {
+                if (sub == 0) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (lane == (r & 31) && r < rows) a.part_ml[(long)part * NR + r] = make_float2(has_o ? s.mref[r] : -INFINITY, l[r]);
+                }
+            } else {
+                // l becomes the factor of O
+                int i = r0 / p.G, hh = r0 - i * p.G;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    if (r < rows) {
+                        const int h = g * p.G + hh;
+                        const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
+                        const float m = has_o ? s.mref[r] : -INFINITY, mf = fmaxf(m, s2);
+                        const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
+                        const float lt = l[r] * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+                        const float lse = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
+                        l[r] = lt != 0.f ? wgt / lt : 0.f;
+                        if (a.lse && sub == 0 && lane == (r & 31)) a.lse[(long)h * p.T_q + q0 + i] = lse;
+                    }
+                    if (++hh == p.G) {
+                        hh = 0;
+                        ++i;
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < C::OH; ++h) {
+                uint32_t o[NR];
+                if (has_o) {
+                    tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) o[r] = 0u;
+                }
+                if (h == C::OH - 1 && has_o) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.o_free);
+                }
+                const int col = D == 192 ? 64 * h + key : 128 * h + key;
+                if (col >= D || (D == 192 && h == 1 && key < 64)) continue;
+                int i = r0 / p.G, hh = r0 - i * p.G;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    if (r < rows) {
+                        const float x = __uint_as_float(o[r]);
+                        if (part >= 0)
+                            a.part_o[((long)part * NR + r) * D + col] = x;
+                        else
+                            a.o[(((long)q0 + i) * p.h_q + g * p.G + hh) * D + col] =
+                                l[r] == 0.f ? (uint16_t)0 : f16 ? round16<true>(x * l[r]) : round16<false>(x * l[r]);
+                    }
+                    if (++hh == p.G) {
+                        hh = 0;
+                        ++i;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[slot]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// combine: the items that a stretch's end cut
+// ------------------------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
+// blockIdx.x + 1 = the CTA at whose first unit an item may be cut; the first such CTA of an item
+// merges its partials (the CTA before, then every further one up to the item's end), a warp to
+// a row.  The weights are those of an online softmax: 2^(m_k - max).
+template <int D, bool F16>
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, const long long* pre, int n_grid, int rows_held) {
+    const Problem& p = a.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (*reinterpret_cast<volatile const int*>(a.status) != 0) return;
+    const long long W = pre[p.B];
+    const int n = paged_ctas(W, n_grid), c = blockIdx.x + 1;
+    if (c >= n) return;
+    const long long u = (long long)c * W / n;
+    const int b = find_sequence(pre, p.B, u);
+    const PagedSeq sq = paged_seq(p, b);
+    const PagedUnit x = paged_unit(p, sq, rows_held, u - pre[b]);
+    const long long first = u - x.k, last = first + x.cost;
+    if (x.k == 0 || (long long)(c - 1) * W / n > first) return;
+    // CTA y holds a unit of the item iff y W / n < last, i.e. y W < last n
+    const int pieces = (int)min((long long)n - 1, (last * n - 1) / W) - c + 2;
+    const int r0 = x.rt * rows_held, rows = (int)min((long)rows_held, (long)sq.nq * p.G - r0);
+    for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += gridDim.y * kMergeWarps) {
+        // piece y: slot 2 (c - 1) + 1 for the first, 2 (c - 1 + y) for the others
+        float m = -INFINITY, l = 0.f, acc[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+        for (int y0 = 0; y0 < pieces; y0 += 32) {
+            const int y = y0 + lane;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (y < pieces) ml = a.part_ml[(long)(2 * (c - 1 + y) + (y == 0 ? 1 : 0)) * rows_held + r];
+            float mx = ml.x;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mn = fmaxf(m, mx);
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float keep = ex2(m - base), wy = ex2(ml.x - base);
+            float ls = ml.y * wy;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            l = l * keep + ls;
+            m = mn;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] *= keep;
+            const int cnt = min(32, pieces - y0);
+#pragma unroll 4
+            for (int k = 0; k < cnt; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, wy, k);
+                const int yk = y0 + k;
+                const float* src = a.part_o + ((long)(2 * (c - 1 + yk) + (yk == 0 ? 1 : 0)) * rows_held + r) * D + lane;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wk, src[32 * e], acc[e]);
+            }
+        }
+        const int i = (r0 + r) / p.G, h = x.g * p.G + (r0 + r) - i * p.G;
+        const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
+        const float mf = fmaxf(m, s2);
+        const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
+        const float lt = l * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+        const float f = lt != 0.f ? wgt / lt : 0.f;
+        if (a.lse && lane == 0) a.lse[(long)h * p.T_q + sq.q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
+        uint16_t* out = a.o + (((long)sq.q0 + i) * p.h_q + h) * D + lane;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) out[32 * e] = round16<F16>(f == 0.f ? 0.f : acc[e] * f);
+    }
+}
+
+template <int D, int NR>
+cudaError_t launch_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
+    constexpr size_t smem = sizeof(FewSmem<D, NR>) + 1024;
+    static_assert(smem <= kSmemMax, "the few-row kernel's shared memory");
+    cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    paged_few_kernel<D, NR><<<ctas, kThreadsFew, smem, st>>>(a, tk, tv);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_few_d(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
+    switch (a.few_rows) {
+        case 16: return launch_few<D, 16>(a, tk, tv, ctas, st);
+        case 32: return launch_few<D, 32>(a, tk, tv, ctas, st);
+        case 64: return launch_few<D, 64>(a, tk, tv, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int D>
+cudaError_t launch_merge_d(const PagedArgs& a, const long long* pre, int ctas, int rows, cudaStream_t st) {
+    const dim3 grid(ctas - 1, cdiv(rows < 64 ? rows : 64, kMergeWarps));
+    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, ctas, rows);
+    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, ctas, rows);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st) {
+    paged_prep_kernel<<<1, kPrepThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
+    switch (a.p.d) {
+        case 64: return launch_few_d<64>(a, tk, tv, ctas, st);
+        case 128: return launch_few_d<128>(a, tk, tv, ctas, st);
+        case 192: return launch_few_d<192>(a, tk, tv, ctas, st);
+        case 256: return launch_few_d<256>(a, tk, tv, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, const long long* pre, int ctas, int rows, cudaStream_t st) {
+    if (ctas < 2 || a.no_split) return cudaSuccess;
+    switch (a.p.d) {
+        case 64: return launch_merge_d<64>(a, pre, ctas, rows, st);
+        case 128: return launch_merge_d<128>(a, pre, ctas, rows, st);
+        case 192: return launch_merge_d<192>(a, pre, ctas, rows, st);
+        case 256: return launch_merge_d<256>(a, pre, ctas, rows, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fa

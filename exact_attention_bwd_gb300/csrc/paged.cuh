@@ -1,0 +1,77 @@
+// Packed queries over a paged cache: what the schedule, the kernels and the combine share.
+//
+// Work is counted in (row tile, key tile) units.  A sequence's query rows (position, head of
+// the group) of one key/value head are cut into row tiles; each row tile and key/value head
+// is an item of as many units as it has key tiles in its band (one if it has none: its rows
+// still have to be written).  All units form one line, sequence by sequence, row tile by row
+// tile, head by head, and CTA c of n takes the stretch [c W / n, (c + 1) W / n): every CTA
+// streams the same number of key tiles whatever the lengths are.  An item cut by a stretch's
+// end leaves fp32 partials (at most two per CTA, so the workspace does not depend on the
+// lengths), which the combine merges in the order of the keys.
+#pragma once
+#include "common.cuh"
+
+namespace fa {
+
+constexpr int kKeyTile = 128;
+
+struct PagedSeq {
+    int q0, nq, nk;
+};
+
+// Offsets and lengths are kept within the tensors whatever the arrays hold.
+__device__ __forceinline__ PagedSeq paged_seq(const Problem& p, int b) {
+    PagedSeq s;
+    s.q0 = min(max(p.cu_q[b], 0), p.T_q);
+    s.nq = min(max(p.cu_q[b + 1], s.q0), p.T_q) - s.q0;
+    if (p.seqused_q) s.nq = min(s.nq, max(0, p.seqused_q[b]));
+    s.nk = min(max(p.seqused_k[b], 0), p.s_kv);
+    return s;
+}
+
+// Key tiles [t0, t1) of the rows [r0, r0 + rows) (numbered position * G + head of the group),
+// and the units they cost.
+__device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, long r0, int rows, int& t0, int& t1) {
+    const Band bd{s.nk - s.nq, p.left, p.right, s.nk};
+    const int i0 = (int)(r0 / p.G), i1 = (int)min((long)s.nq - 1, (r0 + rows - 1) / p.G);
+    kv_tile_range(bd, i0, i1, kKeyTile, t0, t1);
+    return max(t1 - t0, 1);
+}
+
+// The largest b in [0, B) with pre[b] <= u (warp-wide; pre is non-decreasing, pre[0] = 0).
+__device__ __forceinline__ int find_sequence(const long long* pre, int B, long long u) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = B - 1;
+    while (hi > lo) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + (lane + 1) * step;
+        const bool le = at <= hi && pre[at] <= u;
+        lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
+        hi = min(hi, lo + step - 1);
+    }
+    return lo;
+}
+
+// CTAs that take part: each has kMinUnits units at least.
+constexpr int kMinUnits = 2;
+__device__ __forceinline__ int paged_ctas(long long W, int n_ctas) {
+    return (int)min((long long)n_ctas, (W + kMinUnits - 1) / kMinUnits);
+}
+
+// Position of unit u within its sequence: the item (row tile, head) and the unit of the item.
+struct PagedUnit {
+    int rt, g, k, cost, t0, t1;
+};
+__device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, long long rem) {
+    PagedUnit x;
+    for (x.rt = 0;; ++x.rt) {
+        x.cost = paged_tiles(p, s, (long)x.rt * rows, rows, x.t0, x.t1);
+        if (rem < (long long)x.cost * p.h_kv) break;
+        rem -= (long long)x.cost * p.h_kv;
+    }
+    x.g = (int)(rem / x.cost);
+    x.k = (int)(rem - (long long)x.g * x.cost);
+    return x;
+}
+
+}  // namespace fa

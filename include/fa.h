@@ -89,6 +89,20 @@
  *    the logical cache length (at most max_blocks_per_seq * page_size); page_size must be
  *    a positive multiple of 128 (the page's builds ask for 256).  Table entries are read
  *    on the device and not checked.
+ *  - block_table with cu_seqlens_q and without cu_seqlens_k (forward only, bf16 and fp16):
+ *    packed queries over a paged cache, the form of a serving step, in which each sequence
+ *    brings its new tokens (one, a few, a chunk of a prompt) and reads its whole cache, those
+ *    tokens' keys included (fa_qk_norm_rope writes them there, fa_page_plan makes the table).
+ *    q, o are [T_q, h_q, d] with T_q = s_q, the LSE is [h_q, T_q]; seqused_k is required and
+ *    gives the keys of each sequence (clamped to [0, s_kv]), s_kv the longest cache that may
+ *    occur.  page_size is a positive multiple of 16.  Offsets are kept within [0, T_q]; rows
+ *    of q that no sequence covers (a padded batch) are left as they were.  What a page holds
+ *    behind a sequence's used keys, NaN and infinities included, has no effect.  A table entry
+ *    that is needed and outside the pool reads as zeros and sets FA_ERR_DEVICE_CHECK in the
+ *    status word.  FA_FLAG_VALIDATE_CU checks cu_seqlens_q (from 0, not decreasing, at most
+ *    T_q) and seqused_k.  max_seqlen_q is used when given (the most query rows of a sequence;
+ *    it picks the kernel's tile, and a wrong one costs time, not correctness).  Results do not
+ *    depend on how other work is scheduled: the same call gives the same bits.
  *
  * FP8 forward (vllm-project/flash-attention README, "FlashAttention-3 beta release":
  * "FP8 forward"): with dtype = FA_DTYPE_E4M3, q, k and v hold e4m3 bytes (1 byte per
@@ -154,7 +168,7 @@ typedef struct fa_params {
     int window_left, window_right;  /* -1 = unbounded side */
     const float *sinks;             /* device fp32 [h_q], or NULL */
     const int32_t *cu_seqlens_q;    /* device int32 [B+1], or NULL for dense tensors */
-    const int32_t *cu_seqlens_k;    /* device int32 [B+1]; required iff cu_seqlens_q */
+    const int32_t *cu_seqlens_k;    /* device int32 [B+1]; required iff cu_seqlens_q, absent with block_table */
     int max_seqlen_q, max_seqlen_k; /* optional hints (0 = unknown); never needed */
     unsigned flags;                 /* FA_FLAG_* */
     /* Partly filled slots and paged caches (see above).  Zero / NULL = not used. */
@@ -199,6 +213,77 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
                  const float *lse, const void *dout, void *dq, void *dk, void *dv, float *dsinks,
                  void *workspace, size_t workspace_bytes, struct CUstream_st *stream);
 
+/* Norm and position rotation of queries and keys (training and serving), ahead of fa_fwd.
+ * For each token t and head, with x the head's d values and w its weight (q_weight or
+ * k_weight, shared by the heads; NULL = ones):
+ *   y = x * w / sqrt(mean(x^2) + eps),
+ * then the pairs (a, b) of y's first rot_dim values turn by the token's angles:
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ * The pairs are (j, j + rot_dim / 2), or with `interleaved` (2j, 2j + 1), j < rot_dim / 2, and use
+ * cos[pos][j], sin[pos][j].  pos is positions[t], or t % seq_len without positions.  A token
+ * at position -1 is padding and is skipped (its outputs are left as they were); any other
+ * position outside [0, max_pos) is skipped too and sets *status (when given) to
+ * FA_ERR_DEVICE_CHECK.  Statistics and products are fp32, outputs are rounded once.
+ * fa_qk_norm_rope writes q_out [T, h_q, d] and k_out [T, h_kv, d] (contiguous).  With k_cache,
+ * v_cache (pools of num_slots rows [h_kv, d]), slots and v it also writes the key's row and a
+ * copy of v's to row slots[t] of the pools (k_out may then be NULL); slot -1 is not stored, one
+ * outside [-1, num_slots) is not stored either and sets *status.  Two tokens with one slot
+ * leave either's row there.  q_out may be q and k_out may be k (contiguous); other overlaps are refused.
+ * fa_qk_norm_rope_bwd takes the inputs and the gradients of q_out and k_out (contiguous) and
+ * writes dq, dk (token strides dq_stride, dk_stride; they may be q and k, or dq_out and
+ * dk_out, in the same layout) and dq_weight, dk_weight (fp32 [d], written whole, summed in a
+ * fixed order: the same bits from call to call).
+ * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
+ * of 8 elements, base pointers 16-byte aligned. */
+typedef struct fa_rope_params {
+    int T;                 /* tokens */
+    int h_q, h_kv, d;
+    int rot_dim;           /* leading values of a head that are rotated (0 = none) */
+    int interleaved;       /* pairs (2j, 2j+1) instead of (j, j + rot_dim/2) */
+    int seq_len;           /* without positions: token t is at position t % seq_len */
+    int max_pos;           /* rows of cos and sin */
+    float eps;
+    int dtype;             /* FA_DTYPE_BF16 or FA_DTYPE_F16 */
+    int weight_f32;        /* the weights are fp32 (0: the tensors' type) */
+    long long q_stride, k_stride, v_stride;   /* elements from token to token of q, k, v */
+    long long dq_stride, dk_stride;           /* gradient only: of dq, dk */
+    const int32_t *positions;                 /* device int32 [T], or NULL */
+    const float *cos, *sin;                   /* device fp32 [max_pos, rot_dim/2] */
+    const void *q_weight, *k_weight;          /* device [d], or NULL (ones) */
+    const int32_t *slots;                     /* device int32 [T]: cache rows, or NULL */
+    long long num_slots;                      /* num_pages * page_size */
+    int32_t *status;                          /* device int32, set on a bad position or slot, never cleared; or NULL */
+} fa_rope_params;
+
+fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k, const void *v, void *q_out, void *k_out,
+                          void *k_cache, void *v_cache, struct CUstream_st *stream);
+size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params *p);
+fa_status fa_qk_norm_rope_bwd(const fa_rope_params *p, const void *q, const void *k, const void *dq_out, const void *dk_out,
+                              void *dq, void *dk, float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                              struct CUstream_st *stream);
+
+/* Page plan of a serving step, from the requests' lengths: request b has cached[b] tokens in
+ * its pages and brings fresh[b] new ones.  Takes the pages they need from free_pages (device
+ * int32 [n_free]) from index *free_head on (NULL: 0), in the order of the requests, and writes
+ *   block_table   the new pages' entries of each row (others are left as they were)
+ *   cu_seqlens_q  [B + 1], seqused_k [B] = cached + fresh (not the arrays cached or fresh)
+ *   positions, slots   [T]: place in its sequence and cache row (page * page_size + offset) of
+ *                 each new token, packed request by request; -1 behind the last one
+ *   free_head_out [1] = *free_head + pages taken (not the same word as free_head)
+ * what fa_qk_norm_rope and fa_fwd take.  Pages past the end of the list or outside
+ * [0, num_pages), table entries outside it, negative lengths (taken as 0), requests beyond
+ * max_blocks_per_seq pages and more than T new tokens set *status (when given) to
+ * FA_ERR_DEVICE_CHECK; the tokens concerned get slot -1 (and lengths are cut to what fits). */
+typedef struct fa_page_plan_params {
+    int B, T;                /* requests; rows of the packed batch (at least the new tokens) */
+    int page_size, max_blocks_per_seq, num_pages;
+    int n_free;              /* entries of free_pages */
+} fa_page_plan_params;
+
+fa_status fa_page_plan(const fa_page_plan_params *p, const int32_t *cached, const int32_t *fresh, const int32_t *free_pages,
+                       const int32_t *free_head, int32_t *block_table, int32_t *cu_seqlens_q, int32_t *seqused_k,
+                       int32_t *positions, int32_t *slots, int32_t *free_head_out, int32_t *status, struct CUstream_st *stream);
+
 /* Synchronises `stream` and returns the status word the kernels of the last call
  * on this workspace left (FA_OK, FA_ERR_TIMEOUT or FA_ERR_DEVICE_CHECK), or
  * FA_ERR_CUDA if the stream itself reports an error. */
@@ -209,7 +294,8 @@ const char *fa_status_string(fa_status s);
 
 /* Per-kernel timing: when enabled, every launch the library makes is bracketed by
  * CUDA events on its stream.  fa_profile_read synchronises on the last launch of
- * the named kernel ("fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post")
+ * the named kernel ("fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post",
+ * "paged_prep", "paged_few", "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan")
  * and writes its duration in milliseconds; returns FA_ERR_INVALID_ARG for an
  * unknown name or a kernel not launched since profiling was enabled. */
 fa_status fa_profile_enable(int on);
