@@ -361,8 +361,9 @@ bool paged_packed(const Problem& p) { return p.block_table && p.cu_q; }
 
 struct PagedPlan {
     bool empty = true;
-    int ctas = 0, few_rows = 0;
-    size_t off_pre = 0, off_o = 0, off_ml = 0, ws_bytes = kStatusBytes;
+    int ctas = 0, few_rows = 0, many_rows = 0;
+    bool many = false;  // the tensor-core kernel takes part
+    size_t off_pre = 0, off_o = 0, off_ml = 0, off_mo = 0, off_mml = 0, ws_bytes = kStatusBytes;
 };
 
 fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
@@ -374,10 +375,20 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
     const long rows = longest * p.G;
     pl.few_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    pl.many = rows > 64 && p.d <= 128;
+    pl.many_rows = 2 * p.P * p.G;
     pl.off_pre = kStatusBytes;
     pl.off_o = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
     pl.off_ml = pl.off_o + align256((size_t)2 * pl.ctas * pl.few_rows * p.d * 4);
     pl.ws_bytes = pl.off_ml + align256((size_t)2 * pl.ctas * pl.few_rows * 8);
+    if (pl.many) {
+        pl.off_mo = pl.ws_bytes;
+        pl.off_mml = pl.off_mo + align256((size_t)2 * pl.ctas * pl.many_rows * p.d * 4);
+        pl.ws_bytes = pl.off_mml + align256((size_t)2 * pl.ctas * pl.many_rows * 8);
+    }
+#ifdef FA_TRACE
+    pl.ws_bytes += align256(kTraceBytes);
+#endif
     return FA_OK;
 }
 
@@ -402,8 +413,8 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.box = p.page_size & -p.page_size;
     if (a.box > kTileRows) a.box = kTileRows;
     a.few_rows = pl.few_rows;
-    a.few_max = 0x7fffffffffffffffL;
-    a.many_rows = pl.few_rows;
+    a.few_max = pl.many ? pl.few_rows : kAllFew;
+    a.many_rows = pl.many_rows;
     a.no_split = (in.flags & FA_FLAG_NO_SPLIT) ? 1 : 0;
     a.validate = (in.flags & FA_FLAG_VALIDATE_CU) ? 1 : 0;
     a.pre = reinterpret_cast<long long*>(ws + pl.off_pre);
@@ -418,6 +429,31 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
     if (e == cudaSuccess) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
     if (e == cudaSuccess) e = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, a.pre, pl.ctas, a.few_rows, st); });
+    if (e != cudaSuccess || !pl.many) return cuda_status(e);
+    // sequences of more rows: the tensor-core kernel, 2 P G rows to an item
+    FwdArgs f{};
+    CUtensorMap tq;
+    if (!encode_bhsd(&tq, q, p.d, p.h_q, p.T_q, 1, p.G, p.P, f16)) return FA_ERR_CUDA;
+    f.p = p;
+    f.n_splits = 1;
+    f.kt = kTileRows;
+    f.n_items = 1;
+    f.n_ctas = pl.ctas;
+    f.o = a.o;
+    f.lse = lse;
+    f.status = status;
+    f.pre = a.pre + p.B + 1;
+    f.num_pages = a.num_pages;
+    f.box = a.box;
+    f.no_split = a.no_split;
+    f.o_part = a.part_o = reinterpret_cast<float*>(ws + pl.off_mo);
+    f.part_ml = a.part_ml = reinterpret_cast<float2*>(ws + pl.off_mml);
+#ifdef FA_TRACE
+    f.trace = reinterpret_cast<unsigned long long*>(ws + pl.ws_bytes - align256(kTraceBytes));
+    if (cudaMemsetAsync(f.trace, 0, kTraceBytes, st) != cudaSuccess) return FA_ERR_CUDA;
+#endif
+    e = timed(kFwd, st, [&] { return launch_fwd_paged(f, tq, tk, tv, st); });
+    if (e == cudaSuccess) e = timed(kCombine, st, [&] { return launch_paged_merge(a, f.pre, pl.ctas, a.many_rows, st); });
     return cuda_status(e);
 }
 

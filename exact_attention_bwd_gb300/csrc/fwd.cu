@@ -40,7 +40,14 @@
 // previous item's epilogue; two barriers hand the shared resources over: q_empty (the
 // previous item's S MMAs, which read the Q tiles, have completed) and o_free[k] (the
 // epilogue has read O_k out of tensor memory before the next P V overwrites it).
+//
+// The PG instantiation is the same kernel over a paged cache with packed queries: its CTAs
+// take stretches of the line of units of paged.cuh (items may be cut; a cut item's rows go to
+// the partials un-normalised, with their maximum and sum), the producer warp loads each key
+// tile page by page, and value rows that no query of the item sees are cleared in shared
+// memory before the product (a page's unused rows may hold anything, and 0 * NaN is NaN).
 #include "fwd_items.cuh"
+#include "paged.cuh"
 #include "trace.cuh"
 
 namespace fa {
@@ -87,6 +94,8 @@ struct ItemInfo {
     int q0, k0, tma_b;  // first query / key row of the sequence, outer TMA coordinate
     int u0, u1;         // union key-tile range of the two tiles (u1 <= u0: none)
     int s0[2], t0[2], t1[2];  // first query position and key-tile range of each tile
+    // PG only: used keys, keys that any row of the item may see, partial slot (-1: whole item)
+    int nk, lo, hi, part;
 };
 constexpr int kItemSlots = 3;
 // arrivals that free an item slot: producer, MMA issuer and the eight softmax warps
@@ -111,7 +120,7 @@ struct __align__(1024) FwdSmem {
     int abort_flag;
 };
 
-template <int D, bool F16, int KT>
+template <int D, bool F16, int KT, bool PG>
 __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                const __grid_constant__ CUtensorMap tmv) {
@@ -124,6 +133,13 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     const int warp = tid >> 5, lane = tid & 31;
     // an earlier CTA of this launch gave up: do not start
     if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
+    long long pg_units = 0;
+    int pg_ctas = 0;
+    if constexpr (PG) {
+        pg_units = a.pre[p.B];
+        pg_ctas = paged_ctas(pg_units, (int)gridDim.x);
+        if ((int)blockIdx.x >= pg_ctas) return;
+    }
 
     // ---------------- setup ----------------
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
@@ -172,7 +188,77 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     // branch so the register allocator sees it on every path.
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(C::REG_LOW) : "memory");
-    if (warp == 0) {
+    if (PG && warp == 0) {
+        // ================= TMA producer, paged cache (the whole warp) =================
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        const uint32_t qbox = (uint32_t)(p.P * p.G) * 128u;
+        const int boxes = kKeyTile / a.box;
+        int gt = 0, n_q = 0, k_issued = 0, v_issued = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, ab)) != 0; };
+        for (int n = 0; ok; ++n) {
+            const int slot = n % kItemSlots;
+            if (!(ok = wait(&s.item_full[slot], (n / kItemSlots) & 1))) break;
+            const ItemInfo& it = s.item[slot];
+            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, nk = it.nk;
+            const int32_t* table = p.block_table + (long)it.b * p.max_blocks;
+            const int qr0 = it.q0 + it.s0[0], qr1 = it.q0 + it.s0[1];
+            const bool on0 = it.t1[0] > it.t0[0], on1 = it.t1[1] > it.t0[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[slot]);
+            if (end) break;
+            if (u1 <= u0) continue;
+            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used keys
+            // or for a table entry outside the pool; the next tile's entry is fetched ahead
+            auto entry = [&](int t) {
+                const int j = t * kKeyTile + lane * a.box;
+                return lane < boxes && t < u1 && j < nk ? table[j / p.page_size] : a.num_pages;
+            };
+            int next = entry(u0);
+            if (n_q > 0 && !(ok = wait(&s.q_empty, (n_q - 1) & 1))) break;
+            if (lane == 0) {
+                mbar_expect_tx(&s.q_full, qbox * C::KCH * ((on0 ? 1u : 0u) + (on1 ? 1u : 0u)));
+                for (int c = 0; c < C::KCH; ++c) {
+                    if (on0) tma_load_4d(&s.q[0][c * C::CHUNK_BYTES], &tmq, &s.q_full, c * 64, g * p.G, qr0, 0);
+                    if (on1) tma_load_4d(&s.q[1][c * C::CHUNK_BYTES], &tmq, &s.q_full, c * 64, g * p.G, qr1, 0);
+                }
+            }
+            ++n_q;
+            for (int j = u0; j < u1; ++j, ++gt) {
+                const int st = gt % C::STAGES;
+                const uint32_t ph = (gt / C::STAGES) & 1;
+                int page = next;
+                next = entry(j + 1);
+                const int key = j * kKeyTile + lane * a.box, row = key % p.page_size;
+                if (lane < boxes && (unsigned)page >= (unsigned)a.num_pages) {
+                    if (key < nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    page = a.num_pages;
+                }
+                if (!(ok = wait(&s.k_empty[st], ph ^ 1))) break;
+                if (lane == 0) mbar_expect_tx(&s.k_full[st], C::KV_BYTES);
+                __syncwarp();
+                if (lane < boxes)
+                    for (int c = 0; c < C::KCH; ++c)
+                        tma_load_4d(&s.k[st][c * C::KV_CHUNK + lane * a.box * 128], &tmk, &s.k_full[st], c * 64, g, row, page);
+                ++k_issued;
+                if (!(ok = wait(&s.v_empty[st], ph ^ 1))) break;
+                if (lane == 0) mbar_expect_tx(&s.v_full[st], C::KV_BYTES);
+                __syncwarp();
+                if (lane < boxes)
+                    for (int c = 0; c < C::KCH; ++c)
+                        tma_load_4d(&s.v[st][c * C::KV_CHUNK + lane * a.box * 128], &tmv, &s.v_full[st], c * 64, g, row, page);
+                ++v_issued;
+            }
+        }
+        // wait for every copy still in flight before the CTA may exit
+        for (int back = 1; back <= C::STAGES; ++back) {
+            if (k_issued - back >= 0) mbar_wait_quiet(&s.k_full[(k_issued - back) % C::STAGES], ((k_issued - back) / C::STAGES) & 1);
+            if (v_issued - back >= 0) mbar_wait_quiet(&s.v_full[(v_issued - back) % C::STAGES], ((v_issued - back) / C::STAGES) & 1);
+        }
+        if (n_q > 0) mbar_wait_quiet(&s.q_full, (n_q - 1) & 1);
+    } else if (warp == 0) {
         // ================= TMA producer =================
         if (lane == 0) {
             Tracer tr;
@@ -384,9 +470,53 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // come from those intervals (their hull), since a tile's rows may span sequences.
         int n = 0;
         bool ok = true;
-        for (int idx = blockIdx.x, step = first_step(a.snake); idx < a.n_items;
+        // PG: the CTA's stretch of the line of units, and the sequence the walk is in
+        long long pu = (long long)blockIdx.x * pg_units / max(pg_ctas, 1);
+        const long long pu_end = ((long long)blockIdx.x + 1) * pg_units / max(pg_ctas, 1);
+        long long pb = 0, pe = 0;
+        int seq = 0;
+        PagedSeq ps{};
+        for (int idx = blockIdx.x, step = first_step(a.snake); PG ? pu < pu_end : idx < a.n_items;
              idx += step, step = 2 * (int)gridDim.x - step) {
-            FwdItem w = fwd_item(a, idx, KT);
+            FwdItem w;
+            int part = -1;
+            if constexpr (PG) {
+                if (pu >= pe) {
+                    seq = find_sequence(a.pre, p.B, pu);
+                    pb = a.pre[seq];
+                    pe = a.pre[seq + 1];
+                    ps = paged_seq(p, seq);
+                }
+                const PagedUnit x = paged_unit(p, ps, 2 * p.P * p.G, pu - pb);
+                if (a.no_split && x.k > 0) {  // the item belongs to the CTA that holds its first unit
+                    pu += x.cost - x.k;
+                    continue;
+                }
+                const int take = a.no_split ? x.cost : (int)min((long long)(x.cost - x.k), pu_end - pu);
+                part = take == x.cost ? -1 : 2 * (int)blockIdx.x + (x.k == 0 ? 1 : 0);
+                pu += take;
+                w.sv = SeqView{seq, ps.q0, ps.nq, 0, ps.nk, 0};
+                w.band = Band{ps.nk - ps.nq, p.left, p.right, ps.nk};
+                w.g = x.g;
+                w.split = 0;
+                w.tail = false;
+                w.live = true;
+                w.u0 = x.t0 + x.k;
+                w.u1 = min(w.u0 + take, x.t1);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    w.ti[k].s0 = (2 * x.rt + k) * p.P;
+                    w.ti[k].active = w.ti[k].s0 < ps.nq;
+                    w.ti[k].t0 = w.ti[k].t1 = 0;
+                    if (w.ti[k].active) {
+                        kv_tile_range(w.band, w.ti[k].s0, min(w.ti[k].s0 + p.P, ps.nq) - 1, KT, w.ti[k].t0, w.ti[k].t1);
+                        w.ti[k].t0 = max(w.ti[k].t0, w.u0);
+                        w.ti[k].t1 = max(min(w.ti[k].t1, w.u1), w.ti[k].t0);
+                    }
+                }
+            } else {
+                w = fwd_item(a, idx, KT);
+            }
             if (!w.live) continue;
             const int slot = n % kItemSlots;
             if (n >= kItemSlots) {
@@ -447,6 +577,12 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
                     it.t0[k] = w.ti[k].t0;
                     it.t1[k] = w.ti[k].t1;
                 }
+                if constexpr (PG) {
+                    it.nk = w.sv.nk;
+                    it.lo = w.band.lo(w.ti[0].s0);
+                    it.hi = w.band.hi(min(w.ti[0].s0 + 2 * p.P, w.sv.nq) - 1);
+                    it.part = part;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_full[slot]);
@@ -474,6 +610,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         const uint32_t tO = tmem + lane_base + C::o_col(k);
         const float c = p.scale_log2;
         uint32_t scount = 0, ocount = 0;  // S tiles and O tiles received (carried across items)
+        int gt0 = 0;                      // PG: key tiles of the items before this one
         bool ok = true;
         Tracer tr;
         tr.init((warp & 3) == 0 ? a.trace : nullptr, 2 + k);
@@ -509,6 +646,28 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             // one TMEM read of the whole S row (KT fp32 columns)
             const int j0 = j * KT;
             const bool edge = (j0 < jlo || j0 + KT - 1 > jhi);
+            if constexpr (PG) {
+                // value rows outside every row's band: cleared by tile 0's group where it takes part (the
+                // P V of tile 1 is issued behind that of tile 0), else by tile 1's
+                const ItemInfo& itm = s.item[slot];
+                const int lo = itm.lo, hi = itm.hi;
+                if ((j0 < lo || j0 + KT - 1 > hi) && (k == 0 || j < itm.t0[0] || j >= itm.t1[0])) {
+                    const int vt = gt0 + j - itm.u0, st = vt % C::STAGES;
+                    const bool there = mbar_wait(&s.v_full[st], (vt / C::STAGES) & 1, ab);
+                    if (there && (j0 + r < lo || j0 + r > hi)) {
+#pragma unroll
+                        for (int x = 0; x < C::KCH; ++x)
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                *reinterpret_cast<uint4*>(&s.v[st][x * C::KV_CHUNK + r * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    if (!__all_sync(0xffffffffu, there)) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
             uint32_t sr[KT];
             if constexpr (KT == 128) tmem_ld_32x32b_x128(tS, sr);
             else tmem_ld_32x32b_x64(tS, sr);
@@ -602,7 +761,9 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             ok = __all_sync(0xffffffffu, wt);
             tc_fence_after();
         }
-        const bool split_mode = a.n_splits > 1 || itm.tail;
+        const int part = PG ? itm.part : -1;
+        if constexpr (PG) gt0 += max(itm.u1 - itm.u0, 0);
+        const bool split_mode = PG ? part >= 0 : a.n_splits > 1 || itm.tail;
         // 32-byte stores where the base allows (the rows, 128 or more bytes, keep the alignment)
         const bool o_al32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
         const bool part_al32 = (reinterpret_cast<uintptr_t>(a.o_part) & 31u) == 0;
@@ -623,9 +784,14 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         const long row_base = itm.tail ? a.tail_row0 : 0;
         const long nrows = (long)p.B * p.h_q * p.s_q - row_base;
         const long prow = ((long)sv.b * p.h_q + h) * p.s_q + i - row_base;
+        // PG: rows of a partial slot are those of the item, tile by tile; O stays un-normalised
+        const long pg_row = (long)part * (2 * p.P * p.G) + k * p.P * p.G + r;
+        if (PG && split_mode) oscale = 1.f;
         if (row_valid) {
             if (!split_mode) {
                 if (a.lse) a.lse[lse_index(p, sv, i, h)] = lse;
+            } else if (PG) {
+                a.part_ml[pg_row] = make_float2(m_used, l);
             } else {
                 a.lse_part[(long)split * nrows + prow] = lse;
             }
@@ -665,7 +831,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
                         }
                     }
                 } else {
-                    float* op = a.o_part + ((long)split * nrows + prow) * D;
+                    float* op = a.o_part + (PG ? pg_row : (long)split * nrows + prow) * D;
                     if (part_al32) {
 #pragma unroll
                         for (int t = 0; t < D / 8; ++t) {
@@ -690,7 +856,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
 #pragma unroll
                 for (int t = 0; t < D / 8; ++t) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0, 0, 0, 0);
             } else {
-                float* op = a.o_part + ((long)split * nrows + prow) * D;
+                float* op = a.o_part + (PG ? pg_row : (long)split * nrows + prow) * D;
 #pragma unroll
                 for (int t = 0; t < D / 4; ++t) reinterpret_cast<float4*>(op)[t] = make_float4(0, 0, 0, 0);
             }
@@ -711,20 +877,20 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
 
 }  // namespace
 
-template <int D, bool F16, int KT>
+template <int D, bool F16, int KT, bool PG = false>
 static cudaError_t launch_fwd_k(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t st) {
     using C = FwdCfg<D, KT>;
     const size_t smem = sizeof(FwdSmem<D, KT>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, F16, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, F16, KT, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // the warp groups' setmaxnreg shares must fit in the registers the CTA is launched with
     // (an increase beyond them would never be granted)
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, fwd_kernel<D, F16, KT>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, fwd_kernel<D, F16, KT, PG>)) != cudaSuccess) return e;
     if (fa.numRegs * kThreadsFwd < 128 * C::REG_LOW + 256 * C::REG_HIGH) return cudaErrorLaunchOutOfResources;
     if (a.n_items <= 0 || a.n_ctas <= 0) return cudaSuccess;
-    fwd_kernel<D, F16, KT><<<(unsigned)a.n_ctas, kThreadsFwd, smem, st>>>(a, tq, tk, tv);
+    fwd_kernel<D, F16, KT, PG><<<(unsigned)a.n_ctas, kThreadsFwd, smem, st>>>(a, tq, tk, tv);
     return cudaGetLastError();
 }
 
@@ -734,6 +900,16 @@ static cudaError_t launch_fwd_d(const FwdArgs& a, const CUtensorMap& tq, const C
     if constexpr (D == 64)
         if (a.kt == 64) return launch_fwd_k<D, F16, 64>(a, tq, tk, tv, st);
     return launch_fwd_k<D, F16, 128>(a, tq, tk, tv, st);
+}
+
+cudaError_t launch_fwd_paged(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             cudaStream_t st) {
+    const bool f16 = a.p.dtype == FA_DTYPE_F16;
+    switch (a.p.d) {
+        case 64: return f16 ? launch_fwd_k<64, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<64, false, 128, true>(a, tq, tk, tv, st);
+        case 128: return f16 ? launch_fwd_k<128, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<128, false, 128, true>(a, tq, tk, tv, st);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 cudaError_t launch_fwd(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -65,6 +65,11 @@ struct FwdArgs {
     const float* k_descale;
     const float* v_descale;
     unsigned long long* trace;  // trace builds only: the workspace's trace region (else null)
+    // packed queries over a paged cache only (paged.cuh): units before each sequence, pool
+    // pages, rows of one K / V copy, whole items only, statistics of the partials in o_part
+    const long long* pre;
+    int num_pages, box, no_split;
+    float2* part_ml;
 };
 
 // ------------------------------------------------------------------------------------------
@@ -145,6 +150,8 @@ struct PagedArgs {
     float2* part_ml;    // [2 CTAs][rows] reference maximum (log2 units) and sum
     int* status;
 };
+// PagedArgs::few_max of a call whose every sequence is the few-row kernel's
+constexpr long kAllFew = 0x7fffffffffffffffL;
 
 // ------------------------------------------------------------------------------------------
 // around the attention: norm and rotation of queries and keys, the page plan
@@ -176,6 +183,8 @@ struct PagePlanArgs {
 // host-side launchers (defined next to each kernel)
 cudaError_t launch_fwd(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        cudaStream_t st);
+cudaError_t launch_fwd_paged(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             cudaStream_t st);  // d <= 128
 cudaError_t launch_fwd256(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t st);
 cudaError_t launch_fwd_e4m3(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -58,16 +58,36 @@ __device__ __forceinline__ int paged_ctas(long long W, int n_ctas) {
     return (int)min((long long)n_ctas, (W + kMinUnits - 1) / kMinUnits);
 }
 
-// Position of unit u within its sequence: the item (row tile, head) and the unit of the item.
+// Unit `rem` of a sequence: its item (row tile, head) and the unit of the item.  Warp-wide: a
+// lane to a row tile, 32 at a time.
 struct PagedUnit {
     int rt, g, k, cost, t0, t1;
 };
 __device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, long long rem) {
+    const int lane = threadIdx.x & 31;
+    const long total = (long)s.nq * p.G;
     PagedUnit x;
-    for (x.rt = 0;; ++x.rt) {
-        x.cost = paged_tiles(p, s, (long)x.rt * rows, rows, x.t0, x.t1);
-        if (rem < (long long)x.cost * p.h_kv) break;
-        rem -= (long long)x.cost * p.h_kv;
+    for (int base = 0;; base += 32) {
+        const long r0 = (long)(base + lane) * rows;
+        int t0 = 0, t1 = 0, cost = 0;
+        if (r0 < total) cost = paged_tiles(p, s, r0, rows, t0, t1);
+        int sum = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, rem < (long long)sum * p.h_kv);
+        if (past || (long)(base + 32) * rows >= total) {  // (the sequence ends: only for a unit outside it)
+            const int src = past ? __ffs(past) - 1 : 0;
+            x.rt = base + src;
+            x.cost = max(__shfl_sync(0xffffffffu, cost, src), 1);
+            x.t0 = __shfl_sync(0xffffffffu, t0, src);
+            x.t1 = __shfl_sync(0xffffffffu, t1, src);
+            rem -= (long long)(__shfl_sync(0xffffffffu, sum, src) - x.cost) * p.h_kv;
+            break;
+        }
+        rem -= (long long)__shfl_sync(0xffffffffu, sum, 31) * p.h_kv;
     }
     x.g = (int)(rem / x.cost);
     x.k = (int)(rem - (long long)x.g * x.cost);

@@ -128,8 +128,8 @@ def test_masks(window, causal, d):
         assert np.all(np.isneginf(z[:, c["cu"][4]].cpu().numpy())) and np.all(from_dev(o)[c["cu"][4]] == 0)
 
 
-@pytest.mark.parametrize("hint", [1, 9])
-def test_sinks(hint):
+@pytest.mark.parametrize("hint", [1, 9, 40])
+def test_sinks(hint):  # hint 40: the tensor-core kernel
     c = case([1, hint, 1], [900, 70, 0], h_q=8, h_kv=2, d=128, page=16, sinks=True)
     compare(c, hint=hint)
 
