@@ -133,12 +133,8 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     const int warp = tid >> 5, lane = tid & 31;
     // an earlier CTA of this launch gave up: do not start
     if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
-    long long pg_units = 0;
-    int pg_ctas = 0;
     if constexpr (PG) {
-        pg_units = a.pre[p.B];
-        pg_ctas = paged_ctas(pg_units, (int)gridDim.x);
-        if ((int)blockIdx.x >= pg_ctas) return;
+        if ((int)blockIdx.x >= a.line->n) return;
     }
 
     // ---------------- setup ----------------
@@ -471,9 +467,12 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         int n = 0;
         bool ok = true;
         // PG: the CTA's stretch of the line of units, and the sequence the walk is in
-        long long pu = (long long)blockIdx.x * pg_units / max(pg_ctas, 1);
-        const long long pu_end = ((long long)blockIdx.x + 1) * pg_units / max(pg_ctas, 1);
-        long long pb = 0, pe = 0;
+        long long pu = 0, pu_end = 0, pb = 0, pe = 0;
+        if constexpr (PG) {
+            const PagedLine line = *a.line;
+            pu = line.start(blockIdx.x);
+            pu_end = line.start(blockIdx.x + 1);
+        }
         int seq = 0;
         PagedSeq ps{};
         for (int idx = blockIdx.x, step = first_step(a.snake); PG ? pu < pu_end : idx < a.n_items;

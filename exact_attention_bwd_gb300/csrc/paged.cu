@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
                 const bool few = rows <= a.few_max;
                 const int step = few ? a.few_rows : a.many_rows;
                 long long w = 0;
-                for (long r = 0; r < rows; r += step) {
+#pragma unroll 1
+                for (int r = 0; r < (int)rows; r += step) {
                     int t0, t1;
                     w += paged_tiles(p, s, r, step, t0, t1);
                 }
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         }
         __syncthreads();
         long long b0 = run0, b1 = run1;
+#pragma unroll 1
         for (int w = 0; w < 32; ++w) {
             if (w < warp) {
                 b0 += warp_sum[0][w];
@@ -90,6 +92,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         a.pre[0] = 0;
         a.pre[p.B + 1] = 0;
         *a.status = bad_any ? kStatusDeviceCheck : kStatusOk;
+        a.line[0] = paged_line(run0, a.few_ctas);
+    } else if (tid == 32) {
+        a.line[1] = paged_line(run1, a.many_ctas);
     }
 }
 
@@ -137,9 +142,8 @@ struct __align__(1024) FewSmem {
     uint8_t ring[C::RING][C::UNIT];
     uint8_t q[C::Q_BUFS][C::Q_BYTES];
     uint8_t p[2][C::P_BYTES];
-    float mref[NR], alpha[NR];  // reference maxima of the item's rows (log2 units), last change as a factor
-    float wmax[4][NR];
-    float lsum[4][NR];
+    alignas(16) float mref[NR];   // reference maxima of the item's rows (log2 units)
+    alignas(16) float alpha[NR];  // their last change as a factor; the epilogue's factor of O
     uint64_t full[C::RING], empty[C::RING];
     uint64_t q_full[C::Q_BUFS], q_empty[C::Q_BUFS];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain;
@@ -175,14 +179,7 @@ __device__ __forceinline__ bool vote_or(bool x) {
     return r != 0;
 }
 __device__ __forceinline__ bool vote_and(bool x) { return !vote_or(!x); }
-
-// Largest value over the warp, by the order of its bits as an integer.
-__device__ __forceinline__ float warp_max(float x) {
-    const int i = __float_as_int(x);
-    const int key = i >= 0 ? i : i ^ 0x7fffffff;
-    const int m = __reduce_max_sync(0xffffffffu, key);
-    return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
-}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kThreadsFew, 1)
@@ -195,9 +192,8 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     const bool f16 = p.dtype == FA_DTYPE_F16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (*reinterpret_cast<volatile int*>(a.status) != 0) return;
-    const long long W = a.pre[p.B];
-    const int n_ctas = paged_ctas(W, (int)gridDim.x), cta = blockIdx.x;
-    if (cta >= n_ctas) return;
+    const int cta = blockIdx.x;
+    if (cta >= a.line->n) return;
 
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
     if (tid == 0) {
@@ -361,8 +357,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
         }
     } else if (warp == 3) {
         // ================= scheduler =================
-        long long u = (long long)cta * W / n_ctas;
-        const long long u_end = (long long)(cta + 1) * W / n_ctas;
+        const PagedLine line = *a.line;
+        long long u = line.start(cta);
+        const long long u_end = line.start(cta + 1);
         int it = 0, b = -1;
         uint32_t qi = 0;
         bool ok = true;
@@ -422,7 +419,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                     const int e = y + 32 * z + lane, r = e / (D / 8), col = e % (D / 8);
                     v[z] = make_uint4(0, 0, 0, 0);
                     if (r < rows) {
-                        const int i = (r0 + r) / p.G, h = x.g * p.G + (r0 + r) - i * p.G;
+                        const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), h = x.g * p.G + (r0 + r) - i * p.G;
                         v[z] = *reinterpret_cast<const uint4*>(a.q + (((long)sq.q0 + i) * p.h_q + h) * D + 8 * col);
                     }
                 }
@@ -456,6 +453,12 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             p_at[x] = (key >> 6) * (NR * 128) + (((((key & 63) >> 3) ^ x) & 7) << 4) + (key & 7) * 2;
+        // A [row][key] array of floats over both P buffers, for what is summed or turned across the
+        // keys while no P V is in flight: TPR threads to a row, each starting at another element of it
+        // so that a warp's reads fall into different banks.
+        float* grid = reinterpret_cast<float*>(s.p[0]);
+        constexpr int TPR = kKeyTile / NR;
+        const int my_row = key / TPR, row_at = my_row * kKeyTile + key % TPR;
         uint32_t gt = 0;  // tiles done
         bool ok = true;
         for (int it = 0;; ++it) {
@@ -466,8 +469,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             const FewItem& w = s.item[slot];
             const int t0 = w.t0, t1 = w.t1, off = w.nk - w.nq, nk = w.nk, lo = w.lo, hi = w.hi, r0 = w.r0;
             // a tile inside [in_lo, in_hi] is seen by every row
-            const int in_lo = p.left >= 0 ? (r0 + w.rows - 1) / p.G + off - p.left : 0;
-            const int in_hi = p.right >= 0 ? min(nk - 1, r0 / p.G + off + p.right) : nk - 1;
+            const unsigned G = (unsigned)p.G;
+            const int in_lo = p.left >= 0 ? (int)((unsigned)(r0 + w.rows - 1) / G) + off - p.left : 0;
+            const int in_hi = p.right >= 0 ? min(nk - 1, (int)((unsigned)r0 / G) + off + p.right) : nk - 1;
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
@@ -508,10 +512,15 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 }
                 bool over = t == t0;  // the item's first tile sets the references
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float x = __uint_as_float(sr[r]) * c;
-                    sr[r] = __float_as_uint(x);
-                    over = over || x > s.mref[r] + 8.f;
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4*>(&s.mref[r]);
+                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = __uint_as_float(sr[r + e]) * c;
+                        sr[r + e] = __float_as_uint(x);
+                        over = over || x > m[e] + 8.f;
+                    }
                 }
                 if (vote_or(over || !ok)) {
                     if (!vote_and(ok)) {
@@ -520,32 +529,36 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                     }
                     // some score passes its row's reference by more than 2^8: the references move to the
                     // maxima so far, sums and O follow
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const float x = warp_max(__uint_as_float(sr[r]));
-                        if (lane == 0) s.wmax[sub][r] = x;
-                    }
-                    vote_or(false);  // all four warps' maxima are in
-                    if (key < NR) {
-                        const float x = fmaxf(fmaxf(s.wmax[0][key], s.wmax[1][key]), fmaxf(s.wmax[2][key], s.wmax[3][key]));
-                        const float m = t == t0 ? -INFINITY : s.mref[key], mn = fmaxf(m, x);
-                        s.alpha[key] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
-                        s.mref[key] = mn;
-                    }
-                    if (t > t0) {  // O holds P V of the tile before
+                    if (t > t0) {  // O holds P V of the tile before, both P buffers are free
                         ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, ab)) && ok;
                         tc_fence_after();
                     }
-                    vote_or(false);  // the new references are in
-                    if (t > t0) {
 #pragma unroll
-                        for (int r = 0; r < NR; ++r) l[r] *= s.alpha[r];
+                    for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = __uint_as_float(sr[r]);
+                    softmax_sync();
+                    float x = -INFINITY;
+#pragma unroll 4
+                    for (int y = 0; y < NR; ++y) x = fmaxf(x, grid[row_at + TPR * ((y + my_row) % NR)]);
+#pragma unroll
+                    for (int o = TPR / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    if (key % TPR == 0) {
+                        const float m = t == t0 ? -INFINITY : s.mref[my_row], mn = fmaxf(m, x);
+                        s.alpha[my_row] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
+                        s.mref[my_row] = mn;
+                    }
+                    softmax_sync();  // the new references are in
+                    if (t > t0) {
+                        float al[NR];
+#pragma unroll
+                        for (int r = 0; r < NR; r += 4) *reinterpret_cast<float4*>(&al[r]) = *reinterpret_cast<const float4*>(&s.alpha[r]);
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) l[r] *= al[r];
 #pragma unroll
                         for (int h = 0; h < C::OH; ++h) {
                             uint32_t o[NR];
                             tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
 #pragma unroll
-                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s.alpha[r]);
+                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * al[r]);
                             tmem_st_cols<NR>(tmem + lane_base + cO + NR * h, o);
                         }
                     }
@@ -555,11 +568,19 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                     ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf], ((gt - 2) >> 1) & 1, ab)) && ok;
                 }
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float m = s.mref[r];
-                    const float e = ex2(__uint_as_float(sr[r]) - (m == -INFINITY ? 0.f : m));
-                    l[r] += e;
-                    *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[r & 7] + 128 * r]) = f16 ? round16<true>(e) : round16<false>(e);
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4*>(&s.mref[r]);
+                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float e0 = ex2(__uint_as_float(sr[r + e]) - (m[e] == -INFINITY ? 0.f : m[e]));
+                        const float e1 = ex2(__uint_as_float(sr[r + e + 1]) - (m[e + 1] == -INFINITY ? 0.f : m[e + 1]));
+                        l[r + e] += e0;
+                        l[r + e + 1] += e1;
+                        const uint32_t w2 = f16 ? pack16<true>(e0, e1) : pack16<false>(e0, e1);
+                        *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e) & 7] + 128 * (r + e)]) = (uint16_t)w2;
+                        *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e + 1) & 7] + 128 * (r + e + 1)]) = (uint16_t)(w2 >> 16);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -573,77 +594,76 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab)) && ok;
                 tc_fence_after();
             }
-            // row sums over the keys: the lanes, then the four warps
+            // sums of the rows over the keys
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float x = l[r];
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane == 0) s.lsum[sub][r] = x;
-            }
+            for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = l[r];
             if (!vote_and(ok)) break;
             const int rows = w.rows, part = w.part, g = w.g, q0 = w.q0;
+            {
+                float x = 0.f;
+#pragma unroll 4
+                for (int y = 0; y < NR; ++y) x += grid[row_at + TPR * ((y + my_row) % NR)];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] = (s.lsum[0][r] + s.lsum[1][r]) + (s.lsum[2][r] + s.lsum[3][r]);
-            if (part >= 0) {
-                if (sub == 0) {
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (lane == (r & 31) && r < rows) a.part_ml[(long)part * NR + r] = make_float2(has_o ? s.mref[r] : -INFINITY, l[r]);
-                }
-            } else {
-                // l becomes the factor of O
-                int i = r0 / p.G, hh = r0 - i * p.G;
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    if (r < rows) {
-                        const int h = g * p.G + hh;
+                for (int o = TPR / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (key % TPR == 0 && my_row < rows) {
+                    const float m = has_o ? s.mref[my_row] : -INFINITY;
+                    if (part >= 0) {
+                        a.part_ml[(long)part * NR + my_row] = make_float2(m, x);
+                        s.alpha[my_row] = 1.f;
+                    } else {
+                        const int i = (int)((unsigned)(r0 + my_row) / (unsigned)p.G), h = g * p.G + r0 + my_row - i * p.G;
                         const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-                        const float m = has_o ? s.mref[r] : -INFINITY, mf = fmaxf(m, s2);
+                        const float mf = fmaxf(m, s2);
                         const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
-                        const float lt = l[r] * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
-                        const float lse = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
-                        l[r] = lt != 0.f ? wgt / lt : 0.f;
-                        if (a.lse && sub == 0 && lane == (r & 31)) a.lse[(long)h * p.T_q + q0 + i] = lse;
-                    }
-                    if (++hh == p.G) {
-                        hh = 0;
-                        ++i;
+                        const float lt = x * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+                        s.alpha[my_row] = lt != 0.f ? wgt / lt : 0.f;
+                        if (a.lse) a.lse[(long)h * p.T_q + q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
                     }
                 }
             }
+            softmax_sync();
+            // O^T to rows: through shared memory (the P buffers), a warp to a row, 4 columns to a lane
 #pragma unroll
             for (int h = 0; h < C::OH; ++h) {
-                uint32_t o[NR];
                 if (has_o) {
+                    uint32_t o[NR];
                     tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) o[r] = 0u;
-                }
-                if (h == C::OH - 1 && has_o) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.o_free);
-                }
-                const int col = D == 192 ? 64 * h + key : 128 * h + key;
-                if (col >= D || (D == 192 && h == 1 && key < 64)) continue;
-                int i = r0 / p.G, hh = r0 - i * p.G;
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    if (r < rows) {
-                        const float x = __uint_as_float(o[r]);
-                        if (part >= 0)
-                            a.part_o[((long)part * NR + r) * D + col] = x;
-                        else
-                            a.o[(((long)q0 + i) * p.h_q + g * p.G + hh) * D + col] =
-                                l[r] == 0.f ? (uint16_t)0 : f16 ? round16<true>(x * l[r]) : round16<false>(x * l[r]);
+                    if (h == C::OH - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.o_free);
                     }
-                    if (++hh == p.G) {
-                        hh = 0;
-                        ++i;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = __uint_as_float(o[r]);
+                }
+                softmax_sync();
+                const bool mine = D == 64 ? lane < 16 : D == 192 && h == 1 ? lane >= 16 : true;
+                const int col = (D == 192 ? 64 : 128) * h + 4 * lane;
+                if (mine) {
+#pragma unroll 1
+                    for (int r = sub; r < rows; r += 4) {
+                        float4 x = *reinterpret_cast<const float4*>(&grid[r * kKeyTile + 4 * lane]);
+                        const float f = s.alpha[r];
+                        if (f == 0.f || !has_o) {
+                            x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        } else {
+                            x.x *= f;
+                            x.y *= f;
+                            x.z *= f;
+                            x.w *= f;
+                        }
+                        if (part >= 0) {
+                            *reinterpret_cast<float4*>(&a.part_o[((long)part * NR + r) * D + col]) = x;
+                        } else {
+                            const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), hh = g * p.G + r0 + r - i * p.G;
+                            uint2 v;
+                            v.x = f16 ? pack16<true>(x.x, x.y) : pack16<false>(x.x, x.y);
+                            v.y = f16 ? pack16<true>(x.z, x.w) : pack16<false>(x.z, x.w);
+                            *reinterpret_cast<uint2*>(&a.o[(((long)q0 + i) * p.h_q + hh) * D + col]) = v;
+                        }
                     }
                 }
+                softmax_sync();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
@@ -666,22 +686,20 @@ constexpr int kMergeWarps = 8;
 // merges its partials (the CTA before, then every further one up to the item's end), a warp to
 // a row.  The weights are those of an online softmax: 2^(m_k - max).
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, const long long* pre, int n_grid, int rows_held) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, const long long* pre, const PagedLine* at, int rows_held) {
     const Problem& p = a.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (*reinterpret_cast<volatile const int*>(a.status) != 0) return;
-    const long long W = pre[p.B];
-    const int n = paged_ctas(W, n_grid), c = blockIdx.x + 1;
-    if (c >= n) return;
-    const long long u = (long long)c * W / n;
+    const PagedLine line = *at;
+    const int c = blockIdx.x + 1;
+    if (c >= line.n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
+    const long long u = line.start(c);
     const int b = find_sequence(pre, p.B, u);
     const PagedSeq sq = paged_seq(p, b);
     const PagedUnit x = paged_unit(p, sq, rows_held, u - pre[b]);
     const long long first = u - x.k, last = first + x.cost;
-    if (x.k == 0 || (long long)(c - 1) * W / n > first) return;
-    // CTA y holds a unit of the item iff y W / n < last, i.e. y W < last n
-    const int pieces = (int)min((long long)n - 1, (last * n - 1) / W) - c + 2;
-    const int r0 = x.rt * rows_held, rows = (int)min((long)rows_held, (long)sq.nq * p.G - r0);
+    if (x.k == 0 || line.start(c - 1) > first) return;
+    const int pieces = line.owner(last - 1) - c + 2;
+    const int r0 = x.rt * rows_held, rows = min(rows_held, sq.nq * p.G - r0);
     for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += gridDim.y * kMergeWarps) {
         // piece y: slot 2 (c - 1) + 1 for the first, 2 (c - 1 + y) for the others
         float m = -INFINITY, l = 0.f, acc[D / 32];
@@ -714,7 +732,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
                 for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wk, src[32 * e], acc[e]);
             }
         }
-        const int i = (r0 + r) / p.G, h = x.g * p.G + (r0 + r) - i * p.G;
+        const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), h = x.g * p.G + (r0 + r) - i * p.G;
         const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
         const float mf = fmaxf(m, s2);
         const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
@@ -748,10 +766,12 @@ cudaError_t launch_few_d(const PagedArgs& a, const CUtensorMap& tk, const CUtens
 }
 
 template <int D>
-cudaError_t launch_merge_d(const PagedArgs& a, const long long* pre, int ctas, int rows, cudaStream_t st) {
+cudaError_t launch_merge_d(const PagedArgs& a, int which, int ctas, int rows, cudaStream_t st) {
     const dim3 grid(ctas - 1, cdiv(rows < 64 ? rows : 64, kMergeWarps));
-    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, ctas, rows);
-    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, ctas, rows);
+    const long long* pre = a.pre + which * (a.p.B + 1);
+    const PagedLine* line = a.line + which;
+    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, line, rows);
+    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, line, rows);
     return cudaGetLastError();
 }
 
@@ -772,13 +792,13 @@ cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CU
     }
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, const long long* pre, int ctas, int rows, cudaStream_t st) {
+cudaError_t launch_paged_merge(const PagedArgs& a, int which, int ctas, int rows, cudaStream_t st) {
     if (ctas < 2 || a.no_split) return cudaSuccess;
     switch (a.p.d) {
-        case 64: return launch_merge_d<64>(a, pre, ctas, rows, st);
-        case 128: return launch_merge_d<128>(a, pre, ctas, rows, st);
-        case 192: return launch_merge_d<192>(a, pre, ctas, rows, st);
-        case 256: return launch_merge_d<256>(a, pre, ctas, rows, st);
+        case 64: return launch_merge_d<64>(a, which, ctas, rows, st);
+        case 128: return launch_merge_d<128>(a, which, ctas, rows, st);
+        case 192: return launch_merge_d<192>(a, which, ctas, rows, st);
+        case 256: return launch_merge_d<256>(a, which, ctas, rows, st);
         default: return cudaErrorInvalidValue;
     }
 }
