@@ -364,15 +364,15 @@ struct PagedPlan {
     bool empty = true;
     int ctas = 0, few_rows = 0, many_rows = 0;
     bool many = false;  // the tensor-core kernel takes part
-    size_t off_pre = 0, off_line = 0, off_o = 0, off_ml = 0, off_mo = 0, off_mml = 0, ws_bytes = kStatusBytes;
+    size_t off_pre = 0, off_line = 0, off_cut = 0, off_o = 0, off_ml = 0, off_mo = 0, off_mml = 0, ws_bytes = kStatusBytes;
 };
 
 fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl = PagedPlan();
     if (!supported_d(p.d)) return FA_ERR_UNSUPPORTED;
     if (p.B == 0 || p.T_q == 0) return FA_OK;
-    // a sequence's rows, and the units of its row tiles of one position, are counted in 32 bits
-    if ((long)p.T_q * p.G > 0x7fffffffL - 256 || ((long)p.s_kv / kKeyTile + 2) * p.h_kv > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    // a sequence's rows are counted in 32 bits
+    if ((long)p.T_q * p.G > 0x7fffffffL - 256) return FA_ERR_UNSUPPORTED;
     pl.empty = false;
     pl.ctas = sm_count();
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
@@ -382,7 +382,8 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.many_rows = 2 * p.P * p.G;
     pl.off_pre = kStatusBytes;
     pl.off_line = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
-    pl.off_o = pl.off_line + align256(2 * sizeof(PagedLine));
+    pl.off_cut = pl.off_line + align256(2 * sizeof(PagedLine));
+    pl.off_o = pl.off_cut + align256((size_t)2 * pl.ctas * sizeof(PagedCut));
     pl.off_ml = pl.off_o + align256((size_t)2 * pl.ctas * pl.few_rows * p.d * 4);
     pl.ws_bytes = pl.off_ml + align256((size_t)2 * pl.ctas * pl.few_rows * 8);
     if (pl.many) {
@@ -424,8 +425,11 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.pre = reinterpret_cast<long long*>(ws + pl.off_pre);
     a.line = reinterpret_cast<PagedLine*>(ws + pl.off_line);
     a.few_ctas = a.many_ctas = pl.ctas;
-    a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
-    a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+    a.cut = reinterpret_cast<PagedCut*>(ws + pl.off_cut);
+    a.part_o[0] = reinterpret_cast<float*>(ws + pl.off_o);
+    a.part_ml[0] = reinterpret_cast<float2*>(ws + pl.off_ml);
+    a.part_o[1] = reinterpret_cast<float*>(ws + pl.off_mo);
+    a.part_ml[1] = reinterpret_cast<float2*>(ws + pl.off_mml);
     a.status = status;
     CUtensorMap tk, tv;
     const bool f16 = p.dtype == FA_DTYPE_F16;
@@ -434,8 +438,8 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
         return FA_ERR_CUDA;
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
     if (e == cudaSuccess) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
-    if (e == cudaSuccess) e = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, 0, pl.ctas, a.few_rows, st); });
-    if (e != cudaSuccess || !pl.many) return cuda_status(e);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    if (!pl.many) return cuda_status(timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); }));
     // sequences of more rows: the tensor-core kernel, 2 P G rows to an item
     FwdArgs f{};
     CUtensorMap tq;
@@ -453,14 +457,15 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     f.num_pages = a.num_pages;
     f.box = a.box;
     f.no_split = a.no_split;
-    f.o_part = a.part_o = reinterpret_cast<float*>(ws + pl.off_mo);
-    f.part_ml = a.part_ml = reinterpret_cast<float2*>(ws + pl.off_mml);
+    f.cut = a.cut + pl.ctas;
+    f.o_part = a.part_o[1];
+    f.part_ml = a.part_ml[1];
 #ifdef FA_TRACE
     f.trace = reinterpret_cast<unsigned long long*>(ws + pl.ws_bytes - align256(kTraceBytes));
     if (cudaMemsetAsync(f.trace, 0, kTraceBytes, st) != cudaSuccess) return FA_ERR_CUDA;
 #endif
     e = timed(kFwd, st, [&] { return launch_fwd_paged(f, tq, tk, tv, st); });
-    if (e == cudaSuccess) e = timed(kCombine, st, [&] { return launch_paged_merge(a, 1, pl.ctas, a.many_rows, st); });
+    if (e == cudaSuccess) e = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, true, st); });
     return cuda_status(e);
 }
 

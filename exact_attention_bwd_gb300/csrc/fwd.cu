@@ -193,10 +193,12 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         const int boxes = kKeyTile / a.box;
         int gt = 0, n_q = 0, k_issued = 0, v_issued = 0;
         bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, ab)) != 0; };
+        Tracer tr;
+        tr.init(a.trace, 0);
+        auto wait = [&](TraceBarrier b, uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, twait(tr, b, bar, ph, ab)) != 0; };
         for (int n = 0; ok; ++n) {
             const int slot = n % kItemSlots;
-            if (!(ok = wait(&s.item_full[slot], (n / kItemSlots) & 1))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
             const ItemInfo& it = s.item[slot];
             const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, nk = it.nk;
             const int32_t* table = p.block_table + (long)it.b * p.max_blocks;
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
             if (end) break;
             if (u1 <= u0) continue;
+            tr.item(n);
             // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used keys
             // or for a table entry outside the pool; the next tile's entry is fetched ahead
             auto entry = [&](int t) {
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
                 return lane < boxes && t < u1 && j < nk ? table[j / p.page_size] : a.num_pages;
             };
             int next = entry(u0);
-            if (n_q > 0 && !(ok = wait(&s.q_empty, (n_q - 1) & 1))) break;
+            if (n_q > 0 && !(ok = wait(kBQEmpty, &s.q_empty, (n_q - 1) & 1))) break;
             if (lane == 0) {
                 mbar_expect_tx(&s.q_full, qbox * C::KCH * ((on0 ? 1u : 0u) + (on1 ? 1u : 0u)));
                 for (int c = 0; c < C::KCH; ++c) {
@@ -232,14 +235,14 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
                     if (key < nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
                     page = a.num_pages;
                 }
-                if (!(ok = wait(&s.k_empty[st], ph ^ 1))) break;
+                if (!(ok = wait(kBKEmpty, &s.k_empty[st], ph ^ 1))) break;
                 if (lane == 0) mbar_expect_tx(&s.k_full[st], C::KV_BYTES);
                 __syncwarp();
                 if (lane < boxes)
                     for (int c = 0; c < C::KCH; ++c)
                         tma_load_4d(&s.k[st][c * C::KV_CHUNK + lane * a.box * 128], &tmk, &s.k_full[st], c * 64, g, row, page);
                 ++k_issued;
-                if (!(ok = wait(&s.v_empty[st], ph ^ 1))) break;
+                if (!(ok = wait(kBVEmpty, &s.v_empty[st], ph ^ 1))) break;
                 if (lane == 0) mbar_expect_tx(&s.v_full[st], C::KV_BYTES);
                 __syncwarp();
                 if (lane < boxes)
@@ -466,42 +469,25 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // come from those intervals (their hull), since a tile's rows may span sequences.
         int n = 0;
         bool ok = true;
-        // PG: the CTA's stretch of the line of units, and the sequence the walk is in
-        long long pu = 0, pu_end = 0, pb = 0, pe = 0;
-        if constexpr (PG) {
-            const PagedLine line = *a.line;
-            pu = line.start(blockIdx.x);
-            pu_end = line.start(blockIdx.x + 1);
-        }
-        int seq = 0;
-        PagedSeq ps{};
-        for (int idx = blockIdx.x, step = first_step(a.snake); PG ? pu < pu_end : idx < a.n_items;
+        // PG: the walk over the CTA's stretch of the line of units
+        PagedWalk walk(PG ? *a.line : PagedLine{}, blockIdx.x);
+        for (int idx = blockIdx.x, step = first_step(a.snake); PG || idx < a.n_items;
              idx += step, step = 2 * (int)gridDim.x - step) {
             FwdItem w;
             int part = -1;
             if constexpr (PG) {
-                if (pu >= pe) {
-                    seq = find_sequence(a.pre, p.B, pu);
-                    pb = a.pre[seq];
-                    pe = a.pre[seq + 1];
-                    ps = paged_seq(p, seq);
-                }
-                const PagedUnit x = paged_unit(p, ps, 2 * p.P * p.G, pu - pb);
-                if (a.no_split && x.k > 0) {  // the item belongs to the CTA that holds its first unit
-                    pu += x.cost - x.k;
-                    continue;
-                }
-                const int take = a.no_split ? x.cost : (int)min((long long)(x.cost - x.k), pu_end - pu);
-                part = take == x.cost ? -1 : 2 * (int)blockIdx.x + (x.k == 0 ? 1 : 0);
-                pu += take;
-                w.sv = SeqView{seq, ps.q0, ps.nq, 0, ps.nk, 0};
+                if (!walk.next(p, a.pre, *a.line, blockIdx.x, 2 * p.P * p.G, a.no_split)) break;
+                const PagedSeq& ps = walk.seq;
+                const PagedUnit& x = walk.x;
+                part = walk.from_start && walk.to_end ? -1 : 2 * (int)blockIdx.x + (walk.from_start ? 1 : 0);
+                w.u0 = walk.t0;
+                w.u1 = walk.t1;
+                w.sv = SeqView{walk.b, ps.q0, ps.nq, 0, ps.nk, 0};
                 w.band = Band{ps.nk - ps.nq, p.left, p.right, ps.nk};
                 w.g = x.g;
                 w.split = 0;
                 w.tail = false;
                 w.live = true;
-                w.u0 = x.t0 + x.k;
-                w.u1 = min(w.u0 + take, x.t1);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     w.ti[k].s0 = (2 * x.rt + k) * p.P;
@@ -587,6 +573,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             if (lane == 0) mbar_arrive(&s.item_full[slot]);
             ++n;
         }
+        if (PG && lane == 0) a.cut[blockIdx.x] = walk.cut;
         if (ok) {
             // the end marker
             const int slot = n % kItemSlots;
@@ -645,28 +632,6 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             // one TMEM read of the whole S row (KT fp32 columns)
             const int j0 = j * KT;
             const bool edge = (j0 < jlo || j0 + KT - 1 > jhi);
-            if constexpr (PG) {
-                // value rows outside every row's band: cleared by tile 0's group where it takes part (the
-                // P V of tile 1 is issued behind that of tile 0), else by tile 1's
-                const ItemInfo& itm = s.item[slot];
-                const int lo = itm.lo, hi = itm.hi;
-                if ((j0 < lo || j0 + KT - 1 > hi) && (k == 0 || j < itm.t0[0] || j >= itm.t1[0])) {
-                    const int vt = gt0 + j - itm.u0, st = vt % C::STAGES;
-                    const bool there = mbar_wait(&s.v_full[st], (vt / C::STAGES) & 1, ab);
-                    if (there && (j0 + r < lo || j0 + r > hi)) {
-#pragma unroll
-                        for (int x = 0; x < C::KCH; ++x)
-#pragma unroll
-                            for (int y = 0; y < 8; ++y)
-                                *reinterpret_cast<uint4*>(&s.v[st][x * C::KV_CHUNK + r * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    if (!__all_sync(0xffffffffu, there)) {
-                        ok = false;
-                        break;
-                    }
-                }
-            }
             uint32_t sr[KT];
             if constexpr (KT == 128) tmem_ld_32x32b_x128(tS, sr);
             else tmem_ld_32x32b_x64(tS, sr);
@@ -741,6 +706,28 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             else tmem_st_32x32b_x32(tS, sr);
             l += sum;
             if (KT == 64 && __any_sync(0xffffffffu, rescale)) rescale_o();
+            if constexpr (PG) {
+                // value rows outside every row's band: cleared by tile 0's group where it takes part (the
+                // P V of tile 1 is issued behind that of tile 0), else by tile 1's
+                const ItemInfo& itm = s.item[slot];
+                const int lo = itm.lo, hi = itm.hi;
+                if ((j0 < lo || j0 + KT - 1 > hi) && (k == 0 || j < itm.t0[0] || j >= itm.t1[0])) {
+                    const int vt = gt0 + j - itm.u0, st = vt % C::STAGES;
+                    const bool there = mbar_wait(&s.v_full[st], (vt / C::STAGES) & 1, ab);
+                    if (there && (j0 + r < lo || j0 + r > hi)) {
+#pragma unroll
+                        for (int x = 0; x < C::KCH; ++x)
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                *reinterpret_cast<uint4*>(&s.v[st][x * C::KV_CHUNK + r * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    if (!__all_sync(0xffffffffu, there)) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.p_full[k]);

@@ -69,6 +69,7 @@ struct FwdArgs {
     // pages, rows of one K / V copy, whole items only, statistics of the partials in o_part
     const long long* pre;
     const struct PagedLine* line;
+    struct PagedCut* cut;
     int num_pages, box, no_split;
     float2* part_ml;
 };
@@ -148,9 +149,10 @@ struct PagedArgs {
     int validate;       // check the offsets and lengths first
     long long* pre;     // [2][B + 1] units before each sequence: few-row work, the rest
     struct PagedLine* line;  // [2] their lines
+    struct PagedCut* cut;    // [2][CTAs] the items that the CTAs' stretches cut
     int few_ctas, many_ctas; // grids that share the lines
-    float* part_o;      // [2 CTAs][rows][d] un-normalised partial outputs
-    float2* part_ml;    // [2 CTAs][rows] reference maximum (log2 units) and sum
+    float* part_o[2];   // [2][2 CTAs][rows][d] un-normalised partial outputs
+    float2* part_ml[2]; // [2][2 CTAs][rows] reference maximum (log2 units) and sum
     int* status;
 };
 // PagedArgs::few_max of a call whose every sequence is the few-row kernel's
@@ -202,7 +204,7 @@ cudaError_t launch_bwd_main(const BwdArgs& a, const CUtensorMap& tq, const CUten
 cudaError_t launch_bwd_post(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
 cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
-cudaError_t launch_paged_merge(const PagedArgs& a, int which, int ctas, int rows, cudaStream_t st);  // which: 0 few rows, 1 the rest
+cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st);  // many: both kernels' items
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int ctas, cudaStream_t st);
 int norm_rope_bwd_ctas(long rows, int d, int sms);

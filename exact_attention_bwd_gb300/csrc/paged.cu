@@ -23,10 +23,10 @@ namespace {
 // ------------------------------------------------------------------------------------------
 // schedule: the line of units
 // ------------------------------------------------------------------------------------------
-constexpr int kPrepThreads = 1024;
+constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArgs a) {
-    __shared__ long long warp_sum[2][32];
+    __shared__ long long warp_sum[2][kPrepWarps];
     __shared__ int bad_any;
     const Problem& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -51,9 +51,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
 #pragma unroll 1
                 for (int r = 0; r < (int)rows; r += step) {
                     int t0, t1;
-                    w += paged_tiles(p, s, r, step, t0, t1);
+                    w += paged_tiles(p, s, r, step, few ? kFewLead : kManyLead, t0, t1);
                 }
-                (few ? w0 : w1) = w * p.h_kv;
+                (few ? w0 : w1) = w;
             }
         }
         long long s0 = w0, s1 = w1;
@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         }
         __syncthreads();
         long long b0 = run0, b1 = run1;
-#pragma unroll 1
-        for (int w = 0; w < 32; ++w) {
+#pragma unroll
+        for (int w = 0; w < kPrepWarps; ++w) {
             if (w < warp) {
                 b0 += warp_sum[0][w];
                 b1 += warp_sum[1][w];
@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         a.pre[0] = 0;
         a.pre[p.B + 1] = 0;
         *a.status = bad_any ? kStatusDeviceCheck : kStatusOk;
-        a.line[0] = paged_line(run0, a.few_ctas);
+        a.line[0] = paged_line(run0 * p.h_kv, kFewLead, a.few_ctas);
     } else if (tid == 32) {
-        a.line[1] = paged_line(run1, a.many_ctas);
+        a.line[1] = paged_line(run1 * p.h_kv, kManyLead, a.many_ctas);
     }
 }
 
@@ -358,27 +358,14 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     } else if (warp == 3) {
         // ================= scheduler =================
         const PagedLine line = *a.line;
-        long long u = line.start(cta);
-        const long long u_end = line.start(cta + 1);
-        int it = 0, b = -1;
+        PagedWalk walk(line, cta);
+        int it = 0;
         uint32_t qi = 0;
         bool ok = true;
-        PagedSeq sq{};
-        long long pb = 0, pe = 0;  // units before and up to the end of the sequence
-        while (ok && u < u_end) {
-            if (u >= pe) {
-                b = find_sequence(a.pre, p.B, u);
-                pb = a.pre[b];
-                pe = a.pre[b + 1];
-                sq = paged_seq(p, b);
-            }
-            const PagedUnit x = paged_unit(p, sq, NR, u - pb);
-            if (a.no_split && x.k > 0) {  // the item belongs to the CTA that holds its first unit
-                u += x.cost - x.k;
-                continue;
-            }
-            const int take = a.no_split ? x.cost : (int)min((long long)(x.cost - x.k), u_end - u);
-            const int t0 = x.t0 + x.k, t1 = min(t0 + take, x.t1);
+        while (ok && walk.next(p, a.pre, line, cta, NR, a.no_split)) {
+            const PagedUnit& x = walk.x;
+            const int t0 = walk.t0, t1 = walk.t1;
+            const PagedSeq& sq = walk.seq;
             const int r0 = x.rt * NR, rows = min(NR, sq.nq * p.G - r0);
             const int slot = it % kItems;
             if (it >= kItems && !(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_empty[slot], ((it / kItems) - 1) & 1, ab)))) break;
@@ -386,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 const Band bd{sq.nk - sq.nq, p.left, p.right, sq.nk};
                 FewItem& w = s.item[slot];
                 w.end = 0;
-                w.b = b;
+                w.b = walk.b;
                 w.q0 = sq.q0;
                 w.nq = sq.nq;
                 w.nk = sq.nk;
@@ -397,11 +384,10 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 w.t1 = t1;
                 w.lo = bd.lo(r0 / p.G);
                 w.hi = bd.hi((r0 + rows - 1) / p.G);
-                w.part = take == x.cost ? -1 : 2 * cta + (x.k == 0 ? 1 : 0);
+                w.part = walk.from_start && walk.to_end ? -1 : 2 * cta + (walk.from_start ? 1 : 0);
                 mbar_arrive(&s.item_full[slot]);
             }
             ++it;
-            u += take;
             if (t1 <= t0) continue;
             // Q rows of the item, in the 128-byte-swizzled layout the MMA reads; zeros past them
             const int qb = (int)(qi % C::Q_BUFS);
@@ -434,6 +420,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             if (lane == 0) mbar_arrive(&s.q_full[qb]);
             ++qi;
         }
+        if (lane == 0) a.cut[cta] = walk.cut;
         if (ok) {
             const int slot = it % kItems;
             if (it < kItems || __all_sync(0xffffffffu, mbar_wait(&s.item_empty[slot], ((it / kItems) - 1) & 1, ab))) {
@@ -492,23 +479,6 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
                         if (r < ra || r > rb) sr[r] = __float_as_uint(-INFINITY);
-                    // values at keys that no row sees may be anything (unused rows of a page): 0 * NaN
-                    // would reach every row, so they are cleared
-                    bool there = true;
-#pragma unroll
-                    for (int h = 0; h < KU; ++h) {
-                        const uint32_t n = 2 * KU * gt + KU + h;
-                        const int sl = C::slot_of(n);
-                        there = mbar_wait(&s.full[sl], (n / RING) & 1, ab) && there;
-                        if (there && (j < lo || j > hi)) {
-#pragma unroll
-                            for (int x = 0; x < C::UC / 64; ++x)
-#pragma unroll
-                                for (int y = 0; y < 8; ++y)
-                                    *reinterpret_cast<uint4*>(&s.ring[sl][x * C::CHUNK + key * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    ok = __all_sync(0xffffffffu, there) && ok;
                 }
                 bool over = t == t0;  // the item's first tile sets the references
 #pragma unroll
@@ -582,6 +552,25 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                         *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e + 1) & 7] + 128 * (r + e + 1)]) = (uint16_t)(w2 >> 16);
                     }
                 }
+                if (edge) {
+                    // values at keys that no row sees may be anything (unused rows of a page): 0 * NaN
+                    // would reach every row, so they are cleared
+                    bool there = true;
+#pragma unroll
+                    for (int h = 0; h < KU; ++h) {
+                        const uint32_t n = 2 * KU * gt + KU + h;
+                        const int sl = C::slot_of(n);
+                        there = mbar_wait(&s.full[sl], (n / RING) & 1, ab) && there;
+                        if (there && (j < lo || j > hi)) {
+#pragma unroll
+                            for (int x = 0; x < C::UC / 64; ++x)
+#pragma unroll
+                                for (int y = 0; y < 8; ++y)
+                                    *reinterpret_cast<uint4*>(&s.ring[sl][x * C::CHUNK + key * 128 + y * 16]) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, there) && ok;
+                }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -608,7 +597,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 if (key % TPR == 0 && my_row < rows) {
                     const float m = has_o ? s.mref[my_row] : -INFINITY;
                     if (part >= 0) {
-                        a.part_ml[(long)part * NR + my_row] = make_float2(m, x);
+                        a.part_ml[0][(long)part * NR + my_row] = make_float2(m, x);
                         s.alpha[my_row] = 1.f;
                     } else {
                         const int i = (int)((unsigned)(r0 + my_row) / (unsigned)p.G), h = g * p.G + r0 + my_row - i * p.G;
@@ -653,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                             x.w *= f;
                         }
                         if (part >= 0) {
-                            *reinterpret_cast<float4*>(&a.part_o[((long)part * NR + r) * D + col]) = x;
+                            *reinterpret_cast<float4*>(&a.part_o[0][((long)part * NR + r) * D + col]) = x;
                         } else {
                             const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), hh = g * p.G + r0 + r - i * p.G;
                             uint2 v;
@@ -682,66 +671,85 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 // ------------------------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-// blockIdx.x + 1 = the CTA at whose first unit an item may be cut; the first such CTA of an item
-// merges its partials (the CTA before, then every further one up to the item's end), a warp to
-// a row.  The weights are those of an online softmax: 2^(m_k - max).
+// blockIdx.x: the CTA that holds the start of a cut item; a warp merges kMergeRows of its rows from
+// the partials of that CTA (its slot 1) and the next ones (their slot 0), in the order of the
+// keys.  The weights are those of an online softmax: 2^(m_k - max).  blockIdx.y numbers the row
+// groups of the few-row kernel's items, then those of the other's.
+constexpr int kMergeRows = 2;
+constexpr int kMergeRowsCta = kMergeWarps * kMergeRows;
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, const long long* pre, const PagedLine* at, int rows_held) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, int few_groups) {
+    constexpr int VW = D / 32;  // columns of a lane, consecutive
     const Problem& p = a.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const PagedLine line = *at;
-    const int c = blockIdx.x + 1;
-    if (c >= line.n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
-    const long long u = line.start(c);
-    const int b = find_sequence(pre, p.B, u);
-    const PagedSeq sq = paged_seq(p, b);
-    const PagedUnit x = paged_unit(p, sq, rows_held, u - pre[b]);
-    const long long first = u - x.k, last = first + x.cost;
-    if (x.k == 0 || line.start(c - 1) > first) return;
-    const int pieces = line.owner(last - 1) - c + 2;
-    const int r0 = x.rt * rows_held, rows = min(rows_held, sq.nq * p.G - r0);
-    for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += gridDim.y * kMergeWarps) {
-        // piece y: slot 2 (c - 1) + 1 for the first, 2 (c - 1 + y) for the others
-        float m = -INFINITY, l = 0.f, acc[D / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+    const int which = (int)blockIdx.y < few_groups ? 0 : 1;
+    const int held = which ? a.many_rows : a.few_rows;
+    const int r1 = (((int)blockIdx.y - (which ? few_groups : 0)) * kMergeWarps + warp) * kMergeRows;
+    if (c >= a.line[which].n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
+    const PagedCut cut = a.cut[which * gridDim.x + c];
+    if (r1 >= cut.rows) return;
+    // the partials' row of piece y, row r
+    auto at = [&](int y, int r) { return (long)(2 * (c + y) + (y == 0 ? 1 : 0)) * held + r; };
+    float m[kMergeRows], l[kMergeRows], acc[kMergeRows][VW];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        for (int y0 = 0; y0 < pieces; y0 += 32) {
-            const int y = y0 + lane;
+    for (int z = 0; z < kMergeRows; ++z) {
+        m[z] = -INFINITY;
+        l[z] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) acc[z][e] = 0.f;
+    }
+    for (int y0 = 0; y0 < cut.pieces; y0 += 32) {
+        const int y = y0 + lane, cnt = min(32, cut.pieces - y0);
+        float wy[kMergeRows];
+#pragma unroll
+        for (int z = 0; z < kMergeRows; ++z) {
+            const int r = min(r1 + z, cut.rows - 1);  // a row past the end is the last one again, not stored
             float2 ml = make_float2(-INFINITY, 0.f);
-            if (y < pieces) ml = a.part_ml[(long)(2 * (c - 1 + y) + (y == 0 ? 1 : 0)) * rows_held + r];
+            if (lane < cnt) ml = a.part_ml[which][at(y, r)];
             float mx = ml.x;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float mn = fmaxf(m, mx);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float keep = ex2(m - base), wy = ex2(ml.x - base);
-            float ls = ml.y * wy;
+            const float mn = fmaxf(m[z], mx);
+            const float base = mn == -INFINITY ? 0.f : mn, keep = ex2(m[z] - base);
+            wy[z] = ex2(ml.x - base);
+            float ls = ml.y * wy[z];
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-            l = l * keep + ls;
-            m = mn;
+            l[z] = l[z] * keep + ls;
+            m[z] = mn;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] *= keep;
-            const int cnt = min(32, pieces - y0);
-#pragma unroll 4
-            for (int k = 0; k < cnt; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wy, k);
-                const int yk = y0 + k;
-                const float* src = a.part_o + ((long)(2 * (c - 1 + yk) + (yk == 0 ? 1 : 0)) * rows_held + r) * D + lane;
+            for (int e = 0; e < VW; ++e) acc[z][e] *= keep;
+        }
+#pragma unroll 2
+        for (int k = 0; k < cnt; ++k) {
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wk, src[32 * e], acc[e]);
+            for (int z = 0; z < kMergeRows; ++z) {
+                const float wk = __shfl_sync(0xffffffffu, wy[z], k);
+                const float* src = a.part_o[which] + at(y0 + k, min(r1 + z, cut.rows - 1)) * D + VW * lane;
+#pragma unroll
+                for (int e = 0; e < VW; e += 2) {
+                    const float2 x = *reinterpret_cast<const float2*>(src + e);
+                    acc[z][e] = fmaf(wk, x.x, acc[z][e]);
+                    acc[z][e + 1] = fmaf(wk, x.y, acc[z][e + 1]);
+                }
             }
         }
-        const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), h = x.g * p.G + (r0 + r) - i * p.G;
-        const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-        const float mf = fmaxf(m, s2);
-        const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
-        const float lt = l * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
-        const float f = lt != 0.f ? wgt / lt : 0.f;
-        if (a.lse && lane == 0) a.lse[(long)h * p.T_q + sq.q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
-        uint16_t* out = a.o + (((long)sq.q0 + i) * p.h_q + h) * D + lane;
+    }
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) out[32 * e] = round16<F16>(f == 0.f ? 0.f : acc[e] * f);
+    for (int z = 0; z < kMergeRows; ++z) {
+        const int r = r1 + z;
+        if (r >= cut.rows) break;
+        const int i = (int)((unsigned)(cut.r0 + r) / (unsigned)p.G), h = cut.g * p.G + (cut.r0 + r) - i * p.G;
+        const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
+        const float mf = fmaxf(m[z], s2);
+        const float wgt = m[z] == -INFINITY ? 0.f : ex2(m[z] - mf);
+        const float lt = l[z] * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+        const float f = lt != 0.f ? wgt / lt : 0.f;
+        if (a.lse && lane == 0) a.lse[(long)h * p.T_q + cut.q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (((long)cut.q0 + i) * p.h_q + h) * D + VW * lane);
+#pragma unroll
+        for (int e = 0; e < VW; e += 2) out[e / 2] = f == 0.f ? 0u : pack16<F16>(acc[z][e] * f, acc[z][e + 1] * f);
     }
 }
 
@@ -766,12 +774,9 @@ cudaError_t launch_few_d(const PagedArgs& a, const CUtensorMap& tk, const CUtens
 }
 
 template <int D>
-cudaError_t launch_merge_d(const PagedArgs& a, int which, int ctas, int rows, cudaStream_t st) {
-    const dim3 grid(ctas - 1, cdiv(rows < 64 ? rows : 64, kMergeWarps));
-    const long long* pre = a.pre + which * (a.p.B + 1);
-    const PagedLine* line = a.line + which;
-    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, line, rows);
-    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, pre, line, rows);
+cudaError_t launch_merge_d(const PagedArgs& a, const dim3& grid, int few_groups, cudaStream_t st) {
+    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, few_groups);
+    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, few_groups);
     return cudaGetLastError();
 }
 
@@ -792,13 +797,15 @@ cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CU
     }
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int which, int ctas, int rows, cudaStream_t st) {
-    if (ctas < 2 || a.no_split) return cudaSuccess;
+cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st) {
+    if (a.few_ctas < 2 || a.no_split) return cudaSuccess;
+    const int few_groups = cdiv(a.few_rows, kMergeRowsCta);
+    const dim3 grid(a.few_ctas, few_groups + (many ? cdiv(a.many_rows, kMergeRowsCta) : 0));
     switch (a.p.d) {
-        case 64: return launch_merge_d<64>(a, which, ctas, rows, st);
-        case 128: return launch_merge_d<128>(a, which, ctas, rows, st);
-        case 192: return launch_merge_d<192>(a, which, ctas, rows, st);
-        case 256: return launch_merge_d<256>(a, which, ctas, rows, st);
+        case 64: return launch_merge_d<64>(a, grid, few_groups, st);
+        case 128: return launch_merge_d<128>(a, grid, few_groups, st);
+        case 192: return launch_merge_d<192>(a, grid, few_groups, st);
+        case 256: return launch_merge_d<256>(a, grid, few_groups, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -1,13 +1,14 @@
 // Packed queries over a paged cache: what the schedule, the kernels and the combine share.
 //
-// Work is counted in (row tile, key tile) units.  A sequence's query rows (position, head of
-// the group) of one key/value head are cut into row tiles; each row tile and key/value head
-// is an item of as many units as it has key tiles in its band (one if it has none: its rows
-// still have to be written).  All units form one line, sequence by sequence, row tile by row
-// tile, head by head, and each of n CTAs takes an equal stretch of it: every CTA streams the
-// same number of key tiles whatever the lengths are.  An item cut by a stretch's end leaves
-// fp32 partials (at most two per CTA, so the workspace does not depend on the lengths), which
-// the combine merges in the order of the keys.
+// Work is counted in key tiles of a row tile.  A sequence's query rows (position, head of the
+// group) of one key/value head are cut into row tiles; each head and row tile is an item of
+// a few units for its prologue and epilogue, which cost about as much as so many tiles (`lead`),
+// and one unit for each key tile in its band (one if it has none: its rows still have to be
+// written).  All units form one line, sequence by sequence, head by head, row tile by row tile,
+// and each of n CTAs takes an equal stretch of it, so the CTAs finish together whatever the
+// lengths are; neighbours on the line, which run at the same time, share a head's keys in L2.
+// A stretch's end among an item's tiles cuts it (one among its lead stands for the item's start): the pieces leave fp32 partials, at most two per CTA, so the workspace
+// does not depend on the lengths, and the combine merges them in the order of the keys.
 #pragma once
 #include "common.cuh"
 
@@ -29,21 +30,30 @@ __device__ __forceinline__ PagedSeq paged_seq(const Problem& p, int b) {
     return s;
 }
 
+// The lead of an item in tiles, by what levels the CTAs' finishing times best
+#ifndef FA_FEW_LEAD
+#define FA_FEW_LEAD 2
+#endif
+#ifndef FA_MANY_LEAD
+#define FA_MANY_LEAD 2
+#endif
+constexpr int kFewLead = FA_FEW_LEAD, kManyLead = FA_MANY_LEAD;
+
 // Key tiles [t0, t1) of the rows [r0, r0 + rows) (numbered position * G + head of the group; r0 is
-// one of them, rows * G in all fit 32 bits), and the units they cost.
-__device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, int r0, int rows, int& t0, int& t1) {
+// one of them, nq * G fits 32 bits), and the units of the item.
+__device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, int r0, int rows, int lead, int& t0, int& t1) {
     const Band bd{s.nk - s.nq, p.left, p.right, s.nk};
     const unsigned G = (unsigned)p.G;
     const int i0 = (int)((unsigned)r0 / G), i1 = min(s.nq - 1, (int)((unsigned)(r0 + rows - 1) / G));
     kv_tile_range(bd, i0, i1, kKeyTile, t0, t1);
-    return max(t1 - t0, 1);
+    return lead + max(t1 - t0, 1);
 }
 
 // The line of one kernel's units as the preparation leaves it: n CTAs take part, CTA c's stretch
 // is [start(c), start(c + 1)), the first `more` stretches one unit longer than `each`.
 struct PagedLine {
     long long units;
-    int n, more;
+    int lead, n, more;
     long long each;
     __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
     // the CTA that holds unit u
@@ -52,66 +62,118 @@ struct PagedLine {
         return u < head ? (int)(u / (each + 1)) : more + (int)((u - head) / each);
     }
 };
-// Each CTA has kMinUnits units at least.
-constexpr int kMinUnits = 2;
-__device__ __forceinline__ PagedLine paged_line(long long units, int n_ctas) {
+// Each CTA has more units than a lead.
+__device__ __forceinline__ PagedLine paged_line(long long units, int lead, int n_ctas) {
     PagedLine x;
     x.units = units;
-    x.n = (int)min((long long)n_ctas, (units + kMinUnits - 1) / kMinUnits);
+    x.lead = lead;
+    x.n = (int)min((long long)n_ctas, (units + lead) / (lead + 1));
     x.each = x.n > 0 ? units / x.n : 0;
     x.more = x.n > 0 ? (int)(units % x.n) : 0;
     return x;
 }
 
-// The largest b in [0, B) with pre[b] <= u (warp-wide; pre is non-decreasing, pre[0] = 0).
-__device__ __forceinline__ int find_sequence(const long long* pre, int B, long long u) {
+// The sequence of unit u: the largest b in [0, B) with pre[b] h_kv <= u, where pre[b] counts the
+// units of one head ahead of sequence b (warp-wide; pre is non-decreasing, pre[0] = 0).
+__device__ __forceinline__ int find_sequence(const long long* pre, int B, int h_kv, long long u) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = B - 1;
 #pragma unroll 1
     while (hi > lo) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * step;
-        const bool le = at <= hi && pre[at] <= u;
+        const bool le = at <= hi && pre[at] * h_kv <= u;
         lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
         hi = min(hi, lo + step - 1);
     }
     return lo;
 }
 
-// Unit `rem` of a sequence: its item (row tile, head) and the unit of the item.  Warp-wide: a
-// lane to a row tile, 32 at a time.
+// Unit `rem` of a sequence with `per_head` units to a head: its item (head, row tile), the unit of
+// the item and the item's units and key tiles.  Warp-wide: a lane to a row tile, 32 at a time.
 struct PagedUnit {
     int rt, g, k, cost, t0, t1;
 };
-__device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, long long rem) {
+__device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, int lead, long long rem,
+                                                long long per_head) {
     const int lane = threadIdx.x & 31;
     const int tiles = (s.nq * p.G + rows - 1) / rows;
     PagedUnit x;
+    x.g = rem < per_head ? 0 : (int)(rem / per_head);
+    rem -= x.g * per_head;
     int base = 0, src = 0, sum = 0, cost = 0, t0 = 0, t1 = 0;
 #pragma unroll 1
     for (;; base += 32) {
         t0 = t1 = cost = 0;
-        if (base + lane < tiles) cost = paged_tiles(p, s, (base + lane) * rows, rows, t0, t1);
+        if (base + lane < tiles) cost = paged_tiles(p, s, (base + lane) * rows, rows, lead, t0, t1);
         sum = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, rem < (long long)sum * p.h_kv);
+        const unsigned past = __ballot_sync(0xffffffffu, rem < sum);
         src = past ? __ffs(past) - 1 : 31;
         if (past || base + 32 >= tiles) break;  // (no lane is past only for a unit outside the sequence)
-        rem -= (long long)__shfl_sync(0xffffffffu, sum, 31) * p.h_kv;
+        rem -= __shfl_sync(0xffffffffu, sum, 31);
     }
     x.rt = base + src;
-    x.cost = max(__shfl_sync(0xffffffffu, cost, src), 1);
+    x.cost = __shfl_sync(0xffffffffu, cost, src);
     x.t0 = __shfl_sync(0xffffffffu, t0, src);
     x.t1 = __shfl_sync(0xffffffffu, t1, src);
-    rem -= (long long)(__shfl_sync(0xffffffffu, sum, src) - x.cost) * p.h_kv;
-    // rem < cost h_kv, which fits 32 bits
-    x.g = (int)((unsigned)rem / (unsigned)x.cost);
-    x.k = (int)((unsigned)rem - (unsigned)(x.g * x.cost));
+    x.k = (int)rem - (__shfl_sync(0xffffffffu, sum, src) - x.cost);
     return x;
 }
+
+// An item cut behind its start: the CTA that holds the start leaves this for the combine.
+struct PagedCut {
+    int q0, g;        // first query row of the sequence, key/value head
+    int r0, rows;     // first row and rows (0: the CTA's stretch cuts no item behind its start)
+    int pieces;       // its CTAs, this one and the next ones
+};
+
+// The walk of one warp over its CTA's stretch, piece by piece.
+struct PagedWalk {
+    long long u, end;          // next unit, end of the stretch
+    int lead;
+    long long before = 0, per_head = 0, after = 0;  // the sequence's: units ahead of it, of a head, up to its end
+    int b = 0;
+    PagedSeq seq{};
+    __device__ __forceinline__ PagedWalk(const PagedLine& line, int cta) : u(line.start(cta)), end(line.start(cta + 1)), lead(line.lead) {}
+    PagedUnit x;               // the piece's item
+    int t0 = 0, t1 = 0;        // its key tiles
+    bool from_start = true, to_end = true;  // whether it is the item's start and end
+    PagedCut cut{0, 0, 0, 0, 0};
+    // Moves to the next piece; false: the stretch is done
+    __device__ __forceinline__ bool next(const Problem& p, const long long* pre, const PagedLine& line, int cta, int rows, bool no_split) {
+        while (u < end) {
+            if (u >= after) {
+                b = find_sequence(pre, p.B, p.h_kv, u);
+                before = pre[b] * p.h_kv;
+                per_head = pre[b + 1] - pre[b];
+                after = before + per_head * p.h_kv;
+                seq = paged_seq(p, b);
+            }
+            x = paged_unit(p, seq, rows, lead, u - before, per_head);
+            if (no_split && x.k > lead) {  // the item is the CTA's that holds its start
+                u += x.cost - x.k;
+                continue;
+            }
+            const long long start = u - x.k;
+            if (end - start <= lead) break;  // the item's start counts for the next CTA
+            from_start = x.k <= lead;
+            to_end = no_split || end - start >= x.cost;
+            t0 = x.t0 + (from_start ? 0 : x.k - lead);
+            t1 = to_end ? x.t1 : x.t0 + (int)(end - start) - lead;
+            u = to_end ? start + x.cost : end;
+            if (from_start && !to_end) {
+                const int r0 = x.rt * rows;
+                cut = PagedCut{seq.q0, x.g, r0, min(rows, seq.nq * p.G - r0), line.owner(start + x.cost - 1) - cta + 1};
+            }
+            return true;
+        }
+        return false;
+    }
+};
 
 }  // namespace fa

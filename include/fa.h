@@ -98,8 +98,8 @@
  *    occur.  page_size is a positive multiple of 16.  Offsets are kept within [0, T_q]; rows
  *    of q that no sequence covers (a padded batch) are left as they were.  What a page holds
  *    behind a sequence's used keys, NaN and infinities included, has no effect.  A table entry
- *    that is needed and outside the pool reads as zeros and sets FA_ERR_DEVICE_CHECK in the
- *    status word.  FA_FLAG_VALIDATE_CU checks cu_seqlens_q (from 0, not decreasing, at most
+ *    that is needed and outside the pool is not followed and sets FA_ERR_DEVICE_CHECK in the
+ *    status word (the outputs are then unspecified).  FA_FLAG_VALIDATE_CU checks cu_seqlens_q (from 0, not decreasing, at most
  *    T_q) and seqused_k.  max_seqlen_q is used when given (the most query rows of a sequence;
  *    it picks the kernel's tile, and a wrong one costs time, not correctness).  Results do not
  *    depend on how other work is scheduled: the same call gives the same bits.
