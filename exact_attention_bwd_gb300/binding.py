@@ -95,6 +95,8 @@ def load(build_if_missing: bool = True):
     kernels record per-role event traces into the workspace; see trace.py) is loaded
     instead of the product library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -272,8 +274,9 @@ def _type_code(t):
 
 
 def _stream():
+    """torch's current stream of the current device, as the C ABI takes it."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check_tensors(q, named):
@@ -334,6 +337,11 @@ def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks
     descale = (q, k, v) fp32 [B * h_kv] factors or None (all 1).  The output has the
     inputs' type (bf16 for e4m3 inputs)."""
     import torch
+    if block_table is not None and cu_q is not None and cu_k is None:
+        if descale is not None:
+            raise TypeError("descale factors apply to e4m3 (uint8) inputs only")
+        return _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace, seqused_k,
+                              block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q)
     fp8 = q.dtype == torch.uint8
     if _type_code(q.dtype) is None or k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must all be bfloat16, all float16 or all uint8 (e4m3 bytes); "
@@ -344,7 +352,7 @@ def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks
     p = make_params(q, k, causal=causal, window=window, softmax_scale=softmax_scale, sinks=sinks, cu_q=cu_q,
                     cu_k=cu_k, flags=flags, seqused_k=seqused_k, block_table=block_table, s_kv=s_kv,
                     dtype=_type_code(q.dtype), q_descale=dq_, k_descale=dk_, v_descale=dv_,
-                    seqused_q=seqused_q, wait_limit_ns=wait_limit_ns, max_seqlen_q=max_seqlen_q)
+                    seqused_q=seqused_q, wait_limit_ns=wait_limit_ns)
     lse_shape = (p.B, p.h_q, p.s_q) if cu_q is None else (p.h_q, p.s_q)
     _check_tensors(q, [("k", k, None, _kv_shape(p, k, cu_q, block_table)), ("v", v, None, k.shape),
                        ("out", out, torch.bfloat16 if fp8 else q.dtype, q.shape), ("lse", lse, torch.float32, lse_shape),
@@ -420,22 +428,81 @@ def _on_device(t, call, *args, **kw):
         return call(*args, **kw)
 
 
-def _elsewhere(t):
+def _device_index(t):
+    """The index of t's CUDA device."""
     import torch
     if not isinstance(t, torch.Tensor):
-        raise TypeError("torch tensors are wanted")
-    if t.device.type != "cuda":
-        raise ValueError(f"the tensors must be CUDA tensors; the first is on {t.device}")
-    return t.device.index != torch.cuda.current_device()
+        raise TypeError(f"a torch tensor is wanted, not {type(t).__name__}")
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"the tensors must be CUDA tensors; one is on {t.device}")
+    return i
 
 
-def _check_vector(name, t, like, dtype, n):
-    if t is None:
-        return
-    if t.device != like.device or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {like.device}")
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements; it has {t.numel()}")
+def _check(dev, *named):
+    """Each (name, tensor or None, dtype, element count): a contiguous tensor of that type and size
+    on device `dev`.  The calls of a serving step are short, so this is written for speed: one
+    expression a tensor, the wording only where it fails."""
+    for name, t, dtype, n in named:
+        if t is None or (t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous()):
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}; every tensor must be on device {dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}; it is {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements; it has {t.numel()}")
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace, seqused_k, block_table, s_kv,
+                   seqused_q, wait_limit_ns, max_seqlen_q):
+    """forward() for packed queries over a paged cache."""
+    import torch
+    dev = _device_index(q)
+    if dev != torch.cuda.current_device():
+        return _on_device(q, _forward_paged, q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace,
+                          seqused_k, block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q)
+    kind = q.dtype
+    code = _type_code(kind)
+    if code is None:
+        raise TypeError(f"q, k, v must all be bfloat16 or all float16; q is {kind}")
+    if q.dim() != 3 or k.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [T, h_q, d], k and v [num_pages, page_size, h_kv, d], block_table [B, max_blocks_per_seq]")
+    if s_kv is None or seqused_k is None:
+        raise ValueError("packed queries over a paged cache need seqused_k and the longest cache's length s_kv")
+    T, h_q, d = q.shape
+    num_pages, page_size, h_kv, dk = k.shape
+    B, blocks = block_table.shape
+    if dk != d or v.shape != k.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must have one shape and q's head dimension {d}")
+    i32, f32 = torch.int32, torch.float32
+    _check(dev, ("q", q, kind, T * h_q * d), ("k", k, kind, k.numel()), ("v", v, kind, v.numel()), ("cu_q", cu_q, i32, B + 1),
+           ("seqused_k", seqused_k, i32, B), ("block_table", block_table, i32, B * blocks), ("sinks", sinks, f32, h_q),
+           ("seqused_q", seqused_q, i32, B))
+    if out is not None or lse is not None or workspace is not None:
+        _check(dev, ("out", out, kind, T * h_q * d), ("lse", lse, f32, h_q * T),
+               ("workspace", workspace, torch.uint8, 0 if workspace is None else workspace.numel()))
+    lib = load()
+    p = FaParams(B, T, s_kv, h_q, h_kv, d, softmax_scale or 0.0, 1 if causal else 0, window[0], window[1],
+                 None if sinks is None else sinks.data_ptr(), cu_q.data_ptr(), None, max_seqlen_q, 0, flags, seqused_k.data_ptr(),
+                 block_table.data_ptr(), page_size, blocks, num_pages, code, None, None, None,
+                 None if seqused_q is None else seqused_q.data_ptr(), wait_limit_ns)
+    ref = ctypes.byref(p)
+    nbytes = lib.fa_fwd_workspace_size(ref)
+    if nbytes == 0:
+        raise FaError(FA_ERR_UNSUPPORTED, "fa_fwd_workspace_size")
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(h_q, T, dtype=f32, device=q.device)
+    rc = lib.fa_fwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                    workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd")
+    return out, lse, workspace
 
 
 def _rows(name, t, like=None):
@@ -459,43 +526,35 @@ def _rows(name, t, like=None):
     return T, h, d, step if T > 1 else h * d
 
 
-def _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status):
+def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status):
     import torch
     T, h_q, d, q_stride = _rows("q", q)
     Tk, h_kv, dk, k_stride = _rows("k", k, q)
-    code = _type_code(q.dtype)
+    kind = q.dtype
+    code = _type_code(kind)
     if code is None or code == FA_DTYPE_E4M3:
-        raise TypeError(f"q and k must be bfloat16 or float16; q is {q.dtype}")
-    if Tk != T or dk != d or k.shape[:-2] != q.shape[:-2]:
+        raise TypeError(f"q and k must be bfloat16 or float16; q is {kind}")
+    if Tk != T or dk != d or k.dim() != q.dim() or k.shape[0] != q.shape[0]:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must have the same tokens and head dimension")
-    p = FaRopeParams()
-    p.T, p.h_q, p.h_kv, p.d, p.eps, p.dtype, p.interleaved = T, h_q, h_kv, d, eps, code, 1 if interleaved else 0
-    p.q_stride, p.k_stride, p.v_stride = q_stride, k_stride, h_kv * d
-    p.dq_stride, p.dk_stride = h_q * d, h_kv * d
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
+    max_pos = half = 0
     if cos is not None:
         max_pos, half = cos.shape
-        _check_vector("cos", cos, q, torch.float32, max_pos * half)
-        _check_vector("sin", sin, q, torch.float32, max_pos * half)
-        p.cos, p.sin, p.max_pos, p.rot_dim = cos.data_ptr(), sin.data_ptr(), max_pos, 2 * half
     wt = q_weight if q_weight is not None else k_weight
-    if wt is not None:
-        if wt.dtype not in (q.dtype, torch.float32):
-            raise TypeError(f"the weights must be {q.dtype} or float32; they are {wt.dtype}")
-        p.weight_f32 = 1 if wt.dtype == torch.float32 else 0
-        _check_vector("q_weight", q_weight, q, wt.dtype, d)
-        _check_vector("k_weight", k_weight, q, wt.dtype, d)
-        p.q_weight = None if q_weight is None else q_weight.data_ptr()
-        p.k_weight = None if k_weight is None else k_weight.data_ptr()
-    if positions is not None:
-        _check_vector("positions", positions, q, torch.int32, T)
-        p.positions = positions.data_ptr()
-    p.seq_len = int(seq_len) if seq_len is not None else max(1, q.shape[1] if q.dim() == 4 else T)
-    if status is not None:
-        _check_vector("status", status, q, torch.int32, 1)
-        p.status = status.data_ptr()
-    return p
+    wtype = kind if wt is None else wt.dtype
+    if wtype is not kind and wtype is not torch.float32:
+        raise TypeError(f"the weights must be {kind} or float32; they are {wtype}")
+    _check(dev, ("cos", cos, torch.float32, max_pos * half), ("sin", sin, torch.float32, max_pos * half),
+           ("q_weight", q_weight, wtype, d), ("k_weight", k_weight, wtype, d), ("positions", positions, torch.int32, T),
+           ("status", status, torch.int32, 1))
+    if seq_len is None:
+        seq_len = max(1, q.shape[1] if q.dim() == 4 else T)
+    return FaRopeParams(T, h_q, h_kv, d, 2 * half, 1 if interleaved else 0, seq_len, max_pos, eps, code, 1 if wtype is not kind else 0,
+                        q_stride, k_stride, h_kv * d, h_q * d, h_kv * d, None if positions is None else positions.data_ptr(),
+                        None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
+                        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                        None, 0, None if status is None else status.data_ptr())
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6, interleaved=False,
@@ -509,10 +568,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
     h_kv, d]) and slots (int32 [T]) keys and values go to the paged cache, and k_out is None
     unless out = (q_out, k_out) gives one.  status: int32 [1] or None."""
     import torch
-    if _elsewhere(q):
+    dev = _device_index(q)
+    if dev != torch.cuda.current_device():
         return _on_device(q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions=positions, seq_len=seq_len, eps=eps,
                           interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status)
-    p = _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    kind = q.dtype
     append = v is not None or k_cache is not None or v_cache is not None or slots is not None
     if append:
         if v is None or k_cache is None or v_cache is None or slots is None:
@@ -520,22 +581,22 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
         if v.shape != k.shape:
             raise ValueError(f"v must have k's shape {tuple(k.shape)}; it has {tuple(v.shape)}")
         p.v_stride = _rows("v", v, q)[3]
-        for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if c.dim() != 4 or c.shape != k_cache.shape or c.shape[2:] != k.shape[-2:]:
-                raise ValueError(f"{name} must be [num_pages, page_size, {p.h_kv}, {p.d}]; it has {tuple(c.shape)}")
-            _check_vector(name, c, q, q.dtype, c.numel())
-        _check_vector("slots", slots, q, torch.int32, p.T)
-        p.slots, p.num_slots = slots.data_ptr(), k_cache.shape[0] * k_cache.shape[1]
+        if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[2:] != k.shape[-2:]:
+            raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be [num_pages, page_size, "
+                             f"{p.h_kv}, {p.d}]")
+        n = k_cache.numel()
+        _check(dev, ("k_cache", k_cache, kind, n), ("v_cache", v_cache, kind, n), ("slots", slots, torch.int32, p.T))
+        p.slots, p.num_slots = slots.data_ptr(), n // (p.h_kv * p.d)
     q_out, k_out = out if out is not None else (None, None)
-    _check_vector("q_out", q_out, q, q.dtype, q.numel())
-    _check_vector("k_out", k_out, q, q.dtype, k.numel())
+    if out is not None:
+        _check(dev, ("q_out", q_out, kind, q.numel()), ("k_out", k_out, kind, k.numel()))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=kind, device=q.device)
     if k_out is None and not append:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    rc = fa_qk_norm_rope(p, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), q_out.data_ptr(),
-                         None if k_out is None else k_out.data_ptr(), None if k_cache is None else k_cache.data_ptr(),
-                         None if v_cache is None else v_cache.data_ptr(), _stream())
+        k_out = torch.empty(k.shape, dtype=kind, device=q.device)
+    rc = load().fa_qk_norm_rope(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr() if append else None, q_out.data_ptr(),
+                                None if k_out is None else k_out.data_ptr(), k_cache.data_ptr() if append else None,
+                                v_cache.data_ptr() if append else None, torch._C._cuda_getCurrentRawStream(dev))
     if rc != FA_OK:
         raise FaError(rc, "fa_qk_norm_rope")
     return q_out, k_out
@@ -549,34 +610,35 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     are the gradients of its outputs.  grads: (dq, dk, dq_weight, dk_weight) to write, dq and dk at
     any token stride (slices of a fused projection's gradient); the weights' are fp32 [d]."""
     import torch
-    if _elsewhere(q):
+    dev = _device_index(q)
+    if dev != torch.cuda.current_device():
         return _on_device(q, qk_norm_rope_backward, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions=positions,
                           seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status)
-    p = _rope_params(q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
-    for name, g, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if g.shape != x.shape:
-            raise ValueError(f"{name} must have shape {tuple(x.shape)}; it has {tuple(g.shape)}")
-        _check_vector(name, g, q, q.dtype, x.numel())
+    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    kind = q.dtype
+    _check(dev, ("dq_out", dq_out, kind, q.numel()), ("dk_out", dk_out, kind, k.numel()))
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError(f"dq_out and dk_out must have the shapes {tuple(q.shape)} and {tuple(k.shape)}")
     if grads is None:
-        dq, dk = torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        dq, dk = torch.empty(q.shape, dtype=kind, device=q.device), torch.empty(k.shape, dtype=kind, device=q.device)
         dwq, dwk = torch.empty(2, p.d, dtype=torch.float32, device=q.device).unbind()
     else:
         dq, dk, dwq, dwk = grads
-        for name, g, x in (("dq", dq, q), ("dk", dk, k)):
-            if g.shape != x.shape:
-                raise ValueError(f"{name} must have shape {tuple(x.shape)}; it has {tuple(g.shape)}")
+        if dq.shape != q.shape or dk.shape != k.shape:
+            raise ValueError(f"dq and dk must have the shapes {tuple(q.shape)} and {tuple(k.shape)}")
         p.dq_stride, p.dk_stride = _rows("dq", dq, q)[3], _rows("dk", dk, q)[3]
-        _check_vector("dq_weight", dwq, q, torch.float32, p.d)
-        _check_vector("dk_weight", dwk, q, torch.float32, p.d)
-    nbytes = fa_qk_norm_rope_bwd_workspace_size(p)
+        _check(dev, ("dq_weight", dwq, torch.float32, p.d), ("dk_weight", dwk, torch.float32, p.d))
+    lib, ref = load(), ctypes.byref(p)
+    nbytes = lib.fa_qk_norm_rope_bwd_workspace_size(ref)
     if nbytes == 0:
         raise FaError(FA_ERR_UNSUPPORTED, "fa_qk_norm_rope_bwd_workspace_size")
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
-        _check_vector("workspace", workspace, q, torch.uint8, workspace.numel())
-    rc = fa_qk_norm_rope_bwd(p, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                             dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream())
+        _check(dev, ("workspace", workspace, torch.uint8, workspace.numel()))
+    rc = lib.fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                 dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 torch._C._cuda_getCurrentRawStream(dev))
     if rc != FA_OK:
         raise FaError(rc, "fa_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
@@ -590,29 +652,30 @@ def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, t
     index free_head ([1], None: 0) on; tokens: rows of the packed batch (positions and slots are
     -1 behind the last new token).  out: the five results' tensors to write, status: [1] or None."""
     import torch
-    if _elsewhere(cached):
+    dev = _device_index(cached)
+    if dev != torch.cuda.current_device():
         return _on_device(cached, page_plan, cached, fresh, block_table, free_pages, page_size=page_size, num_pages=num_pages,
                           tokens=tokens, free_head=free_head, out=out, status=status)
     B, i32 = cached.numel(), torch.int32
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks_per_seq]")
     blocks, n_free = block_table.shape[1], free_pages.numel()
-    for name, t, n in (("cached", cached, B), ("fresh", fresh, B), ("block_table", block_table, B * blocks),
-                       ("free_pages", free_pages, n_free), ("free_head", free_head, 1), ("status", status, 1)):
-        _check_vector(name, t, cached, i32, n)
-    sizes = (B + 1, B, tokens, tokens, 1)
+    _check(dev, ("cached", cached, i32, B), ("fresh", fresh, i32, B), ("block_table", block_table, i32, B * blocks),
+           ("free_pages", free_pages, i32, n_free), ("free_head", free_head, i32, 1), ("status", status, i32, 1))
     if out is None:
-        out = torch.empty(2 * (B + tokens + 1), dtype=i32, device=cached.device).split(sizes)
+        out = torch.empty(2 * (B + tokens + 1), dtype=i32, device=cached.device).split_with_sizes((B + 1, B, tokens, tokens, 1))
     else:
-        for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"), out, sizes):
-            _check_vector(name, t, cached, i32, n)
+        _check(dev, *((name, t, i32, n) for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"),
+                                                              out, (B + 1, B, tokens, tokens, 1))))
+    cu, used, positions, slots, head_out = out
     p = FaPagePlanParams(B, tokens, page_size, blocks, num_pages, n_free)
-    rc = fa_page_plan(p, cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(),
-                      None if free_head is None else free_head.data_ptr(), block_table.data_ptr(),
-                      *(t.data_ptr() for t in out), None if status is None else status.data_ptr(), _stream())
+    rc = load().fa_page_plan(ctypes.byref(p), cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(),
+                             None if free_head is None else free_head.data_ptr(), block_table.data_ptr(), cu.data_ptr(),
+                             used.data_ptr(), positions.data_ptr(), slots.data_ptr(), head_out.data_ptr(),
+                             None if status is None else status.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if rc != FA_OK:
         raise FaError(rc, "fa_page_plan")
-    return tuple(out)
+    return cu, used, positions, slots, head_out
 
 
 def device_status(workspace) -> int:
