@@ -621,7 +621,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
         raise ValueError(f"dq_out and dk_out must have the shapes {tuple(q.shape)} and {tuple(k.shape)}")
     if grads is None:
         dq, dk = torch.empty(q.shape, dtype=kind, device=q.device), torch.empty(k.shape, dtype=kind, device=q.device)
-        dwq, dwk = torch.empty(2, p.d, dtype=torch.float32, device=q.device).unbind()
+        dwq, dwk = (torch.empty(p.d, dtype=torch.float32, device=q.device) for _ in range(2))
     else:
         dq, dk, dwq, dwk = grads
         if dq.shape != q.shape or dk.shape != k.shape:
@@ -663,7 +663,8 @@ def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, t
     _check(dev, ("cached", cached, i32, B), ("fresh", fresh, i32, B), ("block_table", block_table, i32, B * blocks),
            ("free_pages", free_pages, i32, n_free), ("free_head", free_head, i32, 1), ("status", status, i32, 1))
     if out is None:
-        out = torch.empty(2 * (B + tokens + 1), dtype=i32, device=cached.device).split_with_sizes((B + 1, B, tokens, tokens, 1))
+        # (five allocations take less host time than one and five views of it: 9.4 against 12.3 us)
+        out = [torch.empty(n, dtype=i32, device=cached.device) for n in (B + 1, B, tokens, tokens, 1)]
     else:
         _check(dev, *((name, t, i32, n) for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"),
                                                               out, (B + 1, B, tokens, tokens, 1))))

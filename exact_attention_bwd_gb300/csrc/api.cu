@@ -889,13 +889,13 @@ fa_status fa_qk_norm_rope(const fa_rope_params* in, const void* q, const void* k
     a.slots = in->slots;
     a.num_slots = (long)in->num_slots;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, st); }));
+    return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* in) {
     RopeArgs a;
     if (normalise_rope(in, a) != FA_OK) return 0;
-    const int ctas = norm_rope_bwd_ctas((long)a.T * a.h_q, a.d, sm_count());
+    const int ctas = norm_rope_bwd_ctas(a, sm_count());
     return align256((size_t)2 * ctas * a.d * 4);
 }
 
@@ -908,7 +908,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const voi
     const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;
     if (in->dq_stride < wq || in->dk_stride < wk || in->dq_stride % 8 || in->dk_stride % 8) return FA_ERR_INVALID_ARG;
     if (!dq_weight || !dk_weight || !workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
-    const int ctas = norm_rope_bwd_ctas((long)a.T * a.h_q, a.d, sm_count());
+    const int ctas = norm_rope_bwd_ctas(a, sm_count());
     if (ws_bytes < align256((size_t)2 * ctas * a.d * 4)) return FA_ERR_WORKSPACE;
     if (a.T > 0) {
         if (!q || !k || !dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
@@ -936,7 +936,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const voi
     a.dwk = dk_weight;
     a.dw_part = reinterpret_cast<float*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return cuda_status(timed(kNormRopeBwd, st, [&] { return launch_norm_rope_bwd(a, ctas, st); }));
+    return cuda_status(timed(kNormRopeBwd, st, [&] { return launch_norm_rope_bwd(a, sm_count(), st); }));
 }
 
 fa_status fa_page_plan(const fa_page_plan_params* in, const int32_t* cached, const int32_t* fresh, const int32_t* free_pages,

@@ -176,7 +176,7 @@ struct RopeArgs {
     uint16_t *dq, *dk;
     float *dwq, *dwk, *dw_part;
     int* status;
-    int segments;              // warps per token
+    int unit_rows;             // rows a warp takes at a time
 };
 
 struct PagePlanArgs {
@@ -205,9 +205,9 @@ cudaError_t launch_bwd_post(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
 cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st);  // many: both kernels' items
-cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t st);
-cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int ctas, cudaStream_t st);
-int norm_rope_bwd_ctas(long rows, int d, int sms);
+cudaError_t launch_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int sms, cudaStream_t st);
+int norm_rope_bwd_ctas(const RopeArgs& a, int sms);  // rows of dw_part for each weight
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st);
 
 // Number of 16-byte-aligned KV tiles etc. shared by planner and kernels.

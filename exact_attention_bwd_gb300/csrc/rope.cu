@@ -10,110 +10,161 @@
 // Statistics and products are fp32; each output is rounded once to the 16-bit type.
 //
 // Both are streams: 2 (forward) or 3 (gradient) passes over the rows, nothing to reuse but
-// the angles and the weights, so HBM bounds them and the layout only has to keep enough
-// 16-byte loads in flight.  A row is held by d / 16 lanes (4 at d = 192): a lane takes pairs of
-// 8-value units that rotate with each other (unit p with p + rot / 16 when pairs lie half the
-// rotated part apart, both members of each pair in one unit when they are adjacent), so the
-// rotation needs no exchange between lanes, and the row sums are a few shuffles.
+// the angles and the weights, so HBM bounds them and what counts is the bytes in flight.  One
+// CTA per SM of 8 warps, each on its own: a warp walks over units (some rows of one token, of q,
+// k or v) and keeps the next units' rows and angles on their way into its own shared-memory
+// buffers by bulk copies, so that the loads do not wait for its arithmetic nor take registers.
+// (Loads into registers, 4 row batches a warp at 16 warps per SM, reached 58 % of the copy rate.)
+// A row is held by d / 16 lanes (16 at d = 192, four of them idle): a lane has two 8-value units
+// that rotate with each other (unit p and p + rot / 16 when pairs lie half the rotated part
+// apart; both members of each pair in one unit when they are adjacent), so the rotation needs no
+// exchange between lanes, and the row sums are a few shuffles.
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kBufs = 3;           // units in flight per warp
+constexpr int kUnitBytes = 8192;   // rows of a unit at most (gradient: half of it x, half dy)
 
 template <int D>
 struct RowCfg {
-    static constexpr int PAIRS = D / 16;                   // pairs of 8-value units of a row
-    static constexpr int LANES = D == 192 ? 4 : PAIRS;     // lanes that hold a row
-    static constexpr int PPL = PAIRS / LANES;              // pairs a lane holds
-    static constexpr int ROWS = 32 / LANES;                // rows of a warp at a time
-    static constexpr int STEPS = D == 192 ? 2 : 4;         // row batches in flight
+    static constexpr int PAIRS = D / 16;               // lanes with values
+    static constexpr int LANES = D == 192 ? 16 : PAIRS;  // lanes of a row
+    static constexpr int ROWS = 32 / LANES;            // rows of a warp at a time
+    // rows of a unit: whole batches of 2 ROWS
+    static constexpr int MAX_ROWS = kUnitBytes / (2 * D) / (2 * ROWS) * (2 * ROWS);
 };
 
-// The two units (8 values each, their index in the row) of pair i.
+// Shared memory of a warp's buffer: rows (kUnitBytes), cos and sin of the token
+template <int D>
+struct __align__(128) RowBuf {
+    uint8_t rows[kUnitBytes];
+    float cos[D / 2], sin[D / 2];
+};
+struct RowMeta {
+    int pos, slot;
+};
+template <int D>
+struct WarpSmem {
+    RowBuf<D> buf[kBufs];
+    uint64_t full[kBufs];
+    RowMeta meta[kBufs];
+};
+
+// The lane's angles from the token's row of the tables: for pairs half the rotated part apart
+// c[e], s[e] are those of values 2e, 2e + 1 of unit 0 (and unit 1), e < 4; for adjacent ones
+// c[e].x, s[e].x is the angle of the pair e (e < 4 in unit 0, the others in unit 1).  Values
+// behind the rotated part get cos 1, sin 0.
+template <bool ADJ>
+struct Angles {
+    float2 c[ADJ ? 8 : 4], s[ADJ ? 8 : 4];
+    __device__ __forceinline__ void load(const float* cs, const float* sn, int u0, int u1, int rot) {
+        if constexpr (ADJ) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int u = h ? u1 : u0;
+                float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (8 * u < rot) {
+                    x = *reinterpret_cast<const float4*>(cs + 4 * u);
+                    y = *reinterpret_cast<const float4*>(sn + 4 * u);
+                }
+                c[4 * h] = make_float2(x.x, x.x);
+                c[4 * h + 1] = make_float2(x.y, x.y);
+                c[4 * h + 2] = make_float2(x.z, x.z);
+                c[4 * h + 3] = make_float2(x.w, x.w);
+                s[4 * h] = make_float2(-y.x, y.x);
+                s[4 * h + 1] = make_float2(-y.y, y.y);
+                s[4 * h + 2] = make_float2(-y.z, y.z);
+                s[4 * h + 3] = make_float2(-y.w, y.w);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (16 * u0 < rot) {
+                    x = *reinterpret_cast<const float4*>(cs + 8 * u0 + 4 * h);
+                    y = *reinterpret_cast<const float4*>(sn + 8 * u0 + 4 * h);
+                }
+                c[2 * h] = make_float2(x.x, x.y);
+                c[2 * h + 1] = make_float2(x.z, x.w);
+                s[2 * h] = make_float2(y.x, y.y);
+                s[2 * h + 1] = make_float2(y.z, y.w);
+            }
+        }
+    }
+    // Turns the lane's 16 values (unit 0 in v[0..3], unit 1 in v[4..7]); BACK: by minus the angle.
+    template <bool BACK>
+    __device__ __forceinline__ void turn(float2* v) const {
+        if constexpr (ADJ) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 sw = make_float2(v[e].y, v[e].x);
+                const float2 ss = BACK ? make_float2(s[e].y, s[e].x) : s[e];
+                v[e] = __ffma2_rn(sw, ss, __fmul2_rn(v[e], c[e]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 a = v[e], b = v[e + 4], ns = make_float2(-s[e].x, -s[e].y);
+                v[e] = __ffma2_rn(b, BACK ? s[e] : ns, __fmul2_rn(a, c[e]));
+                v[e + 4] = __ffma2_rn(a, BACK ? ns : s[e], __fmul2_rn(b, c[e]));
+            }
+        }
+    }
+};
+
+// The two units (8 values each, their index in the row) of lane i of a row.
 template <int D, bool ADJ>
-__device__ __forceinline__ void pair_units(int i, int rot, int& u0, int& u1) {
-    if constexpr (ADJ) {
+__device__ __forceinline__ void lane_units(int i, int rot, int& u0, int& u1) {
+    const int h = rot >> 4;  // units of half the rotated part
+    if (ADJ || i < h) {
         u0 = i;
-        u1 = i + D / 16;
-    } else {
-        const int h = rot >> 4;  // units of half the rotated part
-        if (i < h) {
-            u0 = i;
-            u1 = i + h;
-        } else {  // behind the rotated part
-            u0 = 2 * i;
-            u1 = 2 * i + 1;
+        u1 = i + (ADJ ? D / 16 : h);
+    } else {  // behind the rotated part
+        u0 = 2 * i;
+        u1 = 2 * i + 1;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void widen8(const uint4& x, float2* v) {
+    v[0] = make_float2(lo16<F16>(x.x), hi16<F16>(x.x));
+    v[1] = make_float2(lo16<F16>(x.y), hi16<F16>(x.y));
+    v[2] = make_float2(lo16<F16>(x.z), hi16<F16>(x.z));
+    v[3] = make_float2(lo16<F16>(x.w), hi16<F16>(x.w));
+}
+template <bool F16>
+__device__ __forceinline__ uint4 narrow8(const float2* v) {
+    return make_uint4(pack16<F16>(v[0].x, v[0].y), pack16<F16>(v[1].x, v[1].y), pack16<F16>(v[2].x, v[2].y),
+                      pack16<F16>(v[3].x, v[3].y));
+}
+
+// The lane's 16 weights (null: ones).
+template <bool F16>
+__device__ __forceinline__ void load_weight(const RopeArgs& a, const void* w, int u0, int u1, float2* v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int u = h ? u1 : u0;
+        if (!w) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * h + e] = make_float2(1.f, 1.f);
+        } else if (a.weight_f32) {
+            const float4* src = reinterpret_cast<const float4*>(w) + 2 * u;
+            const float4 x = src[0], y = src[1];
+            v[4 * h] = make_float2(x.x, x.y);
+            v[4 * h + 1] = make_float2(x.z, x.w);
+            v[4 * h + 2] = make_float2(y.x, y.y);
+            v[4 * h + 3] = make_float2(y.z, y.w);
+        } else {
+            widen8<F16>(reinterpret_cast<const uint4*>(w)[u], v + 4 * h);
         }
     }
 }
 
-// cos and sin that the pair's 8 products need: value e of unit 0 (and e of unit 1) for pairs half
-// the rotated part apart; members 2e, 2e + 1 of unit 0 (e < 4) and unit 1 (e >= 4) for adjacent ones.
-template <bool ADJ>
-__device__ __forceinline__ void load_angles(const float* row_c, const float* row_s, int u0, int u1, int rot, float* c,
-                                            float* n) {
-    auto four = [&](const float* src, float* dst) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(src));
-        dst[0] = x.x; dst[1] = x.y; dst[2] = x.z; dst[3] = x.w;
-    };
-    const bool on0 = ADJ ? 8 * u0 < rot : 16 * u0 < rot, on1 = ADJ ? 8 * u1 < rot : on0;
-    const int at0 = ADJ ? 4 * u0 : 8 * u0, at1 = ADJ ? 4 * u1 : 8 * u0 + 4;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        n[e] = 0.f;
-    }
-    if (on0) {
-        four(row_c + at0, c);
-        four(row_s + at0, n);
-    }
-    if (on1) {
-        four(row_c + at1, c + 4);
-        four(row_s + at1, n + 4);
-    }
-}
-
-// Rotates the pair's 16 values (unit 0 in v[0..7], unit 1 in v[8..15]); BACK: by minus the angle.
-template <bool ADJ, bool BACK>
-__device__ __forceinline__ void turn(float* v, const float* c, const float* n) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int ia = ADJ ? (e < 4 ? 2 * e : 8 + 2 * (e - 4)) : e, ib = ADJ ? ia + 1 : e + 8;
-        const float a = v[ia], b = v[ib], s = BACK ? -n[e] : n[e];
-        v[ia] = a * c[e] - b * s;
-        v[ib] = b * c[e] + a * s;
-    }
-}
-
-template <bool F16>
-__device__ __forceinline__ void widen8(const uint4& x, float* v) {
-    v[0] = lo16<F16>(x.x); v[1] = hi16<F16>(x.x); v[2] = lo16<F16>(x.y); v[3] = hi16<F16>(x.y);
-    v[4] = lo16<F16>(x.z); v[5] = hi16<F16>(x.z); v[6] = lo16<F16>(x.w); v[7] = hi16<F16>(x.w);
-}
-template <bool F16>
-__device__ __forceinline__ uint4 narrow8(const float* v) {
-    return make_uint4(pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]), pack16<F16>(v[4], v[5]), pack16<F16>(v[6], v[7]));
-}
-
-// 8 weights from unit u (null: ones).
-template <bool F16>
-__device__ __forceinline__ void load_weight8(const RopeArgs& a, const void* w, int u, float* v) {
-    if (!w) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 1.f;
-    } else if (a.weight_f32) {
-        const float4* src = reinterpret_cast<const float4*>(w) + 2 * u;
-        const float4 x = __ldg(src), y = __ldg(src + 1);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    } else {
-        widen8<F16>(__ldg(reinterpret_cast<const uint4*>(w) + u), v);
-    }
-}
-
-// Sum over the lanes that hold a row.
+// Sum over the lanes of a row.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -124,120 +175,184 @@ __device__ __forceinline__ float row_sum(float x) {
 // The token's row of the angle tables, or -1: a padding token (position -1) or one outside the
 // tables, which sets the status.
 __device__ __forceinline__ int position_of(const RopeArgs& a, long t) {
-    const int pos = a.positions ? a.positions[t] : (int)(t % a.seq_len);
+    const int pos = a.positions ? a.positions[t] : (int)((unsigned)t % (unsigned)a.seq_len);
     if (pos >= 0 && pos < a.max_pos) return pos;
     if (pos != -1 && a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
     return -1;
 }
 
-// One warp takes STEPS row batches of one token: the token's query rows, key rows and (append)
-// value rows are numbered one after the other, ROWS of them to a batch.
-template <int D, bool F16, bool ADJ>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const RopeArgs a) {
-    using C = RowCfg<D>;
-    constexpr int LANES = C::LANES, PPL = C::PPL, ROWS = C::ROWS, STEPS = C::STEPS;
-    const int lane = threadIdx.x & 31, li = lane % LANES;
-    const long task = (long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const long t = task / a.segments;
-    if (t >= a.T) return;
-    const int row0 = (int)(task - t * a.segments) * (ROWS * STEPS) + lane / LANES;
-    const int n_rows = a.h_q + a.h_kv + (a.v ? a.h_kv : 0);
-    int u0[PPL], u1[PPL];
-#pragma unroll
-    for (int i = 0; i < PPL; ++i) pair_units<D, ADJ>(li + LANES * i, a.rot, u0[i], u1[i]);
+// The walk of a warp over units u, u + step, ...: unit x of token t, x = u % per_token.
+struct UnitWalk {
+    long t, dt;
+    int x, dx, per_token;
+    __device__ __forceinline__ UnitWalk(unsigned first, unsigned step, unsigned per)
+        : t(first / per), dt(step / per), x((int)(first % per)), dx((int)(step % per)), per_token((int)per) {}
+    __device__ __forceinline__ void next() {
+        t += dt;
+        x += dx;
+        if (x >= per_token) {
+            x -= per_token;
+            ++t;
+        }
+    }
+};
 
-    // every row of the batches, all loads in flight at once
-    uint4 x[STEPS][PPL][2];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        const int r = row0 + s * ROWS;
-        const uint16_t* src = nullptr;
-        if (r < a.h_q) src = a.q + t * a.q_stride + (long)r * D;
-        else if (r < a.h_q + a.h_kv) src = a.k + t * a.k_stride + (long)(r - a.h_q) * D;
-        else if (r < n_rows) src = a.v + t * a.v_stride + (long)(r - a.h_q - a.h_kv) * D;
-#pragma unroll
-        for (int i = 0; i < PPL; ++i) {
-            x[s][i][0] = src ? *reinterpret_cast<const uint4*>(src + 8 * u0[i]) : make_uint4(0, 0, 0, 0);
-            x[s][i][1] = src ? *reinterpret_cast<const uint4*>(src + 8 * u1[i]) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    const int pos = position_of(a, t);
-    if (pos < 0) return;  // the whole warp: one token
-    long slot = -1;
-    if (a.slots) {
-        slot = a.slots[t];
-        if (slot >= a.num_slots || slot < -1) {
-            if (a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
-            slot = -1;
-        }
-    }
-    float c[PPL][8], n[PPL][8];
-#pragma unroll
-    for (int i = 0; i < PPL; ++i)
-        load_angles<ADJ>(a.cos + (long)pos * (a.rot / 2), a.sin + (long)pos * (a.rot / 2), u0[i], u1[i], a.rot, c[i], n[i]);
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        const int r = row0 + s * ROWS;
-        const bool is_q = r < a.h_q, is_v = r >= a.h_q + a.h_kv;
-        float v[PPL][16], ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < PPL; ++i) {
-            widen8<F16>(x[s][i][0], v[i]);
-            widen8<F16>(x[s][i][1], v[i] + 8);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-        }
-        const float rs = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-        if (r >= n_rows) continue;
-        if (!is_v) {
-#pragma unroll
-            for (int i = 0; i < PPL; ++i) {
-                float w[16];
-                load_weight8<F16>(a, is_q ? a.wq : a.wk, u0[i], w);
-                load_weight8<F16>(a, is_q ? a.wq : a.wk, u1[i], w + 8);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[i][e] *= rs * w[e];
-                turn<ADJ, false>(v[i], c[i], n[i]);
-                x[s][i][0] = narrow8<F16>(v[i]);
-                x[s][i][1] = narrow8<F16>(v[i] + 8);
+// One run of units: `heads` rows of each token in groups of a.unit_rows.
+__device__ __forceinline__ int groups_of(const RopeArgs& a, int heads) { return (heads + a.unit_rows - 1) / a.unit_rows; }
+
+template <int D, bool F16, bool ADJ>
+__global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArgs a) {
+    using C = RowCfg<D>;
+    constexpr int LANES = C::LANES, ROWS = C::ROWS;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LANES, lr = lane / LANES;
+    WarpSmem<D>& s = reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp];
+    const bool on = li < C::PAIRS;
+    const int gq = groups_of(a, a.h_q), gk = groups_of(a, a.h_kv), per_token = gq + gk + (a.v ? gk : 0);
+    const unsigned n_warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    // a unit's kind (0 q, 1 k, 2 v), first row and rows
+    auto unit = [&](int x, int& kind, int& r0, int& rows) {
+        kind = x < gq ? 0 : x < gq + gk ? 1 : 2;
+        r0 = (x - (kind > 0 ? gq : 0) - (kind > 1 ? gk : 0)) * a.unit_rows;
+        rows = min(a.unit_rows, (kind ? a.h_kv : a.h_q) - r0);
+    };
+    UnitWalk ahead(me, n_warps, per_token), now = ahead;
+    int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0)
+    auto look = [&]() {
+        if (lane == 0 && ahead.t < a.T) {
+            next_pos = position_of(a, ahead.t);
+            if (a.slots && ahead.x >= gq) {
+                next_slot = a.slots[ahead.t];
+                if (next_slot >= a.num_slots || next_slot < -1) {
+                    if (a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    next_slot = -1;
+                }
             }
         }
-        uint16_t* dst[2] = {nullptr, nullptr};
-        if (is_q) {
-            dst[0] = a.q_out + (t * a.h_q + r) * (long)D;
-        } else {
-            const int h = r - a.h_q - (is_v ? a.h_kv : 0);
-            if (!is_v && a.k_out) dst[0] = a.k_out + (t * a.h_kv + h) * (long)D;
-            if (slot >= 0) dst[1] = (is_v ? a.v_cache : a.k_cache) + (slot * a.h_kv + h) * (long)D;
-        }
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            if (!dst[o]) continue;
-#pragma unroll
-            for (int i = 0; i < PPL; ++i) {
-                *reinterpret_cast<uint4*>(dst[o] + 8 * u0[i]) = x[s][i][0];
-                *reinterpret_cast<uint4*>(dst[o] + 8 * u1[i]) = x[s][i][1];
+    };
+    // starts the copies of the unit `ahead` into buffer b and moves on
+    auto issue = [&](int b) {
+        if (lane == 0 && ahead.t < a.T) {
+            s.meta[b] = RowMeta{next_pos, next_slot};
+            if (next_pos >= 0) {
+                int kind, r0, rows;
+                unit(ahead.x, kind, r0, rows);
+                const uint16_t* src = (kind == 0 ? a.q + ahead.t * a.q_stride : kind == 1 ? a.k + ahead.t * a.k_stride
+                                                                                          : a.v + ahead.t * a.v_stride) + (long)r0 * D;
+                const uint32_t bytes = (uint32_t)rows * D * 2, angle = kind < 2 ? (uint32_t)a.rot * 2 : 0u;
+                mbar_expect_tx(&s.full[b], bytes + 2 * angle);
+                bulk_load(s.buf[b].rows, src, bytes, &s.full[b]);
+                if (angle) {
+                    bulk_load(s.buf[b].cos, a.cos + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
+                    bulk_load(s.buf[b].sin, a.sin + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
+                }
             }
         }
+        ahead.next();
+        look();
+    };
+    if (lane == 0) {
+        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    look();
+    for (int b = 0; b < kBufs; ++b) issue(b);
+    int u0, u1;
+    lane_units<D, ADJ>(on ? li : 0, a.rot, u0, u1);
+    float2 wq[8], wk[8];
+    load_weight<F16>(a, a.wq, u0, u1, wq);
+    load_weight<F16>(a, a.wk, u0, u1, wk);
+    __syncwarp();
+    uint32_t phase = 0;  // bit b: the parity buffer b's next copies complete
+    for (int b = 0; now.t < a.T; now.next(), b = b + 1 == kBufs ? 0 : b + 1) {
+        const RowMeta meta = s.meta[b];
+        if (meta.pos >= 0) {
+            // (bounded; on the way out, the copies of the other buffers end with the same limit)
+            if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
+                if (lane == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout);
+                for (int z = 0; z < kBufs; ++z)
+                    if (z != b && s.meta[z].pos >= 0) mbar_wait_quiet(&s.full[z], (phase >> z) & 1);
+                return;
+            }
+            phase ^= 1u << b;
+            int kind, r0, rows;
+            unit(now.x, kind, r0, rows);
+            const uint8_t* in = s.buf[b].rows;
+            const bool cached = kind > 0 && meta.slot >= 0;
+            uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : kind == 1 && a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
+            uint16_t* out1 = cached ? (kind == 1 ? a.k_cache : a.v_cache) + ((long)meta.slot * a.h_kv + r0) * D : nullptr;
+            if (kind == 2) {
+                if (cached)
+                    for (int y = lane; y < rows * D / 8; y += 32)
+                        reinterpret_cast<uint4*>(out1)[y] = reinterpret_cast<const uint4*>(in)[y];
+            } else if (out0 || out1) {
+                Angles<ADJ> ang;
+                ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
+                // (two row batches at a time, so that one's sums and roots hide behind the other's)
+#pragma unroll 2
+                for (int r = lr; r < rows + lr; r += ROWS) {
+                    const bool live = on && r < rows;
+                    float2 v[8];
+                    {
+                        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+                        if (live) {
+                            x0 = *reinterpret_cast<const uint4*>(in + r * (D * 2) + 16 * u0);
+                            x1 = *reinterpret_cast<const uint4*>(in + r * (D * 2) + 16 * u1);
+                        }
+                        widen8<F16>(x0, v);
+                        widen8<F16>(x1, v + 4);
+                    }
+                    float2 ss = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
+                    const float rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], kind ? wk[e] : wq[e]);
+                    ang.template turn<false>(v);
+                    const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], rs2);
+                    const uint4 y0 = narrow8<F16>(v), y1 = narrow8<F16>(v + 4);
+                    if (live && out0) {
+                        *reinterpret_cast<uint4*>(out0 + r * D + 8 * u0) = y0;
+                        *reinterpret_cast<uint4*>(out0 + r * D + 8 * u1) = y1;
+                    }
+                    if (live && out1) {
+                        *reinterpret_cast<uint4*>(out1 + r * D + 8 * u0) = y0;
+                        *reinterpret_cast<uint4*>(out1 + r * D + 8 * u1) = y1;
+                    }
+                }
+            }
+        }
+        __syncwarp();  // the buffer has been read
+        issue(b);
+        __syncwarp();
     }
 }
 
-// Gradient.  The query rows and the key rows are two runs of row batches; the grid's warps
-// stride over the first, then the second, keeping the weight gradient of the lane's own values
-// in registers.  Each CTA adds its warps' sums in a fixed order and stores them as one row of the
-// workspace; norm_rope_dw_kernel adds the rows, again in a fixed order, so the gradients are the
-// same bits from call to call.
-constexpr int kBwdWarps = 8;
-
+// Gradient: the same walk, over the query rows and then over the key rows, with dy beside x in
+// the buffer and the weight gradient of the lane's own values in registers.  Each CTA adds its
+// warps' sums in a fixed order and stores them as one row of the workspace; norm_rope_dw_kernel
+// adds the rows, again in a fixed order, so the gradients are the same bits from call to call.
 template <int D, bool F16, bool ADJ>
-__global__ void __launch_bounds__(32 * kBwdWarps) norm_rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const RopeArgs a) {
     using C = RowCfg<D>;
-    constexpr int LANES = C::LANES, PPL = C::PPL, ROWS = C::ROWS;
-    __shared__ float part[kBwdWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LANES;
-    int u0[PPL], u1[PPL];
-#pragma unroll
-    for (int i = 0; i < PPL; ++i) pair_units<D, ADJ>(li + LANES * i, a.rot, u0[i], u1[i]);
+    constexpr int LANES = C::LANES, ROWS = C::ROWS;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LANES, lr = lane / LANES;
+    WarpSmem<D>& s = reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp];
+    const bool on = li < C::PAIRS;
+    int u0, u1;
+    lane_units<D, ADJ>(on ? li : 0, a.rot, u0, u1);
+    if (lane == 0) {
+        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const unsigned n_warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    uint32_t phase = 0;
+    bool failed = false;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         const int heads = kind ? a.h_kv : a.h_q;
@@ -245,86 +360,119 @@ __global__ void __launch_bounds__(32 * kBwdWarps) norm_rope_bwd_kernel(const Rop
         const uint16_t* gs = kind ? a.dk_out : a.dq_out;
         uint16_t* ds = kind ? a.dk : a.dq;
         const long xstride = kind ? a.k_stride : a.q_stride, dstride = kind ? a.dk_stride : a.dq_stride;
-        float w[PPL][16], dw[PPL][16];
+        float2 w[8], dw[8];
+        load_weight<F16>(a, kind ? a.wk : a.wq, u0, u1, w);
 #pragma unroll
-        for (int i = 0; i < PPL; ++i) {
-            load_weight8<F16>(a, kind ? a.wk : a.wq, u0[i], w[i]);
-            load_weight8<F16>(a, kind ? a.wk : a.wq, u1[i], w[i] + 8);
+        for (int e = 0; e < 8; ++e) dw[e] = make_float2(0.f, 0.f);
+        UnitWalk ahead(me, n_warps, groups_of(a, heads)), now = ahead;
+        int next_pos = -1;
+        auto look = [&]() {
+            if (lane == 0 && ahead.t < a.T) next_pos = position_of(a, ahead.t);
+        };
+        auto issue = [&](int b) {
+            if (lane == 0 && ahead.t < a.T) {
+                s.meta[b] = RowMeta{next_pos, 0};
+                if (next_pos >= 0) {
+                    const int r0 = ahead.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
+                    const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                    mbar_expect_tx(&s.full[b], 2 * bytes + 2 * angle);
+                    bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
+                    bulk_load(s.buf[b].rows + kUnitBytes / 2, gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
+                    if (angle) {
+                        bulk_load(s.buf[b].cos, a.cos + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
+                        bulk_load(s.buf[b].sin, a.sin + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
+                    }
+                }
+            }
+            ahead.next();
+            look();
+        };
+        look();
+        for (int b = 0; b < kBufs; ++b) issue(b);
+        __syncwarp();
+        for (int b = 0; !failed && now.t < a.T; now.next(), b = b + 1 == kBufs ? 0 : b + 1) {
+            if (s.meta[b].pos >= 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
+                    if (lane == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout);
+                    for (int z = 0; z < kBufs; ++z)
+                        if (z != b && s.meta[z].pos >= 0) mbar_wait_quiet(&s.full[z], (phase >> z) & 1);
+                    failed = true;  // (the CTA's sums below still need every warp)
+                    break;
+                }
+                phase ^= 1u << b;
+                const int r0 = now.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
+                const uint8_t *px = s.buf[b].rows, *pg = px + kUnitBytes / 2;
+                uint16_t* pd = ds + now.t * dstride + (long)r0 * D;
+                Angles<ADJ> ang;
+                ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
+#pragma unroll 2
+                for (int r = lr; r < rows + lr; r += ROWS) {
+                    const bool live = on && r < rows;
+                    float2 v[8], y[8];
+                    {
+                        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, y0 = x0, y1 = x0;
+                        if (live) {
+                            x0 = *reinterpret_cast<const uint4*>(px + r * (D * 2) + 16 * u0);
+                            x1 = *reinterpret_cast<const uint4*>(px + r * (D * 2) + 16 * u1);
+                            y0 = *reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u0);
+                            y1 = *reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u1);
+                        }
+                        widen8<F16>(x0, v);
+                        widen8<F16>(x1, v + 4);
+                        widen8<F16>(y0, y);
+                        widen8<F16>(y1, y + 4);
+                    }
+                    ang.template turn<true>(y);
+                    float2 ss = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) dw[i][e] = 0.f;
+                    for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
+                    // t = g x: what dw and mean(g w xh) sum
+                    float2 t[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] = __fmul2_rn(y[e], v[e]);
+                    float2 sg = __fmul2_rn(t[0], w[0]);
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) sg = __ffma2_rn(t[e], w[e], sg);
+                    const float rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    // dx = r g w - x r^3 mean(g w x)
+                    const float m = -row_sum<LANES>(sg.x + sg.y) * (1.f / D) * rs * rs * rs;
+                    const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dw[e] = __ffma2_rn(t[e], rs2, dw[e]);
+                        y[e] = __fmul2_rn(__fmul2_rn(y[e], w[e]), rs2);
+                        v[e] = __ffma2_rn(v[e], m2, y[e]);
+                    }
+                    if (live) {
+                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u0) = narrow8<F16>(v);
+                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u1) = narrow8<F16>(v + 4);
+                    }
+                }
+            }
+            __syncwarp();  // the buffer has been read
+            issue(b);
+            __syncwarp();
         }
-        const long rows = (long)a.T * heads, step = (long)gridDim.x * kBwdWarps * ROWS;
-        for (long base = ((long)blockIdx.x * kBwdWarps + warp) * ROWS; base < rows; base += step) {
-            const long row = base + lane / LANES;
-            const bool in = row < rows;
-            const long t = in ? row / heads : 0;
-            const long h = in ? row - t * heads : 0;
-            const int pos = in ? position_of(a, t) : -1;
-            const bool live = pos >= 0;
-            uint4 x[PPL][2], g[PPL][2];
-            float c[PPL][8], n[PPL][8];
+        // the warp's lanes with the same values, then the CTA's warps, in order (in the first buffer,
+        // which no copy is under way into)
+        float* part = reinterpret_cast<float*>(reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp].buf[0].rows);
 #pragma unroll
-            for (int i = 0; i < PPL; ++i) {
-                const uint16_t* px = xs + t * xstride + h * D;
-                const uint16_t* pg = gs + (t * heads + h) * D;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                x[i][0] = live ? *reinterpret_cast<const uint4*>(px + 8 * u0[i]) : zero;
-                x[i][1] = live ? *reinterpret_cast<const uint4*>(px + 8 * u1[i]) : zero;
-                g[i][0] = live ? *reinterpret_cast<const uint4*>(pg + 8 * u0[i]) : zero;
-                g[i][1] = live ? *reinterpret_cast<const uint4*>(pg + 8 * u1[i]) : zero;
-                load_angles<ADJ>(a.cos + (long)max(pos, 0) * (a.rot / 2), a.sin + (long)max(pos, 0) * (a.rot / 2), u0[i],
-                                 u1[i], a.rot, c[i], n[i]);
-            }
-            float ss = 0.f, sg = 0.f;
-            float v[PPL][16], y[PPL][16];
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int i = 0; i < PPL; ++i) {
-                widen8<F16>(x[i][0], v[i]);
-                widen8<F16>(x[i][1], v[i] + 8);
-                widen8<F16>(g[i][0], y[i]);
-                widen8<F16>(g[i][1], y[i] + 8);
-                turn<ADJ, true>(y[i], c[i], n[i]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    ss = fmaf(v[i][e], v[i][e], ss);
-                    sg = fmaf(y[i][e] * w[i][e], v[i][e], sg);
-                }
-            }
-            const float rs = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-            // mean(g w xh) with xh = x r
-            const float mg = row_sum<LANES>(sg) * rs * (1.f / D);
-#pragma unroll
-            for (int i = 0; i < PPL; ++i) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float xh = v[i][e] * rs;
-                    dw[i][e] = fmaf(y[i][e], xh, dw[i][e]);
-                    v[i][e] = rs * (y[i][e] * w[i][e] - xh * mg);
-                }
-                if (live) {
-                    uint16_t* pd = ds + t * dstride + h * D;
-                    *reinterpret_cast<uint4*>(pd + 8 * u0[i]) = narrow8<F16>(v[i]);
-                    *reinterpret_cast<uint4*>(pd + 8 * u1[i]) = narrow8<F16>(v[i] + 8);
-                }
-            }
-        }
-        // the warp's lanes with the same values, then the CTA's warps, in order
-#pragma unroll
-        for (int i = 0; i < PPL; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float x = dw[i][e];
+            for (int h = 0; h < 2; ++h) {
+                float x = h ? dw[e].y : dw[e].x;
 #pragma unroll
                 for (int o = 16; o >= LANES; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane < LANES) part[warp][8 * (e < 8 ? u0[i] : u1[i]) + (e & 7)] = x;
+                if (lane < C::PAIRS) part[8 * (e < 4 ? u0 : u1) + 2 * (e & 3) + h] = x;
             }
         __syncthreads();
-        for (int j = threadIdx.x; j < D; j += 32 * kBwdWarps) {
+        for (int j = threadIdx.x; j < D; j += 32 * kWarps) {
             float x = 0.f;
 #pragma unroll
-            for (int k = 0; k < kBwdWarps; ++k) x += part[k][j];
+            for (int k = 0; k < kWarps; ++k) x += reinterpret_cast<const float*>(reinterpret_cast<WarpSmem<D>*>(smem_raw)[k].buf[0].rows)[j];
             a.dw_part[((long)kind * gridDim.x + blockIdx.x) * D + j] = x;
         }
+        fence_proxy_async_smem();  // the next run's copies overwrite the sums
         __syncthreads();
     }
 }
@@ -345,52 +493,89 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const RopeArgs a, in
     if ((threadIdx.x & 31) == 0) (kind ? a.dwk : a.dwq)[(blockIdx.x % cols) * 32 + y] = x;
 }
 
-template <int D, bool F16>
-cudaError_t launch_fwd_df(RopeArgs a, cudaStream_t st) {
-    using C = RowCfg<D>;
-    const int n_rows = a.h_q + a.h_kv + (a.v ? a.h_kv : 0);
-    a.segments = cdiv(n_rows, C::ROWS * C::STEPS);
-    const long ctas = ((long)a.T * a.segments + kWarps - 1) / kWarps;
-    if (a.adjacent) norm_rope_kernel<D, F16, true><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
-    else norm_rope_kernel<D, F16, false><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
+// Rows of a unit: as many as a buffer holds, fewer where that would leave warps without a unit
+// (a decode step's few tokens: every warp then takes one batch of rows).
+int unit_rows(int d, long rows, int most, int sms) {
+    const int batch = d == 192 || d == 256 ? 2 : 512 / d;
+    long r = rows / ((long)sms * kWarps) / batch * batch;
+    return (int)(r < batch ? batch : r > most ? most : r);
+}
+
+template <int D>
+constexpr int max_rows(bool bwd) { return bwd ? RowCfg<D>::MAX_ROWS / 2 : RowCfg<D>::MAX_ROWS; }
+
+int unit_rows_of(int d, long rows, bool bwd, int sms) {
+    const int most = d == 64 ? max_rows<64>(bwd) : d == 128 ? max_rows<128>(bwd) : d == 192 ? max_rows<192>(bwd) : max_rows<256>(bwd);
+    return unit_rows(d, rows, most, sms);
+}
+
+template <int D, bool F16, bool ADJ>
+cudaError_t launch_fwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
+    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
+    cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<D, F16, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    norm_rope_kernel<D, F16, ADJ><<<ctas, 32 * kWarps, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, bool F16>
-cudaError_t launch_bwd_df(const RopeArgs& a, int ctas, cudaStream_t st) {
-    if (a.adjacent) norm_rope_bwd_kernel<D, F16, true><<<ctas, 32 * kBwdWarps, 0, st>>>(a);
-    else norm_rope_bwd_kernel<D, F16, false><<<ctas, 32 * kBwdWarps, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+template <int D>
+cudaError_t launch_fwd_d(const RopeArgs& a, int ctas, cudaStream_t st) {
+    if (a.f16) return a.adjacent ? launch_fwd_dfa<D, true, true>(a, ctas, st) : launch_fwd_dfa<D, true, false>(a, ctas, st);
+    return a.adjacent ? launch_fwd_dfa<D, false, true>(a, ctas, st) : launch_fwd_dfa<D, false, false>(a, ctas, st);
+}
+
+template <int D, bool F16, bool ADJ>
+cudaError_t launch_bwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
+    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
+    cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D, F16, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    norm_rope_bwd_kernel<D, F16, ADJ><<<ctas, 32 * kWarps, smem, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     norm_rope_dw_kernel<<<2 * (D / 32), 1024, 0, st>>>(a, ctas);
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_bwd_d(const RopeArgs& a, int ctas, cudaStream_t st) {
+    if (a.f16) return a.adjacent ? launch_bwd_dfa<D, true, true>(a, ctas, st) : launch_bwd_dfa<D, true, false>(a, ctas, st);
+    return a.adjacent ? launch_bwd_dfa<D, false, true>(a, ctas, st) : launch_bwd_dfa<D, false, false>(a, ctas, st);
+}
+
+int ctas_for(long units, int sms) {
+    const long need = (units + kWarps - 1) / kWarps;
+    return (int)(need < 1 ? 1 : need < sms ? need : sms);
+}
+
 }  // namespace
 
-cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t st) {
+cudaError_t launch_norm_rope(const RopeArgs& args, int sms, cudaStream_t st) {
+    RopeArgs a = args;
+    const int sets = a.v ? 2 : 1;
+    a.unit_rows = unit_rows_of(a.d, (long)a.T * (a.h_q + sets * a.h_kv), false, sms);
+    const int ctas = ctas_for((long)a.T * (cdiv(a.h_q, a.unit_rows) + sets * cdiv(a.h_kv, a.unit_rows)), sms);
     switch (a.d) {
-        case 64: return a.f16 ? launch_fwd_df<64, true>(a, st) : launch_fwd_df<64, false>(a, st);
-        case 128: return a.f16 ? launch_fwd_df<128, true>(a, st) : launch_fwd_df<128, false>(a, st);
-        case 192: return a.f16 ? launch_fwd_df<192, true>(a, st) : launch_fwd_df<192, false>(a, st);
-        case 256: return a.f16 ? launch_fwd_df<256, true>(a, st) : launch_fwd_df<256, false>(a, st);
+        case 64: return launch_fwd_d<64>(a, ctas, st);
+        case 128: return launch_fwd_d<128>(a, ctas, st);
+        case 192: return launch_fwd_d<192>(a, ctas, st);
+        case 256: return launch_fwd_d<256>(a, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }
 
-int norm_rope_bwd_ctas(long rows, int d, int sms) {
-    const int rows_per_cta = kBwdWarps * (d == 192 ? 8 : 512 / d);
-    const long need = (rows + rows_per_cta - 1) / rows_per_cta;
-    const long most = (long)sms * 2;
-    return (int)(need < 1 ? 1 : need < most ? need : most);
+int norm_rope_bwd_ctas(const RopeArgs& a, int sms) {
+    const int rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
+    return ctas_for((long)a.T * cdiv(a.h_q, rows), sms);
 }
 
-cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_norm_rope_bwd(const RopeArgs& args, int sms, cudaStream_t st) {
+    RopeArgs a = args;
+    a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
+    const int ctas = norm_rope_bwd_ctas(a, sms);
     switch (a.d) {
-        case 64: return a.f16 ? launch_bwd_df<64, true>(a, ctas, st) : launch_bwd_df<64, false>(a, ctas, st);
-        case 128: return a.f16 ? launch_bwd_df<128, true>(a, ctas, st) : launch_bwd_df<128, false>(a, ctas, st);
-        case 192: return a.f16 ? launch_bwd_df<192, true>(a, ctas, st) : launch_bwd_df<192, false>(a, ctas, st);
-        case 256: return a.f16 ? launch_bwd_df<256, true>(a, ctas, st) : launch_bwd_df<256, false>(a, ctas, st);
+        case 64: return launch_bwd_d<64>(a, ctas, st);
+        case 128: return launch_bwd_d<128>(a, ctas, st);
+        case 192: return launch_bwd_d<192>(a, ctas, st);
+        case 256: return launch_bwd_d<256>(a, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }
