@@ -363,7 +363,8 @@ bool paged_packed(const Problem& p) { return p.block_table && p.cu_q; }
 struct PagedPlan {
     bool empty = true;
     int ctas = 0, few_rows = 0, many_rows = 0;
-    bool many = false;  // the tensor-core kernel takes part
+    long few_max = 0;   // sequences of at most this many rows are the few-row kernel's (0: none)
+    bool many = false;  // the others are the tensor-core kernel's
     size_t off_pre = 0, off_line = 0, off_cut = 0, off_o = 0, off_ml = 0, off_mo = 0, off_mml = 0, ws_bytes = kStatusBytes;
 };
 
@@ -377,8 +378,15 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.ctas = sm_count();
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
     const long rows = longest * p.G;
-    pl.few_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    // Every sequence known to have 64 rows at most (or d > 128, where the few-row kernel takes them
+    // all, tile by tile): the few-row kernel alone, its tile the rows.  Else it takes those of a
+    // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
+    // a decode step 38 us where one of 16 takes 22: 20 sequences of 5 heads a group, d = 64), and none
+    // where a token has more than 64.
     pl.many = rows > 64 && p.d <= 128;
+    const long tile = pl.many ? p.G : rows;
+    pl.few_rows = tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
+    pl.few_max = !pl.many ? kAllFew : p.G <= 64 ? pl.few_rows : 0;
     pl.many_rows = 2 * p.P * p.G;
     pl.off_pre = kStatusBytes;
     pl.off_line = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
@@ -418,7 +426,7 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.box = p.page_size & -p.page_size;
     if (a.box > kTileRows) a.box = kTileRows;
     a.few_rows = pl.few_rows;
-    a.few_max = pl.many ? pl.few_rows : kAllFew;
+    a.few_max = pl.few_max;
     a.many_rows = pl.many_rows;
     a.no_split = (in.flags & FA_FLAG_NO_SPLIT) ? 1 : 0;
     a.validate = (in.flags & FA_FLAG_VALIDATE_CU) ? 1 : 0;
@@ -437,7 +445,7 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
         !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16))
         return FA_ERR_CUDA;
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
-    if (e == cudaSuccess) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
+    if (e == cudaSuccess && pl.few_max > 0) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     if (!pl.many) return cuda_status(timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); }));
     // sequences of more rows: the tensor-core kernel, 2 P G rows to an item

@@ -131,6 +131,10 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     const Problem& p = a.p;
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
+    if constexpr (PG) {
+        allow_next_kernel();
+        wait_previous_kernel();
+    }
     // an earlier CTA of this launch gave up: do not start
     if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
     if constexpr (PG) {
@@ -876,6 +880,7 @@ static cudaError_t launch_fwd_k(const FwdArgs& a, const CUtensorMap& tq, const C
     if ((e = cudaFuncGetAttributes(&fa, fwd_kernel<D, F16, KT, PG>)) != cudaSuccess) return e;
     if (fa.numRegs * kThreadsFwd < 128 * C::REG_LOW + 256 * C::REG_HIGH) return cudaErrorLaunchOutOfResources;
     if (a.n_items <= 0 || a.n_ctas <= 0) return cudaSuccess;
+    if constexpr (PG) return launch_after(fwd_kernel<D, F16, KT, PG>, dim3(a.n_ctas), kThreadsFwd, smem, st, a, tq, tk, tv);
     fwd_kernel<D, F16, KT, PG><<<(unsigned)a.n_ctas, kThreadsFwd, smem, st>>>(a, tq, tk, tv);
     return cudaGetLastError();
 }

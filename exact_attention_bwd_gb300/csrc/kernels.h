@@ -176,7 +176,7 @@ struct RopeArgs {
     uint16_t *dq, *dk;
     float *dwq, *dwk, *dw_part;
     int* status;
-    int unit_rows;             // rows a warp takes at a time
+    int unit_rows, warps;      // rows a warp takes at a time, warps that walk over them
 };
 
 struct PagePlanArgs {
@@ -209,6 +209,23 @@ cudaError_t launch_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int sms, cudaStream_t st);
 int norm_rope_bwd_ctas(const RopeArgs& a, int sms);  // rows of dw_part for each weight
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st);
+
+// Launches a kernel that starts while the one before it in the stream ends (its CTAs call
+// wait_previous_kernel before they touch anything that kernel writes).
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 // Number of 16-byte-aligned KV tiles etc. shared by planner and kernels.
 constexpr int kTileRows = 128;

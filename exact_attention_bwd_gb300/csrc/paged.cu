@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
     __shared__ int bad_any;
     const Problem& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    allow_next_kernel();
     long long run0 = 0, run1 = 0;
     bool bad = false;
     if (tid == 0) bad_any = 0;
@@ -191,9 +192,8 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     const Problem& p = a.p;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (*reinterpret_cast<volatile int*>(a.status) != 0) return;
     const int cta = blockIdx.x;
-    if (cta >= a.line->n) return;
+    allow_next_kernel();
 
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
     if (tid == 0) {
@@ -219,6 +219,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
         }
         fence_mbar_init();
     }
+    // the schedule is there; a CTA without work, or one of a call that already failed, leaves
+    wait_previous_kernel();
+    if (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0) return;
     if (warp == 2) {
         tmem_alloc(&s.tmem_base, C::TMEM_COLS);
         tmem_relinquish();
@@ -686,6 +689,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     const int which = (int)blockIdx.y < few_groups ? 0 : 1;
     const int held = which ? a.many_rows : a.few_rows;
     const int r1 = (((int)blockIdx.y - (which ? few_groups : 0)) * kMergeWarps + warp) * kMergeRows;
+    wait_previous_kernel();
     if (c >= a.line[which].n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
     const PagedCut cut = a.cut[which * gridDim.x + c];
     if (r1 >= cut.rows) return;
@@ -759,8 +763,7 @@ cudaError_t launch_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensor
     static_assert(smem <= kSmemMax, "the few-row kernel's shared memory");
     cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    paged_few_kernel<D, NR><<<ctas, kThreadsFew, smem, st>>>(a, tk, tv);
-    return cudaGetLastError();
+    return launch_after(paged_few_kernel<D, NR>, dim3(ctas), kThreadsFew, smem, st, a, tk, tv);
 }
 
 template <int D>
@@ -775,9 +778,8 @@ cudaError_t launch_few_d(const PagedArgs& a, const CUtensorMap& tk, const CUtens
 
 template <int D>
 cudaError_t launch_merge_d(const PagedArgs& a, const dim3& grid, int few_groups, cudaStream_t st) {
-    if (a.p.dtype == FA_DTYPE_F16) paged_merge_kernel<D, true><<<grid, 32 * kMergeWarps, 0, st>>>(a, few_groups);
-    else paged_merge_kernel<D, false><<<grid, 32 * kMergeWarps, 0, st>>>(a, few_groups);
-    return cudaGetLastError();
+    auto kernel = a.p.dtype == FA_DTYPE_F16 ? paged_merge_kernel<D, true> : paged_merge_kernel<D, false>;
+    return launch_after(kernel, grid, 32 * kMergeWarps, 0, st, a, few_groups);
 }
 
 }  // namespace
@@ -799,7 +801,7 @@ cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CU
 
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st) {
     if (a.few_ctas < 2 || a.no_split) return cudaSuccess;
-    const int few_groups = cdiv(a.few_rows, kMergeRowsCta);
+    const int few_groups = a.few_max > 0 ? cdiv(a.few_rows, kMergeRowsCta) : 0;
     const dim3 grid(a.few_ctas, few_groups + (many ? cdiv(a.many_rows, kMergeRowsCta) : 0));
     switch (a.p.d) {
         case 64: return launch_merge_d<64>(a, grid, few_groups, st);

@@ -126,6 +126,13 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) 
 }
 
 // ------------------------------------------------------------------------------------------
+// programmatic dependent launch: the next kernel of the stream may start its CTAs; wait until
+// the kernel before has finished and its writes are visible (at once without the launch attribute)
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------------
 // TMA
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {

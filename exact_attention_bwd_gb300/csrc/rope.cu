@@ -11,7 +11,7 @@
 //
 // Both are streams: 2 (forward) or 3 (gradient) passes over the rows, nothing to reuse but
 // the angles and the weights, so HBM bounds them and what counts is the bytes in flight.  One
-// CTA per SM of 8 warps, each on its own: a warp walks over units (some rows of one token, of q,
+// CTA per SM of 12 warps, each on its own: a warp walks over units (some rows of one token, of q,
 // k or v) and keeps the next units' rows and angles on their way into its own shared-memory
 // buffers by bulk copies, so that the loads do not wait for its arithmetic nor take registers.
 // (Loads into registers, 4 row batches a warp at 16 warps per SM, reached 58 % of the copy rate.)
@@ -25,8 +25,12 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBufs = 3;           // units in flight per warp
+// 12 warps of two 8 KB buffers fill the shared memory.  Measured, forward / gradient of 16384
+// tokens of 32 + 8 heads of 128 and append of 8192 tokens of 16 + 2 heads of 256, us: 54.7 / 85.1 /
+// 32.4; 8 warps of three 64.0 / 103.0 / 39.6; 12 of three 4 KB ones 60.5 / 99.5 / 37.0; 16 of two
+// 4 KB ones 58.1 / 101.1 / 32.8.  (At the copy rate: 50.8 / 75.8 / 25.4.)
+constexpr int kWarps = 12;
+constexpr int kBufs = 2;           // units in flight per warp
 constexpr int kUnitBytes = 8192;   // rows of a unit at most (gradient: half of it x, half dy)
 
 template <int D>
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     WarpSmem<D>& s = reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp];
     const bool on = li < C::PAIRS;
     const int gq = groups_of(a, a.h_q), gk = groups_of(a, a.h_kv), per_token = gq + gk + (a.v ? gk : 0);
-    const unsigned n_warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
     // a unit's kind (0 q, 1 k, 2 v), first row and rows
     auto unit = [&](int x, int& kind, int& r0, int& rows) {
         kind = x < gq ? 0 : x < gq + gk ? 1 : 2;
@@ -217,6 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         rows = min(a.unit_rows, (kind ? a.h_kv : a.h_q) - r0);
     };
     UnitWalk ahead(me, n_warps, per_token), now = ahead;
+    if (me >= n_warps) ahead.t = now.t = a.T;
     int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0)
     auto look = [&]() {
         if (lane == 0 && ahead.t < a.T) {
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
         fence_mbar_init();
     }
     __syncwarp();
-    const unsigned n_warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
     uint32_t phase = 0;
     bool failed = false;
 #pragma unroll 1
@@ -365,6 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[e] = make_float2(0.f, 0.f);
         UnitWalk ahead(me, n_warps, groups_of(a, heads)), now = ahead;
+        if (me >= n_warps) ahead.t = now.t = a.T;
         int next_pos = -1;
         auto look = [&]() {
             if (lane == 0 && ahead.t < a.T) next_pos = position_of(a, ahead.t);
@@ -541,6 +547,22 @@ cudaError_t launch_bwd_d(const RopeArgs& a, int ctas, cudaStream_t st) {
     return a.adjacent ? launch_bwd_dfa<D, false, true>(a, ctas, st) : launch_bwd_dfa<D, false, false>(a, ctas, st);
 }
 
+// Warps that walk: all of the grid's, less a few so that their number has no factor in common with
+// the units of a token and every warp meets units of each size.
+int walking_warps(int ctas, int per_token) {
+    int n = ctas * kWarps;
+    auto common = [](int x, int y) {
+        while (y) {
+            const int z = x % y;
+            x = y;
+            y = z;
+        }
+        return x;
+    };
+    while (n > 1 && common(n, per_token) > 1) --n;
+    return n;
+}
+
 int ctas_for(long units, int sms) {
     const long need = (units + kWarps - 1) / kWarps;
     return (int)(need < 1 ? 1 : need < sms ? need : sms);
@@ -552,7 +574,9 @@ cudaError_t launch_norm_rope(const RopeArgs& args, int sms, cudaStream_t st) {
     RopeArgs a = args;
     const int sets = a.v ? 2 : 1;
     a.unit_rows = unit_rows_of(a.d, (long)a.T * (a.h_q + sets * a.h_kv), false, sms);
-    const int ctas = ctas_for((long)a.T * (cdiv(a.h_q, a.unit_rows) + sets * cdiv(a.h_kv, a.unit_rows)), sms);
+    const int per_token = cdiv(a.h_q, a.unit_rows) + sets * cdiv(a.h_kv, a.unit_rows);
+    const int ctas = ctas_for((long)a.T * per_token, sms);
+    a.warps = (long)a.T * per_token > (long)ctas * kWarps ? walking_warps(ctas, per_token) : ctas * kWarps;
     switch (a.d) {
         case 64: return launch_fwd_d<64>(a, ctas, st);
         case 128: return launch_fwd_d<128>(a, ctas, st);
@@ -571,6 +595,7 @@ cudaError_t launch_norm_rope_bwd(const RopeArgs& args, int sms, cudaStream_t st)
     RopeArgs a = args;
     a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
     const int ctas = norm_rope_bwd_ctas(a, sms);
+    a.warps = ctas * kWarps;
     switch (a.d) {
         case 64: return launch_bwd_d<64>(a, ctas, st);
         case 128: return launch_bwd_d<128>(a, ctas, st);
