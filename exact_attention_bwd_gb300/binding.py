@@ -267,10 +267,15 @@ def make_params(q, k, *, causal=False, window=(-1, -1), softmax_scale=None, sink
     return p
 
 
+_type_codes = {}
+
+
 def _type_code(t):
     """FA_DTYPE_* code of a torch dtype, or None when the library does not take it."""
-    import torch
-    return {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_F16, torch.uint8: FA_DTYPE_E4M3}.get(t)
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_F16, torch.uint8: FA_DTYPE_E4M3})
+    return _type_codes.get(t)
 
 
 def _stream():

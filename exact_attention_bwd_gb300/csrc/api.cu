@@ -50,7 +50,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // 4-D tensor map of 16-bit elements (fp16 if f16, else bf16) over [b][s][h][d] (innermost
 // first: d, h, s, b) with a (64, box_h, box_s, 1) box and 128-byte swizzle.  Out-of-range
 // rows read as zero.
-bool encode_bhsd(CUtensorMap* m, const void* base, int d, int h, int s, int b, int box_h, int box_s, bool f16) {
+bool encode_bhsd(CUtensorMap* m, const void* base, int d, int h, int s, int b, int box_h, int box_s, bool f16,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     auto fn = encoder();
     if (!fn) return false;
     if (s <= 0 || b <= 0) {
@@ -62,7 +63,7 @@ bool encode_bhsd(CUtensorMap* m, const void* base, int d, int h, int s, int b, i
     cuuint32_t box[4] = {64, (cuuint32_t)box_h, (cuuint32_t)box_s, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     CUresult r = fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -441,8 +442,12 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.status = status;
     CUtensorMap tk, tv;
     const bool f16 = p.dtype == FA_DTYPE_F16;
-    if (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16) ||
-        !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16))
+    // a key's row is d * 2 bytes of h_kv times as many: fetched 256 bytes at a time, half of it would be
+    // another head's where d * 2 is 128 or 384 (decode of 32 x 16000 keys, 4 heads: d = 64 111 us against
+    // 126, d = 192 with 2 heads 132 against 146)
+    const CUtensorMapL2promotion promotion = p.d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion) ||
+        !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion))
         return FA_ERR_CUDA;
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
     if (e == cudaSuccess && pl.few_max > 0) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });

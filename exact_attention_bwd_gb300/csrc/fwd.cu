@@ -135,10 +135,11 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         allow_next_kernel();
         wait_previous_kernel();
     }
-    // an earlier CTA of this launch gave up: do not start
-    if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
+    // an earlier CTA of this launch gave up: do not start (PG: nor without work)
     if constexpr (PG) {
-        if ((int)blockIdx.x >= a.line->n) return;
+        if (__syncthreads_or(tid == 0 && ((int)blockIdx.x >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
+    } else {
+        if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
     }
 
     // ---------------- setup ----------------

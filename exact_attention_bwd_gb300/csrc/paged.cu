@@ -121,6 +121,9 @@ struct FewCfg {
     static constexpr int RING = D == 64 ? (FIT > 12 ? 12 : FIT / 2 * 2) : (FIT > 6 ? 6 : FIT);
     static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile and the next K have to fit");
     static constexpr int OH = D > 128 ? 2 : 1;         // 128-lane accumulators of O^T
+    // P^T in shared memory: 64 rows are a whole swizzle row per key, which a thread writes with
+    // eight 16-byte stores (rows innermost); fewer rows lie [row][key], a 2-byte store each
+    static constexpr bool P_MN = NR == 64;
     static constexpr int TMEM_COLS = pow2_at_least(2 * NR + OH * NR);
     // Unit n of the stream: K and V tiles in turn.  At d = 64 the 128-row V^T operand takes the
     // slot behind V's as its second 64 rows (their products, lanes 64 .. 127, are not read): K and V
@@ -143,8 +146,13 @@ struct __align__(1024) FewSmem {
     uint8_t ring[C::RING][C::UNIT];
     uint8_t q[C::Q_BUFS][C::Q_BYTES];
     uint8_t p[2][C::P_BYTES];
-    alignas(16) float mref[NR];   // reference maxima of the item's rows (log2 units)
-    alignas(16) float alpha[NR];  // their last change as a factor; the epilogue's factor of O
+    // reference maxima m of the item's rows (log2 units; -inf: no key so far); what the exponent
+    // adds, -m (0 for -inf); the score (unscaled) past which m moves, (m + 8) / scale; the last
+    // change of m as a factor, in the epilogue the factor of O
+    float mref[NR];
+    alignas(16) float negm[NR];
+    alignas(16) float limit[NR];
+    alignas(16) float alpha[NR];
     uint64_t full[C::RING], empty[C::RING];
     uint64_t q_full[C::Q_BUFS], q_empty[C::Q_BUFS];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain;
@@ -221,7 +229,8 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     }
     // the schedule is there; a CTA without work, or one of a call that already failed, leaves
     wait_previous_kernel();
-    if (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0) return;
+    // (one thread looks, so that all leave or none)
+    if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
     if (warp == 2) {
         tmem_alloc(&s.tmem_base, C::TMEM_COLS);
         tmem_relinquish();
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
         // ================= MMA issuer =================
         if (lane == 0) {
             const uint32_t idS = idesc_16(128, NR, false, false, f16);
-            const uint32_t idO = idesc_16(128, NR, true, false, f16);
+            const uint32_t idO = idesc_16(128, NR, true, C::P_MN, f16);
             uint32_t gt = 0, qi = 0;  // tiles whose S was issued, items with keys
             uint32_t gp = 0;          // tiles whose P V was issued
             bool ok = true;
@@ -337,7 +346,8 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                         const uint64_t vd = sdesc_sw128(v_addr, C::CHUNK, 1024);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            mma_ss(tmem + o_col, vd + 128 * x, pd + (x / 4) * (NR * 8) + 2 * (x % 4), idO, t > 0 || x > 0 ? 1u : 0u);
+                            mma_ss(tmem + o_col, vd + 128 * x, pd + (C::P_MN ? 128 * x : (x / 4) * (NR * 8) + 2 * (x % 4)), idO,
+                                   t > 0 || x > 0 ? 1u : 0u);
                     };
                     for (int h = 0; h < KU; ++h) {
                         const uint32_t n = 2 * KU * gp + KU + h;
@@ -462,9 +472,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             const unsigned G = (unsigned)p.G;
             const int in_lo = p.left >= 0 ? (int)((unsigned)(r0 + w.rows - 1) / G) + off - p.left : 0;
             const int in_hi = p.right >= 0 ? min(nk - 1, (int)((unsigned)r0 / G) + off + p.right) : nk - 1;
-            float l[NR];
+            float2 l[NR / 2];  // sums of the rows 2 r, 2 r + 1 over this key's tiles
 #pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            for (int r = 0; r < NR / 2; ++r) l[r] = make_float2(0.f, 0.f);
             bool gave_up = false;
             for (int t = t0; t < t1; ++t, ++gt) {
                 const int buf = gt & 1, j0 = t * kKeyTile, j = j0 + key;
@@ -486,14 +496,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 bool over = t == t0;  // the item's first tile sets the references
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4*>(&s.mref[r]);
-                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = __uint_as_float(sr[r + e]) * c;
-                        sr[r + e] = __float_as_uint(x);
-                        over = over || x > m[e] + 8.f;
-                    }
+                    const float4 m = *reinterpret_cast<const float4*>(&s.limit[r]);
+                    over = over || __uint_as_float(sr[r]) > m.x || __uint_as_float(sr[r + 1]) > m.y ||
+                           __uint_as_float(sr[r + 2]) > m.z || __uint_as_float(sr[r + 3]) > m.w;
                 }
                 if (vote_or(over || !ok)) {
                     if (!vote_and(ok)) {
@@ -515,24 +520,29 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 #pragma unroll
                     for (int o = TPR / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                     if (key % TPR == 0) {
-                        const float m = t == t0 ? -INFINITY : s.mref[my_row], mn = fmaxf(m, x);
+                        const float m = t == t0 ? -INFINITY : s.mref[my_row], mn = fmaxf(m, x * c);
                         s.alpha[my_row] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
                         s.mref[my_row] = mn;
+                        s.negm[my_row] = mn == -INFINITY ? 0.f : -mn;
+                        s.limit[my_row] = (mn + 8.f) / c;
                     }
                     softmax_sync();  // the new references are in
                     if (t > t0) {
-                        float al[NR];
+                        constexpr int OC = NR < 32 ? NR : 32;  // columns of O at a time
 #pragma unroll
-                        for (int r = 0; r < NR; r += 4) *reinterpret_cast<float4*>(&al[r]) = *reinterpret_cast<const float4*>(&s.alpha[r]);
+                        for (int r = 0; r < NR; r += 4) {
+                            const float4 al = *reinterpret_cast<const float4*>(&s.alpha[r]);
+                            l[r / 2] = __fmul2_rn(l[r / 2], make_float2(al.x, al.y));
+                            l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(al.z, al.w));
+                        }
+#pragma unroll 1
+                        for (int h = 0; h < C::OH * NR; h += OC) {
+                            uint32_t o[OC];
+                            tmem_ld_cols<OC>(tmem + lane_base + cO + h, o);
+                            const float* al = &s.alpha[h % NR];
 #pragma unroll
-                        for (int r = 0; r < NR; ++r) l[r] *= al[r];
-#pragma unroll
-                        for (int h = 0; h < C::OH; ++h) {
-                            uint32_t o[NR];
-                            tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
-#pragma unroll
-                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * al[r]);
-                            tmem_st_cols<NR>(tmem + lane_base + cO + NR * h, o);
+                            for (int r = 0; r < OC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * al[r]);
+                            tmem_st_cols<OC>(tmem + lane_base + cO + h, o);
                         }
                     }
                 }
@@ -540,21 +550,33 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 if (gt >= 2) {  // the buffer's last P V has completed
                     ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf], ((gt - 2) >> 1) & 1, ab)) && ok;
                 }
+                auto store_p = [&](auto pack) {
+                    const float2 c2 = make_float2(c, c);
+                    uint32_t w2[NR / 2];
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4*>(&s.mref[r]);
-                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+                    for (int r = 0; r < NR; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&s.negm[r]);
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1])), c2, make_float2(m.x, m.y));
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[r + 2]), __uint_as_float(sr[r + 3])), c2, make_float2(m.z, m.w));
+                        const float2 ex = make_float2(ex2(x.x), ex2(x.y)), ey = make_float2(ex2(y.x), ex2(y.y));
+                        l[r / 2] = __fadd2_rn(l[r / 2], ex);
+                        l[r / 2 + 1] = __fadd2_rn(l[r / 2 + 1], ey);
+                        w2[r / 2] = pack(ex.x, ex.y);
+                        w2[r / 2 + 1] = pack(ey.x, ey.y);
+                        if constexpr (C::P_MN) {
+                            // row `key` of the operand: its 16-byte unit u at position u ^ (key & 7)
+                            if (r % 8 == 4)
+                                *reinterpret_cast<uint4*>(&s.p[buf][key * 128 + ((((r >> 3) ^ key) & 7) << 4)]) =
+                                    make_uint4(w2[r / 2 - 2], w2[r / 2 - 1], w2[r / 2], w2[r / 2 + 1]);
+                        } else {
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float e0 = ex2(__uint_as_float(sr[r + e]) - (m[e] == -INFINITY ? 0.f : m[e]));
-                        const float e1 = ex2(__uint_as_float(sr[r + e + 1]) - (m[e + 1] == -INFINITY ? 0.f : m[e + 1]));
-                        l[r + e] += e0;
-                        l[r + e + 1] += e1;
-                        const uint32_t w2 = f16 ? pack16<true>(e0, e1) : pack16<false>(e0, e1);
-                        *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e) & 7] + 128 * (r + e)]) = (uint16_t)w2;
-                        *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e + 1) & 7] + 128 * (r + e + 1)]) = (uint16_t)(w2 >> 16);
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e) & 7] + 128 * (r + e)]) = (uint16_t)(w2[(r + e) / 2] >> (16 * (e & 1)));
+                        }
                     }
-                }
+                };
+                if (f16) store_p([](float x, float y) { return pack16<true>(x, y); });
+                else store_p([](float x, float y) { return pack16<false>(x, y); });
                 if (edge) {
                     // values at keys that no row sees may be anything (unused rows of a page): 0 * NaN
                     // would reach every row, so they are cleared
@@ -588,7 +610,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             }
             // sums of the rows over the keys
 #pragma unroll
-            for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = l[r];
+            for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = r & 1 ? l[r / 2].y : l[r / 2].x;
             if (!vote_and(ok)) break;
             const int rows = w.rows, part = w.part, g = w.g, q0 = w.q0;
             {
