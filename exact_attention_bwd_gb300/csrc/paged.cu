@@ -5,16 +5,22 @@
 // long side: S^T = K Q^T (128 keys x NR rows) and O^T = V^T P^T (d x NR rows), both with the
 // cache tile as the 128-row operand straight from the swizzled tile that TMA wrote, and NR = 16,
 // 32 or 64 columns.  A key is a TMEM lane, so each of 128 threads does the softmax of one key
-// for all rows: NR exponentials a tile and thread, a small part of the time its 128 keys take
-// to arrive.  The online softmax's reference maximum is only moved when some score passes it
-// by more than 2^8 (one vote per tile), so the cross-lane maxima are formed rarely.
+// for all rows.  The online softmax's reference maximum is only moved when some score passes it
+// by more than 2^8 (one vote per tile), so the cross-lane maxima are formed rarely.  A tile's way
+// through the softmax is a chain of latencies, at 32 and 64 rows longer than its keys take to
+// arrive where a tile is 64 KB or less: there (d <= 128) two groups of four warps take the tiles in
+// turn, each an online softmax of its own with its own accumulator, joined at the end.  (Decode of
+// 32 x 16000 keys, 4 heads, one group against two: d = 64 157 / 126 us at 32 rows and 225 / 149 at
+// 64, d = 128 225 / 193 at 64; but d = 64 108 / 111 at 16, and with 2 heads d = 256 203 / 258 at 64.)
 //
-// Warp roles (256 threads, one CTA per SM):
+// Warp roles (one CTA per SM):
 //   warp 0       TMA producer: K and V tiles, page by page, through a ring of [128 keys] units
 //   warp 1       MMA issuer (one thread)
 //   warp 2       owns the TMEM allocation
 //   warp 3       scheduler: finds the CTA's pieces of work, stages each item's Q rows
-//   warps 4..7   softmax (thread = key) and epilogue (thread = column of O)
+//   warps 4..7   softmax (thread = key) and epilogue (thread = column of O, then warp = row)
+//   warps 8..11  with two groups: the softmax of the odd tiles of the CTA's stream (warps 4..7 then
+//                have the even ones) and the epilogue of the second half of the rows
 #include "paged.cuh"
 
 namespace fa {
@@ -102,7 +108,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
 // ------------------------------------------------------------------------------------------
 // few-row kernel
 // ------------------------------------------------------------------------------------------
-constexpr int kThreadsFew = 256;
+// registers after setmaxnreg with two softmax groups: 128 x 72 + 256 x 216 = the launch's 384 x 168
+constexpr int kFewRegLow = 72, kFewRegHigh = 216;
 constexpr int kItems = 4;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -124,7 +131,11 @@ struct FewCfg {
     // P^T in shared memory: 64 rows are a whole swizzle row per key, which a thread writes with
     // eight 16-byte stores (rows innermost); fewer rows lie [row][key], a 2-byte store each
     static constexpr bool P_MN = NR == 64;
-    static constexpr int TMEM_COLS = pow2_at_least(2 * NR + OH * NR);
+    static constexpr int NG = D <= 128 && NR >= 32 ? 2 : 1;  // softmax groups
+    static constexpr int THREADS = 128 + 128 * NG;
+    // scores held at a time; with two groups (fewer registers) 64 rows are read twice, 32 at a time
+    static constexpr int HR = NG == 2 && NR > 32 ? 32 : NR;
+    static constexpr int TMEM_COLS = pow2_at_least(2 * NR + NG * OH * NR);
     // Unit n of the stream: K and V tiles in turn.  At d = 64 the 128-row V^T operand takes the
     // slot behind V's as its second 64 rows (their products, lanes 64 .. 127, are not read): K and V
     // swap slots so that this is the K of the same tile, which is held until then.
@@ -146,13 +157,14 @@ struct __align__(1024) FewSmem {
     uint8_t ring[C::RING][C::UNIT];
     uint8_t q[C::Q_BUFS][C::Q_BYTES];
     uint8_t p[2][C::P_BYTES];
-    // reference maxima m of the item's rows (log2 units; -inf: no key so far); what the exponent
-    // adds, -m (0 for -inf); the score (unscaled) past which m moves, (m + 8) / scale; the last
-    // change of m as a factor, in the epilogue the factor of O
-    float mref[NR];
-    alignas(16) float negm[NR];
-    alignas(16) float limit[NR];
-    alignas(16) float alpha[NR];
+    // Of each softmax group: reference maxima m of the item's rows (log2 units; -inf: no key so
+    // far); what the exponent adds, -m (0 for -inf); minus the score (unscaled) past which m
+    // moves, (m + 8) / scale; the last change of m as a factor, in the epilogue the factor of O; sums
+    float mref[C::NG][NR];
+    alignas(16) float negm[C::NG][NR];
+    alignas(16) float limit[C::NG][NR];
+    alignas(16) float alpha[C::NG][NR];
+    float lsum[C::NG][NR];
     uint64_t full[C::RING], empty[C::RING];
     uint64_t q_full[C::Q_BUFS], q_empty[C::Q_BUFS];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain;
@@ -165,7 +177,8 @@ struct __align__(1024) FewSmem {
 // NR consecutive fp32 TMEM columns of the warp's 32 lanes.
 template <int NR>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t* r) {
-    if constexpr (NR == 16) tmem_ld_32x32b_x16(addr, r);
+    if constexpr (NR == 8) tmem_ld_32x32b_x8(addr, r);
+    else if constexpr (NR == 16) tmem_ld_32x32b_x16(addr, r);
     else if constexpr (NR == 32) tmem_ld_32x32b_x32(addr, r);
     else tmem_ld_32x32b_x64(addr, r);
 }
@@ -176,22 +189,27 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t* r) {
     else tmem_st_32x32b_x64(addr, r);
 }
 
-// Votes of the four softmax warps (named barrier 1): what one of them decides all decide, so no
-// warp is left waiting for another that gave up.
-__device__ __forceinline__ bool vote_or(bool x) {
+// Votes of softmax threads (named barriers: 1 + group for a group's four warps, 3 for both
+// groups): what one of them decides all decide, so no warp is left waiting for another that gave
+// up.  The barriers' numbers are immediates.
+template <int BAR, int THREADS>
+__device__ __forceinline__ bool vote_at(bool x) {
     uint32_t r;
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "n"(BAR), "n"(THREADS)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ bool vote_and(bool x) { return !vote_or(!x); }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool group_or(int grp, bool x) { return grp ? vote_at<2, 128>(x) : vote_at<1, 128>(x); }
+__device__ __forceinline__ void group_sync(int grp) {
+    if (grp) asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+    else asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+}
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreadsFew, 1)
+__global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using C = FewCfg<D, NR>;
     constexpr int RING = C::RING, KU = C::KU;
@@ -219,11 +237,11 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
         }
-        mbar_init(&s.o_free, 4);
+        mbar_init(&s.o_free, 4 * C::NG);
         mbar_init(&s.drain, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], 6);  // producer, MMA issuer, four softmax warps
+            mbar_init(&s.item_empty[i], 2 + 4 * C::NG);  // producer, MMA issuer, softmax warps
         }
         fence_mbar_init();
     }
@@ -239,8 +257,11 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    constexpr uint32_t cS = 0, cO = 2 * NR;  // TMEM columns of the two S buffers and of O
+    // TMEM columns: the two S buffers (tile g's is g & 1), group x's O^T at cO + OH NR x
+    constexpr uint32_t cS = 0, cO = 2 * NR;
 
+    if (warp < 4) {
+    if constexpr (C::NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFewRegLow) : "memory");
     if (warp == 0) {
         // ================= TMA producer =================
         tma_prefetch_desc(&tmk);
@@ -332,11 +353,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 tc_fence_after();
                 const uint32_t q_addr = smem_u32(s.q[qb]);
                 if (!(ok = issue_s(q_addr))) break;
+                if (nt > 1 && !(ok = issue_s(q_addr))) break;
+                if (nt <= 2) tc_commit(&s.q_empty[qb]);  // the item's last S is issued
                 for (int t = 0; t < nt; ++t, ++gp) {
-                    if (t + 1 < nt) {
-                        if (!(ok = issue_s(q_addr))) break;
-                    }
-                    if (t + 2 == nt || nt == 1) tc_commit(&s.q_empty[qb]);  // the item's last S is issued
                     const int pb = gp & 1;
                     if (!(ok = mbar_wait(&s.p_full[pb], (gp >> 1) & 1, ab))) break;
                     // the previous item's O has been read
@@ -347,21 +366,27 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
                             mma_ss(tmem + o_col, vd + 128 * x, pd + (C::P_MN ? 128 * x : (x / 4) * (NR * 8) + 2 * (x % 4)), idO,
-                                   t > 0 || x > 0 ? 1u : 0u);
+                                   t >= C::NG || x > 0 ? 1u : 0u);
                     };
+                    const uint32_t o_col = cO + (C::NG == 2 ? C::OH * NR * pb : 0);
                     for (int h = 0; h < KU; ++h) {
                         const uint32_t n = 2 * KU * gp + KU + h;
                         if (!(ok = wait_unit(n))) break;
                         tc_fence_after();
                         const int sl = C::slot_of(n);
-                        issue_pv(cO + NR * h, smem_u32(s.ring[sl]));
+                        issue_pv(o_col + NR * h, smem_u32(s.ring[sl]));
                         // d = 192: columns 64 .. 191 again as the second accumulator
-                        if (D == 192) issue_pv(cO + NR, smem_u32(s.ring[sl]) + C::CHUNK);
+                        if (D == 192) issue_pv(o_col + NR, smem_u32(s.ring[sl]) + C::CHUNK);
                         tc_commit(&s.empty[sl]);
                     }
                     if (!ok) break;
                     if (D == 64) tc_commit(&s.empty[C::slot_of(2 * gp)]);
                     tc_commit(&s.pv_done[pb]);
+                    // S of the tile after next, into the buffer whose P has just been taken
+                    if (t + 2 < nt) {
+                        if (!(ok = issue_s(q_addr))) break;
+                        if (t + 3 == nt) tc_commit(&s.q_empty[qb]);
+                    }
                 }
                 ++qi;
             }
@@ -443,28 +468,41 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 }
             }
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        if constexpr (C::NG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kFewRegHigh) : "memory");
         // ================= softmax: one thread per key =================
-        const int key = tid - 128, sub = warp & 3;
+        constexpr int HR = C::HR, NG = C::NG;
+        const int grp = NG == 2 ? (warp - 4) >> 2 : 0, key = tid & 127, sub = warp & 3;
         const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
+        const uint32_t tO = tmem + lane_base + cO + C::OH * NR * grp;
         const float c = p.scale_log2;
-        // byte offset of this key in row r of a P buffer: p_at[r & 7] + 128 r
+        // byte offset of this key in row r of a [row][key] P buffer: p_at[r & 7] + 128 r
         uint32_t p_at[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             p_at[x] = (key >> 6) * (NR * 128) + (((((key & 63) >> 3) ^ x) & 7) << 4) + (key & 7) * 2;
-        // A [row][key] array of floats over both P buffers, for what is summed or turned across the
-        // keys while no P V is in flight: TPR threads to a row, each starting at another element of it
-        // so that a warp's reads fall into different banks.
-        float* grid = reinterpret_cast<float*>(s.p[0]);
-        constexpr int TPR = kKeyTile / NR;
+        // A [row][key] array of floats over the group's P buffers (both, or one of two: then half of the
+        // rows at a time), for what is summed or turned across the keys while none of the group's P V
+        // is in flight: TPR threads to a row, each starting at another element of it so that a warp's
+        // reads fall into different banks.
+        float* grid = reinterpret_cast<float*>(s.p[grp]);
+        constexpr int GR = NR / NG, TPR = kKeyTile / GR;
         const int my_row = key / TPR, row_at = my_row * kKeyTile + key % TPR;
-        uint32_t gt = 0;  // tiles done
+        auto across = [&](auto op, float x) {  // of the array's row my_row, in every thread of the row
+#pragma unroll 4
+            for (int y = 0; y < GR; ++y) x = op(x, grid[row_at + TPR * ((y + my_row) % GR)]);
+#pragma unroll
+            for (int o = TPR / 2; o >= 1; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+            return x;
+        };
+        const bool leads = key % TPR == 0;
+        uint32_t gt = 0;  // tiles of the CTA's stream before the item
         bool ok = true;
         for (int it = 0;; ++it) {
             const int slot = it % kItems;
             ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (it / kItems) & 1, ab)) && ok;
-            if (!vote_and(ok)) break;
+            if (vote_at<3, 128 * NG>(!ok)) break;
             if (s.item[slot].end) break;
             const FewItem& w = s.item[slot];
             const int t0 = w.t0, t1 = w.t1, off = w.nk - w.nq, nk = w.nk, lo = w.lo, hi = w.hi, r0 = w.r0;
@@ -475,103 +513,128 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
             float2 l[NR / 2];  // sums of the rows 2 r, 2 r + 1 over this key's tiles
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r) l[r] = make_float2(0.f, 0.f);
-            bool gave_up = false;
-            for (int t = t0; t < t1; ++t, ++gt) {
-                const int buf = gt & 1, j0 = t * kKeyTile, j = j0 + key;
-                ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (gt >> 1) & 1, ab)) && ok;
-                tc_fence_after();
-                uint32_t sr[NR];
-                tmem_ld_cols<NR>(tmem + lane_base + cS + NR * buf, sr);
+            const int first = t0 + (NG == 2 ? (gt ^ grp) & 1 : 0);  // the group's tiles: first, first + NG, ...
+            uint32_t g = gt + (first - t0);           // index of the tile in the CTA's stream
+            for (int t = first; t < t1; t += NG, g += NG) {
+                const int buf = NG == 2 ? grp : g & 1;
+                const uint32_t tS = tmem + lane_base + cS + NR * buf;
+                uint8_t* pbuf = s.p[buf];
+                const int j0 = t * kKeyTile, j = j0 + key;
                 const bool edge = j0 < in_lo || j0 + kKeyTile - 1 > in_hi;
+                // rows [ra, rb] see key j: positions j - off - right <= i <= j - off + left
+                int ra = 0, rb = NR - 1;
                 if (edge) {
-                    // rows that see key j: positions j - off - right <= i <= j - off + left
-                    int ra = 0, rb = NR - 1;
                     if (p.right >= 0) ra = (int)max(min(((long)j - off - p.right) * p.G - r0, (long)NR), 0l);
                     if (p.left >= 0) rb = (int)min(max(((long)j - off + p.left + 1) * p.G - 1 - r0, -1l), (long)NR);
                     if (j >= nk) ra = NR;
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (r < ra || r > rb) sr[r] = __float_as_uint(-INFINITY);
                 }
-                bool over = t == t0;  // the item's first tile sets the references
+                // HR scores of this key from row r0 on, masked
+                auto scores = [&](int h, uint32_t* sr) {
+                    tmem_ld_cols<HR>(tS + h, sr);
+                    if (edge) {
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(&s.limit[r]);
-                    over = over || __uint_as_float(sr[r]) > m.x || __uint_as_float(sr[r + 1]) > m.y ||
-                           __uint_as_float(sr[r + 2]) > m.z || __uint_as_float(sr[r + 3]) > m.w;
-                }
-                if (vote_or(over || !ok)) {
-                    if (!vote_and(ok)) {
-                        gave_up = true;
-                        break;
+                        for (int r = 0; r < HR; ++r)
+                            if (h + r < ra || h + r > rb) sr[r] = __float_as_uint(-INFINITY);
                     }
+                };
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (g >> 1) & 1, ab)) && ok;
+                tc_fence_after();
+                uint32_t sr[HR];
+                // (a maximum rather than a chain of comparisons: 149 against 191 us at d = 64 and 64 rows)
+                float past[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // largest score - limit
+#pragma unroll
+                for (int h = 0; h < NR; h += HR) {
+                    scores(h, sr);
+#pragma unroll
+                    for (int r = 0; r < HR; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&s.limit[grp][h + r]);
+                        const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1])), make_float2(m.x, m.y));
+                        const float2 y = __fadd2_rn(make_float2(__uint_as_float(sr[r + 2]), __uint_as_float(sr[r + 3])), make_float2(m.z, m.w));
+                        past[(r >> 2) & 3] = max3(past[(r >> 2) & 3], fmaxf(x.x, x.y), fmaxf(y.x, y.y));
+                    }
+                }
+                // (the item's first tile sets the references)
+                const bool over = t == first || fmaxf(fmaxf(past[0], past[1]), fmaxf(past[2], past[3])) > 0.f;
+                if (group_or(grp, over || !ok)) {
+                    if (group_or(grp, !ok)) break;
                     // some score passes its row's reference by more than 2^8: the references move to the
                     // maxima so far, sums and O follow
-                    if (t > t0) {  // O holds P V of the tile before, both P buffers are free
-                        ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, ab)) && ok;
+                    if (t > first) {  // O holds P V of the group's tile before, its P buffers are free
+                        ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(g - NG) & 1], ((g - NG) >> 1) & 1, ab)) && ok;
                         tc_fence_after();
                     }
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = __uint_as_float(sr[r]);
-                    softmax_sync();
-                    float x = -INFINITY;
-#pragma unroll 4
-                    for (int y = 0; y < NR; ++y) x = fmaxf(x, grid[row_at + TPR * ((y + my_row) % NR)]);
+                    for (int h = 0; h < NR; h += GR) {
+                        uint32_t x8[GR];
+                        tmem_ld_cols<GR>(tS + h, x8);
 #pragma unroll
-                    for (int o = TPR / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                    if (key % TPR == 0) {
-                        const float m = t == t0 ? -INFINITY : s.mref[my_row], mn = fmaxf(m, x * c);
-                        s.alpha[my_row] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
-                        s.mref[my_row] = mn;
-                        s.negm[my_row] = mn == -INFINITY ? 0.f : -mn;
-                        s.limit[my_row] = (mn + 8.f) / c;
+                        for (int r = 0; r < GR; ++r)
+                            grid[r * kKeyTile + key] = edge && (h + r < ra || h + r > rb) ? -INFINITY : __uint_as_float(x8[r]);
+                        group_sync(grp);
+                        const float x = across([](float a, float b) { return fmaxf(a, b); }, -INFINITY);
+                        if (leads) {
+                            const float m = t == first ? -INFINITY : s.mref[grp][h + my_row], mn = fmaxf(m, x * c);
+                            s.alpha[grp][h + my_row] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
+                            s.mref[grp][h + my_row] = mn;
+                            s.negm[grp][h + my_row] = mn == -INFINITY ? 0.f : -mn;
+                            // (no key so far: any finite score passes)
+                            s.limit[grp][h + my_row] = mn == -INFINITY ? INFINITY : -(mn + 8.f) / c;
+                        }
+                        group_sync(grp);
                     }
-                    softmax_sync();  // the new references are in
-                    if (t > t0) {
-                        constexpr int OC = NR < 32 ? NR : 32;  // columns of O at a time
+                    if (t > first) {
 #pragma unroll
                         for (int r = 0; r < NR; r += 4) {
-                            const float4 al = *reinterpret_cast<const float4*>(&s.alpha[r]);
+                            const float4 al = *reinterpret_cast<const float4*>(&s.alpha[grp][r]);
                             l[r / 2] = __fmul2_rn(l[r / 2], make_float2(al.x, al.y));
                             l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(al.z, al.w));
                         }
+                        constexpr int OC = NR < 32 ? NR : 32;  // columns of O at a time
 #pragma unroll 1
                         for (int h = 0; h < C::OH * NR; h += OC) {
                             uint32_t o[OC];
-                            tmem_ld_cols<OC>(tmem + lane_base + cO + h, o);
-                            const float* al = &s.alpha[h % NR];
+                            tmem_ld_cols<OC>(tO + h, o);
+                            const float* al = &s.alpha[grp][h % NR];
 #pragma unroll
                             for (int r = 0; r < OC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * al[r]);
-                            tmem_st_cols<OC>(tmem + lane_base + cO + h, o);
+                            tmem_st_cols<OC>(tO + h, o);
                         }
                     }
                 }
                 // P^T of this key: 16-bit (the MMA's operand type), the sums from the unrounded values
-                if (gt >= 2) {  // the buffer's last P V has completed
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf], ((gt - 2) >> 1) & 1, ab)) && ok;
+                if (g >= 2) {  // the buffer's last P V has completed
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[buf], ((g - 2) >> 1) & 1, ab)) && ok;
                 }
                 auto store_p = [&](auto pack) {
                     const float2 c2 = make_float2(c, c);
-                    uint32_t w2[NR / 2];
 #pragma unroll
-                    for (int r = 0; r < NR; r += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&s.negm[r]);
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1])), c2, make_float2(m.x, m.y));
-                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[r + 2]), __uint_as_float(sr[r + 3])), c2, make_float2(m.z, m.w));
-                        const float2 ex = make_float2(ex2(x.x), ex2(x.y)), ey = make_float2(ex2(y.x), ex2(y.y));
-                        l[r / 2] = __fadd2_rn(l[r / 2], ex);
-                        l[r / 2 + 1] = __fadd2_rn(l[r / 2 + 1], ey);
-                        w2[r / 2] = pack(ex.x, ex.y);
-                        w2[r / 2 + 1] = pack(ey.x, ey.y);
-                        if constexpr (C::P_MN) {
-                            // row `key` of the operand: its 16-byte unit u at position u ^ (key & 7)
-                            if (r % 8 == 4)
-                                *reinterpret_cast<uint4*>(&s.p[buf][key * 128 + ((((r >> 3) ^ key) & 7) << 4)]) =
-                                    make_uint4(w2[r / 2 - 2], w2[r / 2 - 1], w2[r / 2], w2[r / 2 + 1]);
-                        } else {
+                    for (int h = 0; h < NR; h += HR) {
+                        if (NR > HR) scores(h, sr);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint16_t*>(&s.p[buf][p_at[(r + e) & 7] + 128 * (r + e)]) = (uint16_t)(w2[(r + e) / 2] >> (16 * (e & 1)));
+                        for (int r = 0; r < HR; r += 8) {
+                            uint32_t w2[4];
+#pragma unroll
+                            for (int e = 0; e < 8; e += 4) {
+                                const float4 m = *reinterpret_cast<const float4*>(&s.negm[grp][h + r + e]);
+                                const uint32_t* z = sr + r + e;
+                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), c2, make_float2(m.x, m.y));
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(z[2]), __uint_as_float(z[3])), c2, make_float2(m.z, m.w));
+                                const float2 ex = make_float2(ex2(x.x), ex2(x.y)), ey = make_float2(ex2(y.x), ex2(y.y));
+                                float2* sum = l + (h + r + e) / 2;
+                                sum[0] = __fadd2_rn(sum[0], ex);
+                                sum[1] = __fadd2_rn(sum[1], ey);
+                                w2[e / 2] = pack(ex.x, ex.y);
+                                w2[e / 2 + 1] = pack(ey.x, ey.y);
+                            }
+                            if constexpr (C::P_MN) {
+                                // row `key` of the operand: its 16-byte unit u at position u ^ (key & 7)
+                                *reinterpret_cast<uint4*>(&pbuf[key * 128 + (((((h + r) >> 3) ^ key) & 7) << 4)]) =
+                                    make_uint4(w2[0], w2[1], w2[2], w2[3]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint16_t*>(&pbuf[p_at[e] + 128 * (h + r + e)]) = (uint16_t)(w2[e / 2] >> (16 * (e & 1)));
+                            }
                         }
                     }
                 };
@@ -583,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                     bool there = true;
 #pragma unroll
                     for (int h = 0; h < KU; ++h) {
-                        const uint32_t n = 2 * KU * gt + KU + h;
+                        const uint32_t n = 2 * KU * g + KU + h;
                         const int sl = C::slot_of(n);
                         there = mbar_wait(&s.full[sl], (n / RING) & 1, ab) && there;
                         if (there && (j < lo || j > hi)) {
@@ -601,75 +664,99 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.p_full[buf]);
             }
-            if (gave_up) break;
             // ---------------- epilogue ----------------
             const bool has_o = t1 > t0;
-            if (has_o) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab)) && ok;
+            // whether each group had a tile (of two, group gt & 1 has the item's first)
+            const bool had0 = has_o && (NG == 1 || t1 - t0 > 1 || (gt & 1) == 0);
+            const bool had1 = NG == 2 && has_o && (t1 - t0 > 1 || (gt & 1) == 1);
+            const bool had = grp == 0 ? had0 : had1;
+            if (had) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(g - NG) & 1], ((g - NG) >> 1) & 1, ab)) && ok;
                 tc_fence_after();
             }
-            // sums of the rows over the keys
+            gt += max(t1 - t0, 0);
+            // the group's sums over its keys
 #pragma unroll
-            for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = r & 1 ? l[r / 2].y : l[r / 2].x;
-            if (!vote_and(ok)) break;
-            const int rows = w.rows, part = w.part, g = w.g, q0 = w.q0;
-            {
-                float x = 0.f;
-#pragma unroll 4
-                for (int y = 0; y < NR; ++y) x += grid[row_at + TPR * ((y + my_row) % NR)];
+            for (int h = 0; h < NR; h += GR) {
 #pragma unroll
-                for (int o = TPR / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (key % TPR == 0 && my_row < rows) {
-                    const float m = has_o ? s.mref[my_row] : -INFINITY;
-                    if (part >= 0) {
-                        a.part_ml[0][(long)part * NR + my_row] = make_float2(m, x);
-                        s.alpha[my_row] = 1.f;
-                    } else {
-                        const int i = (int)((unsigned)(r0 + my_row) / (unsigned)p.G), h = g * p.G + r0 + my_row - i * p.G;
-                        const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-                        const float mf = fmaxf(m, s2);
-                        const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
-                        const float lt = x * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
-                        s.alpha[my_row] = lt != 0.f ? wgt / lt : 0.f;
-                        if (a.lse) a.lse[(long)h * p.T_q + q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
-                    }
+                for (int r = 0; r < GR; ++r) grid[r * kKeyTile + key] = r & 1 ? l[(h + r) / 2].y : l[(h + r) / 2].x;
+                group_sync(grp);
+                const float x = across([](float a, float b) { return a + b; }, 0.f);
+                if (leads) {
+                    s.lsum[grp][h + my_row] = x;
+                    if (!had) s.mref[grp][h + my_row] = -INFINITY;
                 }
+                group_sync(grp);
             }
-            softmax_sync();
-            // O^T to rows: through shared memory (the P buffers), a warp to a row, 4 columns to a lane
+            if (vote_at<3, 128 * NG>(!ok)) break;
+            tc_fence_after();
+            const int rows = w.rows, part = w.part, gh = w.g, q0 = w.q0;
+            const int h0 = grp * GR;  // the group finishes the rows [h0, h0 + GR)
+            if (leads && h0 + my_row < rows) {
+                const int r = h0 + my_row;
+                const float ma = s.mref[0][r], mb = s.mref[NG - 1][r], m = fmaxf(ma, mb);
+                float fa = ma == -INFINITY ? 0.f : ex2(ma - m), fb = NG == 1 || mb == -INFINITY ? 0.f : ex2(mb - m);
+                const float sum = s.lsum[0][r] * fa + (NG == 2 ? s.lsum[NG - 1][r] * fb : 0.f);
+                if (part >= 0) {
+                    a.part_ml[0][(long)part * NR + r] = make_float2(m, sum);
+                } else {
+                    const int i = (int)((unsigned)(r0 + r) / G), h = gh * p.G + r0 + r - i * p.G;
+                    const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
+                    const float mf = fmaxf(m, s2);
+                    const float wgt = m == -INFINITY ? 0.f : ex2(m - mf);
+                    const float lt = sum * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+                    const float f = lt != 0.f ? wgt / lt : 0.f;
+                    fa *= f;
+                    fb *= f;
+                    if (a.lse) a.lse[(long)h * p.T_q + q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
+                }
+                s.alpha[0][r] = fa;
+                if (NG == 2) s.alpha[NG - 1][r] = fb;
+            }
+            group_sync(grp);
+            // O^T to rows: through shared memory (the P buffer), a warp to a row, 4 columns to a lane
 #pragma unroll
             for (int h = 0; h < C::OH; ++h) {
                 if (has_o) {
-                    uint32_t o[NR];
-                    tmem_ld_cols<NR>(tmem + lane_base + cO + NR * h, o);
+                    const uint32_t at = tmem + lane_base + cO + NR * h + h0;
+                    constexpr int OC = GR < 32 ? GR : 32;  // rows at a time
+#pragma unroll
+                    for (int y = 0; y < GR; y += OC) {
+                        // (an accumulator that no tile went into holds anything)
+                        uint32_t o[OC];
+                        tmem_ld_cols<OC>(at + y, o);
+#pragma unroll
+                        for (int r = 0; r < OC; ++r) o[r] = had0 ? __float_as_uint(__uint_as_float(o[r]) * s.alpha[0][h0 + y + r]) : 0u;
+                        if constexpr (NG == 2) {
+                            uint32_t o1[OC];
+                            tmem_ld_cols<OC>(at + C::OH * NR + y, o1);
+                            if (had1)
+#pragma unroll
+                                for (int r = 0; r < OC; ++r)
+                                    o[r] = __float_as_uint(fmaf(__uint_as_float(o1[r]), s.alpha[NG - 1][h0 + y + r], __uint_as_float(o[r])));
+                        }
+#pragma unroll
+                        for (int r = 0; r < OC; ++r) grid[(y + r) * kKeyTile + key] = __uint_as_float(o[r]);
+                    }
                     if (h == C::OH - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.o_free);
                     }
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) grid[r * kKeyTile + key] = __uint_as_float(o[r]);
                 }
-                softmax_sync();
+                group_sync(grp);
                 const bool mine = D == 64 ? lane < 16 : D == 192 && h == 1 ? lane >= 16 : true;
                 const int col = (D == 192 ? 64 : 128) * h + 4 * lane;
                 if (mine) {
 #pragma unroll 1
-                    for (int r = sub; r < rows; r += 4) {
-                        float4 x = *reinterpret_cast<const float4*>(&grid[r * kKeyTile + 4 * lane]);
-                        const float f = s.alpha[r];
-                        if (f == 0.f || !has_o) {
-                            x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        } else {
-                            x.x *= f;
-                            x.y *= f;
-                            x.z *= f;
-                            x.w *= f;
-                        }
+                    for (int rr = sub; rr < GR && h0 + rr < rows; rr += 4) {
+                        const int r = h0 + rr;
+                        float4 x = *reinterpret_cast<const float4*>(&grid[rr * kKeyTile + 4 * lane]);
+                        if (!has_o || (s.alpha[0][r] == 0.f && s.alpha[NG - 1][r] == 0.f)) x = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (part >= 0) {
                             *reinterpret_cast<float4*>(&a.part_o[0][((long)part * NR + r) * D + col]) = x;
                         } else {
-                            const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), hh = g * p.G + r0 + r - i * p.G;
+                            const int i = (int)((unsigned)(r0 + r) / G), hh = gh * p.G + r0 + r - i * p.G;
                             uint2 v;
                             v.x = f16 ? pack16<true>(x.x, x.y) : pack16<false>(x.x, x.y);
                             v.y = f16 ? pack16<true>(x.z, x.w) : pack16<false>(x.z, x.w);
@@ -677,7 +764,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
                         }
                     }
                 }
-                softmax_sync();
+                group_sync(grp);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
@@ -785,7 +872,14 @@ cudaError_t launch_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensor
     static_assert(smem <= kSmemMax, "the few-row kernel's shared memory");
     cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(paged_few_kernel<D, NR>, dim3(ctas), kThreadsFew, smem, st, a, tk, tv);
+    if (FewCfg<D, NR>::NG == 2) {
+        // the warp groups' setmaxnreg shares must fit in the registers the CTA is launched with (an
+        // increase beyond them would never be granted)
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, paged_few_kernel<D, NR>)) != cudaSuccess) return e;
+        if (fa.numRegs * FewCfg<D, NR>::THREADS < 128 * kFewRegLow + 256 * kFewRegHigh) return cudaErrorLaunchOutOfResources;
+    }
+    return launch_after(paged_few_kernel<D, NR>, dim3(ctas), FewCfg<D, NR>::THREADS, smem, st, a, tk, tv);
 }
 
 template <int D>
