@@ -317,29 +317,51 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         if (lane == 0) {
             const uint32_t idS = idesc_16(128, NR, false, false, f16);
             const uint32_t idO = idesc_16(128, NR, true, C::P_MN, f16);
-            uint32_t gt = 0, qi = 0;  // tiles whose S was issued, items with keys
-            uint32_t gp = 0;          // tiles whose P V was issued
+            uint32_t gt = 0, qi = 0;  // tiles of the CTA's stream before the item, items with keys
             bool ok = true;
-            auto wait_unit = [&](uint32_t n) { return mbar_wait(&s.full[C::slot_of(n)], (n / RING) & 1, ab); };
-            auto issue_s = [&](uint32_t q_addr) {
+            // the KU units from n on have arrived
+            auto arrived = [&](uint32_t n) {
+                bool y = true;
+#pragma unroll
+                for (int h = 0; h < KU; ++h) y = y && mbar_test(&s.full[C::slot_of(n + h)], ((n + h) / RING) & 1);
+                return y;
+            };
+            auto issue_s = [&](uint32_t g, uint32_t q_addr) {
+#pragma unroll
                 for (int h = 0; h < KU; ++h) {
-                    const uint32_t n = 2 * KU * gt + h;
-                    if (!wait_unit(n)) return false;
-                    tc_fence_after();
-                    const int sl = C::slot_of(n);
+                    const int sl = C::slot_of(2 * KU * g + h);
                     const uint64_t kd = sdesc_sw128(smem_u32(s.ring[sl]), 16, 1024);
                     const uint64_t qd = sdesc_sw128(q_addr + h * (C::UC / 64) * NR * 128, 16, 1024);
 #pragma unroll
                     for (int c = 0; c < C::UC / 64; ++c)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            mma_ss(tmem + cS + NR * (gt & 1), kd + c * (C::CHUNK >> 4) + 2 * x, qd + c * (NR * 8) + 2 * x, idS,
+                            mma_ss(tmem + cS + NR * (g & 1), kd + c * (C::CHUNK >> 4) + 2 * x, qd + c * (NR * 8) + 2 * x, idS,
                                    h > 0 || c > 0 || x > 0 ? 1u : 0u);
                     if (D != 64) tc_commit(&s.empty[sl]);
                 }
-                tc_commit(&s.s_full[gt & 1]);
-                ++gt;
-                return true;
+                tc_commit(&s.s_full[g & 1]);
+            };
+            auto issue_pv = [&](uint32_t g, bool start) {
+                const uint64_t pd = sdesc_sw128(smem_u32(s.p[g & 1]), 16, 1024);
+                auto product = [&](uint32_t o_col, uint32_t v_addr) {
+                    const uint64_t vd = sdesc_sw128(v_addr, C::CHUNK, 1024);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        mma_ss(tmem + o_col, vd + 128 * x, pd + (C::P_MN ? 128 * x : (x / 4) * (NR * 8) + 2 * (x % 4)), idO,
+                               !start || x > 0 ? 1u : 0u);
+                };
+                const uint32_t o_col = cO + (C::NG == 2 ? C::OH * NR * (g & 1) : 0);
+#pragma unroll
+                for (int h = 0; h < KU; ++h) {
+                    const int sl = C::slot_of(2 * KU * g + KU + h);
+                    product(o_col + NR * h, smem_u32(s.ring[sl]));
+                    // d = 192: columns 64 .. 191 again as the second accumulator
+                    if (D == 192) product(o_col + NR, smem_u32(s.ring[sl]) + C::CHUNK);
+                    tc_commit(&s.empty[sl]);
+                }
+                if (D == 64) tc_commit(&s.empty[C::slot_of(2 * g)]);
+                tc_commit(&s.pv_done[g & 1]);
             };
             for (int it = 0; ok; ++it) {
                 const int slot = it % kItems;
@@ -350,44 +372,70 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 if (nt <= 0) continue;
                 const int qb = (int)(qi % C::Q_BUFS);
                 if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
-                tc_fence_after();
                 const uint32_t q_addr = smem_u32(s.q[qb]);
-                if (!(ok = issue_s(q_addr))) break;
-                if (nt > 1 && !(ok = issue_s(q_addr))) break;
-                if (nt <= 2) tc_commit(&s.q_empty[qb]);  // the item's last S is issued
-                for (int t = 0; t < nt; ++t, ++gp) {
-                    const int pb = gp & 1;
-                    if (!(ok = mbar_wait(&s.p_full[pb], (gp >> 1) & 1, ab))) break;
-                    // the previous item's O has been read
-                    if (t == 0 && qi > 0 && !(ok = mbar_wait(&s.o_free, (qi - 1) & 1, ab))) break;
-                    const uint64_t pd = sdesc_sw128(smem_u32(s.p[pb]), 16, 1024);
-                    auto issue_pv = [&](uint32_t o_col, uint32_t v_addr) {
-                        const uint64_t vd = sdesc_sw128(v_addr, C::CHUNK, 1024);
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            mma_ss(tmem + o_col, vd + 128 * x, pd + (C::P_MN ? 128 * x : (x / 4) * (NR * 8) + 2 * (x % 4)), idO,
-                                   t >= C::NG || x > 0 ? 1u : 0u);
-                    };
-                    const uint32_t o_col = cO + (C::NG == 2 ? C::OH * NR * pb : 0);
-                    for (int h = 0; h < KU; ++h) {
-                        const uint32_t n = 2 * KU * gp + KU + h;
-                        if (!(ok = wait_unit(n))) break;
-                        tc_fence_after();
-                        const int sl = C::slot_of(n);
-                        issue_pv(o_col + NR * h, smem_u32(s.ring[sl]));
-                        // d = 192: columns 64 .. 191 again as the second accumulator
-                        if (D == 192) issue_pv(o_col + NR, smem_u32(s.ring[sl]) + C::CHUNK);
-                        tc_commit(&s.empty[sl]);
+                if constexpr (KU > 1 || D == 192) {
+                    // The ring holds two tiles at most, so either product's operands may come first:
+                    // whichever has them goes, P V before S (tile j's S goes into the buffer whose scores
+                    // were tile j - 2's, so it may run two tiles ahead).  Against the fixed order below:
+                    // 16000 keys, 2 heads, 64 rows, d = 256 189 / 218 us, d = 192 155 / 177.
+                    int js = 0, jv = 0;  // tiles whose S, whose P V was issued
+                    uint32_t idle = 0;
+                    unsigned long long since = 0;
+                    while (jv < nt) {
+                        const uint32_t gv = gt + jv, gs = gt + js;
+                        if (jv < js && mbar_test(&s.p_full[gv & 1], (gv >> 1) & 1) && arrived(2 * KU * gv + KU) &&
+                            (jv > 0 || qi == 0 || mbar_test(&s.o_free, (qi - 1) & 1))) {  // (the previous item's O has been read)
+                            tc_fence_after();
+                            issue_pv(gv, jv < C::NG);
+                            ++jv;
+                            idle = 0;
+                            since = 0;
+                        } else if (js < nt && js <= jv + 1 && arrived(2 * KU * gs)) {
+                            tc_fence_after();
+                            issue_s(gs, q_addr);
+                            if (++js == nt) tc_commit(&s.q_empty[qb]);
+                            idle = 0;
+                            since = 0;
+                        } else {
+                            // nothing yet; the bound on all of it (the clock every 32 rounds)
+                            if ((++idle & 31) == 0) {
+                                const unsigned long long now = globaltimer();
+                                if (since == 0) since = now;
+                                if (ab.raised() || now - since > ab.limit) {
+                                    ab.raise(kStatusTimeout);
+                                    ok = false;
+                                    break;
+                                }
+                            }
+                        }
                     }
-                    if (!ok) break;
-                    if (D == 64) tc_commit(&s.empty[C::slot_of(2 * gp)]);
-                    tc_commit(&s.pv_done[pb]);
-                    // S of the tile after next, into the buffer whose P has just been taken
-                    if (t + 2 < nt) {
-                        if (!(ok = issue_s(q_addr))) break;
-                        if (t + 3 == nt) tc_commit(&s.q_empty[qb]);
+                } else {
+                    // S two tiles ahead, in a fixed order (a deep ring: looking for what is ready costs more
+                    // than it finds, 400 against 393 us for 64 requests at d = 128)
+                    auto wait_units = [&](uint32_t n) {
+                        bool y = true;
+#pragma unroll
+                        for (int h = 0; h < KU; ++h) y = y && mbar_wait(&s.full[C::slot_of(n + h)], ((n + h) / RING) & 1, ab);
+                        tc_fence_after();
+                        return y;
+                    };
+                    for (int t = -2; t < nt; ++t) {
+                        if (t >= 0) {
+                            const uint32_t g = gt + t;
+                            if (!(ok = mbar_wait(&s.p_full[g & 1], (g >> 1) & 1, ab))) break;
+                            // the previous item's O has been read
+                            if (t == 0 && qi > 0 && !(ok = mbar_wait(&s.o_free, (qi - 1) & 1, ab))) break;
+                            if (!(ok = wait_units(2 * KU * g + KU))) break;
+                            issue_pv(g, t < C::NG);
+                        }
+                        if (t + 2 < nt) {
+                            if (!(ok = wait_units(2 * KU * (gt + t + 2)))) break;
+                            issue_s(gt + t + 2, q_addr);
+                            if (t + 3 == nt) tc_commit(&s.q_empty[qb]);
+                        }
                     }
                 }
+                gt += nt;
                 ++qi;
             }
             tc_commit(&s.drain);
