@@ -379,16 +379,15 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.ctas = sm_count();
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
     const long rows = longest * p.G;
-    // Every sequence known to have 64 rows at most (or d > 128, where the few-row kernel takes them
-    // all, tile by tile): the few-row kernel alone, its tile the rows.  Else it takes those of a
+    // Every sequence known to have 64 rows at most: the few-row kernel alone, its tile the rows.  Else it takes those of a
     // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
     // a decode step 38 us where one of 16 takes 22: 20 sequences of 5 heads a group, d = 64), and none
     // where a token has more than 64.
-    pl.many = rows > 64 && p.d <= 128;
+    pl.many = rows > 64;
     const long tile = pl.many ? p.G : rows;
     pl.few_rows = tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
     pl.few_max = !pl.many ? kAllFew : p.G <= 64 ? pl.few_rows : 0;
-    pl.many_rows = 2 * p.P * p.G;
+    pl.many_rows = (p.d <= 128 ? 2 : 1) * p.P * p.G;
     pl.off_pre = kStatusBytes;
     pl.off_line = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
     pl.off_cut = pl.off_line + align256(2 * sizeof(PagedLine));
@@ -453,7 +452,8 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     if (e == cudaSuccess && pl.few_max > 0) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     if (!pl.many) return cuda_status(timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); }));
-    // sequences of more rows: the tensor-core kernel, 2 P G rows to an item
+    // sequences of more rows: the tensor-core kernels, 2 P G rows to an item (P G at d = 192 / 256,
+    // whose key tiles, and copies, are 64 rows at most)
     FwdArgs f{};
     CUtensorMap tq;
     if (!encode_bhsd(&tq, q, p.d, p.h_q, p.T_q, 1, p.G, p.P, f16)) return FA_ERR_CUDA;
@@ -468,7 +468,10 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     f.pre = a.pre + p.B + 1;
     f.line = a.line + 1;
     f.num_pages = a.num_pages;
-    f.box = a.box;
+    f.box = p.d <= 128 || a.box <= 64 ? a.box : 64;
+    if (f.box != a.box && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion) ||
+                           !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion)))
+        return FA_ERR_CUDA;
     f.no_split = a.no_split;
     f.cut = a.cut + pl.ctas;
     f.o_part = a.part_o[1];

@@ -897,6 +897,7 @@ static cudaError_t launch_fwd_d(const FwdArgs& a, const CUtensorMap& tq, const C
 cudaError_t launch_fwd_paged(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              cudaStream_t st) {
     const bool f16 = a.p.dtype == FA_DTYPE_F16;
+    if (a.p.d >= 192) return launch_fwd256_paged(a, tq, tk, tv, st);
     switch (a.p.d) {
         case 64: return f16 ? launch_fwd_k<64, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<64, false, 128, true>(a, tq, tk, tv, st);
         case 128: return f16 ? launch_fwd_k<128, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<128, false, 128, true>(a, tq, tk, tv, st);

@@ -119,7 +119,7 @@ def test_ragged_chunks(d, h_q, h_kv, hint):
 
 @pytest.mark.parametrize("window,causal", [((100, -1), True), ((0, -1), True), ((200, 30), False), ((-1, 0), False), ((-1, -1), False),
                                            ((5, 300), False)])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
 def test_masks(window, causal, d):
     """Windows and no mask; rows that see nothing (fewer keys than queries) give 0 and -inf."""
     c = case([1, 40, 200, 3, 20], [500, 40, 777, 130, 6], h_q=4, h_kv=2, d=d, page=48)
@@ -144,6 +144,10 @@ def test_few_units_and_many_pieces():
     compare(case([1], [40000], h_q=4, h_kv=1, d=128, page=64), hint=1)
     compare(case([3], [9000], h_q=2, h_kv=1, d=256, page=128, sinks=True), hint=3)
     compare(case([1, 1], [60, 300], h_q=2, h_kv=2, d=64, page=16), hint=1)
+    # long chunks of one sequence: items of the tensor-core kernels cut many times
+    compare(case([100], [12000], h_q=4, h_kv=1, d=128, page=64, sinks=True))
+    compare(case([100], [7000], h_q=4, h_kv=1, d=256, page=256, sinks=True))
+    compare(case([130, 1], [5000, 900], h_q=3, h_kv=1, d=192, page=16, kind="f16"))
 
 
 def test_many_sequences():
@@ -167,11 +171,12 @@ def test_a_small_hint_costs_no_correctness():
     compare(case([1, 60, 1], [300, 600, 70], h_q=8, h_kv=2, d=128, page=16), hint=1)
 
 
-def test_what_lies_behind_the_used_keys_has_no_effect():
+@pytest.mark.parametrize("d", [128, 256])
+def test_what_lies_behind_the_used_keys_has_no_effect(d):
     """NaN and infinities in unused rows of a page, in unused pages and at keys before every row's
     window leave O and LSE as they are, bit for bit."""
     import torch
-    c = case([1, 30, 2], [77, 333, 150], h_q=8, h_kv=2, d=128, page=32)
+    c = case([1, 30, 2], [77, 333, 150], h_q=8, h_kv=2, d=d, page=32)
     for window in ((-1, -1), (40, -1)):
         o, z = compare(c, window=window)
         seen = np.zeros((c["pool"], c["page"]), bool)
