@@ -94,8 +94,9 @@ struct ItemInfo {
     int q0, k0, tma_b;  // first query / key row of the sequence, outer TMA coordinate
     int u0, u1;         // union key-tile range of the two tiles (u1 <= u0: none)
     int s0[2], t0[2], t1[2];  // first query position and key-tile range of each tile
-    // PG only: used keys, keys that any row of the item may see, partial slot (-1: whole item)
-    int nk, lo, hi, part;
+    // PG only: used keys, keys that any row of the item may see, partial slot (-1: whole item),
+    // key tiles of the CTA's items before this one
+    int nk, lo, hi, part, before;
 };
 constexpr int kItemSlots = 3;
 // arrivals that free an item slot: producer, MMA issuer and the eight softmax warps
@@ -120,14 +121,25 @@ struct __align__(1024) FwdSmem {
     int abort_flag;
 };
 
+// A warp's own copy of a value that all its lanes hold.  The paged scheduler's walk needs all
+// registers of its warp group, and what other roles share with it would be spilled for it and
+// loaded again in their loops; what comes out of a shuffle is a value of its own.
+__device__ __forceinline__ int own_copy(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t own_copy(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+template <class T>
+__device__ __forceinline__ T& own_shared(T& shared) {
+    return *reinterpret_cast<T*>(__cvta_shared_to_generic(own_copy(smem_u32(&shared))));
+}
+
 template <int D, bool F16, int KT, bool PG>
 __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                const __grid_constant__ CUtensorMap tmv) {
     using C = FwdCfg<D, KT>;
     extern __shared__ uint8_t smem_raw[];
-    FwdSmem<D, KT>& s =
+    FwdSmem<D, KT>& smem =
         *reinterpret_cast<FwdSmem<D, KT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    FwdSmem<D, KT>& s = smem;
     const Problem& p = a.p;
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
@@ -182,7 +194,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem_base = s.tmem_base, tmem = tmem_base;
     // registers: 384 x 168 at launch (one CTA per SM; 384 x 80 with two); the producer/MMA
     // group hands part of its share to the two softmax groups (128 x 56 + 256 x 224 = 64512;
     // 128 x 48 + 256 x 96 = 30720).  The change is made at the top of each warp group's
@@ -191,6 +203,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(C::REG_LOW) : "memory");
     if (PG && warp == 0) {
         // ================= TMA producer, paged cache (the whole warp) =================
+        FwdSmem<D, KT>& s = own_shared(smem);
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
@@ -327,6 +340,8 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // ================= MMA issuer =================
         // Everything the issue path touches lives in registers (no per-tile arrays indexed
         // at run time), so consecutive MMAs go out back to back.
+        FwdSmem<D, KT>& s = PG ? own_shared(smem) : smem;
+        const uint32_t tmem = PG ? own_copy(tmem_base) : tmem_base;
         if (lane == 0) {
             Tracer tr;
             tr.init(a.trace, 1);
@@ -472,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // live one to the other roles through the item ring: lane 0 writes the item, every
         // lane the allowed key interval of 8 of its 256 rows.  In token mode the key-tile ranges
         // come from those intervals (their hull), since a tile's rows may span sequences.
-        int n = 0;
+        int n = 0, before = 0;
         bool ok = true;
         // PG: the walk over the CTA's stretch of the line of units
         PagedWalk walk(PG ? *a.line : PagedLine{}, blockIdx.x);
@@ -572,6 +587,8 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
                     it.lo = w.band.lo(w.ti[0].s0);
                     it.hi = w.band.hi(min(w.ti[0].s0 + 2 * p.P, w.sv.nq) - 1);
                     it.part = part;
+                    it.before = before;
+                    before += max(w.u1 - w.u0, 0);
                 }
             }
             __syncwarp();
@@ -594,6 +611,9 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" :: "n"(C::REG_HIGH) : "memory");
         // ================= softmax: one thread per row =================
+        FwdSmem<D, KT>& s = PG ? own_shared(smem) : smem;
+        const int warp = PG ? own_copy(tid >> 5) : tid >> 5;
+        const uint32_t tmem = PG ? own_copy(tmem_base) : tmem_base;
         const int k = (warp - 4) >> 2;           // query tile
         const int r = ((warp & 3) << 5) | lane;  // row = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) << 5) << 16;
@@ -601,7 +621,6 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         const uint32_t tO = tmem + lane_base + C::o_col(k);
         const float c = p.scale_log2;
         uint32_t scount = 0, ocount = 0;  // S tiles and O tiles received (carried across items)
-        int gt0 = 0;                      // PG: key tiles of the items before this one
         bool ok = true;
         Tracer tr;
         tr.init((warp & 3) == 0 ? a.trace : nullptr, 2 + k);
@@ -711,13 +730,14 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             else tmem_st_32x32b_x32(tS, sr);
             l += sum;
             if (KT == 64 && __any_sync(0xffffffffu, rescale)) rescale_o();
-            if constexpr (PG) {
-                // value rows outside every row's band: cleared by tile 0's group where it takes part (the
-                // P V of tile 1 is issued behind that of tile 0), else by tile 1's
+            if (PG && !poly_ok) {
+                // value rows outside every row's band (in a tile with masked entries, then): cleared by
+                // tile 0's group where it takes part (the P V of tile 1 is issued behind that of tile 0),
+                // else by tile 1's
                 const ItemInfo& itm = s.item[slot];
                 const int lo = itm.lo, hi = itm.hi;
                 if ((j0 < lo || j0 + KT - 1 > hi) && (k == 0 || j < itm.t0[0] || j >= itm.t1[0])) {
-                    const int vt = gt0 + j - itm.u0, st = vt % C::STAGES;
+                    const int vt = itm.before + j - itm.u0, st = vt % C::STAGES;
                     const bool there = mbar_wait(&s.v_full[st], (vt / C::STAGES) & 1, ab);
                     if (there && (j0 + r < lo || j0 + r > hi)) {
 #pragma unroll
@@ -753,7 +773,6 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             tc_fence_after();
         }
         const int part = PG ? itm.part : -1;
-        if constexpr (PG) gt0 += max(itm.u1 - itm.u0, 0);
         const bool split_mode = PG ? part >= 0 : a.n_splits > 1 || itm.tail;
         // 32-byte stores where the base allows (the rows, 128 or more bytes, keep the alignment)
         const bool o_al32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
