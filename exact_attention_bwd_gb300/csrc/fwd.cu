@@ -121,16 +121,6 @@ struct __align__(1024) FwdSmem {
     int abort_flag;
 };
 
-// A warp's own copy of a value that all its lanes hold.  The paged scheduler's walk needs all
-// registers of its warp group, and what other roles share with it would be spilled for it and
-// loaded again in their loops; what comes out of a shuffle is a value of its own.
-__device__ __forceinline__ int own_copy(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __forceinline__ uint32_t own_copy(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-template <class T>
-__device__ __forceinline__ T& own_shared(T& shared) {
-    return *reinterpret_cast<T*>(__cvta_shared_to_generic(own_copy(smem_u32(&shared))));
-}
-
 template <int D, bool F16, int KT, bool PG>
 __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,

@@ -30,10 +30,14 @@ namespace {
 // schedule: the line of units
 // ------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
+// row tiles that a thread counts by itself; longer sequences are counted by all threads together (one
+// of 262144 tokens, four heads a group, by one thread: 273 us)
+constexpr int kPrepAlone = 32;
 
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArgs a) {
     __shared__ long long warp_sum[2][kPrepWarps];
-    __shared__ int bad_any;
+    __shared__ unsigned long long units_of[kPrepThreads];
+    __shared__ int bad_any, n_long, long_ones[kPrepThreads];
     const Problem& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_next_kernel();
@@ -44,6 +48,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
     for (int base = 0; base < p.B; base += kPrepThreads) {
         const int b = base + tid;
         long long w0 = 0, w1 = 0;
+        bool is_long = false, few = false;
+        if (tid == 0) n_long = 0;
+        __syncthreads();
         if (b < p.B) {
             if (a.validate) {
                 bad = bad || (b == 0 && p.cu_q[0] != 0) || p.cu_q[b + 1] < p.cu_q[b] || p.cu_q[b + 1] > p.T_q ||
@@ -52,17 +59,42 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
             const PagedSeq s = paged_seq(p, b);
             const long rows = (long)s.nq * p.G;
             if (rows > 0) {
-                const bool few = rows <= a.few_max;
+                few = rows <= a.few_max;
                 const int step = few ? a.few_rows : a.many_rows;
+                is_long = rows > (long)kPrepAlone * step;
                 long long w = 0;
+                if (is_long) {
+                    units_of[tid] = 0;
+                    long_ones[atomicAdd(&n_long, 1)] = b;
+                } else {
 #pragma unroll 1
-                for (int r = 0; r < (int)rows; r += step) {
-                    int t0, t1;
-                    w += paged_tiles(p, s, r, step, few ? kFewLead : kManyLead, t0, t1);
+                    for (int r = 0; r < (int)rows; r += step) {
+                        int t0, t1;
+                        w += paged_tiles(p, s, r, step, t0, t1);
+                    }
                 }
                 (few ? w0 : w1) = w;
             }
         }
+        __syncthreads();
+#pragma unroll 1
+        for (int e = 0; e < n_long; ++e) {
+            const int bl = long_ones[e];
+            const PagedSeq s = paged_seq(p, bl);
+            const long rows = (long)s.nq * p.G;
+            const int step = rows <= a.few_max ? a.few_rows : a.many_rows;
+            long long w = 0;
+#pragma unroll 1
+            for (long r = (long)tid * step; r < rows; r += (long)kPrepThreads * step) {
+                int t0, t1;
+                w += paged_tiles(p, s, (int)r, step, t0, t1);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (lane == 0) atomicAdd(&units_of[bl - base], (unsigned long long)w);
+        }
+        __syncthreads();
+        if (is_long) (few ? w0 : w1) = (long long)units_of[tid];
         long long s0 = w0, s1 = w1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -99,9 +131,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         a.pre[0] = 0;
         a.pre[p.B + 1] = 0;
         *a.status = bad_any ? kStatusDeviceCheck : kStatusOk;
-        a.line[0] = paged_line(run0 * p.h_kv, kFewLead, a.few_ctas);
+        a.line[0] = paged_line(run0 * p.h_kv, a.few_ctas);
     } else if (tid == 32) {
-        a.line[1] = paged_line(run1 * p.h_kv, kManyLead, a.many_ctas);
+        a.line[1] = paged_line(run1 * p.h_kv, a.many_ctas);
     }
 }
 
@@ -214,7 +246,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     using C = FewCfg<D, NR>;
     constexpr int RING = C::RING, KU = C::KU;
     extern __shared__ uint8_t smem_raw[];
-    FewSmem<D, NR>& s = *reinterpret_cast<FewSmem<D, NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    FewSmem<D, NR>& smem = *reinterpret_cast<FewSmem<D, NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    FewSmem<D, NR>& s = smem;
     const Problem& p = a.p;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -256,7 +289,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem_base = s.tmem_base, tmem = tmem_base;
     // TMEM columns: the two S buffers (tile g's is g & 1), group x's O^T at cO + OH NR x
     constexpr uint32_t cS = 0, cO = 2 * NR;
 
@@ -264,6 +297,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     if constexpr (C::NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFewRegLow) : "memory");
     if (warp == 0) {
         // ================= TMA producer =================
+        FewSmem<D, NR>& s = C::NG == 2 ? own_shared(smem) : smem;
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
         const int boxes = kKeyTile / a.box;
@@ -314,6 +348,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
             mbar_wait_quiet(&s.full[C::slot_of(n - back)], ((n - back) / RING) & 1);
     } else if (warp == 1) {
         // ================= MMA issuer =================
+        FewSmem<D, NR>& s = C::NG == 2 ? own_shared(smem) : smem;
+        const uint32_t tmem = C::NG == 2 ? own_copy(tmem_base) : tmem_base;
         if (lane == 0) {
             const uint32_t idS = idesc_16(128, NR, false, false, f16);
             const uint32_t idO = idesc_16(128, NR, true, C::P_MN, f16);
@@ -520,6 +556,9 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     } else {
         if constexpr (C::NG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kFewRegHigh) : "memory");
         // ================= softmax: one thread per key =================
+        FewSmem<D, NR>& s = C::NG == 2 ? own_shared(smem) : smem;
+        const uint32_t tmem = C::NG == 2 ? own_copy(tmem_base) : tmem_base;
+        const int warp = C::NG == 2 ? own_copy(tid >> 5) : tid >> 5;
         constexpr int HR = C::HR, NG = C::NG;
         const int grp = NG == 2 ? (warp - 4) >> 2 : 0, key = tid & 127, sub = warp & 3;
         const uint32_t lane_base = (uint32_t)(sub * 32) << 16;

@@ -7,8 +7,9 @@
 // written).  All units form one line, sequence by sequence, head by head, row tile by row tile,
 // and each of n CTAs takes an equal stretch of it, so the CTAs finish together whatever the
 // lengths are; neighbours on the line, which run at the same time, share a head's keys in L2.
-// A stretch's end among an item's tiles cuts it (one among its lead stands for the item's start): the pieces leave fp32 partials, at most two per CTA, so the workspace
-// does not depend on the lengths, and the combine merges them in the order of the keys.
+// A stretch's end among an item's tiles cuts it (one among its lead stands for the item's start):
+// the pieces leave fp32 partials, at most two per CTA, so the workspace does not depend on the
+// lengths, and the combine merges them in the order of the keys.
 #pragma once
 #include "common.cuh"
 
@@ -30,30 +31,25 @@ __device__ __forceinline__ PagedSeq paged_seq(const Problem& p, int b) {
     return s;
 }
 
-// The lead of an item in tiles, by what levels the CTAs' finishing times best
-#ifndef FA_FEW_LEAD
-#define FA_FEW_LEAD 2
-#endif
-#ifndef FA_MANY_LEAD
-#define FA_MANY_LEAD 2
-#endif
-constexpr int kFewLead = FA_FEW_LEAD, kManyLead = FA_MANY_LEAD;
+// The lead of an item in tiles: flat from 1 to 4 for both kernels (8 chunks of 1024 tokens 707 / 703 /
+// 705 / 707 us, a mixed batch at d = 64 65 / 65 / 64 / 66).
+constexpr int kLead = 2;
 
 // Key tiles [t0, t1) of the rows [r0, r0 + rows) (numbered position * G + head of the group; r0 is
 // one of them, nq * G fits 32 bits), and the units of the item.
-__device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, int r0, int rows, int lead, int& t0, int& t1) {
+__device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, int r0, int rows, int& t0, int& t1) {
     const Band bd{s.nk - s.nq, p.left, p.right, s.nk};
     const unsigned G = (unsigned)p.G;
     const int i0 = (int)((unsigned)r0 / G), i1 = min(s.nq - 1, (int)((unsigned)(r0 + rows - 1) / G));
     kv_tile_range(bd, i0, i1, kKeyTile, t0, t1);
-    return lead + max(t1 - t0, 1);
+    return kLead + max(t1 - t0, 1);
 }
 
 // The line of one kernel's units as the preparation leaves it: n CTAs take part, CTA c's stretch
 // is [start(c), start(c + 1)), the first `more` stretches one unit longer than `each`.
 struct PagedLine {
     long long units;
-    int lead, n, more;
+    int n, more;
     long long each;
     __device__ __forceinline__ long long start(int c) const { return c * each + min(c, more); }
     // the CTA that holds unit u
@@ -63,11 +59,10 @@ struct PagedLine {
     }
 };
 // Each CTA has more units than a lead.
-__device__ __forceinline__ PagedLine paged_line(long long units, int lead, int n_ctas) {
+__device__ __forceinline__ PagedLine paged_line(long long units, int n_ctas) {
     PagedLine x;
     x.units = units;
-    x.lead = lead;
-    x.n = (int)min((long long)n_ctas, (units + lead) / (lead + 1));
+    x.n = (int)min((long long)n_ctas, (units + kLead) / (kLead + 1));
     x.each = x.n > 0 ? units / x.n : 0;
     x.more = x.n > 0 ? (int)(units % x.n) : 0;
     return x;
@@ -90,22 +85,28 @@ __device__ __forceinline__ int find_sequence(const long long* pre, int B, int h_
 }
 
 // Unit `rem` of a sequence with `per_head` units to a head: its item (head, row tile), the unit of
-// the item and the item's units and key tiles.  Warp-wide: a lane to a row tile, 32 at a time.
+// the item and the item's units and key tiles.  Warp-wide: a lane to a row tile, 32 at a time, from
+// where the last look at the same head ended (units only move forward).
 struct PagedUnit {
     int rt, g, k, cost, t0, t1;
 };
-__device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, int lead, long long rem,
-                                                long long per_head) {
+struct PagedLook {
+    int g = -1, base = 0;  // head, first of the 32 row tiles
+    long long units = 0;   // of the head ahead of them
+};
+__device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, long long rem, long long per_head,
+                                                PagedLook& look) {
     const int lane = threadIdx.x & 31;
     const int tiles = (s.nq * p.G + rows - 1) / rows;
     PagedUnit x;
     x.g = rem < per_head ? 0 : (int)(rem / per_head);
-    rem -= x.g * per_head;
-    int base = 0, src = 0, sum = 0, cost = 0, t0 = 0, t1 = 0;
+    if (look.g != x.g) look = PagedLook{x.g, 0, 0};
+    rem -= x.g * per_head + look.units;
+    int base = look.base, src = 0, sum = 0, cost = 0, t0 = 0, t1 = 0;
 #pragma unroll 1
     for (;; base += 32) {
         t0 = t1 = cost = 0;
-        if (base + lane < tiles) cost = paged_tiles(p, s, (base + lane) * rows, rows, lead, t0, t1);
+        if (base + lane < tiles) cost = paged_tiles(p, s, (base + lane) * rows, rows, t0, t1);
         sum = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -115,8 +116,11 @@ __device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq
         const unsigned past = __ballot_sync(0xffffffffu, rem < sum);
         src = past ? __ffs(past) - 1 : 31;
         if (past || base + 32 >= tiles) break;  // (no lane is past only for a unit outside the sequence)
-        rem -= __shfl_sync(0xffffffffu, sum, 31);
+        const int skipped = __shfl_sync(0xffffffffu, sum, 31);
+        rem -= skipped;
+        look.units += skipped;
     }
+    look.base = base;
     x.rt = base + src;
     x.cost = __shfl_sync(0xffffffffu, cost, src);
     x.t0 = __shfl_sync(0xffffffffu, t0, src);
@@ -135,11 +139,11 @@ struct PagedCut {
 // The walk of one warp over its CTA's stretch, piece by piece.
 struct PagedWalk {
     long long u, end;          // next unit, end of the stretch
-    int lead;
     long long before = 0, per_head = 0, after = 0;  // the sequence's: units ahead of it, of a head, up to its end
     int b = 0;
     PagedSeq seq{};
-    __device__ __forceinline__ PagedWalk(const PagedLine& line, int cta) : u(line.start(cta)), end(line.start(cta + 1)), lead(line.lead) {}
+    PagedLook look;
+    __device__ __forceinline__ PagedWalk(const PagedLine& line, int cta) : u(line.start(cta)), end(line.start(cta + 1)) {}
     PagedUnit x;               // the piece's item
     int t0 = 0, t1 = 0;        // its key tiles
     bool from_start = true, to_end = true;  // whether it is the item's start and end
@@ -153,18 +157,19 @@ struct PagedWalk {
                 per_head = pre[b + 1] - pre[b];
                 after = before + per_head * p.h_kv;
                 seq = paged_seq(p, b);
+                look.g = -1;
             }
-            x = paged_unit(p, seq, rows, lead, u - before, per_head);
-            if (no_split && x.k > lead) {  // the item is the CTA's that holds its start
+            x = paged_unit(p, seq, rows, u - before, per_head, look);
+            if (no_split && x.k > kLead) {  // the item is the CTA's that holds its start
                 u += x.cost - x.k;
                 continue;
             }
             const long long start = u - x.k;
-            if (end - start <= lead) break;  // the item's start counts for the next CTA
-            from_start = x.k <= lead;
+            if (end - start <= kLead) break;  // the item's start counts for the next CTA
+            from_start = x.k <= kLead;
             to_end = no_split || end - start >= x.cost;
-            t0 = x.t0 + (from_start ? 0 : x.k - lead);
-            t1 = to_end ? x.t1 : x.t0 + (int)(end - start) - lead;
+            t0 = x.t0 + (from_start ? 0 : x.k - kLead);
+            t1 = to_end ? x.t1 : x.t0 + (int)(end - start) - kLead;
             u = to_end ? start + x.cost : end;
             if (from_start && !to_end) {
                 const int r0 = x.rt * rows;
@@ -175,5 +180,16 @@ struct PagedWalk {
         return false;
     }
 };
+
+// A warp's own copy of a value that all its lanes hold.  Where the warp groups split the registers
+// between them, the walk needs more than its group has, and what other roles share with it would be
+// spilled for it and loaded again in their loops; what comes out of a shuffle is a value of its own.
+// (8 chunks of 1024 tokens 776 / 706 us; decode of 32 x 16000 keys at d = 64 and 40 rows 151 / 140.)
+__device__ __forceinline__ int own_copy(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t own_copy(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+template <class T>
+__device__ __forceinline__ T& own_shared(T& shared) {
+    return *reinterpret_cast<T*>(__cvta_shared_to_generic(own_copy(smem_u32(&shared))));
+}
 
 }  // namespace fa
