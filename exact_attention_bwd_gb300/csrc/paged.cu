@@ -484,6 +484,12 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         int it = 0;
         uint32_t qi = 0;
         bool ok = true;
+        // Q rows: a lane takes a 16-byte unit of every ROWS-th row; from one to the next the head moves by
+        // step_h in the group, with the tokens in between and one more where it wraps
+        constexpr int ROWS = D == 192 ? 1 : 256 / D, LANES = ROWS * (D / 8);
+        const int row = D == 192 ? 0 : lane / (D / 8), col = lane - row * (D / 8);
+        const unsigned step_h = (unsigned)ROWS % (unsigned)p.G;
+        const long step = ((long)(ROWS / p.G) * p.h_q + step_h) * D;
         while (ok && walk.next(p, a.pre, line, cta, NR, a.no_split)) {
             const PagedUnit& x = walk.x;
             const int t0 = walk.t0, t1 = walk.t1;
@@ -516,27 +522,25 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
             if (qi >= (uint32_t)C::Q_BUFS &&
                 !(ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty[qb], ((qi / C::Q_BUFS) - 1) & 1, ab))))
                 break;
-            constexpr int UNITS = NR * D / 8;  // 16-byte units
-            constexpr int BATCH = 4;
-            static_assert(UNITS % (32 * BATCH) == 0, "whole batches of the warp");
-#pragma unroll 1
-            for (int y = 0; y < UNITS; y += 32 * BATCH) {
-                uint4 v[BATCH];
-#pragma unroll
-                for (int z = 0; z < BATCH; ++z) {
-                    const int e = y + 32 * z + lane, r = e / (D / 8), col = e % (D / 8);
-                    v[z] = make_uint4(0, 0, 0, 0);
-                    if (r < rows) {
-                        const int i = (int)((unsigned)(r0 + r) / (unsigned)p.G), h = x.g * p.G + (r0 + r) - i * p.G;
-                        v[z] = *reinterpret_cast<const uint4*>(a.q + (((long)sq.q0 + i) * p.h_q + h) * D + 8 * col);
+            // (asynchronous copies, all of them in flight at once: through registers, four at a time,
+            // the 64 rows of d = 256 took 16 round trips, and verifying 5 tokens of 16 / 2 heads in 32
+            // sequences 73 us against 62)
+            if (lane < LANES) {
+                unsigned i = (unsigned)(r0 + row) / (unsigned)p.G, h = (unsigned)(r0 + row) - i * p.G;
+                const uint16_t* src = a.q + (((long)sq.q0 + i) * p.h_q + x.g * p.G + h) * D + 8 * col;
+                uint8_t* to = &s.q[qb][(col >> 3) * NR * 128];
+#pragma unroll 4
+                for (int r = row; r < NR; r += ROWS) {
+                    copy16_async(to + r * 128 + (((col ^ r) & 7) << 4), r < rows ? src : a.q, r < rows);
+                    h += step_h;
+                    src += step;
+                    if (h >= (unsigned)p.G) {
+                        h -= p.G;
+                        src += (long)(p.h_q - p.G) * D;
                     }
                 }
-#pragma unroll
-                for (int z = 0; z < BATCH; ++z) {
-                    const int e = y + 32 * z + lane, r = e / (D / 8), col = e % (D / 8);
-                    *reinterpret_cast<uint4*>(&s.q[qb][(col >> 3) * NR * 128 + r * 128 + (((col ^ r) & 7) << 4)]) = v[z];
-                }
             }
+            copies_wait();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.q_full[qb]);

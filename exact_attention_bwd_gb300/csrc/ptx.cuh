@@ -141,6 +141,15 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) 
 }
 
 // ------------------------------------------------------------------------------------------
+// 16 bytes from global to shared memory without a register (zeros unless `there`), and the wait for
+// all that this thread has started
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy16_async(void* to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------------
 // programmatic dependent launch: the next kernel of the stream may start its CTAs; wait until
 // the kernel before has finished and its writes are visible (at once without the launch attribute)
 // ------------------------------------------------------------------------------------------
