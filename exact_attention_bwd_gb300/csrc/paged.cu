@@ -874,30 +874,19 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
 // ------------------------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-// blockIdx.x: the CTA that holds the start of a cut item; a warp merges kMergeRows of its rows from
-// the partials of that CTA (its slot 1) and the next ones (their slot 0), in the order of the
-// keys.  The weights are those of an online softmax: 2^(m_k - max).  blockIdx.y numbers the row
-// groups of the few-row kernel's items, then those of the other's.
-constexpr int kMergeRows = 2;
-constexpr int kMergeRowsCta = kMergeWarps * kMergeRows;
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, int few_groups) {
+// A warp merges R rows of a cut item, from r1 on, from the partials of the CTA c that holds its start
+// (slot 1) and of the next ones (their slot 0), in the order of the keys.  The weights are those of
+// an online softmax: 2^(m_k - max).
+template <int D, bool F16, int R>
+__device__ __forceinline__ void merge_rows(const PagedArgs& a, const PagedCut& cut, int which, int c, int r1) {
     constexpr int VW = D / 32;  // columns of a lane, consecutive
     const Problem& p = a.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
-    const int which = (int)blockIdx.y < few_groups ? 0 : 1;
-    const int held = which ? a.many_rows : a.few_rows;
-    const int r1 = (((int)blockIdx.y - (which ? few_groups : 0)) * kMergeWarps + warp) * kMergeRows;
-    wait_previous_kernel();
-    if (c >= a.line[which].n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
-    const PagedCut cut = a.cut[which * gridDim.x + c];
-    if (r1 >= cut.rows) return;
+    const int lane = threadIdx.x & 31, held = which ? a.many_rows : a.few_rows;
     // the partials' row of piece y, row r
     auto at = [&](int y, int r) { return (long)(2 * (c + y) + (y == 0 ? 1 : 0)) * held + r; };
-    float m[kMergeRows], l[kMergeRows], acc[kMergeRows][VW];
+    float m[R], l[R], acc[R][VW];
 #pragma unroll
-    for (int z = 0; z < kMergeRows; ++z) {
+    for (int z = 0; z < R; ++z) {
         m[z] = -INFINITY;
         l[z] = 0.f;
 #pragma unroll
@@ -905,9 +894,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     }
     for (int y0 = 0; y0 < cut.pieces; y0 += 32) {
         const int y = y0 + lane, cnt = min(32, cut.pieces - y0);
-        float wy[kMergeRows];
+        float wy[R];
 #pragma unroll
-        for (int z = 0; z < kMergeRows; ++z) {
+        for (int z = 0; z < R; ++z) {
             const int r = min(r1 + z, cut.rows - 1);  // a row past the end is the last one again, not stored
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < cnt) ml = a.part_ml[which][at(y, r)];
@@ -928,7 +917,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
 #pragma unroll 2
         for (int k = 0; k < cnt; ++k) {
 #pragma unroll
-            for (int z = 0; z < kMergeRows; ++z) {
+            for (int z = 0; z < R; ++z) {
                 const float wk = __shfl_sync(0xffffffffu, wy[z], k);
                 const float* src = a.part_o[which] + at(y0 + k, min(r1 + z, cut.rows - 1)) * D + VW * lane;
 #pragma unroll
@@ -941,7 +930,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
         }
     }
 #pragma unroll
-    for (int z = 0; z < kMergeRows; ++z) {
+    for (int z = 0; z < R; ++z) {
         const int r = r1 + z;
         if (r >= cut.rows) break;
         const int i = (int)((unsigned)(cut.r0 + r) / (unsigned)p.G), h = cut.g * p.G + (cut.r0 + r) - i * p.G;
@@ -954,6 +943,27 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
         uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (((long)cut.q0 + i) * p.h_q + h) * D + VW * lane);
 #pragma unroll
         for (int e = 0; e < VW; e += 2) out[e / 2] = f == 0.f ? 0u : pack16<F16>(acc[z][e] * f, acc[z][e + 1] * f);
+    }
+}
+
+// blockIdx.x: the CTA that holds the start of a cut item.  blockIdx.y numbers the row groups of the
+// few-row kernel's items, a row to a warp, then those of the other's, two to a warp: there are many
+// of them.  (A decode step of 4 sequences one row 16.5 us, two 17.7; verifying 5 tokens in 32
+// sequences 60.7 / 62.0; but a mixed batch with chunks of 387 tokens 69.5 / 64.9.)
+constexpr int kFewMergeRows = 1, kManyMergeRows = 2;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs a, int few_groups) {
+    const int warp = threadIdx.x >> 5, c = blockIdx.x, which = (int)blockIdx.y < few_groups ? 0 : 1;
+    wait_previous_kernel();
+    // (read ahead of the checks: without a stretch, or in a failed call, it holds anything)
+    const PagedCut cut = a.cut[which * gridDim.x + c];
+    if (c >= a.line[which].n || *reinterpret_cast<volatile const int*>(a.status) != 0) return;
+    const int unit = ((int)blockIdx.y - (which ? few_groups : 0)) * kMergeWarps + warp;
+    if (which) {
+        if (unit * kManyMergeRows < cut.rows) merge_rows<D, F16, kManyMergeRows>(a, cut, 1, c, unit * kManyMergeRows);
+    } else {
+        if (unit * kFewMergeRows < cut.rows) merge_rows<D, F16, kFewMergeRows>(a, cut, 0, c, unit * kFewMergeRows);
     }
 }
 
@@ -1008,8 +1018,8 @@ cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CU
 
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st) {
     if (a.few_ctas < 2 || a.no_split) return cudaSuccess;
-    const int few_groups = a.few_max > 0 ? cdiv(a.few_rows, kMergeRowsCta) : 0;
-    const dim3 grid(a.few_ctas, few_groups + (many ? cdiv(a.many_rows, kMergeRowsCta) : 0));
+    const int few_groups = a.few_max > 0 ? cdiv(a.few_rows, kMergeWarps * kFewMergeRows) : 0;
+    const dim3 grid(a.few_ctas, few_groups + (many ? cdiv(a.many_rows, kMergeWarps * kManyMergeRows) : 0));
     switch (a.p.d) {
         case 64: return launch_merge_d<64>(a, grid, few_groups, st);
         case 128: return launch_merge_d<128>(a, grid, few_groups, st);
