@@ -176,7 +176,7 @@ struct RopeArgs {
     uint16_t *dq, *dk;
     float *dwq, *dwk, *dw_part;
     int* status;
-    int unit_rows, warps;      // rows a warp takes at a time, warps that walk over them
+    int unit_rows, kv_rows, warps;  // rows a warp takes at a time (of k and v together), warps that walk over them
 };
 
 struct PagePlanArgs {

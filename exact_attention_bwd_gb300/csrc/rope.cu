@@ -12,7 +12,7 @@
 // Both are streams: 2 (forward) or 3 (gradient) passes over the rows, nothing to reuse but
 // the angles and the weights, so HBM bounds them and what counts is the bytes in flight.  One
 // CTA per SM of 12 warps, each on its own: a warp walks over units (some rows of one token, of q,
-// k or v) and keeps the next units' rows and angles on their way into its own shared-memory
+// or of k and v) and keeps the next units' rows and angles on their way into its own shared-memory
 // buffers by bulk copies, so that the loads do not wait for its arithmetic nor take registers.
 // (Loads into registers, 4 row batches a warp at 16 warps per SM, reached 58 % of the copy rate.)
 // A row is held by d / 16 lanes (16 at d = 192, four of them idle): a lane has two 8-value units
@@ -26,8 +26,8 @@ namespace fa {
 namespace {
 
 // 12 warps of two 8 KB buffers fill the shared memory.  Measured, forward / gradient of 16384
-// tokens of 32 + 8 heads of 128 and append of 8192 tokens of 16 + 2 heads of 256, us: 54.7 / 85.1 /
-// 32.4; 8 warps of three 64.0 / 103.0 / 39.6; 12 of three 4 KB ones 60.5 / 99.5 / 37.0; 16 of two
+// tokens of 32 + 8 heads of 128 and append of 8192 tokens of 16 + 2 heads of 256 (with v in units of
+// its own), us: 54.7 / 85.1 / 32.4; 8 warps of three 64.0 / 103.0 / 39.6; 12 of three 4 KB ones 60.5 / 99.5 / 37.0; 16 of two
 // 4 KB ones 58.1 / 101.1 / 32.8.  (At the copy rate: 50.8 / 75.8 / 25.4.)
 constexpr int kWarps = 12;
 constexpr int kBufs = 2;           // units in flight per warp
@@ -201,8 +201,8 @@ struct UnitWalk {
     }
 };
 
-// One run of units: `heads` rows of each token in groups of a.unit_rows.
-__device__ __forceinline__ int groups_of(const RopeArgs& a, int heads) { return (heads + a.unit_rows - 1) / a.unit_rows; }
+// One run of units: `heads` rows of each token in groups of `rows`.
+__device__ __forceinline__ int groups_of(int heads, int rows) { return (heads + rows - 1) / rows; }
 
 template <int D, bool F16, bool ADJ>
 __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArgs a) {
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LANES, lr = lane / LANES;
     WarpSmem<D>& s = reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp];
     const bool on = li < C::PAIRS;
-    const int gq = groups_of(a, a.h_q), gk = groups_of(a, a.h_kv), per_token = gq + gk + (a.v ? gk : 0);
+    const int gq = groups_of(a.h_q, a.unit_rows), per_token = gq + groups_of(a.h_kv, a.kv_rows);
     const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
-    // a unit's kind (0 q, 1 k, 2 v), first row and rows
+    // a unit's kind (0 q, 1 k and, in an append, v), first row and rows
     auto unit = [&](int x, int& kind, int& r0, int& rows) {
-        kind = x < gq ? 0 : x < gq + gk ? 1 : 2;
-        r0 = (x - (kind > 0 ? gq : 0) - (kind > 1 ? gk : 0)) * a.unit_rows;
-        rows = min(a.unit_rows, (kind ? a.h_kv : a.h_q) - r0);
+        kind = x < gq ? 0 : 1;
+        r0 = kind ? (x - gq) * a.kv_rows : x * a.unit_rows;
+        rows = kind ? min(a.kv_rows, a.h_kv - r0) : min(a.unit_rows, a.h_q - r0);
     };
     UnitWalk ahead(me, n_warps, per_token), now = ahead;
     if (me >= n_warps) ahead.t = now.t = a.T;
@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
             if (next_pos >= 0) {
                 int kind, r0, rows;
                 unit(ahead.x, kind, r0, rows);
-                const uint16_t* src = (kind == 0 ? a.q + ahead.t * a.q_stride : kind == 1 ? a.k + ahead.t * a.k_stride
-                                                                                          : a.v + ahead.t * a.v_stride) + (long)r0 * D;
-                const uint32_t bytes = (uint32_t)rows * D * 2, angle = kind < 2 ? (uint32_t)a.rot * 2 : 0u;
-                mbar_expect_tx(&s.full[b], bytes + 2 * angle);
+                const bool with_v = kind && a.v;
+                const uint16_t* src = (kind ? a.k + ahead.t * a.k_stride : a.q + ahead.t * a.q_stride) + (long)r0 * D;
+                const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                mbar_expect_tx(&s.full[b], (with_v ? 2 : 1) * bytes + 2 * angle);
                 bulk_load(s.buf[b].rows, src, bytes, &s.full[b]);
+                if (with_v) bulk_load(s.buf[b].rows + kUnitBytes / 2, a.v + ahead.t * a.v_stride + (long)r0 * D, bytes, &s.full[b]);
                 if (angle) {
                     bulk_load(s.buf[b].cos, a.cos + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
                     bulk_load(s.buf[b].sin, a.sin + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
@@ -284,14 +285,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
             int kind, r0, rows;
             unit(now.x, kind, r0, rows);
             const uint8_t* in = s.buf[b].rows;
-            const bool cached = kind > 0 && meta.slot >= 0;
-            uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : kind == 1 && a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
-            uint16_t* out1 = cached ? (kind == 1 ? a.k_cache : a.v_cache) + ((long)meta.slot * a.h_kv + r0) * D : nullptr;
-            if (kind == 2) {
-                if (cached)
-                    for (int y = lane; y < rows * D / 8; y += 32)
-                        reinterpret_cast<uint4*>(out1)[y] = reinterpret_cast<const uint4*>(in)[y];
-            } else if (out0 || out1) {
+            const bool cached = kind && meta.slot >= 0;
+            uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
+            const long in_cache = ((long)meta.slot * a.h_kv + r0) * D;
+            uint16_t* out1 = cached ? a.k_cache + in_cache : nullptr;
+            if (cached)
+                for (int y = lane; y < rows * D / 8; y += 32)
+                    reinterpret_cast<uint4*>(a.v_cache + in_cache)[y] = reinterpret_cast<const uint4*>(in + kUnitBytes / 2)[y];
+            if (out0 || out1) {
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
                 // (two row batches at a time, so that one's sums and roots hide behind the other's)
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
         load_weight<F16>(a, kind ? a.wk : a.wq, u0, u1, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[e] = make_float2(0.f, 0.f);
-        UnitWalk ahead(me, n_warps, groups_of(a, heads)), now = ahead;
+        UnitWalk ahead(me, n_warps, groups_of(heads, a.unit_rows)), now = ahead;
         if (me >= n_warps) ahead.t = now.t = a.T;
         int next_pos = -1;
         auto look = [&]() {
@@ -572,9 +573,11 @@ int ctas_for(long units, int sms) {
 
 cudaError_t launch_norm_rope(const RopeArgs& args, int sms, cudaStream_t st) {
     RopeArgs a = args;
-    const int sets = a.v ? 2 : 1;
-    a.unit_rows = unit_rows_of(a.d, (long)a.T * (a.h_q + sets * a.h_kv), false, sms);
-    const int per_token = cdiv(a.h_q, a.unit_rows) + sets * cdiv(a.h_kv, a.unit_rows);
+    a.unit_rows = unit_rows_of(a.d, (long)a.T * (a.h_q + (a.v ? 2 : 1) * a.h_kv), false, sms);
+    // (keys and their values in one unit of an append, so that more bytes are in flight: 8192 tokens of
+    // 16 + 2 heads of 256 30.9 us, 32.7 with units of their own)
+    a.kv_rows = a.v ? unit_rows_of(a.d, (long)a.T * (a.h_q + 2 * a.h_kv), true, sms) : a.unit_rows;
+    const int per_token = cdiv(a.h_q, a.unit_rows) + cdiv(a.h_kv, a.kv_rows);
     const int ctas = ctas_for((long)a.T * per_token, sms);
     a.warps = (long)a.T * per_token > (long)ctas * kWarps ? walking_warps(ctas, per_token) : ctas * kWarps;
     switch (a.d) {
