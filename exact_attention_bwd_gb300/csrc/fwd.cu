@@ -133,16 +133,9 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     const Problem& p = a.p;
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
-    if constexpr (PG) {
-        allow_next_kernel();
-        wait_previous_kernel();
-    }
-    // an earlier CTA of this launch gave up: do not start (PG: nor without work)
-    if constexpr (PG) {
-        if (__syncthreads_or(tid == 0 && ((int)blockIdx.x >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
-    } else {
-        if (a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
-    }
+    if constexpr (PG) allow_next_kernel();
+    // an earlier CTA of this launch gave up: do not start (PG: looked at after the setup)
+    if (!PG && a.status && *reinterpret_cast<volatile int*>(a.status) != 0) return;
 
     // ---------------- setup ----------------
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
@@ -181,8 +174,22 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         tmem_alloc(&s.tmem_base, C::TMEM_COLS);
         tmem_relinquish();
     }
+    // PG: the scheduler warp's walk over the CTA's stretch of the line of units
+    PagedWalk walk;
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PG) {
+        wait_previous_kernel();
+        if (warp == 3) walk.start(p, a.pre, a.line, blockIdx.x);
+        // without work, or in a call that already failed (one thread looks, so that all leave or none)
+        const bool leave = __syncthreads_or(tid == 0 && ((int)blockIdx.x >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0));
+        if (leave) {
+            tc_fence_after();
+            if (warp == 2) tmem_dealloc(s.tmem_base, C::TMEM_COLS);
+            return;
+        }
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
     const uint32_t tmem_base = s.tmem_base, tmem = tmem_base;
     // registers: 384 x 168 at launch (one CTA per SM; 384 x 80 with two); the producer/MMA
@@ -479,8 +486,6 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // come from those intervals (their hull), since a tile's rows may span sequences.
         int n = 0, before = 0;
         bool ok = true;
-        // PG: the walk over the CTA's stretch of the line of units
-        PagedWalk walk(PG ? *a.line : PagedLine{}, blockIdx.x);
         for (int idx = blockIdx.x, step = first_step(a.snake); PG || idx < a.n_items;
              idx += step, step = 2 * (int)gridDim.x - step) {
             FwdItem w;

@@ -558,6 +558,8 @@ __global__ void __launch_bounds__(kThreads256, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     allow_next_kernel();
     wait_previous_kernel();
+    PagedWalk walk;
+    if (warp == 3) walk.start(p, a.pre, a.line, cta);
     // without work, or in a call that already failed (one thread looks, so that all leave or none)
     if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
@@ -567,7 +569,6 @@ __global__ void __launch_bounds__(kThreads256, 1)
         tmem_relinquish();
     }
     const PagedLine line = *a.line;
-    PagedWalk walk(line, cta);
     // warp 3 finds the next item while the others work on the current one
     auto find = [&](int x) {
         const bool y = walk.next(p, a.pre, line, cta, p.P * p.G, a.no_split);

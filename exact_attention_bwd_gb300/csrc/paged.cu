@@ -278,17 +278,22 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         }
         fence_mbar_init();
     }
-    // the schedule is there; a CTA without work, or one of a call that already failed, leaves
-    wait_previous_kernel();
-    // (one thread looks, so that all leave or none)
-    if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
     if (warp == 2) {
         tmem_alloc(&s.tmem_base, C::TMEM_COLS);
         tmem_relinquish();
     }
+    // the schedule is there; a CTA without work, or one of a call that already failed, leaves
+    wait_previous_kernel();
+    PagedWalk walk;
+    if (warp == 3) walk.start(p, a.pre, a.line, cta);
+    // (one thread looks, so that all leave or none)
     tc_fence_before();
-    __syncthreads();
+    const bool leave = __syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0));
     tc_fence_after();
+    if (leave) {
+        if (warp == 2) tmem_dealloc(s.tmem_base, C::TMEM_COLS);
+        return;
+    }
     const uint32_t tmem_base = s.tmem_base, tmem = tmem_base;
     // TMEM columns: the two S buffers (tile g's is g & 1), group x's O^T at cO + OH NR x
     constexpr uint32_t cS = 0, cO = 2 * NR;
@@ -480,7 +485,6 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     } else if (warp == 3) {
         // ================= scheduler =================
         const PagedLine line = *a.line;
-        PagedWalk walk(line, cta);
         int it = 0;
         uint32_t qi = 0;
         bool ok = true;
@@ -573,21 +577,13 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             p_at[x] = (key >> 6) * (NR * 128) + (((((key & 63) >> 3) ^ x) & 7) << 4) + (key & 7) * 2;
-        // A [row][key] array of floats over the group's P buffers (both, or one of two: then half of the
-        // rows at a time), for what is summed or turned across the keys while none of the group's P V
-        // is in flight: TPR threads to a row, each starting at another element of it so that a warp's
-        // reads fall into different banks.
+        // The group's P buffer, while none of its P V is in flight: [warp][row] of what is joined across the
+        // keys (thread `key` then takes row `key`), [row][key] of the output on its way to rows.
         float* grid = reinterpret_cast<float*>(s.p[grp]);
-        constexpr int GR = NR / NG, TPR = kKeyTile / GR;
-        const int my_row = key / TPR, row_at = my_row * kKeyTile + key % TPR;
-        auto across = [&](auto op, float x) {  // of the array's row my_row, in every thread of the row
-#pragma unroll 4
-            for (int y = 0; y < GR; ++y) x = op(x, grid[row_at + TPR * ((y + my_row) % GR)]);
-#pragma unroll
-            for (int o = TPR / 2; o >= 1; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-            return x;
+        constexpr int GR = NR / NG;  // rows that the group finishes
+        auto joined = [&](auto op, int row) {  // of the four warps' values of a row
+            return op(op(grid[row], grid[NR + row]), op(grid[2 * NR + row], grid[3 * NR + row]));
         };
-        const bool leads = key % TPR == 0;
         uint32_t gt = 0;  // tiles of the CTA's stream before the item
         bool ok = true;
         for (int it = 0;; ++it) {
@@ -654,25 +650,31 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                         ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[(g - NG) & 1], ((g - NG) >> 1) & 1, ab)) && ok;
                         tc_fence_after();
                     }
+                    // (a loop, 16 rows at a time: this comes once or twice an item, and straight-line code
+                    // for 64 rows took 2.2 us, most of it instruction fetches)
+#pragma unroll 1
+                    for (int h = 0; h < NR; h += 16) {
+                        uint32_t x[16];
+                        tmem_ld_cols<16>(tS + h, x);
+                        float top = -INFINITY;  // lane r: row h + r, over the warp's keys
 #pragma unroll
-                    for (int h = 0; h < NR; h += GR) {
-                        uint32_t x8[GR];
-                        tmem_ld_cols<GR>(tS + h, x8);
-#pragma unroll
-                        for (int r = 0; r < GR; ++r)
-                            grid[r * kKeyTile + key] = edge && (h + r < ra || h + r > rb) ? -INFINITY : __uint_as_float(x8[r]);
-                        group_sync(grp);
-                        const float x = across([](float a, float b) { return fmaxf(a, b); }, -INFINITY);
-                        if (leads) {
-                            const float m = t == first ? -INFINITY : s.mref[grp][h + my_row], mn = fmaxf(m, x * c);
-                            s.alpha[grp][h + my_row] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
-                            s.mref[grp][h + my_row] = mn;
-                            s.negm[grp][h + my_row] = mn == -INFINITY ? 0.f : -mn;
-                            // (no key so far: any finite score passes)
-                            s.limit[grp][h + my_row] = mn == -INFINITY ? INFINITY : -(mn + 8.f) / c;
+                        for (int r = 0; r < 16; ++r) {
+                            const float m = warp_max(edge && (h + r < ra || h + r > rb) ? -INFINITY : __uint_as_float(x[r]));
+                            if (lane == r) top = m;
                         }
-                        group_sync(grp);
+                        if (lane < 16) grid[NR * sub + h + lane] = top;
                     }
+                    group_sync(grp);
+                    if (key < NR) {
+                        const float x = joined([](float a, float b) { return fmaxf(a, b); }, key);
+                        const float m = t == first ? -INFINITY : s.mref[grp][key], mn = fmaxf(m, x * c);
+                        s.alpha[grp][key] = m == mn ? 1.f : ex2(m - mn);  // m = -inf: 0
+                        s.mref[grp][key] = mn;
+                        s.negm[grp][key] = mn == -INFINITY ? 0.f : -mn;
+                        // (no key so far: any finite score passes)
+                        s.limit[grp][key] = mn == -INFINITY ? INFINITY : -(mn + 8.f) / c;
+                    }
+                    group_sync(grp);
                     if (t > first) {
 #pragma unroll
                         for (int r = 0; r < NR; r += 4) {
@@ -766,25 +768,40 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 tc_fence_after();
             }
             gt += max(t1 - t0, 0);
-            // the group's sums over its keys
+            // the group's sums over its keys: half of the rows to each half of the lanes, and so on, until a
+            // lane holds the warp's sums of two rows (64 rows), one (32) or shares one with its neighbour (16)
+            {
+                float v[NR];
 #pragma unroll
-            for (int h = 0; h < NR; h += GR) {
-#pragma unroll
-                for (int r = 0; r < GR; ++r) grid[r * kKeyTile + key] = r & 1 ? l[(h + r) / 2].y : l[(h + r) / 2].x;
-                group_sync(grp);
-                const float x = across([](float a, float b) { return a + b; }, 0.f);
-                if (leads) {
-                    s.lsum[grp][h + my_row] = x;
-                    if (!had) s.mref[grp][h + my_row] = -INFINITY;
+                for (int r = 0; r < NR; r += 2) {
+                    v[r] = l[r / 2].x;
+                    v[r + 1] = l[r / 2].y;
                 }
+                int o = 16;
+#pragma unroll
+                for (int n = NR / 2; n >= NR / 32 && n >= 1; n /= 2, o /= 2) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int r = 0; r < n; ++r) {
+                        const float sent = __shfl_xor_sync(0xffffffffu, up ? v[r] : v[r + n], o);
+                        v[r] = (up ? v[r + n] : v[r]) + sent;
+                    }
+                }
+                if constexpr (NR == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+                if constexpr (NR == 64) *reinterpret_cast<float2*>(&grid[NR * sub + 2 * lane]) = make_float2(v[0], v[1]);
+                else grid[NR * sub + (NR == 32 ? lane : lane >> 1)] = v[0];
                 group_sync(grp);
+                if (key < NR) {
+                    s.lsum[grp][key] = joined([](float a, float b) { return a + b; }, key);
+                    if (!had) s.mref[grp][key] = -INFINITY;
+                }
             }
             if (vote_at<3, 128 * NG>(!ok)) break;
             tc_fence_after();
             const int rows = w.rows, part = w.part, gh = w.g, q0 = w.q0;
             const int h0 = grp * GR;  // the group finishes the rows [h0, h0 + GR)
-            if (leads && h0 + my_row < rows) {
-                const int r = h0 + my_row;
+            if (key < GR && h0 + key < rows) {
+                const int r = h0 + key;
                 const float ma = s.mref[0][r], mb = s.mref[NG - 1][r], m = fmaxf(ma, mb);
                 float fa = ma == -INFINITY ? 0.f : ex2(ma - m), fb = NG == 1 || mb == -INFINITY ? 0.f : ex2(mb - m);
                 const float sum = s.lsum[0][r] * fa + (NG == 2 ? s.lsum[NG - 1][r] * fb : 0.f);

@@ -136,14 +136,29 @@ struct PagedCut {
     int pieces;       // its CTAs, this one and the next ones
 };
 
-// The walk of one warp over its CTA's stretch, piece by piece.
+// The walk of one warp over its CTA's stretch, piece by piece.  Up to 32 sequences are held a lane
+// each from the start, when line, units, offsets and lengths are read side by side; more are looked up one
+// after another (decode of 32 sequences over 4000 keys 56.2 us, 57.2 with lookups).
 struct PagedWalk {
-    long long u, end;          // next unit, end of the stretch
+    long long u = 0, end = 0;  // next unit, end of the stretch
+    bool held = false;
+    long long my_pre = 0, my_units = 0;  // held: the units of a head ahead of the lane's sequence and its own
+    PagedSeq mine{};
     long long before = 0, per_head = 0, after = 0;  // the sequence's: units ahead of it, of a head, up to its end
     int b = 0;
     PagedSeq seq{};
     PagedLook look;
-    __device__ __forceinline__ PagedWalk(const PagedLine& line, int cta) : u(line.start(cta)), end(line.start(cta + 1)) {}
+    __device__ __forceinline__ void start(const Problem& p, const long long* pre, const PagedLine* line, int cta) {
+        const int lane = threadIdx.x & 31;
+        held = p.B <= 32;
+        if (held && lane < p.B) {
+            my_pre = pre[lane];
+            my_units = pre[lane + 1] - my_pre;
+            mine = paged_seq(p, lane);
+        }
+        u = line->start(cta);
+        end = line->start(cta + 1);
+    }
     PagedUnit x;               // the piece's item
     int t0 = 0, t1 = 0;        // its key tiles
     bool from_start = true, to_end = true;  // whether it is the item's start and end
@@ -152,11 +167,18 @@ struct PagedWalk {
     __device__ __forceinline__ bool next(const Problem& p, const long long* pre, const PagedLine& line, int cta, int rows, bool no_split) {
         while (u < end) {
             if (u >= after) {
-                b = find_sequence(pre, p.B, p.h_kv, u);
-                before = pre[b] * p.h_kv;
-                per_head = pre[b + 1] - pre[b];
+                if (held) {
+                    b = 31 - __clz(__ballot_sync(0xffffffffu, (threadIdx.x & 31) < p.B && my_pre * p.h_kv <= u));
+                    before = __shfl_sync(0xffffffffu, my_pre, b) * p.h_kv;
+                    per_head = __shfl_sync(0xffffffffu, my_units, b);
+                    seq = PagedSeq{__shfl_sync(0xffffffffu, mine.q0, b), __shfl_sync(0xffffffffu, mine.nq, b), __shfl_sync(0xffffffffu, mine.nk, b)};
+                } else {
+                    b = find_sequence(pre, p.B, p.h_kv, u);
+                    before = pre[b] * p.h_kv;
+                    per_head = pre[b + 1] - pre[b];
+                    seq = paged_seq(p, b);
+                }
                 after = before + per_head * p.h_kv;
-                seq = paged_seq(p, b);
                 look.g = -1;
             }
             x = paged_unit(p, seq, rows, u - before, per_head, look);

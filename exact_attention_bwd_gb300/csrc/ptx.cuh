@@ -140,6 +140,13 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) 
     return false;
 }
 
+// The largest of the warp's values, in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ------------------------------------------------------------------------------------------
 // 16 bytes from global to shared memory without a register (zeros unless `there`), and the wait for
 // all that this thread has started
