@@ -902,6 +902,17 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, const PagedCut& c
     const int lane = threadIdx.x & 31, held = which ? a.many_rows : a.few_rows;
     // the partials' row of piece y, row r
     auto at = [&](int y, int r) { return (long)(2 * (c + y) + (y == 0 ? 1 : 0)) * held + r; };
+    auto load = [&](int y, int z, float2* x) {  // piece y of row r1 + z; a row past the end is the last one again, not stored
+        const float2* src = reinterpret_cast<const float2*>(a.part_o[which] + at(y, min(r1 + z, cut.rows - 1)) * D + VW * lane);
+#pragma unroll
+        for (int e = 0; e < VW / 2; ++e) x[e] = src[e];
+    };
+    // the first two pieces (there are two at least) are on their way while their weights are worked out
+    float2 ahead[2][R][VW / 2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int z = 0; z < R; ++z) load(k, z, ahead[k][z]);
     float m[R], l[R], acc[R][VW];
 #pragma unroll
     for (int z = 0; z < R; ++z) {
@@ -915,7 +926,7 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, const PagedCut& c
         float wy[R];
 #pragma unroll
         for (int z = 0; z < R; ++z) {
-            const int r = min(r1 + z, cut.rows - 1);  // a row past the end is the last one again, not stored
+            const int r = min(r1 + z, cut.rows - 1);
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < cnt) ml = a.part_ml[which][at(y, r)];
             float mx = ml.x;
@@ -932,20 +943,28 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, const PagedCut& c
 #pragma unroll
             for (int e = 0; e < VW; ++e) acc[z][e] *= keep;
         }
+        auto add = [&](int k, int z, const float2* x) {
+            const float wk = __shfl_sync(0xffffffffu, wy[z], k);
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) {
+                acc[z][2 * e] = fmaf(wk, x[e].x, acc[z][2 * e]);
+                acc[z][2 * e + 1] = fmaf(wk, x[e].y, acc[z][2 * e + 1]);
+            }
+        };
+        int k = 0;
+        if (y0 == 0)
+#pragma unroll
+            for (; k < 2; ++k)
+#pragma unroll
+                for (int z = 0; z < R; ++z) add(k, z, ahead[k][z]);
 #pragma unroll 2
-        for (int k = 0; k < cnt; ++k) {
+        for (; k < cnt; ++k)
 #pragma unroll
             for (int z = 0; z < R; ++z) {
-                const float wk = __shfl_sync(0xffffffffu, wy[z], k);
-                const float* src = a.part_o[which] + at(y0 + k, min(r1 + z, cut.rows - 1)) * D + VW * lane;
-#pragma unroll
-                for (int e = 0; e < VW; e += 2) {
-                    const float2 x = *reinterpret_cast<const float2*>(src + e);
-                    acc[z][e] = fmaf(wk, x.x, acc[z][e]);
-                    acc[z][e + 1] = fmaf(wk, x.y, acc[z][e + 1]);
-                }
+                float2 x[VW / 2];
+                load(y0 + k, z, x);
+                add(k, z, x);
             }
-        }
     }
 #pragma unroll
     for (int z = 0; z < R; ++z) {
