@@ -381,7 +381,7 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     const long rows = longest * p.G;
     // Every sequence known to have 64 rows at most: the few-row kernel alone, its tile the rows.  Else it takes those of a
     // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
-    // a decode step 38 us where one of 16 takes 22: 20 sequences of 5 heads a group, d = 64), and none
+    // a decode step 33 us where one of 16 takes 20: 20 sequences of 5 heads a group, d = 64), and none
     // where a token has more than 64.
     pl.many = rows > 64;
     const long tile = pl.many ? p.G : rows;

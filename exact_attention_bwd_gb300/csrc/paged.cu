@@ -8,10 +8,10 @@
 // for all rows.  The online softmax's reference maximum is only moved when some score passes it
 // by more than 2^8 (one vote per tile), so the cross-lane maxima are formed rarely.  A tile's way
 // through the softmax is a chain of latencies, at 32 and 64 rows longer than its keys take to
-// arrive where a tile is 64 KB or less: there (d <= 128) two groups of four warps take the tiles in
-// turn, each an online softmax of its own with its own accumulator, joined at the end.  (Decode of
-// 32 x 16000 keys, 4 heads, one group against two: d = 64 157 / 126 us at 32 rows and 225 / 149 at
-// 64, d = 128 225 / 193 at 64; but d = 64 108 / 111 at 16, and with 2 heads d = 256 203 / 258 at 64.)
+// arrive where they are few bytes: there (d = 64) two groups of four warps take the tiles in turn, each an
+// online softmax of its own with its own accumulator, joined at the end.  (Decode of 32 x 16000
+// keys, 4 heads, one group against two: d = 64 111 / 111 us at 16 rows, 119 / 117 at 32 and 158 / 128 at
+// 64; d = 128 179 / 181 at 64; with 2 heads d = 256 175 / 193 at 64.)
 //
 // Warp roles (one CTA per SM):
 //   warp 0       TMA producer: K and V tiles, page by page, through a ring of [128 keys] units
@@ -163,7 +163,7 @@ struct FewCfg {
     // P^T in shared memory: 64 rows are a whole swizzle row per key, which a thread writes with
     // eight 16-byte stores (rows innermost); fewer rows lie [row][key], a 2-byte store each
     static constexpr bool P_MN = NR == 64;
-    static constexpr int NG = D <= 128 && NR >= 32 ? 2 : 1;  // softmax groups
+    static constexpr int NG = D == 64 && NR >= 32 ? 2 : 1;  // softmax groups
     static constexpr int THREADS = 128 + 128 * NG;
     // scores held at a time; with two groups (fewer registers) 64 rows are read twice, 32 at a time
     static constexpr int HR = NG == 2 && NR > 32 ? 32 : NR;
@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 if constexpr (KU > 1 || D == 192) {
                     // The ring holds two tiles at most, so either product's operands may come first:
                     // whichever has them goes, P V before S (tile j's S goes into the buffer whose scores
-                    // were tile j - 2's, so it may run two tiles ahead).  Against the fixed order below:
-                    // 16000 keys, 2 heads, 64 rows, d = 256 189 / 218 us, d = 192 155 / 177.
+                    // were tile j - 2's, so it may run two tiles ahead).  The fixed order below
+                    // takes 15 % longer (16000 keys, 2 heads, 64 rows, d = 256 and d = 192).
                     int js = 0, jv = 0;  // tiles whose S, whose P V was issued
                     uint32_t idle = 0;
                     unsigned long long since = 0;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (g >> 1) & 1, ab)) && ok;
                 tc_fence_after();
                 uint32_t sr[HR];
-                // (a maximum rather than a chain of comparisons: 149 against 191 us at d = 64 and 64 rows)
+                // (a maximum rather than a chain of comparisons, which took a quarter longer at d = 64 and 64 rows)
                 float past[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // largest score - limit
 #pragma unroll
                 for (int h = 0; h < NR; h += HR) {
