@@ -15,8 +15,8 @@
 //
 // Warp roles (one CTA per SM):
 //   warp 0       TMA producer: K and V tiles, page by page, through a ring of [128 keys] units
-//   warp 1       MMA issuer (one thread)
-//   warp 2       owns the TMEM allocation
+//   warp 1       MMA issuer (one thread; of P V where warp 2 has S)
+//   warp 2       owns the TMEM allocation; with two issuers the one of S (one thread)
 //   warp 3       scheduler: finds the CTA's pieces of work, stages each item's Q rows
 //   warps 4..7   softmax (thread = key) and epilogue (thread = column of O, then warp = row)
 //   warps 8..11  with two groups: the softmax of the odd tiles of the CTA's stream (warps 4..7 then
@@ -156,8 +156,15 @@ struct FewCfg {
     static constexpr int Q_BYTES = NR * D * 2, P_BYTES = NR * kKeyTile * 2;
     static constexpr int Q_BUFS = Q_BYTES <= 16384 ? 2 : 1;
     static constexpr int FIT = (kSmemMax - 1024 - 4096 - Q_BUFS * Q_BYTES - 2 * P_BYTES) / UNIT;
-    // at d = 64 the ring is even (see slot_of)
-    static constexpr int RING = D == 64 ? (FIT > 12 ? 12 : FIT / 2 * 2) : (FIT > 6 ? 6 : FIT);
+    // MMA issuers.  With two, one thread issues S and another P V, which one thread could not do as fast as
+    // small tiles arrive (16000 keys, 4 heads: d = 64 at 16 / 32 / 64 rows 111 / 117 / 128 us with one, 92 / 95 /
+    // 110 with two, d = 128 at 64 rows 182 / 178; but 164 / 167 at 16).  Each waits for its own units by
+    // the parity of their slots' phases, so K and V must have slots of their own: one unit to a tile
+    // and an even ring (a phase that a thread has not waited for would pass for the one after it).
+    static constexpr int ISSUERS = D == 64 || (D == 128 && NR >= 32) ? 2 : 1;
+    static constexpr int MOST = D == 64 ? 12 : 6;
+    static constexpr int RING = ISSUERS == 2 ? (FIT > MOST ? MOST : FIT / 2 * 2) : (FIT > MOST ? MOST : FIT);
+    static_assert(ISSUERS == 1 || (KU == 1 && RING % 2 == 0), "slots of their own");
     static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile and the next K have to fit");
     static constexpr int OH = D > 128 ? 2 : 1;         // 128-lane accumulators of O^T
     // P^T in shared memory: 64 rows are a whole swizzle row per key, which a thread writes with
@@ -199,7 +206,7 @@ struct __align__(1024) FewSmem {
     float lsum[C::NG][NR];
     uint64_t full[C::RING], empty[C::RING];
     uint64_t q_full[C::Q_BUFS], q_empty[C::Q_BUFS];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free, drain[2];
     uint64_t item_full[kItems], item_empty[kItems];
     FewItem item[kItems];
     uint32_t tmem_base;
@@ -271,10 +278,11 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
             mbar_init(&s.pv_done[i], 1);
         }
         mbar_init(&s.o_free, 4 * C::NG);
-        mbar_init(&s.drain, 1);
+        mbar_init(&s.drain[0], 1);
+        mbar_init(&s.drain[1], 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], 2 + 4 * C::NG);  // producer, MMA issuer, softmax warps
+            mbar_init(&s.item_empty[i], 1 + C::ISSUERS + 4 * C::NG);  // producer, MMA issuers, softmax warps
         }
         fence_mbar_init();
     }
@@ -351,8 +359,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         // every copy still in flight lands before the CTA may exit
         for (uint32_t back = 1; back <= (uint32_t)RING && back <= n; ++back)
             mbar_wait_quiet(&s.full[C::slot_of(n - back)], ((n - back) / RING) & 1);
-    } else if (warp == 1) {
-        // ================= MMA issuer =================
+    } else if (warp == 1 || (C::ISSUERS == 2 && warp == 2)) {
+        // ================= MMA issuer (of two: warp 2 S, warp 1 P V) =================
         FewSmem<D, NR>& s = C::NG == 2 ? own_shared(smem) : smem;
         const uint32_t tmem = C::NG == 2 ? own_copy(tmem_base) : tmem_base;
         if (lane == 0) {
@@ -412,13 +420,20 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 if (end) break;
                 if (nt <= 0) continue;
                 const int qb = (int)(qi % C::Q_BUFS);
-                if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
                 const uint32_t q_addr = smem_u32(s.q[qb]);
-                if constexpr (KU > 1 || D == 192) {
+                // the K or the V unit n of a tile of one unit has arrived
+                auto wait_unit = [&](uint32_t n) {
+                    const bool y = mbar_wait(&s.full[C::slot_of(n)], (n / RING) & 1, ab);
+                    tc_fence_after();
+                    return y;
+                };
+                if constexpr (D > 128) {
+                    if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
                     // The ring holds two tiles at most, so either product's operands may come first:
                     // whichever has them goes, P V before S (tile j's S goes into the buffer whose scores
-                    // were tile j - 2's, so it may run two tiles ahead).  The fixed order below
-                    // takes 15 % longer (16000 keys, 2 heads, 64 rows, d = 256 and d = 192).
+                    // were tile j - 2's, so it may run two tiles ahead).  A fixed order
+                    // takes 15 % longer (16000 keys, 2 heads, 64 rows, d = 256 and d = 192).  (S of tile j
+                    // comes behind P V of tile j - 2, so every earlier phase of its slots has been seen.)
                     int js = 0, jv = 0;  // tiles whose S, whose P V was issued
                     uint32_t idle = 0;
                     unsigned long long since = 0;
@@ -450,37 +465,52 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                             }
                         }
                     }
-                } else {
+                } else if constexpr (C::ISSUERS == 1) {
                     // S two tiles ahead, in a fixed order (a deep ring: looking for what is ready costs more
                     // than it finds, 400 against 393 us for 64 requests at d = 128)
-                    auto wait_units = [&](uint32_t n) {
-                        bool y = true;
-#pragma unroll
-                        for (int h = 0; h < KU; ++h) y = y && mbar_wait(&s.full[C::slot_of(n + h)], ((n + h) / RING) & 1, ab);
-                        tc_fence_after();
-                        return y;
-                    };
+                    if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
                     for (int t = -2; t < nt; ++t) {
                         if (t >= 0) {
                             const uint32_t g = gt + t;
                             if (!(ok = mbar_wait(&s.p_full[g & 1], (g >> 1) & 1, ab))) break;
                             // the previous item's O has been read
                             if (t == 0 && qi > 0 && !(ok = mbar_wait(&s.o_free, (qi - 1) & 1, ab))) break;
-                            if (!(ok = wait_units(2 * KU * g + KU))) break;
+                            if (!(ok = wait_unit(2 * g + 1))) break;
                             issue_pv(g, t < C::NG);
                         }
                         if (t + 2 < nt) {
-                            if (!(ok = wait_units(2 * KU * (gt + t + 2)))) break;
+                            if (!(ok = wait_unit(2 * (gt + t + 2)))) break;
                             issue_s(gt + t + 2, q_addr);
                             if (t + 3 == nt) tc_commit(&s.q_empty[qb]);
+                        }
+                    }
+                } else {
+                    if (warp == 2) {
+                        if (!(ok = mbar_wait(&s.q_full[qb], (qi / C::Q_BUFS) & 1, ab))) break;
+                        for (int t = 0; t < nt; ++t) {
+                            const uint32_t g = gt + t;
+                            // (the buffer's last scores, two tiles ago, have become P)
+                            if (g >= 2 && !(ok = mbar_wait(&s.p_full[g & 1], ((g - 2) >> 1) & 1, ab))) break;
+                            if (!(ok = wait_unit(2 * g))) break;
+                            issue_s(g, q_addr);
+                        }
+                        if (ok) tc_commit(&s.q_empty[qb]);
+                    } else {
+                        for (int t = 0; t < nt; ++t) {
+                            const uint32_t g = gt + t;
+                            if (!(ok = mbar_wait(&s.p_full[g & 1], (g >> 1) & 1, ab))) break;
+                            // the previous item's O has been read
+                            if (t == 0 && qi > 0 && !(ok = mbar_wait(&s.o_free, (qi - 1) & 1, ab))) break;
+                            if (!(ok = wait_unit(2 * g + 1))) break;
+                            issue_pv(g, t < C::NG);
                         }
                     }
                 }
                 gt += nt;
                 ++qi;
             }
-            tc_commit(&s.drain);
-            mbar_wait_quiet(&s.drain, 0);
+            tc_commit(&s.drain[warp - 1]);
+            mbar_wait_quiet(&s.drain[warp - 1], 0);
         }
     } else if (warp == 3) {
         // ================= scheduler =================
