@@ -10,8 +10,8 @@
 // through the softmax is a chain of latencies, at 32 and 64 rows longer than its keys take to
 // arrive where they are few bytes: there (d = 64) two groups of four warps take the tiles in turn, each an
 // online softmax of its own with its own accumulator, joined at the end.  (Decode of 32 x 16000
-// keys, 4 heads, one group against two: d = 64 111 / 111 us at 16 rows, 119 / 117 at 32 and 158 / 128 at
-// 64; d = 128 179 / 181 at 64; with 2 heads d = 256 175 / 193 at 64.)
+// keys, 4 heads, one group against two: d = 64 116 / 95 us at 32 rows and 158 / 110 at 64, none
+// gained at 16; d = 128 179 / 181 at 64; with 2 heads d = 256 175 / 193 at 64.)
 //
 // Warp roles (one CTA per SM):
 //   warp 0       TMA producer: K and V tiles, page by page, through a ring of [128 keys] units
