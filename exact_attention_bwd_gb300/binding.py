@@ -435,10 +435,10 @@ def _on_device(t, call, *args, **kw):
 
 def _device_index(t):
     """The index of t's CUDA device."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"a torch tensor is wanted, not {type(t).__name__}")
-    i = t.get_device()
+    try:
+        i = t.get_device()
+    except AttributeError:
+        raise TypeError(f"a torch tensor is wanted, not {type(t).__name__}") from None
     if i < 0:
         raise ValueError(f"the tensors must be CUDA tensors; one is on {t.device}")
     return i
@@ -465,7 +465,7 @@ def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, o
     """forward() for packed queries over a paged cache."""
     import torch
     dev = _device_index(q)
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return _on_device(q, _forward_paged, q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace,
                           seqused_k, block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q)
     kind = q.dtype
@@ -510,14 +510,16 @@ def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, o
     return out, lse, workspace
 
 
-def _rows(name, t, like=None):
+def _rows(name, t):
     """(tokens, heads, d, elements from token to token) of [T, h, d] or [B, S, h, d] rows, whose
     heads are contiguous and whose tokens lie at one stride (a slice of a fused projection)."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name} must be [T, h, d] or [B, S, h, d]")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise TypeError(f"{name} must have the type and device of q")
     shape, st = t.shape, t.stride()
+    if len(st) == 3:
+        T, h, d = shape
+        if T > 1 and st[2] == 1 and (h == 1 or st[1] == d):
+            return T, h, d, st[0]
+    elif len(st) != 4:
+        raise ValueError(f"{name} must be [T, h, d] or [B, S, h, d]")
     h, d = shape[-2:]
     if t.numel() and (st[-1] != 1 or (h > 1 and st[-2] != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -531,11 +533,18 @@ def _rows(name, t, like=None):
     return T, h, d, step if T > 1 else h * d
 
 
+def _like(name, t, kind, dev):
+    """t has q's type and device."""
+    if t.dtype is not kind or t.get_device() != dev:
+        raise TypeError(f"{name} must have the type and device of q")
+
+
 def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status):
     import torch
     T, h_q, d, q_stride = _rows("q", q)
-    Tk, h_kv, dk, k_stride = _rows("k", k, q)
     kind = q.dtype
+    _like("k", k, kind, dev)
+    Tk, h_kv, dk, k_stride = _rows("k", k)
     code = _type_code(kind)
     if code is None or code == FA_DTYPE_E4M3:
         raise TypeError(f"q and k must be bfloat16 or float16; q is {kind}")
@@ -574,7 +583,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
     unless out = (q_out, k_out) gives one.  status: int32 [1] or None."""
     import torch
     dev = _device_index(q)
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions=positions, seq_len=seq_len, eps=eps,
                           interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status)
     p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
@@ -585,7 +594,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
             raise ValueError("an append takes v, k_cache, v_cache and slots together")
         if v.shape != k.shape:
             raise ValueError(f"v must have k's shape {tuple(k.shape)}; it has {tuple(v.shape)}")
-        p.v_stride = _rows("v", v, q)[3]
+        _like("v", v, kind, dev)
+        p.v_stride = _rows("v", v)[3]
         if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[2:] != k.shape[-2:]:
             raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be [num_pages, page_size, "
                              f"{p.h_kv}, {p.d}]")
@@ -616,7 +626,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     any token stride (slices of a fused projection's gradient); the weights' are fp32 [d]."""
     import torch
     dev = _device_index(q)
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope_backward, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions=positions,
                           seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status)
     p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
@@ -625,13 +635,16 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     if dq_out.shape != q.shape or dk_out.shape != k.shape:
         raise ValueError(f"dq_out and dk_out must have the shapes {tuple(q.shape)} and {tuple(k.shape)}")
     if grads is None:
-        dq, dk = torch.empty(q.shape, dtype=kind, device=q.device), torch.empty(k.shape, dtype=kind, device=q.device)
-        dwq, dwk = (torch.empty(p.d, dtype=torch.float32, device=q.device) for _ in range(2))
+        empty, at = torch.empty, q.device
+        dq, dk = empty(q.shape, dtype=kind, device=at), empty(k.shape, dtype=kind, device=at)
+        dwq, dwk = empty(p.d, dtype=torch.float32, device=at), empty(p.d, dtype=torch.float32, device=at)
     else:
         dq, dk, dwq, dwk = grads
         if dq.shape != q.shape or dk.shape != k.shape:
             raise ValueError(f"dq and dk must have the shapes {tuple(q.shape)} and {tuple(k.shape)}")
-        p.dq_stride, p.dk_stride = _rows("dq", dq, q)[3], _rows("dk", dk, q)[3]
+        _like("dq", dq, kind, dev)
+        _like("dk", dk, kind, dev)
+        p.dq_stride, p.dk_stride = _rows("dq", dq)[3], _rows("dk", dk)[3]
         _check(dev, ("dq_weight", dwq, torch.float32, p.d), ("dk_weight", dwk, torch.float32, p.d))
     lib, ref = load(), ctypes.byref(p)
     nbytes = lib.fa_qk_norm_rope_bwd_workspace_size(ref)
@@ -658,7 +671,7 @@ def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, t
     -1 behind the last new token).  out: the five results' tensors to write, status: [1] or None."""
     import torch
     dev = _device_index(cached)
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return _on_device(cached, page_plan, cached, fresh, block_table, free_pages, page_size=page_size, num_pages=num_pages,
                           tokens=tokens, free_head=free_head, out=out, status=status)
     B, i32 = cached.numel(), torch.int32
@@ -669,7 +682,8 @@ def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, t
            ("free_pages", free_pages, i32, n_free), ("free_head", free_head, i32, 1), ("status", status, i32, 1))
     if out is None:
         # (five allocations take less host time than one and five views of it: 9.4 against 12.3 us)
-        out = [torch.empty(n, dtype=i32, device=cached.device) for n in (B + 1, B, tokens, tokens, 1)]
+        empty, at = torch.empty, cached.device
+        out = [empty(n, dtype=i32, device=at) for n in (B + 1, B, tokens, tokens, 1)]
     else:
         _check(dev, *((name, t, i32, n) for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"),
                                                               out, (B + 1, B, tokens, tokens, 1))))
