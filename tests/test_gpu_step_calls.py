@@ -163,3 +163,59 @@ def test_norm_rope_and_plan_on_a_stream_of_their_own():
             graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(side, want) and torch.equal(replayed, want)
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,new,used,hint", [
+    (64, 8, 1, [1], [60000], 1), (64, 16, 1, [4], [60000], 4), (128, 16, 1, [3], [60000], 3), (192, 8, 1, [1], [40000], 1),
+    (256, 16, 1, [4], [40000], 4), (128, 8, 2, [300, 1], [20000, 9000], 0), (256, 8, 2, [300, 1], [9000, 20000], 0),
+])
+def test_wait_limit_in_every_kernel(d, h_q, h_kv, new, used, hint):
+    """Each variant's waits are bounded: a limit of 1 ns ends the call with a timeout status (or, where
+    nothing had to wait, a right result), and the same call with the default limit is right."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    c = case(new, used, h_q=h_q, h_kv=h_kv, d=d, page=64)
+    args, kw = arguments(c, hint)
+    want, want_lse, ws = fa.forward(*args, **kw)
+    assert fa.device_status(ws) == 0
+    _, _, ws = fa.forward(*args, **kw, wait_limit_ns=1)
+    assert fa.device_status(ws) in (fa.FA_ERR_TIMEOUT, 0)
+    o, z, ws = fa.forward(*args, **kw)
+    assert fa.device_status(ws) == 0
+    assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(z, want_lse)
+
+
+@pytest.mark.parametrize("d,h_q,new", [(64, 8, 1), (64, 8, 4), (64, 16, 4), (128, 8, 1), (128, 8, 4), (128, 16, 4), (192, 8, 1), (192, 16, 4),
+                                       (256, 8, 1), (256, 8, 4), (256, 16, 4)])
+def test_long_streams(d, h_q, new):
+    """Some twenty tiles and several items to a CTA, so that its rings go round many times in every
+    variant of the few-row kernel; against the plain form in 64 bits, call after call the same bits."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    torch.manual_seed(d + h_q + new)
+    rng, page = np.random.default_rng(d + new), 64
+    used = rng.integers(6000, 14000, 40)
+    blocks = -(-used // page)
+    k, v = (torch.randn(int(blocks.sum()), page, 1, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(40 * new, h_q, d, device="cuda", dtype=torch.bfloat16)
+    order, table, at = rng.permutation(int(blocks.sum())), np.zeros((40, blocks.max()), np.int32), 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = order[at:at + n]
+        at += n
+    kw = dict(causal=True, cu_q=i32(np.arange(41) * new), seqused_k=i32(used), block_table=i32(table), s_kv=int(used.max()), max_seqlen_q=new)
+    results = [fa.forward(q, k, v, **kw) for _ in range(3)]
+    o, z, ws = results[0]
+    assert fa.device_status(ws) == 0
+    for x in results[1:]:
+        assert torch.equal(o.view(torch.int16), x[0].view(torch.int16)) and torch.equal(z, x[1])
+    h = HALF["bf16"]
+    for b, n in enumerate(used):
+        rows = slice(b * new, (b + 1) * new)
+        kb, vb = (t[torch.from_numpy(table[b, :blocks[b]]).cuda().long()].view(-1, d)[:n].double() for t in (k, v))
+        s = torch.einsum("ihd,jd->ihj", q[rows].double(), kb) * d ** -0.5
+        i, j = torch.arange(new, device="cuda")[:, None, None], torch.arange(n, device="cuda")
+        s = s.masked_fill(j > i + int(n) - new, -float("inf"))
+        w = torch.softmax(s, -1)
+        want, spread = w @ vb, w @ vb.abs()
+        assert torch.all((o[rows].double() - want).abs() <= h * want.abs() + (h + 2.0 ** -13) * spread + 2.0 ** -24)
+        assert (z[:, rows].double() - torch.logsumexp(s, -1).T).abs().max() <= 3e-4
