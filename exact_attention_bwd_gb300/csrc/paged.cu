@@ -166,6 +166,10 @@ struct FewCfg {
     static constexpr int RING = ISSUERS == 2 ? (FIT > MOST ? MOST : FIT / 2 * 2) : (FIT > MOST ? MOST : FIT);
     static_assert(ISSUERS == 1 || (KU == 1 && RING % 2 == 0), "slots of their own");
     static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile and the next K have to fit");
+    // Some unit of a tile's V takes the slot of a unit of the V before it (d = 256 at 32 and 64 rows,
+    // rings of 5 and 4 units): by parity, a wait for its arrival would also pass while the
+    // one before has not arrived yet.
+    static constexpr bool V_AFTER_V = RING < 3 * KU;
     static constexpr int OH = D > 128 ? 2 : 1;         // 128-lane accumulators of O^T
     // P^T in shared memory: 64 rows are a whole swizzle row per key, which a thread writes with
     // eight 16-byte stores (rows innermost); fewer rows lie [row][key], a 2-byte store each
@@ -767,11 +771,14 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                     // values at keys that no row sees may be anything (unused rows of a page): 0 * NaN
                     // would reach every row, so they are cleared
                     bool there = true;
+                    // (S of this tile may be done ahead of the V before it, which then is still on its way
+                    // into the slot; its product is not: the issuer has that tile's P)
+                    if (C::V_AFTER_V && g >= 1) there = mbar_wait(&s.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, ab);
 #pragma unroll
                     for (int h = 0; h < KU; ++h) {
                         const uint32_t n = 2 * KU * g + KU + h;
                         const int sl = C::slot_of(n);
-                        there = mbar_wait(&s.full[sl], (n / RING) & 1, ab) && there;
+                        there = there && mbar_wait(&s.full[sl], (n / RING) & 1, ab);
                         if (there && (j < lo || j > hi)) {
 #pragma unroll
                             for (int x = 0; x < C::UC / 64; ++x)
