@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                     float2 sg = __fmul2_rn(t[0], w[0]);
 #pragma unroll
                     for (int e = 1; e < 8; ++e) sg = __ffma2_rn(t[e], w[e], sg);
-                    const float rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    // (a lane without a row adds nothing to dw: with eps = 0 its root would be infinite, and 0 * inf NaN)
+                    const float root = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps), rs = live ? root : 0.f;
                     // dx = r g w - x r^3 mean(g w x)
                     const float m = -row_sum<LANES>(sg.x + sg.y) * (1.f / D) * rs * rs * rs;
                     const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m);

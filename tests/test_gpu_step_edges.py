@@ -8,6 +8,7 @@ import pytest
 
 import step_helpers as ref
 from gpu_helpers import from_dev
+from test_gpu_norm_rope import TYPES, dev
 from test_gpu_paged import HALF, case
 from test_gpu_step_calls import arguments, i32
 
@@ -57,3 +58,29 @@ def test_values_behind_their_keys(d, h_q, new):
         want, spread = w @ vb, w @ vb.abs()
         assert torch.all((o[rows].double() - want).abs() <= h * want.abs() + (h + 2.0 ** -13) * spread + 2.0 ** -24)
         assert (z[:, rows].double() - torch.logsumexp(s, -1).T).abs().max() <= 3e-4
+
+
+@pytest.mark.parametrize("T,h_q,h_kv,d,kind", [(5, 3, 2, 64, "bf16"), (7, 5, 2, 128, "f16"), (6, 3, 1, 192, "bf16"), (9, 5, 3, 256, "f16")])
+def test_gradient_without_eps(T, h_q, h_kv, d, kind):
+    """eps = 0, and heads that do not fill a warp's batch of rows: lanes without a row leave the
+    weights' gradients alone."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    rng = np.random.default_rng(d)
+    rot = d // 2
+    x = [dev(rng.standard_normal((T, h, d)), kind) for h in (h_q, h_kv)]
+    dy = [dev(rng.standard_normal((T, h, d)), kind) for h in (h_q, h_kv)]
+    w = [dev(1 + 0.3 * rng.standard_normal(d), kind) for _ in range(2)]
+    cos, sin = ref.angles(T, rot)
+    got = fa.qk_norm_rope_backward(*x, *dy, *w, *(torch.from_numpy(a).cuda() for a in (cos, sin)), eps=0.0)
+    for n in range(2):
+        X, DY, W = (from_dev(t[n]) for t in (x, dy, w))
+        want, want_w, _ = ref.norm_rope_bwd(X, W, cos, sin, 0.0, False, DY)
+        r = 1 / np.sqrt(np.mean(X * X, -1, keepdims=True))
+        c, s = np.abs(cos), np.abs(sin)
+        g = np.abs(ref.rotate(np.abs(DY), c, -s, False, back=True)) + np.abs(ref.rotate(np.abs(DY), c, s, False, back=True))
+        gw, xh = g * np.abs(W), np.abs(X) * r
+        size = r * (gw + xh * np.mean(gw * xh, -1, keepdims=True))
+        assert np.all(np.abs(from_dev(got[n]) - want) <= TYPES[kind] * np.abs(want) + 2.0 ** -17 * size + 2.0 ** -25)
+        err = np.abs(got[2 + n].cpu().numpy().astype(np.float64) - want_w)
+        assert np.all(err <= 2.0 ** -16 * (g * xh).sum((0, 1)) + 1e-30)
