@@ -29,6 +29,9 @@ struct PlanSmem {
     int cached[kThreads], old[kThreads];
 };
 
+// Pages that n tokens take (n and the page below 2^31: their sum fits 32 bits without a sign).
+__device__ __forceinline__ int pages_of(int n, int page) { return (int)(((unsigned)n + (unsigned)page - 1u) / (unsigned)page); }
+
 // A page of the free list, or -1 past its end or outside the pool.
 __device__ __forceinline__ int free_page(const PagePlanArgs& a, long long at, bool& bad) {
     const int pg = at >= 0 && at < a.n_free ? a.free_pages[at] : -1;
@@ -59,8 +62,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanArgs 
             n = max(n, 0);
         }
         const int used = (int)min((long long)c + n, (long long)cap);
-        const int old = (c + a.page_size - 1) / a.page_size;
-        const int np = (used + a.page_size - 1) / a.page_size - old;
+        const int old = pages_of(c, a.page_size), np = pages_of(used, a.page_size) - old;
         // inclusive scans of the token and page counts
         long long sn = n, sp = np;
 #pragma unroll
