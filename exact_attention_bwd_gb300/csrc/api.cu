@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -159,8 +160,10 @@ fa_status normalise(const fa_params* in, Problem& p) {
     p.scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / std::sqrt((float)a.d);
     p.scale_log2 = p.scale * 1.4426950408889634f;
     p.causal = a.causal ? 1 : 0;
-    p.left = a.window_left;
-    p.right = a.window_right;
+    // a window wider than everything it could hide is cut to that, so that a position plus the window
+    // times a group of heads fits 32 bits (windows below 2^22 are passed on as they are)
+    p.left = std::min(a.window_left, std::max(a.s_kv, 1 << 22));
+    p.right = std::min(a.window_right, std::max(a.s_q, 1 << 22));
     if (p.causal) p.right = 0;  // intersection of the causal mask with any right window
     p.sinks = a.sinks;
     p.cu_q = a.cu_seqlens_q;

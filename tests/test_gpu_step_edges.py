@@ -84,3 +84,39 @@ def test_gradient_without_eps(T, h_q, h_kv, d, kind):
         assert np.all(np.abs(from_dev(got[n]) - want) <= TYPES[kind] * np.abs(want) + 2.0 ** -17 * size + 2.0 ** -25)
         err = np.abs(got[2 + n].cpu().numpy().astype(np.float64) - want_w)
         assert np.all(err <= 2.0 ** -16 * (g * xh).sum((0, 1)) + 1e-30)
+
+
+@pytest.mark.parametrize("new,used,d", [([1, 2], [300, 77], 64), ([1, 200], [300, 500], 128), ([300, 3], [300, 9], 256)])
+def test_the_largest_windows(new, used, d):
+    """A window of 2^31 - 1 keys to either side is no window: the same bits."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    args, kw = arguments(case(new, used, h_q=4, h_kv=2, d=d, page=16))
+    kw.pop("causal")
+    for causal in (True, False):
+        want = fa.forward(*args, **kw, causal=causal)
+        for window in ((2 ** 31 - 1, -1), (-1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 2, 2 ** 30)):
+            got = fa.forward(*args, **kw, causal=causal, window=window)
+            assert fa.device_status(got[2]) == 0
+            assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("s_q,s_kv,h_q,h_kv,d", [(130, 300, 4, 2, 64), (300, 300, 16, 1, 128), (70, 260, 4, 4, 256), (1, 500, 8, 2, 128)])
+def test_the_largest_windows_of_dense_calls(s_q, s_kv, h_q, h_kv, d):
+    """The same in the forward and backward of dense batches, against a window that just hides nothing."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    torch.manual_seed(d)
+    new = lambda s, h: torch.randn(2, s, h, d, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, dout, k, v = new(s_q, h_q), new(s_q, h_q), new(s_kv, h_kv), new(s_kv, h_kv)
+    big = 2 ** 31 - 1
+    for plain, largest in (((5000, -1), (big, -1)), ((-1, 5000), (-1, big)), ((5000, 5000), (big, big))):
+        out = []
+        for window in (plain, largest):
+            o, z, ws = fa.forward(q, k, v, window=window)
+            assert fa.device_status(ws) == 0
+            grads = fa.backward(q, k, v, o, z, dout, window=window, flags=fa.FA_FLAG_DETERMINISTIC)
+            assert fa.device_status(grads[-1]) == 0
+            out.append((o, z, *grads[:3]))
+        for x, y in zip(*out):
+            assert torch.isfinite(x.float()).all() and torch.equal(x, y)
