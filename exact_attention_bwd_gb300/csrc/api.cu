@@ -501,6 +501,35 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // Bytes from the first to the last element of T rows of `row` 16-bit values, `stride` apart.
 size_t span16(long T, long stride, long row) { return T > 0 ? ((size_t)(T - 1) * stride + row) * 2 : 0; }
 
+// T rows of `row` 16-bit values, `stride` apart.
+struct Rows {
+    const void* at;
+    long T, stride, row;
+};
+struct Span {
+    const void* at;
+    size_t n;
+};
+
+Rows as_row(const Span& x) { return Rows{x.at, 1, (long)(x.n / 2), (long)(x.n / 2)}; }
+
+bool same(const Rows& x, const Rows& y) { return x.at == y.at && (x.T <= 1 || x.stride == y.stride) && x.row == y.row; }
+
+// Whether two sets of rows share a byte.  Where only their spans do (q and k in one fused projection),
+// the rows say.
+bool share(const Rows& x, const Rows& y) {
+    if (!overlap(x.at, span16(x.T, x.stride, x.row), y.at, span16(y.T, y.stride, y.row))) return false;
+    // in bytes: x's start behind y's, a row, from row to row
+    const long at = (long)(reinterpret_cast<uintptr_t>(x.at) - reinterpret_cast<uintptr_t>(y.at));
+    const long nx = 2 * x.row, ny = 2 * y.row, sx = 2 * x.stride, sy = 2 * y.stride;
+    for (long i = at + nx > 0 ? 0 : -(at + nx) / sx; i < x.T; ++i) {  // (rows before that one end before y starts)
+        const long lo = at + i * sx, j = lo < ny ? 0 : (lo - ny) / sy + 1;  // row i: [lo, lo + nx); the first row of y that ends behind lo
+        if (j < y.T && j * sy < lo + nx) return true;
+        if (sx == sy && lo >= 0) return false;  // the rows behind it lie alike
+    }
+    return false;
+}
+
 fa_status normalise_rope(const fa_rope_params* in, RopeArgs& a) {
     if (!in) return FA_ERR_INVALID_ARG;
     const fa_rope_params& x = *in;
@@ -929,19 +958,31 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const voi
     if (!dq_weight || !dk_weight || !workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
     const int ctas = norm_rope_bwd_ctas(a, sm_count());
     if (ws_bytes < align256((size_t)2 * ctas * a.d * 4)) return FA_ERR_WORKSPACE;
+    const size_t angles = a.rot > 0 ? (size_t)a.max_pos * (a.rot / 2) * 4 : 0, weight = (size_t)a.d * (a.weight_f32 ? 4 : 2);
+    const Span read[] = {{a.positions, (size_t)a.T * 4}, {a.cos, angles}, {a.sin, angles}, {a.wq, weight}, {a.wk, weight}};
+    const Span written[] = {{dq_weight, (size_t)a.d * 4}, {dk_weight, (size_t)a.d * 4}, {workspace, (size_t)2 * ctas * a.d * 4}};
     if (a.T > 0) {
         if (!q || !k || !dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
         if (!aligned16(q) || !aligned16(k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk))
             return FA_ERR_INVALID_ARG;
-        // dq may be q or dq_out, dk may be k or dk_out, in the same layout (strided halves of one
-        // buffer interleave, so their spans say nothing: there, only the same start is looked at)
-        const size_t gq = span16(a.T, wq, wq), gk = span16(a.T, wk, wk);
-        const size_t oq = span16(a.T, (long)in->dq_stride, wq), ok = span16(a.T, (long)in->dk_stride, wk);
-        const bool same_q = dq == q && in->dq_stride == a.q_stride, same_k = dk == k && in->dk_stride == a.k_stride;
-        const bool same_gq = dq == dq_out && in->dq_stride == wq, same_gk = dk == dk_out && in->dk_stride == wk;
-        if ((!same_q && dq == q) || (!same_k && dk == k) || (!same_gq && overlap(dq, oq, dq_out, gq)) ||
-            (!same_gk && overlap(dk, ok, dk_out, gk)) || overlap(dq, oq, dk_out, gk) || overlap(dk, ok, dq_out, gq) || dq == dk)
+        // a row is read whole before its gradient is written: dq may be q or dq_out, dk may be k or dk_out, in
+        // the same layout, and nothing else that the call touches
+        const Rows rq{q, a.T, a.q_stride, wq}, rk{k, a.T, a.k_stride, wk}, gq{dq_out, a.T, wq, wq}, gk{dk_out, a.T, wk, wk};
+        const Rows oq{dq, a.T, (long)in->dq_stride, wq}, ok{dk, a.T, (long)in->dk_stride, wk};
+        if ((!same(oq, rq) && share(oq, rq)) || (!same(oq, gq) && share(oq, gq)) || share(oq, rk) || share(oq, gk) ||
+            (!same(ok, rk) && share(ok, rk)) || (!same(ok, gk) && share(ok, gk)) || share(ok, rq) || share(ok, gq) || share(oq, ok))
             return FA_ERR_INVALID_ARG;
+        for (const Rows& r : {rq, rk, gq, gk, oq, ok})
+            for (const Span& w : written)
+                if (share(r, as_row(w))) return FA_ERR_INVALID_ARG;
+        for (const Span& r : read)
+            if (share(oq, as_row(r)) || share(ok, as_row(r))) return FA_ERR_INVALID_ARG;
+    }
+    for (size_t i = 0; i < 3; ++i) {
+        for (const Span& r : read)
+            if (overlap(written[i].at, written[i].n, r.at, r.n)) return FA_ERR_INVALID_ARG;
+        for (size_t j = 0; j < i; ++j)
+            if (overlap(written[i].at, written[i].n, written[j].at, written[j].n)) return FA_ERR_INVALID_ARG;
     }
     a.q = reinterpret_cast<const uint16_t*>(q);
     a.k = reinterpret_cast<const uint16_t*>(k);

@@ -230,9 +230,10 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * outside [-1, num_slots) is not stored either and sets *status.  Two tokens with one slot
  * leave either's row there.  q_out may be q and k_out may be k (contiguous); other overlaps are refused.
  * fa_qk_norm_rope_bwd takes the inputs and the gradients of q_out and k_out (contiguous) and
- * writes dq, dk (token strides dq_stride, dk_stride; they may be q and k, or dq_out and
- * dk_out, in the same layout) and dq_weight, dk_weight (fp32 [d], written whole, summed in a
- * fixed order: the same bits from call to call).
+ * writes dq, dk (token strides dq_stride, dk_stride; dq may be q or dq_out and dk may be k or
+ * dk_out, in the same layout; rows that share bytes in any other way are refused) and
+ * dq_weight, dk_weight (fp32 [d], written whole, summed in a fixed order: the same bits from
+ * call to call).  These two and the workspace share no byte with anything else of the call.
  * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
  * of 8 elements, base pointers 16-byte aligned. */
 typedef struct fa_rope_params {

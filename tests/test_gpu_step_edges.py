@@ -120,3 +120,27 @@ def test_the_largest_windows_of_dense_calls(s_q, s_kv, h_q, h_kv, d):
             out.append((o, z, *grads[:3]))
         for x, y in zip(*out):
             assert torch.isfinite(x.float()).all() and torch.equal(x, y)
+
+
+def test_gradients_over_their_inputs():
+    """dq and dk over q and k inside one fused projection, over the incoming gradients, and in rows that lie
+    between q's: what does not overlap row by row is taken, with the same bits."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    T, h_q, h_kv, d = 77, 6, 2, 64
+    torch.manual_seed(8)
+    fused = torch.randn(T, 2 * (h_q + 2 * h_kv), d, device="cuda", dtype=torch.bfloat16)
+    dq_out, dk_out = (torch.randn(T, h, d, device="cuda", dtype=torch.bfloat16) for h in (h_q, h_kv))
+    cos, sin = (torch.from_numpy(a).cuda() for a in ref.angles(T, 64))
+    n = h_q + h_kv
+    want = fa.qk_norm_rope_backward(fused[:, :h_q], fused[:, h_q:n], dq_out, dk_out, None, None, cos, sin)
+    dw = lambda: [torch.empty(d, device="cuda") for _ in range(2)]  # noqa: E731
+    for place in ("inputs", "gradients", "between"):
+        x, gq, gk = fused.clone(), dq_out.clone(), dk_out.clone()
+        q, k = x[:, :h_q], x[:, h_q:n]
+        dq, dk = {"inputs": (q, k), "gradients": (gq, gk), "between": (x[:, n + 4:n + 4 + h_q], x[:, n:n + h_kv])}[place]
+        got = fa.qk_norm_rope_backward(q, k, gq, gk, None, None, cos, sin, grads=(dq, dk, *dw()))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), place
+    with pytest.raises(fa.FaError):
+        fa.qk_norm_rope_backward(q, k, gq, gk, None, None, cos, sin, grads=(x[:, 1:1 + h_q], dk, *dw()))
