@@ -445,18 +445,22 @@ def _device_index(t):
 
 
 def _check(dev, *named):
-    """Each (name, tensor or None, dtype, element count): a contiguous tensor of that type and size
-    on device `dev`.  The calls of a serving step are short, so this is written for speed: one
-    expression a tensor, the wording only where it fails."""
-    for name, t, dtype, n in named:
-        if t is None or (t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous()):
+    """Each (name, tensor or None, dtype, size): a contiguous tensor of that type on device `dev`, of the
+    shape `size`, or where that is a number, of so many elements.  The calls of a serving step are short,
+    so this is written for speed: one expression a tensor, the wording only where it fails."""
+    for name, t, dtype, size in named:
+        if t is None or (t.dtype is dtype and t.get_device() == dev and (t.numel() if type(size) is int else t.shape) == size
+                         and t.is_contiguous()):
             continue
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}; every tensor must be on device {dev}")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}; it is {t.dtype}")
-        if t.numel() != n:
-            raise ValueError(f"{name} must have {n} elements; it has {t.numel()}")
+        if type(size) is int:
+            if t.numel() != size:
+                raise ValueError(f"{name} must have {size} elements; it has {t.numel()}")
+        elif t.shape != size:
+            raise ValueError(f"{name} must have the shape {tuple(size)}; it has {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -486,7 +490,7 @@ def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, o
            ("seqused_k", seqused_k, i32, B), ("block_table", block_table, i32, B * blocks), ("sinks", sinks, f32, h_q),
            ("seqused_q", seqused_q, i32, B))
     if out is not None or lse is not None or workspace is not None:
-        _check(dev, ("out", out, kind, T * h_q * d), ("lse", lse, f32, h_q * T),
+        _check(dev, ("out", out, kind, q.shape), ("lse", lse, f32, (h_q, T)),
                ("workspace", workspace, torch.uint8, 0 if workspace is None else workspace.numel()))
     lib = load()
     p = FaParams(B, T, s_kv, h_q, h_kv, d, softmax_scale or 0.0, 1 if causal else 0, window[0], window[1],
@@ -559,7 +563,7 @@ def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, ep
     wtype = kind if wt is None else wt.dtype
     if wtype is not kind and wtype is not torch.float32:
         raise TypeError(f"the weights must be {kind} or float32; they are {wtype}")
-    _check(dev, ("cos", cos, torch.float32, max_pos * half), ("sin", sin, torch.float32, max_pos * half),
+    _check(dev, ("cos", cos, torch.float32, (max_pos, half)), ("sin", sin, torch.float32, (max_pos, half)),
            ("q_weight", q_weight, wtype, d), ("k_weight", k_weight, wtype, d), ("positions", positions, torch.int32, T),
            ("status", status, torch.int32, 1))
     if seq_len is None:
@@ -604,7 +608,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
         p.slots, p.num_slots = slots.data_ptr(), n // (p.h_kv * p.d)
     q_out, k_out = out if out is not None else (None, None)
     if out is not None:
-        _check(dev, ("q_out", q_out, kind, q.numel()), ("k_out", k_out, kind, k.numel()))
+        _check(dev, ("q_out", q_out, kind, q.shape), ("k_out", k_out, kind, k.shape))
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=kind, device=q.device)
     if k_out is None and not append:
@@ -685,8 +689,8 @@ def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, t
         empty, at = torch.empty, cached.device
         out = [empty(n, dtype=i32, device=at) for n in (B + 1, B, tokens, tokens, 1)]
     else:
-        _check(dev, *((name, t, i32, n) for name, t, n in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"),
-                                                              out, (B + 1, B, tokens, tokens, 1))))
+        _check(dev, *((name, t, i32, size) for name, t, size in zip(("cu_seqlens_q", "seqused_k", "positions", "slots", "free_head_out"),
+                                                                    out, ((B + 1,), (B,), (tokens,), (tokens,), 1))))
     cu, used, positions, slots, head_out = out
     p = FaPagePlanParams(B, tokens, page_size, blocks, num_pages, n_free)
     rc = load().fa_page_plan(ctypes.byref(p), cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(),

@@ -86,6 +86,38 @@ def test_gradient_without_eps(T, h_q, h_kv, d, kind):
         assert np.all(err <= 2.0 ** -16 * (g * xh).sum((0, 1)) + 1e-30)
 
 
+def test_results_have_their_shapes():
+    """A result's tensor of the right size and another shape is refused, as in the other forms of the
+    forward: an LSE [T, h_q] would be filled as [h_q, T]."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    c = case([3, 4], [40, 50], h_q=4, h_kv=2, d=64, page=16)
+    args, kw = arguments(c)
+    q = args[0]
+    for bad in (dict(lse=torch.empty(7, 4, device="cuda")), dict(lse=torch.empty(28, device="cuda")),
+                dict(out=torch.empty(4, 7, 64, device="cuda", dtype=q.dtype)), dict(out=torch.empty(7, 256, device="cuda", dtype=q.dtype))):
+        with pytest.raises(ValueError, match="shape"):
+            fa.forward(*args, **kw, **bad)
+    k = torch.randn(7, 2, 64, device="cuda", dtype=q.dtype)
+    cos, sin = (torch.from_numpy(a).cuda() for a in ref.angles(8, 32))
+    rope = dict(positions=i32(np.arange(7)))
+    new = lambda *s: torch.empty(*s, device="cuda", dtype=q.dtype)  # noqa: E731
+    for out in ((new(4, 7, 64), new(7, 2, 64)), (new(7, 4, 64), new(2, 7, 64)), (new(7, 256), None)):
+        with pytest.raises(ValueError, match="shape"):
+            fa.qk_norm_rope(q, k, None, None, cos, sin, **rope, out=out)
+    with pytest.raises(ValueError, match="shape"):
+        fa.qk_norm_rope(q, k, None, None, cos, sin.view(16, 8), **rope)
+    with pytest.raises(ValueError, match="shape"):
+        fa.qk_norm_rope_backward(q, k, q, k, None, None, cos, sin.view(16, 8), **rope)
+    lengths, table = i32([3, 4]), i32(np.zeros((2, 4)))
+    n = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for i, shape in ((0, (1, 3)), (1, (2, 1)), (2, (2, 4)), (3, (4, 2))):
+        out = [n(3), n(2), n(8), n(8), n(1)]
+        out[i] = n(*shape)
+        with pytest.raises(ValueError, match="shape"):
+            fa.page_plan(lengths, lengths, table, i32(np.arange(9)), page_size=16, num_pages=9, tokens=8, out=out)
+
+
 @pytest.mark.parametrize("new,used,d", [([1, 2], [300, 77], 64), ([1, 200], [300, 500], 128), ([300, 3], [300, 9], 256)])
 def test_the_largest_windows(new, used, d):
     """A window of 2^31 - 1 keys to either side is no window: the same bits."""
