@@ -64,7 +64,7 @@ class FaRopeParams(ctypes.Structure):
         ("dq_stride", ctypes.c_longlong), ("dk_stride", ctypes.c_longlong),
         ("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
         ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("slots", ctypes.c_void_p),
-        ("num_slots", ctypes.c_longlong), ("status", ctypes.c_void_p),
+        ("num_slots", ctypes.c_longlong), ("status", ctypes.c_void_p), ("zero_skipped", ctypes.c_int),
     ]
 
 
@@ -584,7 +584,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
     [max_pos, rot_dim / 2] (or None: no rotation); positions int32 [T], by default the token's
     place in its sequence of seq_len (S, or T).  With v, k_cache, v_cache ([num_pages, page_size,
     h_kv, d]) and slots (int32 [T]) keys and values go to the paged cache, and k_out is None
-    unless out = (q_out, k_out) gives one.  status: int32 [1] or None."""
+    unless out = (q_out, k_out) gives one.  A padding token (position -1, or one outside the tables) is
+    skipped: its rows are zero in the tensors made here, and left as they were in given ones and in the
+    cache.  status: int32 [1] or None."""
     import torch
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
@@ -606,13 +608,17 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
         n = k_cache.numel()
         _check(dev, ("k_cache", k_cache, kind, n), ("v_cache", v_cache, kind, n), ("slots", slots, torch.int32, p.T))
         p.slots, p.num_slots = slots.data_ptr(), n // (p.h_kv * p.d)
-    q_out, k_out = out if out is not None else (None, None)
-    if out is not None:
-        _check(dev, ("q_out", q_out, kind, q.shape), ("k_out", k_out, kind, k.shape))
-    if q_out is None:
+    if out is None:
+        p.zero_skipped = 1
         q_out = torch.empty(q.shape, dtype=kind, device=q.device)
-    if k_out is None and not append:
-        k_out = torch.empty(k.shape, dtype=kind, device=q.device)
+        k_out = None if append else torch.empty(k.shape, dtype=kind, device=q.device)
+    else:
+        q_out, k_out = out
+        _check(dev, ("q_out", q_out, kind, q.shape), ("k_out", k_out, kind, k.shape))
+        if q_out is None:
+            q_out = torch.zeros(q.shape, dtype=kind, device=q.device)
+        if k_out is None and not append:
+            k_out = torch.zeros(k.shape, dtype=kind, device=q.device)
     rc = load().fa_qk_norm_rope(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr() if append else None, q_out.data_ptr(),
                                 None if k_out is None else k_out.data_ptr(), k_cache.data_ptr() if append else None,
                                 v_cache.data_ptr() if append else None, torch._C._cuda_getCurrentRawStream(dev))
@@ -627,7 +633,9 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
 
     q, k and the arguments behind dk_out are those of qk_norm_rope; dq_out, dk_out (contiguous)
     are the gradients of its outputs.  grads: (dq, dk, dq_weight, dk_weight) to write, dq and dk at
-    any token stride (slices of a fused projection's gradient); the weights' are fp32 [d]."""
+    any token stride (slices of a fused projection's gradient); the weights' are fp32 [d].  A padding
+    token (position -1, or one outside the tables) has a zero gradient in the tensors made here; in given
+    ones its rows are left as they were."""
     import torch
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
@@ -642,6 +650,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
         empty, at = torch.empty, q.device
         dq, dk = empty(q.shape, dtype=kind, device=at), empty(k.shape, dtype=kind, device=at)
         dwq, dwk = empty(p.d, dtype=torch.float32, device=at), empty(p.d, dtype=torch.float32, device=at)
+        p.zero_skipped = 1
     else:
         dq, dk, dwq, dwk = grads
         if dq.shape != q.shape or dk.shape != k.shape:

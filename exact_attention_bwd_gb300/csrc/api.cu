@@ -562,6 +562,7 @@ fa_status normalise_rope(const fa_rope_params* in, RopeArgs& a) {
     a.wq = x.q_weight;
     a.wk = x.k_weight;
     a.status = x.status;
+    a.zero_skipped = x.zero_skipped ? 1 : 0;
     return FA_OK;
 }
 

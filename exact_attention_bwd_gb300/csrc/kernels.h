@@ -175,6 +175,7 @@ struct RopeArgs {
     const uint16_t *dq_out, *dk_out;
     uint16_t *dq, *dk;
     float *dwq, *dwk, *dw_part;
+    int zero_skipped;          // q_out and k_out (dq and dk) of skipped tokens become 0
     int* status;
     int unit_rows, kv_rows, warps;  // rows a warp takes at a time (of k and v together), warps that walk over them
 };

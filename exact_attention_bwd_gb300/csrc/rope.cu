@@ -273,6 +273,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     uint32_t phase = 0;  // bit b: the parity buffer b's next copies complete
     for (int b = 0; now.t < a.T; now.next(), b = b + 1 == kBufs ? 0 : b + 1) {
         const RowMeta meta = s.meta[b];
+        int kind, r0, rows;
+        unit(now.x, kind, r0, rows);
+        uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
         if (meta.pos >= 0) {
             // (bounded; on the way out, the copies of the other buffers end with the same limit)
             if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
@@ -282,11 +285,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
                 return;
             }
             phase ^= 1u << b;
-            int kind, r0, rows;
-            unit(now.x, kind, r0, rows);
             const uint8_t* in = s.buf[b].rows;
             const bool cached = kind && meta.slot >= 0;
-            uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
             const long in_cache = ((long)meta.slot * a.h_kv + r0) * D;
             uint16_t* out1 = cached ? a.k_cache + in_cache : nullptr;
             if (cached)
@@ -330,6 +330,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
                     }
                 }
             }
+        } else if (a.zero_skipped && out0) {
+            for (int y = lane; y < rows * D / 8; y += 32) reinterpret_cast<uint4*>(out0)[y] = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();  // the buffer has been read
         issue(b);
@@ -398,6 +400,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
         for (int b = 0; b < kBufs; ++b) issue(b);
         __syncwarp();
         for (int b = 0; !failed && now.t < a.T; now.next(), b = b + 1 == kBufs ? 0 : b + 1) {
+            const int r0 = now.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
+            uint16_t* pd = ds + now.t * dstride + (long)r0 * D;
             if (s.meta[b].pos >= 0) {
                 if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
                     if (lane == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout);
@@ -407,9 +411,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                     break;
                 }
                 phase ^= 1u << b;
-                const int r0 = now.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
                 const uint8_t *px = s.buf[b].rows, *pg = px + kUnitBytes / 2;
-                uint16_t* pd = ds + now.t * dstride + (long)r0 * D;
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
 #pragma unroll 2
@@ -456,6 +458,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                         *reinterpret_cast<uint4*>(pd + r * D + 8 * u1) = narrow8<F16>(v + 4);
                     }
                 }
+            } else if (a.zero_skipped) {
+                for (int y = lane; y < rows * D / 8; y += 32) reinterpret_cast<uint4*>(pd)[y] = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();  // the buffer has been read
             issue(b);

@@ -221,7 +221,8 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  *   (a, b) -> (a cos - b sin, b cos + a sin).
  * The pairs are (j, j + rot_dim / 2), or with `interleaved` (2j, 2j + 1), j < rot_dim / 2, and use
  * cos[pos][j], sin[pos][j].  pos is positions[t], or t % seq_len without positions.  A token
- * at position -1 is padding and is skipped (its outputs are left as they were); any other
+ * at position -1 is padding and is skipped (its rows of the outputs are left as they were, or
+ * with zero_skipped become 0; a cache is left alone either way); any other
  * position outside [0, max_pos) is skipped too and sets *status (when given) to
  * FA_ERR_DEVICE_CHECK.  Statistics and products are fp32, outputs are rounded once.
  * fa_qk_norm_rope writes q_out [T, h_q, d] and k_out [T, h_kv, d] (contiguous).  With k_cache,
@@ -233,7 +234,8 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * writes dq, dk (token strides dq_stride, dk_stride; dq may be q or dq_out and dk may be k or
  * dk_out, in the same layout; rows that share bytes in any other way are refused) and
  * dq_weight, dk_weight (fp32 [d], written whole, summed in a fixed order: the same bits from
- * call to call).  These two and the workspace share no byte with anything else of the call.
+ * call to call).  A skipped token adds nothing to them.  They and the workspace share no byte
+ * with anything else of the call.
  * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
  * of 8 elements, base pointers 16-byte aligned. */
 typedef struct fa_rope_params {
@@ -254,6 +256,7 @@ typedef struct fa_rope_params {
     const int32_t *slots;                     /* device int32 [T]: cache rows, or NULL */
     long long num_slots;                      /* num_pages * page_size */
     int32_t *status;                          /* device int32, set on a bad position or slot, never cleared; or NULL */
+    int zero_skipped;                         /* q_out, k_out (dq, dk) of skipped tokens become 0 */
 } fa_rope_params;
 
 fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k, const void *v, void *q_out, void *k_out,

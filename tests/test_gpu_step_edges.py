@@ -154,6 +154,51 @@ def test_the_largest_windows_of_dense_calls(s_q, s_kv, h_q, h_kv, d):
             assert torch.isfinite(x.float()).all() and torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dense", [False, True])
+def test_padding_tokens(dense):
+    """Without tensors to write the binding makes the results, and the rows of tokens that take no part are zero
+    in them rather than whatever the memory held; in given ones, and in the cache, they stay as they were."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    T, h_q, h_kv, d = 66, 9, 5, 128
+    shape = lambda h: (2, T // 2, h, d) if dense else (T, h, d)  # noqa: E731
+    torch.manual_seed(5)
+    new = lambda h: torch.randn(shape(h), device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, dq_out, k, dk_out, v = new(h_q), new(h_q), new(h_kv), new(h_kv), new(h_kv)
+    cos, sin = (torch.from_numpy(a).cuda() for a in ref.angles(50, 64))
+    pos = np.arange(T) % 40
+    pos[[0, 13, 14, 40, 65]] = -1
+    pos[20] = 50  # (outside the table)
+    skip = torch.from_numpy((pos < 0) | (pos >= 50)).cuda()
+    tables, kw = (None, None, cos, sin), dict(positions=i32(pos))
+
+    def poison():  # (what the allocator hands out next)
+        dirty = [torch.full((T * h, d), float("nan"), device="cuda", dtype=torch.bfloat16) for h in (h_q, h_kv) for _ in range(4)]
+        del dirty
+
+    pools = [torch.full((5, 16, h_kv, d), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    append = dict(v=v, k_cache=pools[0], v_cache=pools[1], slots=i32(np.arange(T)))
+    for run, given in (
+            (lambda **o: fa.qk_norm_rope(q, k, *tables, **kw, **o), lambda x: dict(out=x)),
+            (lambda **o: fa.qk_norm_rope(q, k, *tables, **kw, **append, **o), lambda x: dict(out=x)),
+            (lambda **o: fa.qk_norm_rope_backward(q, k, dq_out, dk_out, *tables, **kw, **o), lambda x: dict(grads=x))):
+        poison()
+        got = run()
+        own = tuple(None if x is None else torch.full_like(x, 7.0) for x in got)
+        run(**given(own))
+        for x, y in zip(got[:2], own[:2]):
+            if x is not None:
+                x, y = x.reshape(T, -1), y.reshape(T, -1)
+                assert torch.all(x[skip] == 0) and torch.all(y[skip] == 7) and torch.equal(x[~skip], y[~skip])
+        for x, y in zip(got[2:], own[2:]):
+            assert torch.equal(x, y)
+    for pool in pools:
+        assert torch.all(pool.view(80, -1)[:T][skip] == 7) and not torch.any(pool.view(80, -1)[:T][~skip] == 7)
+    poison()
+    k_new = fa.qk_norm_rope(q, k, *tables, **kw, out=(torch.empty_like(q), None))[1]
+    assert torch.all(k_new.reshape(T, -1)[skip] == 0)
+
+
 def test_gradients_over_their_inputs():
     """dq and dk over q and k inside one fused projection, over the incoming gradients, and in rows that lie
     between q's: what does not overlap row by row is taken, with the same bits."""
