@@ -65,6 +65,7 @@ class FaRopeParams(ctypes.Structure):
         ("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
         ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("slots", ctypes.c_void_p),
         ("num_slots", ctypes.c_longlong), ("status", ctypes.c_void_p), ("zero_skipped", ctypes.c_int),
+        ("wait_limit_ns", ctypes.c_ulonglong),
     ]
 
 
@@ -576,7 +577,7 @@ def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, ep
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6, interleaved=False,
-                 v=None, k_cache=None, v_cache=None, slots=None, out=None, status=None):
+                 v=None, k_cache=None, v_cache=None, slots=None, out=None, status=None, wait_limit_ns=0):
     """Runs fa_qk_norm_rope on torch CUDA tensors; returns (q_out, k_out).
 
     q [T, h_q, d] and k [T, h_kv, d] (or [B, S, h, d]) may be slices of a fused projection;
@@ -586,13 +587,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
     h_kv, d]) and slots (int32 [T]) keys and values go to the paged cache, and k_out is None
     unless out = (q_out, k_out) gives one.  A padding token (position -1, or one outside the tables) is
     skipped: its rows are zero in the tensors made here, and left as they were in given ones and in the
-    cache.  status: int32 [1] or None."""
+    cache.  status: int32 [1] or None (bad positions and slots, and a wait past wait_limit_ns, are then not
+    reported)."""
     import torch
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions=positions, seq_len=seq_len, eps=eps,
-                          interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status)
+                          interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status,
+                          wait_limit_ns=wait_limit_ns)
     p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    p.wait_limit_ns = wait_limit_ns
     kind = q.dtype
     append = v is not None or k_cache is not None or v_cache is not None or slots is not None
     if append:
@@ -628,7 +632,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6,
-                          interleaved=False, grads=None, workspace=None, status=None):
+                          interleaved=False, grads=None, workspace=None, status=None, wait_limit_ns=0):
     """Runs fa_qk_norm_rope_bwd on torch CUDA tensors; returns (dq, dk, dq_weight, dk_weight).
 
     q, k and the arguments behind dk_out are those of qk_norm_rope; dq_out, dk_out (contiguous)
@@ -640,8 +644,10 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope_backward, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions=positions,
-                          seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status)
+                          seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status,
+                          wait_limit_ns=wait_limit_ns)
     p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+    p.wait_limit_ns = wait_limit_ns
     kind = q.dtype
     _check(dev, ("dq_out", dq_out, kind, q.numel()), ("dk_out", dk_out, kind, k.numel()))
     if dq_out.shape != q.shape or dk_out.shape != k.shape:

@@ -563,6 +563,7 @@ fa_status normalise_rope(const fa_rope_params* in, RopeArgs& a) {
     a.wk = x.k_weight;
     a.status = x.status;
     a.zero_skipped = x.zero_skipped ? 1 : 0;
+    a.wait_ns = x.wait_limit_ns ? x.wait_limit_ns : kWaitLimitNsDefault;
     return FA_OK;
 }
 

@@ -177,6 +177,7 @@ struct RopeArgs {
     float *dwq, *dwk, *dw_part;
     int zero_skipped;          // q_out and k_out (dq and dk) of skipped tokens become 0
     int* status;
+    unsigned long long wait_ns;  // bound on each wait
     int unit_rows, kv_rows, warps;  // rows a warp takes at a time (of k and v together), warps that walk over them
 };
 

@@ -129,6 +129,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     }
 }
 
+// The same for a warp on its own, which gives up by itself.  A suspended try can outlast a hint of 1 ns by
+// more than a copy from memory takes, so limits below kShortLimitNs are kept by tests that do not suspend.
+constexpr unsigned long long kShortLimitNs = 100000;
+__device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity, unsigned long long limit) {
+    if (limit >= kShortLimitNs && mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    do {
+        if (limit >= kShortLimitNs ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+    } while (globaltimer() - t0 <= limit);
+    return false;
+}
+
 // Bounded wait used while draining at exit: gives up after the fixed 2 s limit (not the
 // call's limit: every copy and MMA already issued must land before the CTA exits),
 // without touching the abort state (the CTA is already on its way out).

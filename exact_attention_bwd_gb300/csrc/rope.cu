@@ -201,6 +201,19 @@ struct UnitWalk {
     }
 };
 
+// Bits of the buffers with copies on their way (lane 0's; the others leave it alone).  What a warp does when
+// a wait ran out: the status, and then (with the fixed limit) the wait for the copies under way, which
+// must not land in shared memory that is not the warp's any more.
+template <class S>
+__device__ __forceinline__ void give_up(S& s, uint32_t flight, uint32_t phase, int* status) {
+    if ((threadIdx.x & 31) == 0) {
+        if (status) atomicCAS(status, 0, kStatusTimeout);
+        for (int b = 0; b < kBufs; ++b)
+            if ((flight >> b) & 1) mbar_wait_quiet(&s.full[b], (phase >> b) & 1);
+    }
+    __syncwarp();
+}
+
 // One run of units: `heads` rows of each token in groups of `rows`.
 __device__ __forceinline__ int groups_of(int heads, int rows) { return (heads + rows - 1) / rows; }
 
@@ -223,6 +236,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     UnitWalk ahead(me, n_warps, per_token), now = ahead;
     if (me >= n_warps) ahead.t = now.t = a.T;
     int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0)
+    uint32_t flight = 0;                // buffers with copies on their way (lane 0)
     auto look = [&]() {
         if (lane == 0 && ahead.t < a.T) {
             next_pos = position_of(a, ahead.t);
@@ -245,6 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
                 const bool with_v = kind && a.v;
                 const uint16_t* src = (kind ? a.k + ahead.t * a.k_stride : a.q + ahead.t * a.q_stride) + (long)r0 * D;
                 const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                flight |= 1u << b;
                 mbar_expect_tx(&s.full[b], (with_v ? 2 : 1) * bytes + 2 * angle);
                 bulk_load(s.buf[b].rows, src, bytes, &s.full[b]);
                 if (with_v) bulk_load(s.buf[b].rows + kUnitBytes / 2, a.v + ahead.t * a.v_stride + (long)r0 * D, bytes, &s.full[b]);
@@ -277,14 +292,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         unit(now.x, kind, r0, rows);
         uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
         if (meta.pos >= 0) {
-            // (bounded; on the way out, the copies of the other buffers end with the same limit)
-            if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
-                if (lane == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout);
-                for (int z = 0; z < kBufs; ++z)
-                    if (z != b && s.meta[z].pos >= 0) mbar_wait_quiet(&s.full[z], (phase >> z) & 1);
+            if (!__all_sync(0xffffffffu, mbar_wait_within(&s.full[b], (phase >> b) & 1, a.wait_ns))) {
+                give_up(s, flight, phase, a.status);
                 return;
             }
             phase ^= 1u << b;
+            flight &= ~(1u << b);
             const uint8_t* in = s.buf[b].rows;
             const bool cached = kind && meta.slot >= 0;
             const long in_cache = ((long)meta.slot * a.h_kv + r0) * D;
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
     }
     __syncwarp();
     const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
-    uint32_t phase = 0;
+    uint32_t phase = 0, flight = 0;
     bool failed = false;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
@@ -384,6 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                 if (next_pos >= 0) {
                     const int r0 = ahead.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
                     const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                    flight |= 1u << b;
                     mbar_expect_tx(&s.full[b], 2 * bytes + 2 * angle);
                     bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
                     bulk_load(s.buf[b].rows + kUnitBytes / 2, gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
@@ -396,21 +410,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
             ahead.next();
             look();
         };
-        look();
-        for (int b = 0; b < kBufs; ++b) issue(b);
+        if (!failed) {
+            look();
+            for (int b = 0; b < kBufs; ++b) issue(b);
+        }
         __syncwarp();
         for (int b = 0; !failed && now.t < a.T; now.next(), b = b + 1 == kBufs ? 0 : b + 1) {
             const int r0 = now.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
             uint16_t* pd = ds + now.t * dstride + (long)r0 * D;
             if (s.meta[b].pos >= 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait_quiet(&s.full[b], (phase >> b) & 1))) {
-                    if (lane == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout);
-                    for (int z = 0; z < kBufs; ++z)
-                        if (z != b && s.meta[z].pos >= 0) mbar_wait_quiet(&s.full[z], (phase >> z) & 1);
+                if (!__all_sync(0xffffffffu, mbar_wait_within(&s.full[b], (phase >> b) & 1, a.wait_ns))) {
+                    give_up(s, flight, phase, a.status);
                     failed = true;  // (the CTA's sums below still need every warp)
                     break;
                 }
                 phase ^= 1u << b;
+                flight &= ~(1u << b);
                 const uint8_t *px = s.buf[b].rows, *pg = px + kUnitBytes / 2;
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);

@@ -236,6 +236,8 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * dq_weight, dk_weight (fp32 [d], written whole, summed in a fixed order: the same bits from
  * call to call).  A skipped token adds nothing to them.  They and the workspace share no byte
  * with anything else of the call.
+ * A wait that passes wait_limit_ns ends the call's work early and sets *status to FA_ERR_TIMEOUT
+ * (the outputs are then unspecified); without a status word the caller does not learn of it.
  * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
  * of 8 elements, base pointers 16-byte aligned. */
 typedef struct fa_rope_params {
@@ -255,8 +257,9 @@ typedef struct fa_rope_params {
     const void *q_weight, *k_weight;          /* device [d], or NULL (ones) */
     const int32_t *slots;                     /* device int32 [T]: cache rows, or NULL */
     long long num_slots;                      /* num_pages * page_size */
-    int32_t *status;                          /* device int32, set on a bad position or slot, never cleared; or NULL */
+    int32_t *status;                          /* device int32, set on a bad position or slot or a timeout, never cleared; or NULL */
     int zero_skipped;                         /* q_out, k_out (dq, dk) of skipped tokens become 0 */
+    unsigned long long wait_limit_ns;         /* bound on each wait of the kernels; 0 = 2 s */
 } fa_rope_params;
 
 fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k, const void *v, void *q_out, void *k_out,

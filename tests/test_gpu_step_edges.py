@@ -221,3 +221,46 @@ def test_gradients_over_their_inputs():
             assert torch.equal(a, b), place
     with pytest.raises(fa.FaError):
         fa.qk_norm_rope_backward(q, k, gq, gk, None, None, cos, sin, grads=(x[:, 1:1 + h_q], dk, *dw()))
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,kind", [(64, 16, 4, "f16"), (128, 32, 8, "bf16"), (192, 6, 2, "bf16"), (256, 16, 2, "bf16")])
+@pytest.mark.parametrize("form", ["forward", "append", "gradient"])
+@pytest.mark.parametrize("rows", ["in the L2", "in memory", "in memory, positions by place"])
+def test_norm_rope_wait_limit(form, d, h_q, h_kv, kind, rows):
+    """A limit of 1 ns on the waits ends the call with a timeout status, or, where every copy had landed by the
+    time that it was looked for, with a right result.  Copies lag for certain where rows come from memory and
+    neither positions nor slots are read ahead of them (a read takes as long as a copy).  The same call with
+    a long limit, next, has the bits that it had before."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    torch.manual_seed(d)
+    T, page = 8192 if rows == "in the L2" else 2 ** 27 // (h_q * d) // 64 * 64, 64
+    new = lambda h: torch.randn(T, h, d, device="cuda").to(torch.bfloat16 if kind == "bf16" else torch.float16)  # noqa: E731
+    q, k, v, dq_out, dk_out = new(h_q), new(h_kv), new(h_kv), new(h_q), new(h_kv)
+    cos, sin = (torch.from_numpy(a).cuda() for a in ref.angles(8192, d))
+    places = dict(seq_len=8192) if rows.endswith("place") else dict(positions=i32(np.arange(T) % 8192))
+    lags = rows.endswith("place") and form != "append"
+    pools = [torch.zeros(T // page, page, h_kv, d, device="cuda", dtype=q.dtype) for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(**kw):
+        status.zero_()
+        kw.update(**places, status=status)
+        if form == "gradient":
+            return fa.qk_norm_rope_backward(q, k, dq_out, dk_out, None, None, cos, sin, **kw)
+        if form == "forward":
+            return fa.qk_norm_rope(q, k, None, None, cos, sin, **kw)
+        q_out, _ = fa.qk_norm_rope(q, k, None, None, cos, sin, v=v, k_cache=pools[0], v_cache=pools[1], slots=i32(np.arange(T)), **kw)
+        return q_out, pools[0].clone(), pools[1].clone()
+
+    want = run()
+    assert status.item() == 0
+    for _ in range(3):
+        for limit in (1, 10 ** 9):
+            got = run(wait_limit_ns=limit)
+            code = status.item()
+            assert code == 0 or (limit == 1 and code == fa.FA_ERR_TIMEOUT)
+            assert limit > 1 or code == fa.FA_ERR_TIMEOUT or not lags
+            if code == 0:
+                for x, y in zip(got, want):
+                    assert torch.equal(x, y)
