@@ -9,6 +9,7 @@ import pytest
 import step_helpers as ref
 from gpu_helpers import from_dev
 from test_gpu_norm_rope import TYPES, dev
+from test_gpu_page_plan import compare as plan_compare
 from test_gpu_paged import HALF, case
 from test_gpu_step_calls import arguments, i32
 
@@ -116,6 +117,17 @@ def test_results_have_their_shapes():
         out[i] = n(*shape)
         with pytest.raises(ValueError, match="shape"):
             fa.page_plan(lengths, lengths, table, i32(np.arange(9)), page_size=16, num_pages=9, tokens=8, out=out)
+
+
+@pytest.mark.parametrize("P,width,cached,fresh", [
+    (3 << 29, 1, [(3 << 29) - 1, 0], [1, 0]), (3 << 28, 2, [(3 << 28) + 7, 5, 2 * (3 << 28) - 2], [3, 2, 2]), (2 ** 31 - 1, 1, [2 ** 31 - 5, 1], [4, 3]),
+])
+def test_page_plan_of_the_largest_pages(P, width, cached, fresh):
+    """Page sizes and lengths whose sum passes 31 bits."""
+    pages = (2 ** 31 - 1) // P
+    plan_compare(dict(cached=np.asarray(cached, np.int32), fresh=np.asarray(fresh, np.int32),
+                      table=np.tile(np.arange(width, dtype=np.int32) % pages, (len(cached), 1)), free=np.zeros(0, np.int32), head=0, P=P,
+                      num_pages=pages, T=sum(fresh) + 2))
 
 
 @pytest.mark.parametrize("new,used,d", [([1, 2], [300, 77], 64), ([1, 200], [300, 500], 128), ([300, 3], [300, 9], 256)])
