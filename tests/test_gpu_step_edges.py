@@ -276,3 +276,26 @@ def test_norm_rope_wait_limit(form, d, h_q, h_kv, kind, rows):
             if code == 0:
                 for x, y in zip(got, want):
                     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,new,used,hint", [
+    *((d, h, 1, [n], [used], n) for d, used in ((64, 60000), (128, 60000), (192, 40000), (256, 40000)) for h, n in ((8, 1), (16, 2), (16, 4))),
+    (64, 8, 2, [300], [20000], 0), (128, 8, 2, [300], [20000], 0), (128, 8, 2, [300, 1], [20000, 9000], 0), (192, 8, 2, [300], [9000], 0),
+    (256, 8, 2, [300], [9000], 0),
+])
+def test_paged_wait_limit_of_every_kernel(d, h_q, h_kv, new, used, hint):
+    """A limit of 1 ns ends the call with a timeout status in each variant of either kernel (16, 32 and 64 rows;
+    chunks): every CTA waits for dozens of tiles from memory.  The next call, without the limit, is right."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    args, kw = arguments(case(new, used, h_q=h_q, h_kv=h_kv, d=d, page=64), hint)
+    want, want_lse, ws = fa.forward(*args, **kw)
+    assert fa.device_status(ws) == 0
+    flush = torch.empty(64 << 20, device="cuda")  # 256 MB, twice the L2
+    for _ in range(3):
+        flush.fill_(1.0)
+        _, _, ws = fa.forward(*args, **kw, wait_limit_ns=1)
+        assert fa.device_status(ws) == fa.FA_ERR_TIMEOUT
+        o, z, ws = fa.forward(*args, **kw)
+        assert fa.device_status(ws) == 0
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(z, want_lse)
