@@ -229,7 +229,7 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * v_cache (pools of num_slots rows [h_kv, d]), slots and v it also writes the key's row and a
  * copy of v's to row slots[t] of the pools (k_out may then be NULL); slot -1 is not stored, one
  * outside [-1, num_slots) is not stored either and sets *status.  Two tokens with one slot
- * leave either's row there.  q_out may be q and k_out may be k (contiguous); other overlaps are refused.
+ * leave a mix of their rows there (each 16 bytes one's or the other's).  q_out may be q and k_out may be k (contiguous); other overlaps are refused.
  * fa_qk_norm_rope_bwd takes the inputs and the gradients of q_out and k_out (contiguous) and
  * writes dq, dk (token strides dq_stride, dk_stride; dq may be q or dq_out and dk may be k or
  * dk_out, in the same layout; rows that share bytes in any other way are refused) and

@@ -211,6 +211,25 @@ def test_padding_tokens(dense):
     assert torch.all(k_new.reshape(T, -1)[skip] == 0)
 
 
+def test_one_slot_twice():
+    """Two tokens with one slot leave values of either there, eight at a time, and every other row alone."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    T, h_q, h_kv, d, page = 300, 4, 2, 128, 16
+    torch.manual_seed(6)
+    q, k, v = (torch.randn(T, h, d, device="cuda", dtype=torch.bfloat16) for h in (h_q, h_kv, h_kv))
+    slots = np.arange(T) // 2 * 3
+    pools = [torch.full((-(-int(slots.max() + 1) // page), page, h_kv, d), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    _, k_out = fa.qk_norm_rope(q, k, None, None, None, None)
+    fa.qk_norm_rope(q, k, None, None, None, None, v=v, k_cache=pools[0], v_cache=pools[1], slots=i32(slots))
+    for pool, rows in zip(pools, (k_out, v)):
+        pool, rows = pool.view(-1, h_kv * d // 8, 8), rows.reshape(T, -1, 8)
+        first, second = ((pool[slots[::2]] == rows[n::2]).all(-1) for n in range(2))
+        assert torch.all(first | second)
+        others = np.setdiff1d(np.arange(len(pool)), slots)
+        assert torch.all(pool[others] == 7)
+
+
 def test_gradients_over_their_inputs():
     """dq and dk over q and k inside one fused projection, over the incoming gradients, and in rows that lie
     between q's: what does not overlap row by row is taken, with the same bits."""
