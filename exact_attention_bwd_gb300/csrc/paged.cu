@@ -165,7 +165,7 @@ struct FewCfg {
     static constexpr int MOST = D == 64 ? 12 : 6;
     static constexpr int RING = ISSUERS == 2 ? (FIT > MOST ? MOST : FIT / 2 * 2) : (FIT > MOST ? MOST : FIT);
     static_assert(ISSUERS == 1 || (KU == 1 && RING % 2 == 0), "slots of their own");
-    static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile and the next K have to fit");
+    static_assert(RING >= 3 && RING >= 2 * KU, "a K and a V tile have to fit");
     // Some unit of a tile's V takes the slot of a unit of the V before it (d = 256 at 32 and 64 rows,
     // rings of 5 and 4 units): by parity, a wait for its arrival would also pass while the
     // one before has not arrived yet.

@@ -58,7 +58,8 @@ struct PagedLine {
         return u < head ? (int)(u / (each + 1)) : more + (int)((u - head) / each);
     }
 };
-// Each CTA has more units than a lead.
+// With more than one CTA a stretch has kLead units at least (4 units: two of 2).  One that ends among
+// the lead of the item that it starts passes the item on, so a CTA may be left without a tile.
 __device__ __forceinline__ PagedLine paged_line(long long units, int n_ctas) {
     PagedLine x;
     x.units = units;

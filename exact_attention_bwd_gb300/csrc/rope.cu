@@ -356,6 +356,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
 // the buffer and the weight gradient of the lane's own values in registers.  Each CTA adds its
 // warps' sums in a fixed order and stores them as one row of the workspace; norm_rope_dw_kernel
 // adds the rows, again in a fixed order, so the gradients are the same bits from call to call.
+// The sums are fp32: a term carries fp32 roundings already, and with a lane's chain followed by trees over
+// lanes, warps and CTAs the error stays within 2^-16 of the sum of the terms' sizes.
 template <int D, bool F16, bool ADJ>
 __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const RopeArgs a) {
     using C = RowCfg<D>;
