@@ -337,7 +337,8 @@ def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks
     """Runs fa_fwd on torch CUDA tensors; returns (o, lse, workspace).
 
     Packed queries over a paged cache: q [T, h_q, d] with cu_q, seqused_k, block_table and s_kv
-    (no cu_k); max_seqlen_q is the most new tokens of a sequence, if the caller knows it.
+    (no cu_k); max_seqlen_q is the most new tokens of a sequence, if the caller knows it.  Rows that no
+    sequence covers are not written, in given tensors or in those made here.
 
     q, k, v are all bfloat16, all float16, or all uint8 = e4m3 bytes (FA_DTYPE_E4M3);
     descale = (q, k, v) fp32 [B * h_kv] factors or None (all 1).  The output has the

@@ -28,7 +28,7 @@ namespace {
 // 12 warps of two 8 KB buffers fill the shared memory.  Measured, forward / gradient of 16384
 // tokens of 32 + 8 heads of 128 and append of 8192 tokens of 16 + 2 heads of 256 (with v in units of
 // its own), us: 54.7 / 85.1 / 32.4; 8 warps of three 64.0 / 103.0 / 39.6; 12 of three 4 KB ones 60.5 / 99.5 / 37.0; 16 of two
-// 4 KB ones 58.1 / 101.1 / 32.8.  (At the copy rate: 50.8 / 75.8 / 25.4.)
+// 4 KB ones 58.1 / 101.1 / 32.8.  (At the copy rate: 50.1 / 74.8 / 25.0.)
 constexpr int kWarps = 12;
 constexpr int kBufs = 2;           // units in flight per warp
 constexpr int kUnitBytes = 8192;   // rows of a unit at most (gradient: half of it x, half dy)
