@@ -32,7 +32,11 @@ FA_DTYPE_F16 = 2
 
 EXPORTS = ("fa_fwd", "fa_bwd", "fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_read_device_status",
            "fa_status_string", "fa_profile_enable", "fa_profile_read", "fa_version", "fa_fwd_noalloc",
-           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_page_plan")
+           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_page_plan",
+           "fa_qk_norm_rope_append8")
+
+FA_ROPE_MAX_AXES = 4
+FA_ROPE_MAX_PAIRS = 128
 
 FA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -65,8 +69,16 @@ class FaRopeParams(ctypes.Structure):
         ("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
         ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("slots", ctypes.c_void_p),
         ("num_slots", ctypes.c_longlong), ("status", ctypes.c_void_p), ("zero_skipped", ctypes.c_int),
-        ("wait_limit_ns", ctypes.c_ulonglong),
+        ("wait_limit_ns", ctypes.c_ulonglong), ("axes", ctypes.c_int), ("no_norm", ctypes.c_int),
+        ("pair_axis", ctypes.c_ubyte * FA_ROPE_MAX_PAIRS),
     ]
+
+
+class FaCache8Params(ctypes.Structure):
+    """Mirror of ``fa_cache8_params``."""
+    _fields_ = [("B", ctypes.c_int), ("page_size", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("scale_block", ctypes.c_int), ("cu_seqlens_q", ctypes.c_void_p), ("seqused_k", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p)]
 
 
 class FaPagePlanParams(ctypes.Structure):
@@ -135,6 +147,8 @@ def load(build_if_missing: bool = True):
         lib.fa_qk_norm_rope_bwd.restype = ctypes.c_int
         lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [R]
         lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+        lib.fa_qk_norm_rope_append8.argtypes = [R, ctypes.POINTER(FaCache8Params)] + [vp] * 9
+        lib.fa_qk_norm_rope_append8.restype = ctypes.c_int
         lib.fa_page_plan.argtypes = [L] + [vp] * 12
         lib.fa_page_plan.restype = ctypes.c_int
         lib.fa_version.argtypes = []
@@ -182,6 +196,12 @@ def fa_qk_norm_rope_bwd(params: FaRopeParams, q, k, dq_out, dk_out, dq, dk, dq_w
                         stream) -> int:
     return load().fa_qk_norm_rope_bwd(ctypes.byref(params), q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace,
                                       workspace_bytes, stream)
+
+
+def fa_qk_norm_rope_append8(params: FaRopeParams, cache: FaCache8Params, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale,
+                            stream) -> int:
+    return load().fa_qk_norm_rope_append8(ctypes.byref(params), ctypes.byref(cache), q, k, v, q_out, k_cache, v_cache, k_scale,
+                                          v_scale, stream)
 
 
 def fa_page_plan(params: FaPagePlanParams, cached, fresh, free_pages, free_head, block_table, cu_seqlens_q, seqused_k,
@@ -545,7 +565,26 @@ def _like(name, t, kind, dev):
         raise TypeError(f"{name} must have the type and device of q")
 
 
-def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status):
+def _set_axes(p, positions, pair_axis, norm):
+    """The parameters' axes (positions [axes, T], the axis of each pair) and whether there is a norm."""
+    p.no_norm = 0 if norm else 1
+    if pair_axis is None:
+        return
+    p.axes = axes = positions.shape[0]
+    if not 1 <= axes <= FA_ROPE_MAX_AXES:
+        raise ValueError(f"positions must have 1 to {FA_ROPE_MAX_AXES} axes; they have {axes}")
+    if len(pair_axis) != p.rot_dim // 2:
+        raise ValueError(f"pair_axis must have {p.rot_dim // 2} entries, one for each pair; it has {len(pair_axis)}")
+    try:
+        pairs = bytes(pair_axis)
+    except (TypeError, ValueError):
+        pairs = b"\xff"
+    if pairs and max(pairs) >= axes:
+        raise ValueError(f"pair_axis must hold axes (0 to {axes - 1})")
+    ctypes.memmove(p.pair_axis, pairs, len(pairs))
+
+
+def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status, pair_axis, norm):
     import torch
     T, h_q, d, q_stride = _rows("q", q)
     kind = q.dtype
@@ -558,6 +597,10 @@ def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, ep
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must have the same tokens and head dimension")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
+    if pair_axis is not None and (positions is None or positions.dim() < 2):
+        raise ValueError("pair_axis goes with positions [axes, T]")
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("without the norm there are no weights")
     max_pos = half = 0
     if cos is not None:
         max_pos, half = cos.shape
@@ -566,25 +609,32 @@ def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, ep
     if wtype is not kind and wtype is not torch.float32:
         raise TypeError(f"the weights must be {kind} or float32; they are {wtype}")
     _check(dev, ("cos", cos, torch.float32, (max_pos, half)), ("sin", sin, torch.float32, (max_pos, half)),
-           ("q_weight", q_weight, wtype, d), ("k_weight", k_weight, wtype, d), ("positions", positions, torch.int32, T),
+           ("q_weight", q_weight, wtype, d), ("k_weight", k_weight, wtype, d),
+           ("positions", positions, torch.int32, T if pair_axis is None or positions is None else positions.shape[0] * T),
            ("status", status, torch.int32, 1))
     if seq_len is None:
         seq_len = max(1, q.shape[1] if q.dim() == 4 else T)
-    return FaRopeParams(T, h_q, h_kv, d, 2 * half, 1 if interleaved else 0, seq_len, max_pos, eps, code, 1 if wtype is not kind else 0,
+    p = FaRopeParams(T, h_q, h_kv, d, 2 * half, 1 if interleaved else 0, seq_len, max_pos, eps, code, 1 if wtype is not kind else 0,
                         q_stride, k_stride, h_kv * d, h_q * d, h_kv * d, None if positions is None else positions.data_ptr(),
                         None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
                         None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
                         None, 0, None if status is None else status.data_ptr())
+    if not norm or pair_axis is not None:
+        _set_axes(p, positions, pair_axis, norm)
+    return p
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6, interleaved=False,
-                 v=None, k_cache=None, v_cache=None, slots=None, out=None, status=None, wait_limit_ns=0):
+                 v=None, k_cache=None, v_cache=None, slots=None, out=None, status=None, wait_limit_ns=0, pair_axis=None,
+                 norm=True):
     """Runs fa_qk_norm_rope on torch CUDA tensors; returns (q_out, k_out).
 
     q [T, h_q, d] and k [T, h_kv, d] (or [B, S, h, d]) may be slices of a fused projection;
     q_weight, k_weight [d] (or None: ones) have their type or are fp32; cos, sin are fp32
     [max_pos, rot_dim / 2] (or None: no rotation); positions int32 [T], by default the token's
-    place in its sequence of seq_len (S, or T).  With v, k_cache, v_cache ([num_pages, page_size,
+    place in its sequence of seq_len (S, or T).  positions int32 [axes, T] with pair_axis (a sequence:
+    for each pair of the rotated part its axis) turn each pair by its own axis's position; norm=False leaves the norm
+    out (no weights).  With v, k_cache, v_cache ([num_pages, page_size,
     h_kv, d]) and slots (int32 [T]) keys and values go to the paged cache, and k_out is None
     unless out = (q_out, k_out) gives one.  A padding token (position -1, or one outside the tables) is
     skipped: its rows are zero in the tensors made here, and left as they were in given ones and in the
@@ -595,8 +645,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
     if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions=positions, seq_len=seq_len, eps=eps,
                           interleaved=interleaved, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, out=out, status=status,
-                          wait_limit_ns=wait_limit_ns)
-    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+                          wait_limit_ns=wait_limit_ns, pair_axis=pair_axis, norm=norm)
+    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status, pair_axis, norm)
     p.wait_limit_ns = wait_limit_ns
     kind = q.dtype
     append = v is not None or k_cache is not None or v_cache is not None or slots is not None
@@ -633,21 +683,25 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, *, positions=None, seq_len=
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *, positions=None, seq_len=None, eps=1e-6,
-                          interleaved=False, grads=None, workspace=None, status=None, wait_limit_ns=0):
+                          interleaved=False, grads=None, workspace=None, status=None, wait_limit_ns=0, pair_axis=None,
+                          norm=True):
     """Runs fa_qk_norm_rope_bwd on torch CUDA tensors; returns (dq, dk, dq_weight, dk_weight).
 
     q, k and the arguments behind dk_out are those of qk_norm_rope; dq_out, dk_out (contiguous)
     are the gradients of its outputs.  grads: (dq, dk, dq_weight, dk_weight) to write, dq and dk at
     any token stride (slices of a fused projection's gradient); the weights' are fp32 [d].  A padding
     token (position -1, or one outside the tables) has a zero gradient in the tensors made here; in given
-    ones its rows are left as they were."""
+    ones its rows are left as they were.  With norm=False q and k are not read (None will do), and the
+    weights' gradients are None."""
     import torch
+    if not norm:
+        q, k = dq_out, dk_out  # (their shapes)
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
         return _on_device(q, qk_norm_rope_backward, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions=positions,
                           seq_len=seq_len, eps=eps, interleaved=interleaved, grads=grads, workspace=workspace, status=status,
-                          wait_limit_ns=wait_limit_ns)
-    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status)
+                          wait_limit_ns=wait_limit_ns, pair_axis=pair_axis, norm=norm)
+    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, eps, interleaved, status, pair_axis, norm)
     p.wait_limit_ns = wait_limit_ns
     kind = q.dtype
     _check(dev, ("dq_out", dq_out, kind, q.numel()), ("dk_out", dk_out, kind, k.numel()))
@@ -656,7 +710,9 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     if grads is None:
         empty, at = torch.empty, q.device
         dq, dk = empty(q.shape, dtype=kind, device=at), empty(k.shape, dtype=kind, device=at)
-        dwq, dwk = empty(p.d, dtype=torch.float32, device=at), empty(p.d, dtype=torch.float32, device=at)
+        dwq = dwk = None
+        if norm:
+            dwq, dwk = empty(p.d, dtype=torch.float32, device=at), empty(p.d, dtype=torch.float32, device=at)
         p.zero_skipped = 1
     else:
         dq, dk, dwq, dwk = grads
@@ -665,6 +721,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
         _like("dq", dq, kind, dev)
         _like("dk", dk, kind, dev)
         p.dq_stride, p.dk_stride = _rows("dq", dq)[3], _rows("dk", dk)[3]
+        if (dwq is None or dwk is None) == bool(norm):
+            raise ValueError("the weights' gradients are wanted with the norm, and not without it")
         _check(dev, ("dq_weight", dwq, torch.float32, p.d), ("dk_weight", dwk, torch.float32, p.d))
     lib, ref = load(), ctypes.byref(p)
     nbytes = lib.fa_qk_norm_rope_bwd_workspace_size(ref)
@@ -675,11 +733,73 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, *,
     else:
         _check(dev, ("workspace", workspace, torch.uint8, workspace.numel()))
     rc = lib.fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                 dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(),
                                  torch._C._cuda_getCurrentRawStream(dev))
     if rc != FA_OK:
         raise FaError(rc, "fa_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def _cache8(dev, k_cache, v_cache, k_scale, v_scale, h_kv, d):
+    """(num_pages, page_size, scale_block) of an 8-bit cache, whose tensors are checked."""
+    import torch
+    if k_cache.dim() != 4 or k_scale.dim() != 3:
+        raise ValueError(f"k_cache and v_cache must be [num_pages, page_size, {h_kv}, {d}], k_scale and v_scale [num_pages, "
+                         f"page_size / scale_block, {h_kv}]")
+    num_pages, page_size = k_cache.shape[:2]
+    blocks = k_scale.shape[1]
+    if blocks < 1 or page_size % blocks:
+        raise ValueError(f"k_scale has {blocks} blocks for pages of {page_size} rows")
+    pool, scales = (num_pages, page_size, h_kv, d), (num_pages, blocks, h_kv)
+    _check(dev, ("k_cache", k_cache, torch.uint8, pool), ("v_cache", v_cache, torch.uint8, pool),
+           ("k_scale", k_scale, torch.float32, scales), ("v_scale", v_scale, torch.float32, scales))
+    return num_pages, page_size, page_size // blocks
+
+
+def qk_norm_rope_append8(q, k, v, q_weight, k_weight, cos, sin, *, k_cache, v_cache, k_scale, v_scale, cu_q, seqused_k,
+                         block_table, positions, eps=1e-6, interleaved=False, pair_axis=None, norm=True, out=None, status=None,
+                         wait_limit_ns=0):
+    """Runs fa_qk_norm_rope_append8 on torch CUDA tensors; returns q_out [T, h_q, d].
+
+    q, k and v (slices of a fused projection will do), weights, tables, positions (int32 [T] or
+    [axes, T], with pair_axis), norm and status are those of qk_norm_rope.  k_cache, v_cache: uint8 (e4m3
+    bytes) [num_pages, page_size, h_kv, d]; k_scale, v_scale: fp32 [num_pages, page_size / scale_block, h_kv],
+    which gives the block; cu_q [B + 1], seqused_k [B] (the new tokens included) and block_table
+    [B, max_blocks_per_seq] are what page_plan makes and forward takes.  out: q_out to write (rows of
+    skipped tokens are left as they were there, and zero in the one made here)."""
+    import torch
+    dev = _device_index(q)
+    if dev != torch._C._cuda_getDevice():
+        return _on_device(q, qk_norm_rope_append8, q, k, v, q_weight, k_weight, cos, sin, k_cache=k_cache, v_cache=v_cache,
+                          k_scale=k_scale, v_scale=v_scale, cu_q=cu_q, seqused_k=seqused_k, block_table=block_table,
+                          positions=positions, eps=eps, interleaved=interleaved, pair_axis=pair_axis, norm=norm, out=out,
+                          status=status, wait_limit_ns=wait_limit_ns)
+    if positions is None:
+        raise ValueError("an append needs the tokens' positions")
+    p = _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, None, eps, interleaved, status, pair_axis, norm)
+    p.wait_limit_ns = wait_limit_ns
+    kind = q.dtype
+    if v.shape != k.shape:
+        raise ValueError(f"v must have k's shape {tuple(k.shape)}; it has {tuple(v.shape)}")
+    _like("v", v, kind, dev)
+    p.v_stride = _rows("v", v)[3]
+    num_pages, page_size, block = _cache8(dev, k_cache, v_cache, k_scale, v_scale, p.h_kv, p.d)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks_per_seq]")
+    B, blocks = block_table.shape
+    _check(dev, ("cu_q", cu_q, torch.int32, B + 1), ("seqused_k", seqused_k, torch.int32, B),
+           ("block_table", block_table, torch.int32, B * blocks), ("out", out, kind, q.shape))
+    if out is None:
+        p.zero_skipped = 1
+        out = torch.empty(q.shape, dtype=kind, device=q.device)
+    c = FaCache8Params(B, page_size, blocks, num_pages, block, cu_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr())
+    rc = load().fa_qk_norm_rope_append8(ctypes.byref(p), ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                        torch._C._cuda_getCurrentRawStream(dev))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_qk_norm_rope_append8")
+    return out
 
 
 def page_plan(cached, fresh, block_table, free_pages, *, page_size, num_pages, tokens, free_head=None, out=None, status=None):

@@ -93,9 +93,9 @@ bool encode_u8_4d(CUtensorMap* m, const void* base, const cuuint64_t dims[4], co
 // profiling hooks
 // ------------------------------------------------------------------------------------------
 const char* const kKernelNames[] = {"fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post", "paged_prep", "paged_few",
-                                    "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan"};
+                                    "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan", "append8"};
 enum KernelId { kFwd = 0, kDecode, kCombine, kBwdPre, kBwdMain, kBwdPost, kPagedPrep, kPagedFew, kPagedMerge, kNormRope,
-                kNormRopeBwd, kPagePlan, kNumKernels };
+                kNormRopeBwd, kPagePlan, kAppend8, kNumKernels };
 
 struct Profiler {
     std::mutex mu;
@@ -542,7 +542,16 @@ fa_status normalise_rope(const fa_rope_params* in, RopeArgs& a) {
     if (x.rot_dim > 0 && (!x.cos || !x.sin || !aligned16(x.cos) || !aligned16(x.sin) || x.max_pos <= 0)) return FA_ERR_INVALID_ARG;
     if (!aligned16(x.q_weight) || !aligned16(x.k_weight)) return FA_ERR_INVALID_ARG;
     if (!x.positions && (x.seq_len <= 0 || (x.rot_dim > 0 && (x.seq_len < x.T ? x.seq_len : x.T) > x.max_pos))) return FA_ERR_INVALID_ARG;
+    if (x.axes < 0 || x.axes > FA_ROPE_MAX_AXES || (x.axes > 1 && !x.positions)) return FA_ERR_INVALID_ARG;
+    if (x.no_norm && (x.q_weight || x.k_weight)) return FA_ERR_INVALID_ARG;
     a = RopeArgs{};
+    if (x.axes > 1)
+        for (int j = 0; j < x.rot_dim / 2; ++j) {
+            if (x.pair_axis[j] >= x.axes) return FA_ERR_INVALID_ARG;
+            a.pair_axis[j] = x.pair_axis[j];
+        }
+    a.axes = x.axes;
+    a.no_norm = x.no_norm ? 1 : 0;
     a.T = x.T;
     a.h_q = x.h_q;
     a.h_kv = x.h_kv;
@@ -942,6 +951,60 @@ fa_status fa_qk_norm_rope(const fa_rope_params* in, const void* q, const void* k
     return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
 }
 
+fa_status fa_qk_norm_rope_append8(const fa_rope_params* in, const fa_cache8_params* cache, const void* q, const void* k, const void* v,
+                                  void* q_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                  struct CUstream_st* stream) {
+    RopeArgs a;
+    fa_status rc = normalise_rope(in, a);
+    if (rc != FA_OK) return rc;
+    if (!cache) return FA_ERR_INVALID_ARG;
+    const fa_cache8_params& x = *cache;
+    if (x.B < 0 || x.page_size <= 0 || x.page_size % 16 || x.scale_block <= 0 || x.scale_block % 16 || x.page_size % x.scale_block ||
+        x.max_blocks_per_seq <= 0 || x.num_pages <= 0)
+        return FA_ERR_INVALID_ARG;
+    if (a.slots || in->slots) return FA_ERR_INVALID_ARG;  // the table says where a token goes
+    // places in a sequence are 32-bit, and so is the number of units (blocks at most two to a sequence more than the tokens fill)
+    if ((long long)x.max_blocks_per_seq * x.page_size > 0x7fffffffLL - x.page_size || x.B > 0x3fffffff - a.T / x.scale_block || a.h_kv > 65535)
+        return FA_ERR_UNSUPPORTED;
+    if (a.T == 0) return FA_OK;
+    if (in->v_stride < (long long)a.h_kv * a.d || in->v_stride % 8) return FA_ERR_INVALID_ARG;
+    if (!a.positions || !q || !k || !v || !q_out || !k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+    if (x.B > 0 && (!x.cu_seqlens_q || !x.seqused_k || !x.block_table)) return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
+        return FA_ERR_INVALID_ARG;
+    // q_out may be q, in the same layout; nothing else that the call writes shares a byte with anything else of it
+    const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;
+    const size_t pool = (size_t)x.num_pages * x.page_size * wk, scales = (size_t)x.num_pages * (x.page_size / x.scale_block) * a.h_kv * 4;
+    const size_t angles = a.rot > 0 ? (size_t)a.max_pos * (a.rot / 2) * 4 : 0, weight = (size_t)a.d * (a.weight_f32 ? 4 : 2);
+    const Span read[] = {{a.positions, (size_t)a.T * 4 * std::max(a.axes, 1)}, {a.cos, angles}, {a.sin, angles}, {a.wq, weight}, {a.wk, weight},
+                         {x.cu_seqlens_q, ((size_t)x.B + 1) * 4}, {x.seqused_k, (size_t)x.B * 4},
+                         {x.block_table, (size_t)x.B * x.max_blocks_per_seq * 4},
+                         {k, span16(a.T, a.k_stride, wk)}, {v, span16(a.T, (long)in->v_stride, wk)}};
+    const Span written[] = {{q_out, span16(a.T, wq, wq)}, {k_cache, pool}, {v_cache, pool}, {k_scale, scales}, {v_scale, scales}};
+    const size_t nq = span16(a.T, a.q_stride, wq);
+    for (int i = 0; i < 5; ++i) {
+        const bool own = i == 0 && q_out == q && a.q_stride == wq;
+        if (!own && overlap(written[i].at, written[i].n, q, nq)) return FA_ERR_INVALID_ARG;
+        for (const Span& r : read)
+            if (overlap(written[i].at, written[i].n, r.at, r.n)) return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i].at, written[i].n, written[j].at, written[j].n)) return FA_ERR_INVALID_ARG;
+    }
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.k = reinterpret_cast<const uint16_t*>(k);
+    a.v = reinterpret_cast<const uint16_t*>(v);
+    a.v_stride = (long)in->v_stride;
+    a.q_out = reinterpret_cast<uint16_t*>(q_out);
+    const Append8Args c{x.B, a.T, x.scale_block, x.page_size, x.max_blocks_per_seq, x.num_pages, x.cu_seqlens_q, x.seqused_k,
+                        x.block_table, reinterpret_cast<uint8_t*>(k_cache), reinterpret_cast<uint8_t*>(v_cache), k_scale, v_scale};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (timed(kAppend8, st, [&] { return launch_append8(a, c, st); }) != cudaSuccess) return FA_ERR_CUDA;
+    a.k = a.v = nullptr;  // the queries
+    a.h_kv = 0;
+    a.after = x.B > 0;
+    return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
+}
+
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* in) {
     RopeArgs a;
     if (normalise_rope(in, a) != FA_OK) return 0;
@@ -957,14 +1020,21 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const voi
     if (rc != FA_OK) return rc;
     const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;
     if (in->dq_stride < wq || in->dk_stride < wk || in->dq_stride % 8 || in->dk_stride % 8) return FA_ERR_INVALID_ARG;
-    if (!dq_weight || !dk_weight || !workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    // (without the norm there are no weights, and the inputs are not read)
+    if (a.no_norm ? dq_weight || dk_weight : !dq_weight || !dk_weight) return FA_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    if (a.no_norm) {
+        q = k = nullptr;
+        a.q_stride = wq;
+        a.k_stride = wk;
+    }
     const int ctas = norm_rope_bwd_ctas(a, sm_count());
     if (ws_bytes < align256((size_t)2 * ctas * a.d * 4)) return FA_ERR_WORKSPACE;
     const size_t angles = a.rot > 0 ? (size_t)a.max_pos * (a.rot / 2) * 4 : 0, weight = (size_t)a.d * (a.weight_f32 ? 4 : 2);
-    const Span read[] = {{a.positions, (size_t)a.T * 4}, {a.cos, angles}, {a.sin, angles}, {a.wq, weight}, {a.wk, weight}};
+    const Span read[] = {{a.positions, (size_t)a.T * 4 * std::max(a.axes, 1)}, {a.cos, angles}, {a.sin, angles}, {a.wq, weight}, {a.wk, weight}};
     const Span written[] = {{dq_weight, (size_t)a.d * 4}, {dk_weight, (size_t)a.d * 4}, {workspace, (size_t)2 * ctas * a.d * 4}};
     if (a.T > 0) {
-        if (!q || !k || !dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
+        if ((!a.no_norm && (!q || !k)) || !dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
         if (!aligned16(q) || !aligned16(k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk))
             return FA_ERR_INVALID_ARG;
         // a row is read whole before its gradient is written: dq may be q or dq_out, dk may be k or dk_out, in

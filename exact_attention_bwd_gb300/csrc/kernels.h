@@ -178,7 +178,18 @@ struct RopeArgs {
     int zero_skipped;          // q_out and k_out (dq and dk) of skipped tokens become 0
     int* status;
     unsigned long long wait_ns;  // bound on each wait
+    int axes, no_norm;         // position axes (0 or 1: one, positions [T]; else [axes][T]), y = x turned
+    uint8_t pair_axis[FA_ROPE_MAX_PAIRS];
+    int after;                 // the launch runs beside the kernel ahead of it and ends behind it
     int unit_rows, kv_rows, warps;  // rows a warp takes at a time (of k and v together), warps that walk over them
+};
+
+// The e4m3 cache of an append: new tokens of sequence b take places [used[b] - n, used[b]), n = cu[b + 1] - cu[b].
+struct Append8Args {
+    int B, T, block, page_size, max_blocks, num_pages;
+    const int32_t *cu, *used, *table;
+    uint8_t *k_cache, *v_cache;  // [num_pages, page_size, h_kv, d]
+    float *k_scale, *v_scale;    // [num_pages, page_size / block, h_kv]
 };
 
 struct PagePlanArgs {
@@ -210,6 +221,7 @@ cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
 cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st);  // many: both kernels' items
 cudaError_t launch_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append8(const RopeArgs& a, const Append8Args& c, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int sms, cudaStream_t st);
 int norm_rope_bwd_ctas(const RopeArgs& a, int sms);  // rows of dw_part for each weight
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st);

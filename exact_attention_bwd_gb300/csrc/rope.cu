@@ -19,8 +19,12 @@
 // that rotate with each other (unit p and p + rot / 16 when pairs lie half the rotated part
 // apart; both members of each pair in one unit when they are adjacent), so the rotation needs no
 // exchange between lanes, and the row sums are a few shuffles.
-#include "kernels.h"
-#include "ptx.cuh"
+//
+// The EXT instantiations take several position axes and leave the norm out on demand.  A token's
+// angles are then no row of the tables: pair j's come from the row of its own axis's position, so
+// the warp gathers them, four bytes a lane, by asynchronous copies that arrive on the unit's barrier
+// like its rows.  Without the norm y is x turned, and dx is dy turned back: x is not read.
+#include "rope.cuh"
 
 namespace fa {
 namespace {
@@ -31,16 +35,6 @@ namespace {
 // 4 KB ones 58.1 / 101.1 / 32.8.  (At the copy rate: 50.1 / 74.8 / 25.0.)
 constexpr int kWarps = 12;
 constexpr int kBufs = 2;           // units in flight per warp
-constexpr int kUnitBytes = 8192;   // rows of a unit at most (gradient: half of it x, half dy)
-
-template <int D>
-struct RowCfg {
-    static constexpr int PAIRS = D / 16;               // lanes with values
-    static constexpr int LANES = D == 192 ? 16 : PAIRS;  // lanes of a row
-    static constexpr int ROWS = 32 / LANES;            // rows of a warp at a time
-    // rows of a unit: whole batches of 2 ROWS
-    static constexpr int MAX_ROWS = kUnitBytes / (2 * D) / (2 * ROWS) * (2 * ROWS);
-};
 
 // Shared memory of a warp's buffer: rows (kUnitBytes), cos and sin of the token
 template <int D>
@@ -58,122 +52,39 @@ struct WarpSmem {
     RowMeta meta[kBufs];
 };
 
-// The lane's angles from the token's row of the tables: for pairs half the rotated part apart
-// c[e], s[e] are those of values 2e, 2e + 1 of unit 0 (and unit 1), e < 4; for adjacent ones
-// c[e].x, s[e].x is the angle of the pair e (e < 4 in unit 0, the others in unit 1).  Values
-// behind the rotated part get cos 1, sin 0.
-template <bool ADJ>
-struct Angles {
-    float2 c[ADJ ? 8 : 4], s[ADJ ? 8 : 4];
-    __device__ __forceinline__ void load(const float* cs, const float* sn, int u0, int u1, int rot) {
-        if constexpr (ADJ) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int u = h ? u1 : u0;
-                float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (8 * u < rot) {
-                    x = *reinterpret_cast<const float4*>(cs + 4 * u);
-                    y = *reinterpret_cast<const float4*>(sn + 4 * u);
-                }
-                c[4 * h] = make_float2(x.x, x.x);
-                c[4 * h + 1] = make_float2(x.y, x.y);
-                c[4 * h + 2] = make_float2(x.z, x.z);
-                c[4 * h + 3] = make_float2(x.w, x.w);
-                s[4 * h] = make_float2(-y.x, y.x);
-                s[4 * h + 1] = make_float2(-y.y, y.y);
-                s[4 * h + 2] = make_float2(-y.z, y.z);
-                s[4 * h + 3] = make_float2(-y.w, y.w);
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (16 * u0 < rot) {
-                    x = *reinterpret_cast<const float4*>(cs + 8 * u0 + 4 * h);
-                    y = *reinterpret_cast<const float4*>(sn + 8 * u0 + 4 * h);
-                }
-                c[2 * h] = make_float2(x.x, x.y);
-                c[2 * h + 1] = make_float2(x.z, x.w);
-                s[2 * h] = make_float2(y.x, y.y);
-                s[2 * h + 1] = make_float2(y.z, y.w);
-            }
-        }
-    }
-    // Turns the lane's 16 values (unit 0 in v[0..3], unit 1 in v[4..7]); BACK: by minus the angle.
-    template <bool BACK>
-    __device__ __forceinline__ void turn(float2* v) const {
-        if constexpr (ADJ) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 sw = make_float2(v[e].y, v[e].x);
-                const float2 ss = BACK ? make_float2(s[e].y, s[e].x) : s[e];
-                v[e] = __ffma2_rn(sw, ss, __fmul2_rn(v[e], c[e]));
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 a = v[e], b = v[e + 4], ns = make_float2(-s[e].x, -s[e].y);
-                v[e] = __ffma2_rn(b, BACK ? s[e] : ns, __fmul2_rn(a, c[e]));
-                v[e + 4] = __ffma2_rn(a, BACK ? ns : s[e], __fmul2_rn(b, c[e]));
-            }
-        }
-    }
-};
-
-// The two units (8 values each, their index in the row) of lane i of a row.
-template <int D, bool ADJ>
-__device__ __forceinline__ void lane_units(int i, int rot, int& u0, int& u1) {
-    const int h = rot >> 4;  // units of half the rotated part
-    if (ADJ || i < h) {
-        u0 = i;
-        u1 = i + (ADJ ? D / 16 : h);
-    } else {  // behind the rotated part
-        u0 = 2 * i;
-        u1 = 2 * i + 1;
-    }
+// The position of axis x of token t, or -1: padding, or outside the tables, which sets the status.
+// (`on`: lane x < axes has one; the others return 0.)
+__device__ __forceinline__ int position_of_axis(const RopeArgs& a, long t, int x, bool on) {
+    if (!on) return 0;
+    const int pos = a.positions ? a.positions[x * (long)a.T + t] : (int)((unsigned)t % (unsigned)a.seq_len);
+    if (pos >= 0 && pos < a.max_pos) return pos;
+    if (pos != -1 && a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
+    return -1;
 }
 
-template <bool F16>
-__device__ __forceinline__ void widen8(const uint4& x, float2* v) {
-    v[0] = make_float2(lo16<F16>(x.x), hi16<F16>(x.x));
-    v[1] = make_float2(lo16<F16>(x.y), hi16<F16>(x.y));
-    v[2] = make_float2(lo16<F16>(x.z), hi16<F16>(x.z));
-    v[3] = make_float2(lo16<F16>(x.w), hi16<F16>(x.w));
-}
-template <bool F16>
-__device__ __forceinline__ uint4 narrow8(const float2* v) {
-    return make_uint4(pack16<F16>(v[0].x, v[0].y), pack16<F16>(v[1].x, v[1].y), pack16<F16>(v[2].x, v[2].y),
-                      pack16<F16>(v[3].x, v[3].y));
-}
-
-// The lane's 16 weights (null: ones).
-template <bool F16>
-__device__ __forceinline__ void load_weight(const RopeArgs& a, const void* w, int u0, int u1, float2* v) {
+// The axes of the pairs lane, lane + 32, ... (a byte each).
+__device__ __forceinline__ uint32_t lane_axes(const RopeArgs& a, int lane) {
+    uint32_t x = 0;
+    if (a.axes > 1)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int u = h ? u1 : u0;
-        if (!w) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * h + e] = make_float2(1.f, 1.f);
-        } else if (a.weight_f32) {
-            const float4* src = reinterpret_cast<const float4*>(w) + 2 * u;
-            const float4 x = src[0], y = src[1];
-            v[4 * h] = make_float2(x.x, x.y);
-            v[4 * h + 1] = make_float2(x.z, x.w);
-            v[4 * h + 2] = make_float2(y.x, y.y);
-            v[4 * h + 3] = make_float2(y.z, y.w);
-        } else {
-            widen8<F16>(reinterpret_cast<const uint4*>(w)[u], v + 4 * h);
-        }
-    }
-}
-
-// Sum over the lanes of a row.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        for (int i = 0; i < 4; ++i) x |= (uint32_t)a.pair_axis[lane + 32 * i] << (8 * i);
     return x;
+}
+
+// Starts the copies of a token's angles (pos: lane x's position of axis x), each pair from the row of
+// its axis; every lane arrives on the barrier when its own have landed.
+__device__ __forceinline__ void gather_angles(const RopeArgs& a, uint32_t axes, int pos, float* cs, float* sn, uint64_t* bar) {
+    const int lane = threadIdx.x & 31, half = a.rot / 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = lane + 32 * i;
+        const int at = __shfl_sync(0xffffffffu, pos, (axes >> (8 * i)) & 0xff);
+        if (j < half) {
+            copy4_async(cs + j, a.cos + (long)at * half + j);
+            copy4_async(sn + j, a.sin + (long)at * half + j);
+        }
+    }
+    mbar_arrive_copies(bar);
 }
 
 // The token's row of the angle tables, or -1: a padding token (position -1) or one outside the
@@ -217,7 +128,7 @@ __device__ __forceinline__ void give_up(S& s, uint32_t flight, uint32_t phase, i
 // One run of units: `heads` rows of each token in groups of `rows`.
 __device__ __forceinline__ int groups_of(int heads, int rows) { return (heads + rows - 1) / rows; }
 
-template <int D, bool F16, bool ADJ>
+template <int D, bool F16, bool ADJ, bool EXT>
 __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArgs a) {
     using C = RowCfg<D>;
     constexpr int LANES = C::LANES, ROWS = C::ROWS;
@@ -235,9 +146,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     };
     UnitWalk ahead(me, n_warps, per_token), now = ahead;
     if (me >= n_warps) ahead.t = now.t = a.T;
-    int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0)
+    int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0; EXT: next_pos of axis `lane`)
     uint32_t flight = 0;                // buffers with copies on their way (lane 0)
+    const uint32_t axes = EXT ? lane_axes(a, lane) : 0;
     auto look = [&]() {
+        if constexpr (EXT) {
+            if (ahead.t < a.T) {
+                next_pos = position_of_axis(a, ahead.t, lane, lane < max(a.axes, 1));
+                if (__any_sync(0xffffffffu, next_pos < 0)) next_pos = -1;
+            }
+            if (lane == 0 && ahead.t < a.T && a.slots && ahead.x >= gq) {
+                next_slot = a.slots[ahead.t];
+                if (next_slot >= a.num_slots || next_slot < -1) {
+                    if (a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    next_slot = -1;
+                }
+            }
+            return;
+        }
         if (lane == 0 && ahead.t < a.T) {
             next_pos = position_of(a, ahead.t);
             if (a.slots && ahead.x >= gq) {
@@ -251,6 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     };
     // starts the copies of the unit `ahead` into buffer b and moves on
     auto issue = [&](int b) {
+        if (EXT && ahead.t < a.T && next_pos >= 0) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
         if (lane == 0 && ahead.t < a.T) {
             s.meta[b] = RowMeta{next_pos, next_slot};
             if (next_pos >= 0) {
@@ -258,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
                 unit(ahead.x, kind, r0, rows);
                 const bool with_v = kind && a.v;
                 const uint16_t* src = (kind ? a.k + ahead.t * a.k_stride : a.q + ahead.t * a.q_stride) + (long)r0 * D;
-                const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                const uint32_t bytes = (uint32_t)rows * D * 2, angle = EXT ? 0u : (uint32_t)a.rot * 2;
                 flight |= 1u << b;
                 mbar_expect_tx(&s.full[b], (with_v ? 2 : 1) * bytes + 2 * angle);
                 bulk_load(s.buf[b].rows, src, bytes, &s.full[b]);
@@ -273,7 +200,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         look();
     };
     if (lane == 0) {
-        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], 1);
+        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], EXT ? 33 : 1);  // (lane 0's arrival, and the lanes' copies)
         fence_mbar_init();
     }
     __syncwarp();
@@ -294,6 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         if (meta.pos >= 0) {
             if (!__all_sync(0xffffffffu, mbar_wait_within(&s.full[b], (phase >> b) & 1, a.wait_ns))) {
                 give_up(s, flight, phase, a.status);
+                if (EXT && a.after) wait_previous_kernel();
                 return;
             }
             phase ^= 1u << b;
@@ -325,10 +253,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
                     float2 ss = __fmul2_rn(v[0], v[0]);
 #pragma unroll
                     for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
-                    const float rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    float rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    if (EXT && a.no_norm) rs = 1.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], kind ? wk[e] : wq[e]);
-                    ang.template turn<false>(v);
+                    ang.template turn<false, EXT>(v, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
                     const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], rs2);
@@ -350,6 +279,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         issue(b);
         __syncwarp();
     }
+    // (a launch beside the kernel ahead of it: what comes next in the stream waits for both)
+    if (EXT && a.after) wait_previous_kernel();
 }
 
 // Gradient: the same walk, over the query rows and then over the key rows, with dy beside x in
@@ -358,7 +289,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
 // adds the rows, again in a fixed order, so the gradients are the same bits from call to call.
 // The sums are fp32: a term carries fp32 roundings already, and with a lane's chain followed by trees over
 // lanes, warps and CTAs the error stays within 2^-16 of the sum of the terms' sizes.
-template <int D, bool F16, bool ADJ>
+template <int D, bool F16, bool ADJ, bool EXT>
 __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const RopeArgs a) {
     using C = RowCfg<D>;
     constexpr int LANES = C::LANES, ROWS = C::ROWS;
@@ -369,13 +300,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
     int u0, u1;
     lane_units<D, ADJ>(on ? li : 0, a.rot, u0, u1);
     if (lane == 0) {
-        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], 1);
+        for (int b = 0; b < kBufs; ++b) mbar_init(&s.full[b], EXT ? 33 : 1);  // (lane 0's arrival, and the lanes' copies)
         fence_mbar_init();
     }
     __syncwarp();
     const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
     uint32_t phase = 0, flight = 0;
     bool failed = false;
+    const bool norm = !EXT || !a.no_norm;  // without it a unit holds dy alone
+    const uint32_t axes = EXT ? lane_axes(a, lane) : 0;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         const int heads = kind ? a.h_kv : a.h_q;
@@ -391,18 +324,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
         if (me >= n_warps) ahead.t = now.t = a.T;
         int next_pos = -1;
         auto look = [&]() {
-            if (lane == 0 && ahead.t < a.T) next_pos = position_of(a, ahead.t);
+            if constexpr (EXT) {
+                if (ahead.t < a.T) {
+                    next_pos = position_of_axis(a, ahead.t, lane, lane < max(a.axes, 1));
+                    if (__any_sync(0xffffffffu, next_pos < 0)) next_pos = -1;
+                }
+            } else {
+                if (lane == 0 && ahead.t < a.T) next_pos = position_of(a, ahead.t);
+            }
         };
         auto issue = [&](int b) {
+            if (EXT && ahead.t < a.T && next_pos >= 0) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
             if (lane == 0 && ahead.t < a.T) {
                 s.meta[b] = RowMeta{next_pos, 0};
                 if (next_pos >= 0) {
                     const int r0 = ahead.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
-                    const uint32_t bytes = (uint32_t)rows * D * 2, angle = (uint32_t)a.rot * 2;
+                    const uint32_t bytes = (uint32_t)rows * D * 2, angle = EXT ? 0u : (uint32_t)a.rot * 2;
                     flight |= 1u << b;
-                    mbar_expect_tx(&s.full[b], 2 * bytes + 2 * angle);
-                    bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
-                    bulk_load(s.buf[b].rows + kUnitBytes / 2, gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
+                    mbar_expect_tx(&s.full[b], (norm ? 2 : 1) * bytes + 2 * angle);
+                    if (norm) bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
+                    bulk_load(s.buf[b].rows + (norm ? kUnitBytes / 2 : 0), gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
                     if (angle) {
                         bulk_load(s.buf[b].cos, a.cos + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
                         bulk_load(s.buf[b].sin, a.sin + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
@@ -428,9 +369,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                 }
                 phase ^= 1u << b;
                 flight &= ~(1u << b);
-                const uint8_t *px = s.buf[b].rows, *pg = px + kUnitBytes / 2;
+                const uint8_t *px = s.buf[b].rows, *pg = px + (norm ? kUnitBytes / 2 : 0);
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
+                if (EXT && !norm) {
+#pragma unroll 2
+                    for (int r = lr; r < rows; r += ROWS) {
+                        if (!on) continue;
+                        float2 y[8];
+                        widen8<F16>(*reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u0), y);
+                        widen8<F16>(*reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u1), y + 4);
+                        ang.template turn<true, true>(y, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
+                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u0) = narrow8<F16>(y);
+                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u1) = narrow8<F16>(y + 4);
+                    }
+                } else
 #pragma unroll 2
                 for (int r = lr; r < rows + lr; r += ROWS) {
                     const bool live = on && r < rows;
@@ -448,7 +401,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                         widen8<F16>(y0, y);
                         widen8<F16>(y1, y + 4);
                     }
-                    ang.template turn<true>(y);
+                    ang.template turn<true, EXT>(y, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
                     float2 ss = __fmul2_rn(v[0], v[0]);
 #pragma unroll
                     for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
@@ -482,6 +435,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
             issue(b);
             __syncwarp();
         }
+        if (EXT && !norm) continue;  // (no weights)
         // the warp's lanes with the same values, then the CTA's warps, in order (in the first buffer,
         // which no copy is under way into)
         float* part = reinterpret_cast<float*>(reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp].buf[0].rows);
@@ -538,13 +492,23 @@ int unit_rows_of(int d, long rows, bool bwd, int sms) {
     return unit_rows(d, rows, most, sms);
 }
 
+template <int D, bool F16, bool ADJ, bool EXT>
+cudaError_t launch_fwd_dfae(const RopeArgs& a, int ctas, cudaStream_t st) {
+    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
+    cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<D, F16, ADJ, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if constexpr (EXT)
+        if (a.after) return launch_after(norm_rope_kernel<D, F16, ADJ, EXT>, dim3(ctas), 32 * kWarps, smem, st, a);
+    norm_rope_kernel<D, F16, ADJ, EXT><<<ctas, 32 * kWarps, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Whether a call takes the instantiations with several axes, without the norm, or beside another kernel.
+bool extended(const RopeArgs& a) { return a.axes > 1 || a.no_norm || a.after; }
+
 template <int D, bool F16, bool ADJ>
 cudaError_t launch_fwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
-    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
-    cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<D, F16, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    norm_rope_kernel<D, F16, ADJ><<<ctas, 32 * kWarps, smem, st>>>(a);
-    return cudaGetLastError();
+    return extended(a) ? launch_fwd_dfae<D, F16, ADJ, true>(a, ctas, st) : launch_fwd_dfae<D, F16, ADJ, false>(a, ctas, st);
 }
 
 template <int D>
@@ -553,13 +517,19 @@ cudaError_t launch_fwd_d(const RopeArgs& a, int ctas, cudaStream_t st) {
     return a.adjacent ? launch_fwd_dfa<D, false, true>(a, ctas, st) : launch_fwd_dfa<D, false, false>(a, ctas, st);
 }
 
+template <int D, bool F16, bool ADJ, bool EXT>
+cudaError_t launch_bwd_dfae(const RopeArgs& a, int ctas, cudaStream_t st) {
+    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
+    cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D, F16, ADJ, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    norm_rope_bwd_kernel<D, F16, ADJ, EXT><<<ctas, 32 * kWarps, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <int D, bool F16, bool ADJ>
 cudaError_t launch_bwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
-    constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
-    cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D, F16, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    norm_rope_bwd_kernel<D, F16, ADJ><<<ctas, 32 * kWarps, smem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const cudaError_t e = extended(a) ? launch_bwd_dfae<D, F16, ADJ, true>(a, ctas, st) : launch_bwd_dfae<D, F16, ADJ, false>(a, ctas, st);
+    if (e != cudaSuccess || a.no_norm) return e;
     norm_rope_dw_kernel<<<2 * (D / 32), 1024, 0, st>>>(a, ctas);
     return cudaGetLastError();
 }
@@ -612,13 +582,13 @@ cudaError_t launch_norm_rope(const RopeArgs& args, int sms, cudaStream_t st) {
 }
 
 int norm_rope_bwd_ctas(const RopeArgs& a, int sms) {
-    const int rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
+    const int rows = unit_rows_of(a.d, (long)a.T * a.h_q, !a.no_norm, sms);
     return ctas_for((long)a.T * cdiv(a.h_q, rows), sms);
 }
 
 cudaError_t launch_norm_rope_bwd(const RopeArgs& args, int sms, cudaStream_t st) {
     RopeArgs a = args;
-    a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
+    a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, !a.no_norm, sms);
     const int ctas = norm_rope_bwd_ctas(a, sms);
     a.warps = ctas * kWarps;
     switch (a.d) {

@@ -236,10 +236,18 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * dq_weight, dk_weight (fp32 [d], written whole, summed in a fixed order: the same bits from
  * call to call).  A skipped token adds nothing to them.  They and the workspace share no byte
  * with anything else of the call.
+ * Several position axes (text, images, video: time, height, width): with axes = 2 to FA_ROPE_MAX_AXES
+ * positions is [axes][T] (and must be given), and pair j turns by cos[pos][j], sin[pos][j] at its own
+ * axis's position, pos = positions[pair_axis[j]][t].  The axes share the tables.  A token with -1 on
+ * some axis is padding; one with another position outside [0, max_pos) on some axis sets *status.
+ * Without the norm (no_norm; the weights must be NULL): y = x.  The gradient then reads neither q nor k,
+ * which may be NULL, and has no weights' gradients (dq_weight and dk_weight must be NULL).
  * A wait that passes wait_limit_ns ends the call's work early and sets *status to FA_ERR_TIMEOUT
  * (the outputs are then unspecified); without a status word the caller does not learn of it.
  * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
  * of 8 elements, base pointers 16-byte aligned. */
+#define FA_ROPE_MAX_AXES 4
+#define FA_ROPE_MAX_PAIRS 128
 typedef struct fa_rope_params {
     int T;                 /* tokens */
     int h_q, h_kv, d;
@@ -260,10 +268,43 @@ typedef struct fa_rope_params {
     int32_t *status;                          /* device int32, set on a bad position or slot or a timeout, never cleared; or NULL */
     int zero_skipped;                         /* q_out, k_out (dq, dk) of skipped tokens become 0 */
     unsigned long long wait_limit_ns;         /* bound on each wait of the kernels; 0 = 2 s */
+    int axes;              /* position axes; 0 or 1: one */
+    int no_norm;           /* y = x turned */
+    unsigned char pair_axis[FA_ROPE_MAX_PAIRS];  /* with several axes: the axis of pair j < rot_dim / 2 */
 } fa_rope_params;
 
 fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k, const void *v, void *q_out, void *k_out,
                           void *k_cache, void *v_cache, struct CUstream_st *stream);
+
+/* Norm and rotation with append to a cache in 8 bits: queries and keys as in fa_qk_norm_rope, the keys
+ * and a copy of v to pools of e4m3 bytes k_cache, v_cache [num_pages, page_size, h_kv, d] with a
+ * scale for each block of scale_block rows of a page and each head, k_scale, v_scale
+ * [num_pages, page_size / scale_block, h_kv]: a byte stands for its e4m3 value times its block's scale.
+ * The new tokens of sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 and the last of its
+ * seqused_k[b] keys (as fa_page_plan leaves them and fa_fwd takes them); key j is row j % page_size of
+ * page block_table[b * max_blocks_per_seq + j / page_size].  For each block that gets new rows
+ *   s = max(old scale, smallest power of two with (largest finite |x| of its new rows) <= 448 s),
+ * (at least 2^-126; the old scale counts as 0 where the block's first row is a new one and where it is no
+ * positive finite number), new rows become e4m3(x / s), rounded once from fp32 (infinities: the largest
+ * value, NaN: NaN), the block's rows ahead of them are rescaled where s has grown
+ * (e4m3(byte * old / s)), rows behind them are left as they were.  A block that gets new rows must be the
+ * writing sequence's alone.  positions must be given (they drive the rotation; the table and the
+ * lengths say where a token goes); slots must be NULL, zero_skipped and q_out are as in fa_qk_norm_rope, q_out may be q
+ * (contiguous).  A token that fa_qk_norm_rope would skip is not stored; nor is one of no sequence, and one whose
+ * place is negative or behind the table or whose page is outside the pool, which sets *status.
+ * page_size a positive multiple of 16, scale_block a positive multiple of 16 that divides it. */
+typedef struct fa_cache8_params {
+    int B;                        /* sequences */
+    int page_size, max_blocks_per_seq, num_pages;
+    int scale_block;              /* rows of a page that share a scale */
+    const int32_t *cu_seqlens_q;  /* device int32 [B + 1] */
+    const int32_t *seqused_k;     /* device int32 [B] */
+    const int32_t *block_table;   /* device int32 [B * max_blocks_per_seq] */
+} fa_cache8_params;
+
+fa_status fa_qk_norm_rope_append8(const fa_rope_params *p, const fa_cache8_params *cache, const void *q, const void *k, const void *v,
+                                  void *q_out, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                  struct CUstream_st *stream);
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params *p);
 fa_status fa_qk_norm_rope_bwd(const fa_rope_params *p, const void *q, const void *k, const void *dq_out, const void *dk_out,
                               void *dq, void *dk, float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
