@@ -54,7 +54,8 @@ class FaParams(ctypes.Structure):
         ("max_blocks_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
         ("dtype", ctypes.c_int), ("q_descale", ctypes.c_void_p), ("k_descale", ctypes.c_void_p),
         ("v_descale", ctypes.c_void_p), ("seqused_q", ctypes.c_void_p),
-        ("wait_limit_ns", ctypes.c_ulonglong),
+        ("wait_limit_ns", ctypes.c_ulonglong), ("cache_dtype", ctypes.c_int), ("scale_block", ctypes.c_int),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
     ]
 
 
@@ -353,12 +354,14 @@ def _kv_shape(p, k, cu_q, block_table):
 
 def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks=None, cu_q=None, cu_k=None,
             flags=0, out=None, lse=None, workspace=None, seqused_k=None, block_table=None, s_kv=None,
-            descale=None, seqused_q=None, wait_limit_ns=0, max_seqlen_q=0):
+            descale=None, seqused_q=None, wait_limit_ns=0, max_seqlen_q=0, cache_scale=None):
     """Runs fa_fwd on torch CUDA tensors; returns (o, lse, workspace).
 
     Packed queries over a paged cache: q [T, h_q, d] with cu_q, seqused_k, block_table and s_kv
     (no cu_k); max_seqlen_q is the most new tokens of a sequence, if the caller knows it.  Rows that no
-    sequence covers are not written, in given tensors or in those made here.
+    sequence covers are not written, in given tensors or in those made here.  cache_scale = (k_scale,
+    v_scale), fp32 [num_pages, page_size / scale_block, h_kv], with k and v uint8 (e4m3 bytes) is the
+    same over a cache in 8 bits, as qk_norm_rope_append8 fills it; q is bfloat16 or float16.
 
     q, k, v are all bfloat16, all float16, or all uint8 = e4m3 bytes (FA_DTYPE_E4M3);
     descale = (q, k, v) fp32 [B * h_kv] factors or None (all 1).  The output has the
@@ -368,7 +371,9 @@ def forward(q, k, v, *, causal=False, window=(-1, -1), softmax_scale=None, sinks
         if descale is not None:
             raise TypeError("descale factors apply to e4m3 (uint8) inputs only")
         return _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace, seqused_k,
-                              block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q)
+                              block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q, cache_scale)
+    if cache_scale is not None:
+        raise ValueError("cache_scale goes with packed queries over a paged cache (cu_q, seqused_k and block_table, no cu_k)")
     fp8 = q.dtype == torch.uint8
     if _type_code(q.dtype) is None or k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must all be bfloat16, all float16 or all uint8 (e4m3 bytes); "
@@ -487,13 +492,13 @@ def _check(dev, *named):
 
 
 def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace, seqused_k, block_table, s_kv,
-                   seqused_q, wait_limit_ns, max_seqlen_q):
+                   seqused_q, wait_limit_ns, max_seqlen_q, cache_scale):
     """forward() for packed queries over a paged cache."""
     import torch
     dev = _device_index(q)
     if dev != torch._C._cuda_getDevice():
         return _on_device(q, _forward_paged, q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, out, lse, workspace,
-                          seqused_k, block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q)
+                          seqused_k, block_table, s_kv, seqused_q, wait_limit_ns, max_seqlen_q, cache_scale)
     kind = q.dtype
     code = _type_code(kind)
     if code is None:
@@ -508,7 +513,13 @@ def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, o
     if dk != d or v.shape != k.shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must have one shape and q's head dimension {d}")
     i32, f32 = torch.int32, torch.float32
-    _check(dev, ("q", q, kind, T * h_q * d), ("k", k, kind, k.numel()), ("v", v, kind, v.numel()), ("cu_q", cu_q, i32, B + 1),
+    stored = kind
+    if cache_scale is not None:
+        if code == FA_DTYPE_E4M3:
+            raise TypeError("over a cache in 8 bits q is bfloat16 or float16")
+        stored, (k_scale, v_scale) = torch.uint8, cache_scale
+        block = _cache8(dev, k, v, k_scale, v_scale, h_kv, d)[2]
+    _check(dev, ("q", q, kind, T * h_q * d), ("k", k, stored, k.numel()), ("v", v, stored, v.numel()), ("cu_q", cu_q, i32, B + 1),
            ("seqused_k", seqused_k, i32, B), ("block_table", block_table, i32, B * blocks), ("sinks", sinks, f32, h_q),
            ("seqused_q", seqused_q, i32, B))
     if out is not None or lse is not None or workspace is not None:
@@ -519,6 +530,8 @@ def _forward_paged(q, k, v, causal, window, softmax_scale, sinks, cu_q, flags, o
                  None if sinks is None else sinks.data_ptr(), cu_q.data_ptr(), None, max_seqlen_q, 0, flags, seqused_k.data_ptr(),
                  block_table.data_ptr(), page_size, blocks, num_pages, code, None, None, None,
                  None if seqused_q is None else seqused_q.data_ptr(), wait_limit_ns)
+    if cache_scale is not None:
+        p.cache_dtype, p.scale_block, p.k_scale, p.v_scale = FA_DTYPE_E4M3, block, k_scale.data_ptr(), v_scale.data_ptr()
     ref = ctypes.byref(p)
     nbytes = lib.fa_fwd_workspace_size(ref)
     if nbytes == 0:

@@ -178,6 +178,14 @@ fa_status normalise(const fa_params* in, Problem& p) {
     p.seqused_q = a.seqused_q;
     p.seqused_k = a.seqused_k;
     p.block_table = a.block_table;
+    // a cache in 8 bits: packed queries over pages only, its queries in 16 bits
+    if (a.cache_dtype != 0 && a.cache_dtype != FA_DTYPE_E4M3) return FA_ERR_INVALID_ARG;
+    if (a.cache_dtype == FA_DTYPE_E4M3) {
+        if (!a.block_table || !a.cu_seqlens_q || a.cu_seqlens_k) return FA_ERR_UNSUPPORTED;
+        if (!a.k_scale || !a.v_scale || a.scale_block <= 0 || a.scale_block % 16 || a.page_size <= 0 || a.page_size % a.scale_block)
+            return FA_ERR_INVALID_ARG;
+        p.cache8 = 1;
+    }
     if (a.block_table) {
         const bool packed = p.cu_q != nullptr;  // packed queries over a paged cache
         if (packed && (p.cu_k || p.dtype == FA_DTYPE_E4M3)) return FA_ERR_UNSUPPORTED;
@@ -382,6 +390,12 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.ctas = sm_count();
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
     const long rows = longest * p.G;
+    if (p.cache8) {
+        const int most = p.d <= 128 ? 32 : 16;
+        pl.few_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : most;
+        pl.few_max = kAllFew;
+        pl.many_rows = most;
+    } else {
     // Every sequence known to have 64 rows at most: the few-row kernel alone, its tile the rows.  Else it takes those of a
     // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
     // a decode step 33 us where one of 16 takes 20: 20 sequences of 5 heads a group, d = 64), and none
@@ -391,6 +405,7 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.few_rows = tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
     pl.few_max = !pl.many ? kAllFew : p.G <= 64 ? pl.few_rows : 0;
     pl.many_rows = (p.d <= 128 ? 2 : 1) * p.P * p.G;
+    }
     pl.off_pre = kStatusBytes;
     pl.off_line = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
     pl.off_cut = pl.off_line + align256(2 * sizeof(PagedLine));
@@ -442,6 +457,14 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.part_o[1] = reinterpret_cast<float*>(ws + pl.off_mo);
     a.part_ml[1] = reinterpret_cast<float2*>(ws + pl.off_mml);
     a.status = status;
+    if (p.cache8) {
+        const Cache8 kv{reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(v), in.k_scale, in.v_scale, in.scale_block,
+                        p.page_size / in.scale_block};
+        cudaError_t e8 = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
+        if (e8 == cudaSuccess) e8 = timed(kPagedFew, st, [&] { return launch_paged8_few(a, kv, pl.ctas, st); });
+        if (e8 == cudaSuccess) e8 = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); });
+        return cuda_status(e8);
+    }
     CUtensorMap tk, tv;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     // a key's row is d * 2 bytes of h_kv times as many: fetched 256 bytes at a time, half of it would be

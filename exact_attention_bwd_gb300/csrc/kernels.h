@@ -28,6 +28,7 @@ struct Problem {
     const int32_t* block_table;  // [B * max_blocks] pages of a paged K/V cache, or null
     int page_size, max_blocks;
     int dtype;                // input element type (FA_DTYPE_*)
+    int cache8;               // the paged cache holds e4m3 bytes with block scales (packed queries only)
     unsigned long long wait_ns;  // bound on each pipeline wait (ns) before a CTA gives up
 };
 
@@ -155,6 +156,12 @@ struct PagedArgs {
     float2* part_ml[2]; // [2][2 CTAs][rows] reference maximum (log2 units) and sum
     int* status;
 };
+// The 8-bit cache: pools of e4m3 bytes, scales [num_pages, blocks, h_kv] of `block` rows each.
+struct Cache8 {
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    int block, blocks;
+};
 // PagedArgs::few_max of a call whose every sequence is the few-row kernel's
 constexpr long kAllFew = 0x7fffffffffffffffL;
 
@@ -219,6 +226,7 @@ cudaError_t launch_bwd_main(const BwdArgs& a, const CUtensorMap& tq, const CUten
 cudaError_t launch_bwd_post(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
 cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
+cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st);  // many: both kernels' items
 cudaError_t launch_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_append8(const RopeArgs& a, const Append8Args& c, cudaStream_t st);

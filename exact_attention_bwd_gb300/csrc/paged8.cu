@@ -1,0 +1,535 @@
+// Attention of packed queries over a paged e4m3 cache with a scale for each block of tokens and head
+// (include/fa.h, fa_params.cache_dtype), few query rows per key/value head.
+//
+// The true keys and values are K = k8 ks, V = v8 vs, with one ks and vs for 16 keys and more, so the scales
+// stay out of the products: ks multiplies the scores, vs the probabilities.  Every e4m3
+// value is an fp16 value, and so is a query row once its largest value has been brought near 2^7 by a
+// power of two (what falls below fp16's range there is 2^-31 of it and less), so both
+// products run on fp16 operands, the first without any rounding, for bf16 queries too.  P vs
+// is rounded to fp16 (2^-11, where the 16-bit cache's kernels round P to the inputs' type).
+//
+// A decode step reads each byte of the cache once and does little with it: what counts is that the
+// bytes keep coming.  Each warp streams its own 16 keys of every 128-key tile through a private ring
+// of asynchronous copies and keeps its own online softmax, so the warps wait for each other only where
+// an item ends and their states are joined.  With the cache on the long side of the products
+// (mma.sync, S^T = K Q^T: 16 keys x 8 rows, O^T = V^T P^T: 16 of d x 8 rows) a tile of 8 rows wastes
+// nothing; converted to fp16 in registers, a byte passes shared memory once, where the
+// 5th-generation tensor cores would want it stored again as 16-bit operands, five bytes of shared memory
+// traffic for each of the cache's, more than the memory's rate leaves.
+//
+// The contraction's order is free, so the fragments need no transposition on the way from shared memory: a lane
+// takes 16 consecutive bytes of a key's row for four k-steps of S^T, and for O^T 2, 4 or 8
+// consecutive columns' bytes of its four keys, which byte permutes pair up.
+//
+// Rounding: per row a running reference m of the scores (moved where some score passes it by 2^9) and a
+// power of two u with P' = P vs u <= 2^9, so that neither blocks of tiny nor of huge values leave fp16's range:
+// what a row's product loses is relative to its own largest term.
+#include "paged.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps8 = 8;
+constexpr int kThreads = 32 * kWarps8;
+constexpr int kGroup = 16;                    // keys of a warp in a tile: they share a page and a scale
+constexpr int kMergeCols = 64;                // columns that the warps join at a time
+constexpr float kNoRef = -1e30f;              // reference of a row without a key so far
+constexpr float kNoUnit = 8.507059173e37f;    // u of a row without a value so far: 2^126
+constexpr float kTop = 512.f;                 // P and P vs u stay below
+
+template <int D, int NT>
+struct Few8Cfg {
+    static constexpr int NR = 8 * NT;
+    static constexpr int CPR = D / 16;              // 16-byte chunks of a row
+    static constexpr int GROUP_BYTES = kGroup * D;  // K (or V) rows of a warp's group
+    static constexpr int STAGES = D == 64 ? 10 : D == 128 ? 6 : D == 192 ? 4 : 3;
+    static constexpr int MT = D / 16;               // 16-row tiles of O^T
+    static constexpr int Q_STRIDE = 2 * D + 16;     // bytes of a query row
+    static constexpr bool Q_REGS = NT * D <= 256;   // query fragments held in registers
+    static constexpr int FIFO = STAGES + 2;         // pieces whose tiles are under way
+};
+
+struct Piece8 {
+    int q0, off, nk, r0;     // first query row, nk - nq, keys, first row
+    int rows, g, part, t0;   // rows, head, partial slot or -1, first tile
+    int t1, in_lo, in_hi, lo;  // end; keys that every row sees; keys that any row sees
+    int hi, pad[3];
+};
+
+template <int D, int NT>
+struct __align__(128) Few8Smem {
+    using C = Few8Cfg<D, NT>;
+    uint8_t ring[kWarps8][C::STAGES][2][C::GROUP_BYTES];
+    uint8_t q[C::NR * C::Q_STRIDE];
+    float merge[kWarps8][8][kMergeCols];
+    float scale[kWarps8][C::STAGES][2];
+    float qf[C::NR];                 // the power of two that a query row was divided by
+    float m[kWarps8][C::NR], l[kWarps8][C::NR], u[kWarps8][C::NR];  // the warps' states; u becomes the weight of its output
+    float f[C::NR];                  // factor of a whole item's output
+    Piece8 fifo[kWarps8][C::FIFO];
+};
+
+// Where chunk `col` of row `row` of a group lies: so that the lanes' reads of a fragment fall into different banks
+// (K: 16 bytes of two neighbouring rows at four neighbouring chunks; V: of four rows two apart at the chunks of two lanes).
+template <int D, bool V>
+__device__ __forceinline__ int at_chunk(int row, int col) {
+    if constexpr (!V) {
+        return row * D + ((D == 128 || D == 256 ? col ^ ((row & 1) << 2) : col) << 4);
+    } else {
+        const int t = (row >> 1) & 3;
+        if constexpr (D == 64) return (row >> 1) * 128 + (((((row & 1) << 2) | col) ^ (t << 1)) << 4);
+        else if constexpr (D == 128) return row * D + ((col ^ (t << 1)) << 4);
+        else if constexpr (D == 192) return row * D + ((col ^ t) << 4);
+        else return row * D + ((col ^ ((t & 1) | ((t & 2) << 1))) << 4);
+    }
+}
+
+// Two e4m3 bytes (the low or the high half of a word) as an fp16 pair, the lower byte low.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void copies_wait_but() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+
+// The power of two at or below x (x > 0 and normal).
+__device__ __forceinline__ float power_below(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs a, const Cache8 kv) {
+    using C = Few8Cfg<D, NT>;
+    constexpr int NR = C::NR, S = C::STAGES;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Few8Smem<D, NT>& s = *reinterpret_cast<Few8Smem<D, NT>*>(smem_raw);
+    const Problem& p = a.p;
+    const bool f16 = p.dtype == FA_DTYPE_F16;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int lg = lane >> 2, lt = lane & 3;  // a fragment's row (or column) and its pair
+    const unsigned G = (unsigned)p.G;
+    allow_next_kernel();
+    wait_previous_kernel();
+    // (one thread looks, so that all leave or none)
+    if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
+
+    // ---- the warp's stream: pieces of the CTA's stretch, tile by tile, S tiles ahead of the arithmetic ----
+    PagedWalk walk;
+    const PagedLine line = *a.line;
+    walk.start(p, a.pre, a.line, cta);
+    int at_t = 0, end_t = 0;          // tiles of the piece that is being fetched
+    int b_lo = 0, b_hi = 0, b_g = 0;  // its keys that any row sees, its head
+    const int32_t* table = nullptr;
+    int issued = 0, pushed = 0;       // tiles, pieces
+    bool more = true;
+    auto fetch = [&]() {
+        if (more && at_t >= end_t) {
+            while ((more = walk.next(p, a.pre, line, cta, NR, a.no_split))) {
+                const PagedSeq& sq = walk.seq;
+                const int r0 = walk.x.rt * NR, rows = min(NR, sq.nq * p.G - r0), off = sq.nk - sq.nq;
+                const int part = walk.from_start && walk.to_end ? -1 : 2 * cta + (walk.from_start ? 1 : 0);
+                const Band bd{off, p.left, p.right, sq.nk};
+                at_t = walk.t0;
+                end_t = walk.t1;
+                b_g = walk.x.g;
+                b_lo = bd.lo((int)((unsigned)r0 / G));
+                b_hi = bd.hi((int)((unsigned)(r0 + rows - 1) / G));
+                table = p.block_table + (long)walk.b * p.max_blocks;
+                if (end_t > at_t) {
+                    if (lane == 0) {
+                        Piece8 x;
+                        x.q0 = sq.q0;
+                        x.off = off;
+                        x.nk = sq.nk;
+                        x.r0 = r0;
+                        x.rows = rows;
+                        x.g = b_g;
+                        x.part = part;
+                        x.t0 = at_t;
+                        x.t1 = end_t;
+                        x.lo = b_lo;
+                        x.hi = b_hi;
+                        x.in_lo = p.left >= 0 ? (int)((unsigned)(r0 + rows - 1) / G) + off - p.left : 0;
+                        x.in_hi = p.right >= 0 ? min(sq.nk - 1, (int)((unsigned)r0 / G) + off + p.right) : sq.nk - 1;
+                        s.fifo[warp][pushed % C::FIFO] = x;
+                    }
+                    ++pushed;
+                    break;
+                }
+                // no key for any row (such a piece is whole): its rows are written here
+                for (int r = warp; r < rows; r += kWarps8) {
+                    const int i = (int)((unsigned)(r0 + r) / G), h = b_g * p.G + r0 + r - i * p.G;
+                    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (((long)sq.q0 + i) * p.h_q + h) * D);
+                    for (int x = lane; x < D / 2; x += 32) out[x] = 0u;
+                    if (lane == 0 && a.lse) a.lse[(long)h * p.T_q + sq.q0 + i] = p.sinks ? p.sinks[h] : -INFINITY;
+                }
+            }
+        }
+        if (more) {
+            const int j0 = at_t * kKeyTile + kGroup * warp, st = issued % S;
+            if (j0 <= b_hi && j0 + kGroup > b_lo) {
+                const int page = table[j0 / p.page_size], row = j0 % p.page_size;
+                const bool there = (unsigned)page < (unsigned)a.num_pages;
+                if (!there && lane == 0) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                const long first = there ? (((long)page * p.page_size + row) * p.h_kv + b_g) * D : 0;
+                const long step = (long)p.h_kv * D;
+#pragma unroll
+                for (int y = 0; y < C::CPR / 2; ++y) {
+                    const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR, j = j0 + r;
+                    const bool seen = there && j >= b_lo && j <= b_hi;  // (what lies behind a page's used keys may be anything)
+                    const long from = seen ? first + r * step + 16 * col : 0;
+                    copy16_async(&s.ring[warp][st][0][at_chunk<D, false>(r, col)], kv.k + from, seen);
+                    copy16_async(&s.ring[warp][st][1][at_chunk<D, true>(r, col)], kv.v + from, seen);
+                }
+                if (lane < 2)
+                    copy4_async(&s.scale[warp][st][lane], (lane ? kv.v_scale : kv.k_scale) +
+                                (there ? ((long)page * kv.blocks + row / kv.block) * p.h_kv + b_g : 0));
+            }
+            ++at_t;
+            ++issued;
+        }
+        copies_commit();  // (a group to each call, so that the groups count the tiles)
+    };
+#pragma unroll 1
+    for (int x = 0; x < S; ++x) fetch();
+
+    int done = 0;  // tiles
+#pragma unroll 1
+    for (int piece = 0;; ++piece) {
+        __syncwarp();
+        if (piece >= pushed) break;
+        const Piece8 w = s.fifo[warp][piece % C::FIFO];
+        // ---- the query rows, as fp16 ----
+        __syncthreads();  // (the rows and states of the piece before have been read)
+        for (int r = warp; r < NR; r += kWarps8) {
+            uint32_t x[D / 64];
+            float top = 0.f;
+            if (r < w.rows) {
+                const int i = (int)((unsigned)(w.r0 + r) / G), h = w.g * p.G + w.r0 + r - i * p.G;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (((long)w.q0 + i) * p.h_q + h) * D);
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) x[e] = src[lane + 32 * e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) x[e] = 0u;
+            }
+            float2 v[D / 64];
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+                v[e] = f16 ? make_float2(lo16<true>(x[e]), hi16<true>(x[e])) : make_float2(lo16<false>(x[e]), hi16<false>(x[e]));
+                top = fmaxf(top, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+            }
+            top = warp_max(top);
+            // (rows of zeros, or with infinities, are left as they are)
+            const float unit = top >= 1e-30f && top < INFINITY ? power_below(top) * 0x1p-7f : 1.f, inv = 1.f / unit;
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e)
+                *reinterpret_cast<uint32_t*>(&s.q[r * C::Q_STRIDE + 4 * (lane + 32 * e)]) = pack16<true>(v[e].x * inv, v[e].y * inv);
+            if (lane == 0) s.qf[r] = unit * p.scale_log2;
+        }
+        __syncthreads();
+        // ---- state: rows 8 n + 2 lt and 8 n + 2 lt + 1 ----
+        float m[NT][2], u[NT][2], l[NT][2], qf[NT][2], acc[C::MT][NT][4];
+        uint4 qr[C::Q_REGS ? NT : 1][D / 64][2];
+        auto q_frag = [&](int n, int i, int h) {
+            return *reinterpret_cast<const uint4*>(&s.q[(8 * n + lg) * C::Q_STRIDE + 32 * (lt + 4 * i) + 16 * h]);
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = kNoRef;
+                u[n][e] = kNoUnit;
+                l[n][e] = 0.f;
+                qf[n][e] = s.qf[8 * n + 2 * lt + e];
+            }
+            if constexpr (C::Q_REGS) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) qr[n][i][h] = q_frag(n, i, h);
+            }
+#pragma unroll
+            for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[x][n][e] = 0.f;
+        }
+#pragma unroll 1
+        for (int t = w.t0; t < w.t1; ++t, ++done) {
+            const int st = done % S, j0 = t * kKeyTile + kGroup * warp;
+            copies_wait_but<S - 1>();
+            __syncwarp();
+            if (j0 <= w.hi && j0 + kGroup > w.lo) {
+                const uint8_t *k8 = s.ring[warp][st][0], *v8 = s.ring[warp][st][1];
+                const float ks = s.scale[warp][st][0], vs = s.scale[warp][st][1];
+                // ---- S^T = K Q^T ----
+                float sc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 ka = *reinterpret_cast<const uint4*>(k8 + at_chunk<D, false>(lg, lt + 4 * i));
+                    const uint4 kb = *reinterpret_cast<const uint4*>(k8 + at_chunk<D, false>(lg + 8, lt + 4 * i));
+                    uint4 q0[NT], q1[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        q0[n] = C::Q_REGS ? qr[C::Q_REGS ? n : 0][i][0] : q_frag(n, i, 0);
+                        q1[n] = C::Q_REGS ? qr[C::Q_REGS ? n : 0][i][1] : q_frag(n, i, 1);
+                    }
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t a0 = widen_lo(wa[x]), a1 = widen_lo(wb[x]), a2 = widen_hi(wa[x]), a3 = widen_hi(wb[x]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint4& qq = x < 2 ? q0[n] : q1[n];
+                            mma16816(sc[n], a0, a1, a2, a3, x & 1 ? qq.z : qq.x, x & 1 ? qq.w : qq.y);
+                        }
+                    }
+                }
+                // ---- scores in log2 units; keys j0 + lg and j0 + lg + 8 ----
+                const bool edge = j0 < w.in_lo || j0 + kGroup - 1 > w.in_hi;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float c0 = qf[n][0] * ks, c1 = qf[n][1] * ks;
+                    sc[n][0] *= c0;
+                    sc[n][1] *= c1;
+                    sc[n][2] *= c0;
+                    sc[n][3] *= c1;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = j0 + lg + 8 * h;
+                        // rows [ra, rb] see key j: positions j - off - right <= i <= j - off + left
+                        int ra = 0, rb = NR - 1;
+                        if (p.right >= 0) ra = (int)max(min(((long)j - w.off - p.right) * p.G - w.r0, (long)NR), 0l);
+                        if (p.left >= 0) rb = (int)min(max(((long)j - w.off + p.left + 1) * p.G - 1 - w.r0, -1l), (long)NR);
+                        if (j >= w.nk) ra = NR;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int r = 8 * n + 2 * lt + e;
+                                if (r < ra || r > rb) sc[n][2 * h + e] = -INFINITY;
+                            }
+                    }
+                }
+                // ---- P = 2^(x - m), P' = P vs u ----
+                float pr[NT][4], over = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pr[n][e] = ex2(sc[n][e] - m[n][e & 1]);
+                        over = fmaxf(over, pr[n][e] * fmaxf(1.f, vs * u[n][e & 1]));
+                    }
+                if (__any_sync(0xffffffffu, over > kTop)) {
+                    // some row's reference or unit moves: to the maxima so far
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = fmaxf(sc[n][e], sc[n][2 + e]);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const float mo = m[n][e], mn = fmaxf(mo, top), keep = ex2(mo - mn);
+                            // the largest term so far, at 1 / u in units of the old reference, and of these keys
+                            const float most = fmaxf(keep / u[n][e], ex2(top - mn) * vs);
+                            const float un = most > 0x1p-126f && most < INFINITY ? 1.f / power_below(most) : kNoUnit;
+                            const float f = keep * (un / u[n][e]);
+                            m[n][e] = mn;
+                            l[n][e] *= keep;
+                            u[n][e] = un;
+#pragma unroll
+                            for (int x = 0; x < C::MT; ++x) {
+                                acc[x][n][e] *= f;
+                                acc[x][n][2 + e] *= f;
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) pr[n][2 * h + e] = ex2(sc[n][2 * h + e] - mn);
+                        }
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    l[n][0] += pr[n][0] + pr[n][2];
+                    l[n][1] += pr[n][1] + pr[n][3];
+                    // (a row without a value so far has u = 2^126 and P = 0: 0 * inf would be NaN)
+                    float f0 = vs * u[n][0], f1 = vs * u[n][1];
+                    f0 = f0 > 0x1p100f ? 0x1p100f : f0;
+                    f1 = f1 > 0x1p100f ? 0x1p100f : f1;
+                    pb[n][0] = transpose8x8(pack16<true>(pr[n][0] * f0, pr[n][1] * f1));
+                    pb[n][1] = transpose8x8(pack16<true>(pr[n][2] * f0, pr[n][3] * f1));
+                }
+                // ---- O^T += V^T P^T: the lane's columns are [lg D / 8, (lg + 1) D / 8), its keys 2 lt, 2 lt + 1 and those + 8 ----
+                constexpr int WORDS = D / 32;  // 4-byte words of the lane's columns
+                uint32_t vw[4][WORDS];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int r = 2 * lt + (y & 1) + 8 * (y >> 1);
+                    if constexpr (D >= 128 && D != 192) {
+#pragma unroll
+                        for (int z = 0; z < WORDS / 4; ++z) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(v8 + at_chunk<D, true>(r, lg * (WORDS / 4) + z));
+                            vw[y][4 * z] = x.x;
+                            vw[y][4 * z + 1] = x.y;
+                            vw[y][4 * z + 2] = x.z;
+                            vw[y][4 * z + 3] = x.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < WORDS / 2; ++z) {
+                            const int byte = lg * (D / 8) + 8 * z;
+                            const uint2 x = *reinterpret_cast<const uint2*>(v8 + at_chunk<D, true>(r, byte >> 4) + (byte & 8));
+                            vw[y][2 * z] = x.x;
+                            vw[y][2 * z + 1] = x.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int z = 0; z < WORDS; ++z)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = __byte_perm(vw[0][z], vw[1][z], h ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(vw[2][z], vw[3][z], h ? 0x7362 : 0x5140);
+                        const uint32_t a0 = widen_lo(x), a1 = widen_hi(x), a2 = widen_lo(y), a3 = widen_hi(y);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(acc[2 * z + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    }
+            }
+            __syncwarp();  // the stage has been read
+            fetch();
+        }
+        // ---- the warps' states join ----
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+                if (lg == 0) {
+                    const int r = 8 * n + 2 * lt + e;
+                    s.m[warp][r] = m[n][e];
+                    s.l[warp][r] = l[n][e];
+                    s.u[warp][r] = u[n][e];
+                }
+            }
+        __syncthreads();
+        if (tid < NR) {
+            float top = kNoRef, sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < kWarps8; ++x) top = fmaxf(top, s.m[x][tid]);
+#pragma unroll
+            for (int x = 0; x < kWarps8; ++x) {
+                const float keep = ex2(s.m[x][tid] - top);
+                sum += s.l[x][tid] * keep;
+                s.u[x][tid] = keep / s.u[x][tid];
+            }
+            if (top <= 0.5f * kNoRef) top = -INFINITY;
+            if (tid < w.rows) {
+                if (w.part >= 0) {
+                    a.part_ml[0][(long)w.part * NR + tid] = make_float2(top, sum);
+                    s.f[tid] = 1.f;
+                } else {
+                    const int i = (int)((unsigned)(w.r0 + tid) / G), h = w.g * p.G + w.r0 + tid - i * p.G;
+                    const float s2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
+                    const float mf = fmaxf(top, s2);
+                    const float wgt = top == -INFINITY ? 0.f : ex2(top - mf);
+                    const float lt2 = sum * wgt + (p.sinks && mf != -INFINITY ? ex2(s2 - mf) : 0.f);
+                    s.f[tid] = lt2 != 0.f ? wgt / lt2 : 0.f;
+                    if (a.lse) a.lse[(long)h * p.T_q + w.q0 + i] = lt2 != 0.f ? (mf + log2f(lt2)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float w0 = s.u[warp][8 * n + 2 * lt], w1 = s.u[warp][8 * n + 2 * lt + 1];
+            // (64 columns at a time: of each lane's D / 8 columns eight)
+#pragma unroll
+            for (int y = 0; y < D / kMergeCols; ++y) {
+                if (n + y > 0) __syncthreads();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float* c = acc[4 * y + x][n];
+                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt][8 * lg + 2 * x]) = make_float2(c[0] * w0, c[2] * w0);
+                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt + 1][8 * lg + 2 * x]) = make_float2(c[1] * w1, c[3] * w1);
+                }
+                __syncthreads();
+                const int r = 8 * n + warp;  // a warp to a row
+                if (r < w.rows) {
+                    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < kWarps8; ++x) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&s.merge[x][warp][2 * lane]));
+                    const float f = s.f[r];
+                    const int col = (lane >> 2) * (D / 8) + 8 * y + 2 * (lane & 3);
+                    if (w.part >= 0) {
+                        *reinterpret_cast<float2*>(&a.part_o[0][((long)w.part * NR + r) * D + col]) = o;
+                    } else {
+                        const int i = (int)((unsigned)(w.r0 + r) / G), h = w.g * p.G + w.r0 + r - i * p.G;
+                        const float ox = f == 0.f ? 0.f : o.x * f, oy = f == 0.f ? 0.f : o.y * f;
+                        *reinterpret_cast<uint32_t*>(&a.o[(((long)w.q0 + i) * p.h_q + h) * D + col]) =
+                            f16 ? pack16<true>(ox, oy) : pack16<false>(ox, oy);
+                    }
+                }
+            }
+        }
+    }
+    if (tid == 0) a.cut[cta] = walk.cut;
+}
+
+template <int D, int NT>
+cudaError_t launch_few8(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
+    constexpr size_t smem = sizeof(Few8Smem<D, NT>);
+    static_assert(smem <= 227 * 1024, "the few-row kernel's shared memory");
+    cudaError_t e = cudaFuncSetAttribute(paged8_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(paged8_few_kernel<D, NT>, dim3(ctas), kThreads, smem, st, a, kv);
+}
+
+template <int D>
+cudaError_t launch_few8_d(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
+    switch (a.few_rows) {
+        case 8: return launch_few8<D, 1>(a, kv, ctas, st);
+        case 16: return launch_few8<D, 2>(a, kv, ctas, st);
+        case 32:
+            if constexpr (D <= 128) return launch_few8<D, 4>(a, kv, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
+    switch (a.p.d) {
+        case 64: return launch_few8_d<64>(a, kv, ctas, st);
+        case 128: return launch_few8_d<128>(a, kv, ctas, st);
+        case 192: return launch_few8_d<192>(a, kv, ctas, st);
+        case 256: return launch_few8_d<256>(a, kv, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fa

@@ -104,6 +104,13 @@
  *    it picks the kernel's tile, and a wrong one costs time, not correctness).  Results do not
  *    depend on how other work is scheduled: the same call gives the same bits.
  *
+ *  - the same form over a cache in 8 bits (cache_dtype = FA_DTYPE_E4M3; dtype is the queries' and the
+ *    output's, bf16 or fp16; every head dimension): k and v are pools of e4m3 bytes and the true keys and
+ *    values are byte * scale, with one scale for scale_block rows of a page and a head: k_scale,
+ *    v_scale [num_pages, page_size / scale_block, h_kv] (fp32, not negative).  scale_block is a positive multiple
+ *    of 16 that divides page_size.  fa_qk_norm_rope_append8 fills such a cache.  All else is as above;
+ *    bytes and scales of rows behind a sequence's used keys have no effect.
+ *
  * FP8 forward (vllm-project/flash-attention README, "FlashAttention-3 beta release":
  * "FP8 forward"): with dtype = FA_DTYPE_E4M3, q, k and v hold e4m3 bytes (1 byte per
  * element, same layouts) and the true inputs are q * q_descale[b * h_kv + g] (likewise k,
@@ -191,6 +198,11 @@ typedef struct fa_params {
      * such a failure, which is how the failure path is exercised; outputs of a failed call
      * are unspecified. */
     unsigned long long wait_limit_ns;
+    /* A cache in 8 bits (packed queries over a paged cache only; see above) */
+    int cache_dtype;        /* 0: k and v have the queries' type; FA_DTYPE_E4M3 */
+    int scale_block;        /* rows of a page that share a scale */
+    const float *k_scale;   /* device fp32 [num_pages, page_size / scale_block, h_kv] */
+    const float *v_scale;
 } fa_params;
 
 /* Bytes of workspace fa_fwd / fa_bwd need for these parameters (>= 256: the first

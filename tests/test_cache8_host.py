@@ -133,3 +133,38 @@ def test_rotation_gradient_by_differences():
             e = np.zeros_like(x)
             e[0, i, j] = 1e-3
             assert abs(((turn(x + e) - turn(x - e)) * g).sum() / 2e-3 - back[0, i, j]) < 1e-10
+
+
+# ------------------------------------------------------------------------------------------
+# attention over the cache
+# ------------------------------------------------------------------------------------------
+
+def over_cache8(**kw):
+    from test_step_host import paged
+    return paged(**{**dict(cache_dtype=fa.FA_DTYPE_E4M3, page_size=64, max_blocks_per_seq=8, scale_block=32, k_scale=0x6000, v_scale=0x7000), **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(cache_dtype=2), fa.FA_ERR_INVALID_ARG), (dict(cache_dtype=-1), fa.FA_ERR_INVALID_ARG),
+    (dict(scale_block=0), fa.FA_ERR_INVALID_ARG), (dict(scale_block=8), fa.FA_ERR_INVALID_ARG), (dict(scale_block=48), fa.FA_ERR_INVALID_ARG),
+    (dict(scale_block=128), fa.FA_ERR_INVALID_ARG), (dict(scale_block=-64), fa.FA_ERR_INVALID_ARG), (dict(page_size=0), fa.FA_ERR_INVALID_ARG),
+    (dict(k_scale=None), fa.FA_ERR_INVALID_ARG), (dict(v_scale=None), fa.FA_ERR_INVALID_ARG),
+    (dict(dtype=fa.FA_DTYPE_E4M3), fa.FA_ERR_UNSUPPORTED), (dict(cu_seqlens_k=0x5000), fa.FA_ERR_UNSUPPORTED),
+    (dict(cu_seqlens_q=None), fa.FA_ERR_UNSUPPORTED), (dict(block_table=None, cu_seqlens_k=0x5000), fa.FA_ERR_UNSUPPORTED),
+    (dict(cu_seqlens_q=None, block_table=None), fa.FA_ERR_UNSUPPORTED), (dict(d=96), fa.FA_ERR_UNSUPPORTED), (dict(seqused_k=None), fa.FA_ERR_INVALID_ARG),
+])
+def test_forward_refuses(kw, code):
+    p = over_cache8(**kw)
+    assert fa.fa_fwd(p, A, B, C, D, None, E, 1 << 40, None) == code
+    assert fa.fa_fwd_workspace_size(p) == 0
+
+
+def test_forward_pointers_and_workspace():
+    p = over_cache8()
+    n = fa.fa_fwd_workspace_size(p)
+    assert n > 256 and fa.fa_fwd_workspace_size(over_cache8(max_seqlen_q=1)) < n
+    assert fa.fa_fwd(p, A, B, C, D, None, E, n - 1, None) == fa.FA_ERR_WORKSPACE
+    for bad in ((None, B, C, D, E), (A, None, C, D, E), (A, B, None, D, E), (A, B, C, None, E), (A, B, C, D, None), (MISAL, B, C, D, E),
+                (A, MISAL, C, D, E), (A, B, MISAL, D, E), (A, B, C, MISAL, E), (A, B, C, D, MISAL)):
+        assert fa.fa_fwd(p, *bad[:4], None, bad[4], n, None) == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_bwd(p, *([A] * 9), None, E, 1 << 40, None) == fa.FA_ERR_UNSUPPORTED
