@@ -125,6 +125,19 @@ cudaError_t timed(KernelId id, cudaStream_t st, F&& launch) {
     return e;
 }
 
+// 4-D tensor map over a paged pool of bytes [pages][rows][h][d], boxes of `box` whole rows of a head, not
+// swizzled.  Out-of-range pages read as zero.
+bool encode_pages8(CUtensorMap* m, const void* base, int d, int h, int rows, int pages, int box) {
+    auto fn = encoder();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)h, (cuuint64_t)rows, (cuuint64_t)pages};
+    cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)h * d, (cuuint64_t)rows * h * d};
+    cuuint32_t bx[4] = {(cuuint32_t)d, 1, (cuuint32_t)box, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------------------------------------
 // argument normalisation
 // ------------------------------------------------------------------------------------------
@@ -390,22 +403,18 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl.ctas = sm_count();
     const long longest = in.max_seqlen_q > 0 && in.max_seqlen_q < p.T_q ? in.max_seqlen_q : p.T_q;
     const long rows = longest * p.G;
-    if (p.cache8) {
-        const int most = p.d <= 128 ? 32 : 16;
-        pl.few_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : most;
-        pl.few_max = kAllFew;
-        pl.many_rows = most;
-    } else {
     // Every sequence known to have 64 rows at most: the few-row kernel alone, its tile the rows.  Else it takes those of a
     // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
     // a decode step 33 us where one of 16 takes 20: 20 sequences of 5 heads a group, d = 64), and none
     // where a token has more than 64.
-    pl.many = rows > 64;
+    // (A cache in 8 bits: the few-row kernel's tiles are 8 to 32 rows.)
+    const int most = !p.cache8 ? 64 : p.d <= 128 ? 32 : 16;
+    pl.many = rows > most && !(p.cache8 && p.d > 128);
     const long tile = pl.many ? p.G : rows;
-    pl.few_rows = tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
-    pl.few_max = !pl.many ? kAllFew : p.G <= 64 ? pl.few_rows : 0;
+    pl.few_rows = p.cache8 && tile <= 8 ? 8 : tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
+    if (pl.few_rows > most) pl.few_rows = most;
+    pl.few_max = !pl.many ? kAllFew : p.G <= most ? pl.few_rows : 0;
     pl.many_rows = (p.d <= 128 ? 2 : 1) * p.P * p.G;
-    }
     pl.off_pre = kStatusBytes;
     pl.off_line = pl.off_pre + align256((size_t)2 * (p.B + 1) * 8);
     pl.off_cut = pl.off_line + align256(2 * sizeof(PagedLine));
@@ -457,25 +466,22 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     a.part_o[1] = reinterpret_cast<float*>(ws + pl.off_mo);
     a.part_ml[1] = reinterpret_cast<float2*>(ws + pl.off_mml);
     a.status = status;
-    if (p.cache8) {
-        const Cache8 kv{reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(v), in.k_scale, in.v_scale, in.scale_block,
-                        p.page_size / in.scale_block};
-        cudaError_t e8 = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
-        if (e8 == cudaSuccess) e8 = timed(kPagedFew, st, [&] { return launch_paged8_few(a, kv, pl.ctas, st); });
-        if (e8 == cudaSuccess) e8 = timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); });
-        return cuda_status(e8);
-    }
+    Cache8 kv{};
+    if (p.cache8)
+        kv = Cache8{reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(v), in.k_scale, in.v_scale, in.scale_block,
+                    p.page_size / in.scale_block};
     CUtensorMap tk, tv;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     // a key's row is d * 2 bytes of h_kv times as many: fetched 256 bytes at a time, half of it would be
     // another head's where d * 2 is 128 or 384 (decode of 32 x 16000 keys, 4 heads: d = 64 111 us against
     // 126, d = 192 with 2 heads 132 against 146)
     const CUtensorMapL2promotion promotion = p.d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    if (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion) ||
-        !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion))
+    if (!p.cache8 && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion) ||
+                      !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion)))
         return FA_ERR_CUDA;
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
-    if (e == cudaSuccess && pl.few_max > 0) e = timed(kPagedFew, st, [&] { return launch_paged_few(a, tk, tv, pl.ctas, st); });
+    if (e == cudaSuccess && pl.few_max > 0)
+        e = timed(kPagedFew, st, [&] { return p.cache8 ? launch_paged8_few(a, kv, pl.ctas, st) : launch_paged_few(a, tk, tv, pl.ctas, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     if (!pl.many) return cuda_status(timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); }));
     // sequences of more rows: the tensor-core kernels, 2 P G rows to an item (P G at d = 192 / 256,
@@ -495,7 +501,12 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     f.line = a.line + 1;
     f.num_pages = a.num_pages;
     f.box = p.d <= 128 || a.box <= 64 ? a.box : 64;
-    if (f.box != a.box && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion) ||
+    f.cache8 = kv;
+    if (p.cache8) {
+        const int rows8 = f.box < 64 ? f.box : 64;
+        if (!encode_pages8(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, rows8) || !encode_pages8(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, rows8))
+            return FA_ERR_CUDA;
+    } else if (f.box != a.box && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion) ||
                            !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion)))
         return FA_ERR_CUDA;
     f.no_split = a.no_split;

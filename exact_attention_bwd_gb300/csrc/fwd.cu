@@ -46,6 +46,12 @@
 // the partials un-normalised, with their maximum and sum), the producer warp loads each key
 // tile page by page, and value rows that no query of the item sees are cleared in shared
 // memory before the product (a page's unused rows may hold anything, and 0 * NaN is NaN).
+//
+// The C8 instantiation is that over a cache in 8 bits (512 threads): the producer warp loads half tiles
+// of e4m3 bytes and their blocks' scales into a ring of their own, and warps 12..15 turn them into the
+// 16-bit tiles that the products read, byte * scale in the queries' type: exact for scales that are powers of
+// two (an e4m3 value has four significant bits), else rounded once, as a 16-bit cache would hold it.
+#include "cache8.cuh"
 #include "fwd_items.cuh"
 #include "paged.cuh"
 #include "trace.cuh"
@@ -53,7 +59,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreadsFwd = 384;
+constexpr int kThreadsFwd = 384, kThreadsFwd8 = 512;
 #ifndef FA_FWD_EXP_POLY_PAIRS
 #define FA_FWD_EXP_POLY_PAIRS 0
 #endif
@@ -64,8 +70,9 @@ constexpr int kExpPolyPairs = FA_FWD_EXP_POLY_PAIRS;
 // item sees only a few key tiles and its chain of waits, not the tensor pipe, sets the pace.
 // With 64-key tiles the tensor memory of a CTA halves to 256 columns and its shared memory
 // to about 100 KB, so two CTAs share an SM and twice as many query tiles are in flight.
-template <int D, int KT>
+template <int D, int KT, bool C8 = false>
 struct FwdCfg {
+    static constexpr int THREADS = C8 ? kThreadsFwd8 : kThreadsFwd;
     static_assert(KT == 128 || (KT == 64 && D == 64), "64-key tiles only at d = 64");
     static constexpr int KCH = D / 64;                  // 64-column chunks of a row
     static constexpr int TILE_BYTES = 128 * D * 2;      // one Q tile (128 rows)
@@ -82,8 +89,12 @@ struct FwdCfg {
     // registers per thread after setmaxnreg: producer / MMA / TMEM owner / scheduler group,
     // and the two softmax groups; 128 REG_LOW + 256 REG_HIGH stays within what the CTA is
     // launched with (checked before every launch)
-    static constexpr int REG_LOW = KT == 128 ? 56 : 48;
-    static constexpr int REG_HIGH = KT == 128 ? 224 : 96;
+    // (C8: 128 x 48 for the converting warps as well, 65536 in all)
+    static constexpr int REG_LOW = KT == 128 && !C8 ? 56 : 48;
+    static constexpr int REG_HIGH = C8 ? 208 : KT == 128 ? 224 : 96;
+    static constexpr int REG_CONV = 48;
+    // C8: half tiles of bytes under way
+    static constexpr int UNITS8 = D == 64 ? 6 : 3;
 };
 
 // One decoded work item, as the scheduler warp hands it to the other roles.
@@ -99,12 +110,12 @@ struct ItemInfo {
     int nk, lo, hi, part, before;
 };
 constexpr int kItemSlots = 3;
-// arrivals that free an item slot: producer, MMA issuer and the eight softmax warps
+// arrivals that free an item slot: producer, MMA issuer and the eight softmax warps (C8: and four converting ones)
 constexpr int kItemReaders = 10;
 
-template <int D, int KT>
+template <int D, int KT, bool C8>
 struct __align__(1024) FwdSmem {
-    using C = FwdCfg<D, KT>;
+    using C = FwdCfg<D, KT, C8>;
     uint8_t q[2][C::TILE_BYTES];
     uint8_t k[C::STAGES][C::KV_BYTES];
     uint8_t v[C::STAGES][C::KV_BYTES];
@@ -119,17 +130,19 @@ struct __align__(1024) FwdSmem {
     int2 band[kItemSlots][2][128];  // (jlo, jhi) of every row of both query tiles
     uint32_t tmem_base;
     int abort_flag;
+    std::conditional_t<C8, Ring8<D, C::UNITS8>, char> bytes;  // C8: half tiles as the cache holds them
 };
 
-template <int D, bool F16, int KT, bool PG>
-__global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
+template <int D, bool F16, int KT, bool PG, bool C8>
+__global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTAS_PER_SM)
     fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                const __grid_constant__ CUtensorMap tmv) {
-    using C = FwdCfg<D, KT>;
+    using C = FwdCfg<D, KT, C8>;
+    static_assert(!C8 || PG, "a cache in 8 bits is paged");
     extern __shared__ uint8_t smem_raw[];
-    FwdSmem<D, KT>& smem =
-        *reinterpret_cast<FwdSmem<D, KT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    FwdSmem<D, KT>& s = smem;
+    FwdSmem<D, KT, C8>& smem =
+        *reinterpret_cast<FwdSmem<D, KT, C8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    FwdSmem<D, KT, C8>& s = smem;
     const Problem& p = a.p;
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
@@ -143,9 +156,9 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         s.abort_flag = 0;
         mbar_init(&s.q_full, 1);
         for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_full[i], C8 ? 4 : 1);  // (C8: an arrival of each converting warp)
             mbar_init(&s.k_empty[i], 1);
-            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_full[i], C8 ? 4 : 1);
             mbar_init(&s.v_empty[i], 1);
         }
         for (int k = 0; k < 2; ++k) {
@@ -158,15 +171,16 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         mbar_init(&s.drain, 1);
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], kItemReaders);
+            mbar_init(&s.item_empty[i], kItemReaders + (C8 ? 4 : 0));
         }
+        if constexpr (C8) s.bytes.init();
         fence_mbar_init();
     }
     if (p.P * p.G < 128) {
         // rows past P*G of a Q tile are never written by TMA: zero them once
         for (int k = 0; k < 2; ++k)
             for (int c = 0; c < C::KCH; ++c)
-                for (int x = p.P * p.G * 128 + tid * 16; x < 128 * 128; x += kThreadsFwd * 16)
+                for (int x = p.P * p.G * 128 + tid * 16; x < 128 * 128; x += C::THREADS * 16)
                     *reinterpret_cast<uint4*>(&s.q[k][c * C::CHUNK_BYTES + x]) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
@@ -198,9 +212,53 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
     // branch so the register allocator sees it on every path.
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(C::REG_LOW) : "memory");
-    if (PG && warp == 0) {
+    if (C8 && warp == 0) {
+        // ================= TMA producer, paged cache in 8 bits (the whole warp) =================
+        if constexpr (C8) {
+        FwdSmem<D, KT, C8>& s = own_shared(smem);
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        const uint32_t qbox = (uint32_t)(p.P * p.G) * 128u;
+        int n_q = 0;
+        uint32_t units = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int slot = n % kItemSlots;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
+            const ItemInfo& it = s.item[slot];
+            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, nk = it.nk;
+            const int32_t* table = p.block_table + (long)it.b * p.max_blocks;
+            const int qr0 = it.q0 + it.s0[0], qr1 = it.q0 + it.s0[1];
+            const bool on0 = it.t1[0] > it.t0[0], on1 = it.t1[1] > it.t0[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[slot]);
+            if (end) break;
+            if (u1 <= u0) continue;
+            Pages8 pages(a.cache8, p, table, a.num_pages, a.box, nk);
+            pages.look(u0, u1);
+            if (n_q > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty, (n_q - 1) & 1, ab)))) break;
+            if (lane == 0) {
+                mbar_expect_tx(&s.q_full, qbox * C::KCH * ((on0 ? 1u : 0u) + (on1 ? 1u : 0u)));
+                for (int c = 0; c < C::KCH; ++c) {
+                    if (on0) tma_load_4d(&s.q[0][c * C::CHUNK_BYTES], &tmq, &s.q_full, c * 64, g * p.G, qr0, 0);
+                    if (on1) tma_load_4d(&s.q[1][c * C::CHUNK_BYTES], &tmq, &s.q_full, c * 64, g * p.G, qr1, 0);
+                }
+            }
+            ++n_q;
+            for (int j = u0; ok && j < u1; ++j) {
+                pages.take(j, u1, a.status);
+#pragma unroll 1
+                for (int x = 0; ok && x < 4; ++x)  // the halves of K, of V
+                    ok = s.bytes.load(units, pages, x & 1, x < 2 ? tmk : tmv, x < 2 ? a.cache8.k_scale : a.cache8.v_scale, g, ab);
+            }
+        }
+        s.bytes.drain(units);
+        if (n_q > 0) mbar_wait_quiet(&s.q_full, (n_q - 1) & 1);
+        }
+    } else if (PG && warp == 0) {
         // ================= TMA producer, paged cache (the whole warp) =================
-        FwdSmem<D, KT>& s = own_shared(smem);
+        FwdSmem<D, KT, C8>& s = own_shared(smem);
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
@@ -337,7 +395,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
         // ================= MMA issuer =================
         // Everything the issue path touches lives in registers (no per-tile arrays indexed
         // at run time), so consecutive MMAs go out back to back.
-        FwdSmem<D, KT>& s = PG ? own_shared(smem) : smem;
+        FwdSmem<D, KT, C8>& s = PG ? own_shared(smem) : smem;
         const uint32_t tmem = PG ? own_copy(tmem_base) : tmem_base;
         if (lane == 0) {
             Tracer tr;
@@ -603,10 +661,45 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             }
         }
     }
+    } else if (C8 && warp >= 12) {
+        if constexpr (C8) {
+        // ================= C8: bytes to 16-bit tiles, a warp to 16 rows of each half tile =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(C::REG_CONV) : "memory");
+        FwdSmem<D, KT, C8>& s = own_shared(smem);
+        uint32_t units = 0;
+        int gt = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int slot = n % kItemSlots;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
+            const ItemInfo& it = s.item[slot];
+            const int end = it.end, u0 = it.u0, u1 = it.u1, lo = it.lo, hi = it.hi;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[slot]);
+            if (end) break;
+            for (int j = u0; ok && j < u1; ++j, ++gt) {
+                const int st = gt % C::STAGES;
+                const uint32_t ph = (gt / C::STAGES) & 1;
+#pragma unroll 1
+                for (int x = 0; ok && x < 2; ++x) {
+                    uint64_t* empty = x ? &s.v_empty[st] : &s.k_empty[st];
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty, ph ^ 1, ab)))) break;
+                    uint8_t* tile = x ? s.v[st] : s.k[st];
+#pragma unroll 1
+                    for (int h = 0; ok && h < 2; ++h)
+                        ok = s.bytes.template widen<F16>(units, warp - 12, tile + 64 * h * 128, C::KV_CHUNK, j * KT + 64 * h, lo, hi, ab);
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x ? &s.v_full[st] : &s.k_full[st]);
+                }
+            }
+        }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" :: "n"(C::REG_HIGH) : "memory");
         // ================= softmax: one thread per row =================
-        FwdSmem<D, KT>& s = PG ? own_shared(smem) : smem;
+        FwdSmem<D, KT, C8>& s = PG ? own_shared(smem) : smem;
         const int warp = PG ? own_copy(tid >> 5) : tid >> 5;
         const uint32_t tmem = PG ? own_copy(tmem_base) : tmem_base;
         const int k = (warp - 4) >> 2;           // query tile
@@ -704,7 +797,15 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             // pipe (exp2_poly2) to share the load with the MUFU unit.
             const float base = (m_used == -INFINITY) ? 0.f : m_used;
             const bool poly_ok = !__any_sync(0xffffffffu, edge);
-            const float2 c2 = make_float2(c, c), nb2 = make_float2(-base, -base);
+            float cx = c;
+            if (C8 && __any_sync(0xffffffffu, fabsf(base) > 0x1p24f)) {
+                // s c - m is one rounding of its own, and m one of the largest s c: where that is more than a few
+                // units (scores of 2^31 and more), 2^(s c - m) would not end near 1.  The products are rounded first.
+#pragma unroll
+                for (int cc = 0; cc < KT; ++cc) sr[cc] = __float_as_uint(__uint_as_float(sr[cc]) * c);
+                cx = 1.f;
+            }
+            const float2 c2 = make_float2(cx, cx), nb2 = make_float2(-base, -base);
             float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int cc = 0; cc < KT; cc += 2) {
@@ -725,7 +826,7 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
             else tmem_st_32x32b_x32(tS, sr);
             l += sum;
             if (KT == 64 && __any_sync(0xffffffffu, rescale)) rescale_o();
-            if (PG && !poly_ok) {
+            if (PG && !C8 && !poly_ok) {
                 // value rows outside every row's band (in a tile with masked entries, then): cleared by
                 // tile 0's group where it takes part (the P V of tile 1 is issued behind that of tile 0),
                 // else by tile 1's
@@ -882,21 +983,22 @@ __global__ void __launch_bounds__(kThreadsFwd, FwdCfg<D, KT>::CTAS_PER_SM)
 
 }  // namespace
 
-template <int D, bool F16, int KT, bool PG = false>
+template <int D, bool F16, int KT, bool PG = false, bool C8 = false>
 static cudaError_t launch_fwd_k(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t st) {
-    using C = FwdCfg<D, KT>;
-    const size_t smem = sizeof(FwdSmem<D, KT>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, F16, KT, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    using C = FwdCfg<D, KT, C8>;
+    constexpr size_t smem = sizeof(FwdSmem<D, KT, C8>) + 1024;
+    static_assert(smem <= 227 * 1024, "the forward's shared memory");
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, F16, KT, PG, C8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // the warp groups' setmaxnreg shares must fit in the registers the CTA is launched with
     // (an increase beyond them would never be granted)
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, fwd_kernel<D, F16, KT, PG>)) != cudaSuccess) return e;
-    if (fa.numRegs * kThreadsFwd < 128 * C::REG_LOW + 256 * C::REG_HIGH) return cudaErrorLaunchOutOfResources;
+    if ((e = cudaFuncGetAttributes(&fa, fwd_kernel<D, F16, KT, PG, C8>)) != cudaSuccess) return e;
+    if (fa.numRegs * C::THREADS < 128 * C::REG_LOW + 256 * C::REG_HIGH + (C8 ? 128 * C::REG_CONV : 0)) return cudaErrorLaunchOutOfResources;
     if (a.n_items <= 0 || a.n_ctas <= 0) return cudaSuccess;
-    if constexpr (PG) return launch_after(fwd_kernel<D, F16, KT, PG>, dim3(a.n_ctas), kThreadsFwd, smem, st, a, tq, tk, tv);
-    fwd_kernel<D, F16, KT, PG><<<(unsigned)a.n_ctas, kThreadsFwd, smem, st>>>(a, tq, tk, tv);
+    if constexpr (PG) return launch_after(fwd_kernel<D, F16, KT, PG, C8>, dim3(a.n_ctas), C::THREADS, smem, st, a, tq, tk, tv);
+    fwd_kernel<D, F16, KT, PG, C8><<<(unsigned)a.n_ctas, C::THREADS, smem, st>>>(a, tq, tk, tv);
     return cudaGetLastError();
 }
 
@@ -912,6 +1014,11 @@ cudaError_t launch_fwd_paged(const FwdArgs& a, const CUtensorMap& tq, const CUte
                              cudaStream_t st) {
     const bool f16 = a.p.dtype == FA_DTYPE_F16;
     if (a.p.d >= 192) return launch_fwd256_paged(a, tq, tk, tv, st);
+    if (a.p.cache8) {
+        if (a.p.d == 64)
+            return f16 ? launch_fwd_k<64, true, 128, true, true>(a, tq, tk, tv, st) : launch_fwd_k<64, false, 128, true, true>(a, tq, tk, tv, st);
+        return f16 ? launch_fwd_k<128, true, 128, true, true>(a, tq, tk, tv, st) : launch_fwd_k<128, false, 128, true, true>(a, tq, tk, tv, st);
+    }
     switch (a.p.d) {
         case 64: return f16 ? launch_fwd_k<64, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<64, false, 128, true>(a, tq, tk, tv, st);
         case 128: return f16 ? launch_fwd_k<128, true, 128, true>(a, tq, tk, tv, st) : launch_fwd_k<128, false, 128, true>(a, tq, tk, tv, st);

@@ -35,6 +35,12 @@ struct Problem {
 // ------------------------------------------------------------------------------------------
 // forward (tensor-core path)
 // ------------------------------------------------------------------------------------------
+// The 8-bit cache: pools of e4m3 bytes, scales [num_pages, blocks, h_kv] of `block` rows each.
+struct Cache8 {
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    int block, blocks;
+};
 struct FwdArgs {
     Problem p;
     int n_blocks;      // CTA work units along grid.x (before splitting)
@@ -73,6 +79,7 @@ struct FwdArgs {
     struct PagedCut* cut;
     int num_pages, box, no_split;
     float2* part_ml;
+    Cache8 cache8;     // a paged cache in 8 bits only
 };
 
 // ------------------------------------------------------------------------------------------
@@ -155,12 +162,6 @@ struct PagedArgs {
     float* part_o[2];   // [2][2 CTAs][rows][d] un-normalised partial outputs
     float2* part_ml[2]; // [2][2 CTAs][rows] reference maximum (log2 units) and sum
     int* status;
-};
-// The 8-bit cache: pools of e4m3 bytes, scales [num_pages, blocks, h_kv] of `block` rows each.
-struct Cache8 {
-    const uint8_t *k, *v;
-    const float *k_scale, *v_scale;
-    int block, blocks;
 };
 // PagedArgs::few_max of a call whose every sequence is the few-row kernel's
 constexpr long kAllFew = 0x7fffffffffffffffL;

@@ -24,6 +24,7 @@
 // Rounding: per row a running reference m of the scores (moved where some score passes it by 2^9) and a
 // power of two u with P' = P vs u <= 2^9, so that neither blocks of tiny nor of huge values leave fp16's range:
 // what a row's product loses is relative to its own largest term.
+#include "cache8.cuh"
 #include "paged.cuh"
 
 namespace fa {
@@ -82,18 +83,6 @@ __device__ __forceinline__ int at_chunk(int row, int col) {
         else if constexpr (D == 192) return row * D + ((col ^ t) << 4);
         else return row * D + ((col ^ ((t & 1) | ((t & 2) << 1))) << 4);
     }
-}
-
-// Two e4m3 bytes (the low or the high half of a word) as an fp16 pair, the lower byte low.
-__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
-    uint32_t r;
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
-    uint32_t r;
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(w));
-    return r;
 }
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -300,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
                     const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint32_t a0 = widen_lo(wa[x]), a1 = widen_lo(wb[x]), a2 = widen_hi(wa[x]), a3 = widen_hi(wb[x]);
+                        const uint32_t a0 = widen_e4m3x2<false>(wa[x]), a1 = widen_e4m3x2<false>(wb[x]), a2 = widen_e4m3x2<true>(wa[x]), a3 = widen_e4m3x2<true>(wb[x]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint4& qq = x < 2 ? q0[n] : q1[n];
@@ -414,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x = __byte_perm(vw[0][z], vw[1][z], h ? 0x7362 : 0x5140);
                         const uint32_t y = __byte_perm(vw[2][z], vw[3][z], h ? 0x7362 : 0x5140);
-                        const uint32_t a0 = widen_lo(x), a1 = widen_hi(x), a2 = widen_lo(y), a3 = widen_hi(y);
+                        const uint32_t a0 = widen_e4m3x2<false>(x), a1 = widen_e4m3x2<true>(x), a2 = widen_e4m3x2<false>(y), a3 = widen_e4m3x2<true>(y);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816(acc[2 * z + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                     }
