@@ -8,32 +8,37 @@
 
 namespace fa {
 
-// The pages of a 128-key tile, a box of rows to a lane, the next tile's table entries fetched ahead (one warp).
+// The pages of a tile of TILE keys, 16 rows to a lane, worked out a tile ahead (one warp).
+template <int TILE>
 struct Pages8 {
+    static constexpr int GROUPS = TILE / 16;
     const Cache8& c;
     const Problem& p;
     const int32_t* table;
-    int num_pages, box, nk;
-    int next = 0, page = 0, row = 0, tile = 0;
-    __device__ __forceinline__ Pages8(const Cache8& c_, const Problem& p_, const int32_t* t, int pages, int box_, int nk_)
-        : c(c_), p(p_), table(t), num_pages(pages), box(box_), nk(nk_) {}
-    __device__ __forceinline__ int entry(int t, int end) const {
-        const int lane = threadIdx.x & 31, j = t * 128 + lane * box;
-        return lane < 128 / box && t < end && j < nk ? table[j / p.page_size] : num_pages;
+    int num_pages, nk;
+    int ahead_page = 0, ahead_row = 0, ahead_block = 0;  // of the next tile
+    int page = 0, row = 0;                               // page of the lane's rows, first row in it
+    long scale = 0;                                      // place of their scale, head 0 (-1: none)
+    __device__ __forceinline__ Pages8(const Cache8& c_, const Problem& p_, const int32_t* t, int pages, int nk_)
+        : c(c_), p(p_), table(t), num_pages(pages), nk(nk_) {}
+    __device__ __forceinline__ void look(int t, int end) {
+        const int lane = threadIdx.x & 31, key = t * TILE + 16 * lane, at = key / p.page_size;
+        ahead_page = lane < GROUPS && t < end && key < nk ? table[at] : num_pages;
+        ahead_row = key - at * p.page_size;
+        ahead_block = ahead_row / c.block;
     }
-    __device__ __forceinline__ void look(int t, int end) { next = entry(t, end); }
-    // tile t is the one to load; lane x then holds box x's page (the pool's end, which reads as zeros, past the used
-    // keys and for an entry outside the pool, which sets the status) and first row
+    // Tile t is the one to load.  A lane's page is the pool's end, which reads as zeros, past the used keys and for
+    // an entry outside the pool, which sets the status.
     __device__ __forceinline__ void take(int t, int end, int* status) {
-        const int lane = threadIdx.x & 31, key = t * 128 + lane * box;
-        page = next;
-        next = entry(t + 1, end);
-        tile = t;
-        row = key % p.page_size;
-        if (lane < 128 / box && (unsigned)page >= (unsigned)num_pages) {
-            if (key < nk) atomicCAS(status, 0, kStatusDeviceCheck);
+        const int lane = threadIdx.x & 31;
+        page = ahead_page;
+        row = ahead_row;
+        if (lane < GROUPS && (unsigned)page >= (unsigned)num_pages) {
+            if (t * TILE + 16 * lane < nk) atomicCAS(status, 0, kStatusDeviceCheck);
             page = num_pages;
         }
+        scale = page < num_pages ? ((long)page * c.blocks + ahead_block) * p.h_kv : -1;
+        look(t + 1, end);
     }
 };
 
@@ -72,24 +77,20 @@ struct Ring8 {
             mbar_init(&empty[i], 4);  // a converting warp each
         }
     }
-    // Starts the loads of half h of the tile that `pages` holds (a whole warp).
-    __device__ __forceinline__ bool load(uint32_t& n, const Pages8& pages, int h, const CUtensorMap& map, const float* scales, int g,
-                                         const Abort& ab) {
+    // Starts the loads of half h of the tile that `pages` holds, boxes of 16 << log_box rows (a whole warp).
+    template <int TILE>
+    __device__ __forceinline__ bool load(uint32_t& n, const Pages8<TILE>& pages, int h, int log_box, const CUtensorMap& map,
+                                         const float* scales, int g, const Abort& ab) {
         const int lane = threadIdx.x & 31, st = n % UNITS;
-        const int box = min(pages.box, ROWS), step = pages.box / box;  // (a page's 128 rows: two copies)
+        const long at = __shfl_sync(0xffffffffu, pages.scale, 4 * h + (lane & 3));  // lane x < 4: of rows 16 x and on
+        const int src = 4 * h + ((lane << log_box) & 3);                            // lane x < 4 >> log_box: of box x
+        const int page = __shfl_sync(0xffffffffu, pages.page, src), row = __shfl_sync(0xffffffffu, pages.row, src);
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / UNITS) & 1) ^ 1, ab))) return false;
         if (lane == 0) mbar_expect_tx(&full[st], ROWS * D);
-        // lane x < 4: the scale of rows 16 x and on
-        const int at = 64 * h + 16 * (lane & 3), from = at / pages.box;
-        const int page = __shfl_sync(0xffffffffu, pages.page, from), row = __shfl_sync(0xffffffffu, pages.row, from) + at % pages.box;
-        if (lane < 4 && page < pages.num_pages)
-            copy4_async(&scale[st][lane], scales + ((long)page * pages.c.blocks + row / pages.c.block) * pages.p.h_kv + g);
         __syncwarp();
+        if (lane < 4 >> log_box) tma_load_4d(&rows[st][((lane << log_box) * 16) * D], &map, &full[st], 0, g, row, page);
+        if (lane < 4 && at >= 0) copy4_async(&scale[st][lane], scales + at + g);
         mbar_arrive_copies(&full[st]);
-        const int per = ROWS / box;  // boxes of the half
-        const int src = step == 2 ? 0 : h * per + (lane < per ? lane : 0);
-        const int pg = __shfl_sync(0xffffffffu, pages.page, src), r0 = __shfl_sync(0xffffffffu, pages.row, src) + (step == 2 ? 64 * h : 0);
-        if (lane < per) tma_load_4d(&rows[st][lane * box * D], &map, &full[st], 0, g, r0, pg);
         ++n;
         return true;
     }
@@ -98,28 +99,39 @@ struct Ring8 {
         for (uint32_t back = 1; back <= UNITS && back <= n; ++back) mbar_wait_quiet(&full[(n - back) % UNITS], ((n - back) / UNITS) & 1);
     }
     // Rows 16 w and on of the next unit, keys j0 + 16 w and on, to rows of a tile (zeros outside the keys [lo, hi] that
-    // any query sees: what lies there may be anything).  The unit's eight 16-byte chunks of a store
-    // phase fall into different banks: every other group of four chunks stores its second half first.
+    // any query sees: what lies there may be anything).  A lane turns 16 bytes into two 16-byte units, four times over
+    // with their loads ahead; every other group of four chunks takes its second half first, so that the
+    // stores of a phase fall into different banks.
     template <bool F16>
     __device__ __forceinline__ bool widen(uint32_t& n, int w, uint8_t* tile, int chunk_bytes, int j0, int lo, int hi, const Abort& ab) {
+        constexpr int ALL = CPR / 2, BATCH = ALL % 4 == 0 ? 4 : ALL < 4 ? ALL : 3;  // chunks of a lane
         const int lane = threadIdx.x & 31, st = n % UNITS;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / UNITS) & 1, ab))) return false;
         const float f = scale[st][w];
-#pragma unroll 2
-        for (int y = 0; y < CPR / 2; ++y) {
-            const int x = lane + 32 * y, r = 16 * w + x / CPR, c = x % CPR, j = j0 + r;
-            const uint4 b = *reinterpret_cast<const uint4*>(&rows[st][r * D + 16 * c]);
-            uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
-            if (j >= lo && j <= hi) {
-                o0 = make_uint4(scaled_e4m3x2<F16, false>(b.x, f), scaled_e4m3x2<F16, true>(b.x, f), scaled_e4m3x2<F16, false>(b.y, f),
-                                scaled_e4m3x2<F16, true>(b.y, f));
-                o1 = make_uint4(scaled_e4m3x2<F16, false>(b.z, f), scaled_e4m3x2<F16, true>(b.z, f), scaled_e4m3x2<F16, false>(b.w, f),
-                                scaled_e4m3x2<F16, true>(b.w, f));
+        const uint8_t* from = &rows[st][16 * w * D];
+        const bool inside = j0 + 16 * w >= lo && j0 + 16 * w + 15 <= hi;
+#pragma unroll 1
+        for (int y0 = 0; y0 < ALL; y0 += BATCH) {
+            uint2 b[BATCH][2];
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y) {
+                const int x = lane + 32 * (y0 + y), swap = ((x % CPR) >> 2) & 1;
+                b[y][0] = *reinterpret_cast<const uint2*>(from + 16 * x + 8 * swap);
+                b[y][1] = *reinterpret_cast<const uint2*>(from + 16 * x + 8 - 8 * swap);
             }
-            uint8_t* to = tile + (c >> 2) * chunk_bytes + r * 128;
-            const int u = 2 * (c & 3), swap = (c >> 2) & 1;
-            *reinterpret_cast<uint4*>(to + (((u + swap) ^ (r & 7)) << 4)) = swap ? o1 : o0;
-            *reinterpret_cast<uint4*>(to + (((u + 1 - swap) ^ (r & 7)) << 4)) = swap ? o0 : o1;
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y) {
+                const int x = lane + 32 * (y0 + y), r = 16 * w + x / CPR, c = x % CPR, u = 2 * (c & 3), swap = (c >> 2) & 1;
+                uint8_t* to = tile + (c >> 2) * chunk_bytes + r * 128;
+                const bool seen = inside || (j0 + r >= lo && j0 + r <= hi);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4 o = make_uint4(scaled_e4m3x2<F16, false>(b[y][h].x, f), scaled_e4m3x2<F16, true>(b[y][h].x, f),
+                                         scaled_e4m3x2<F16, false>(b[y][h].y, f), scaled_e4m3x2<F16, true>(b[y][h].y, f));
+                    if (!seen) o = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(to + (((u + (swap ^ h)) ^ (r & 7)) << 4)) = o;
+                }
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);

@@ -89,12 +89,14 @@ struct FwdCfg {
     // registers per thread after setmaxnreg: producer / MMA / TMEM owner / scheduler group,
     // and the two softmax groups; 128 REG_LOW + 256 REG_HIGH stays within what the CTA is
     // launched with (checked before every launch)
-    // (C8: 128 x 48 for the converting warps as well, 65536 in all)
+    // (C8: 128 x 80 for the converting warps as well, 65536 in all.  8 chunks of 1024 tokens with 208 / 48, 200 / 64,
+    // 192 / 80 and 184 / 88 registers for softmax and conversion: 982 / 893 / 829 / 838 us; eight converting warps
+    // at 168 / 48: 887.  O follows a moved reference behind P, when the scores are out of the registers.)
     static constexpr int REG_LOW = KT == 128 && !C8 ? 56 : 48;
-    static constexpr int REG_HIGH = C8 ? 208 : KT == 128 ? 224 : 96;
-    static constexpr int REG_CONV = 48;
-    // C8: half tiles of bytes under way
-    static constexpr int UNITS8 = D == 64 ? 6 : 3;
+    static constexpr int REG_HIGH = C8 ? 192 : KT == 128 ? 224 : 96;
+    static constexpr int REG_CONV = 80;
+    // C8: half tiles of bytes under way (d = 128: three 864 us, four 829)
+    static constexpr int UNITS8 = D == 64 ? 6 : 4;
 };
 
 // One decoded work item, as the scheduler warp hands it to the other roles.
@@ -108,6 +110,7 @@ struct ItemInfo {
     // PG only: used keys, keys that any row of the item may see, partial slot (-1: whole item),
     // key tiles of the CTA's items before this one
     int nk, lo, hi, part, before;
+    int nq;  // C8 only: queries of the sequence
 };
 constexpr int kItemSlots = 3;
 // arrivals that free an item slot: producer, MMA issuer and the eight softmax warps (C8: and four converting ones)
@@ -127,7 +130,7 @@ struct __align__(1024) FwdSmem {
     uint64_t drain;
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     ItemInfo item[kItemSlots];
-    int2 band[kItemSlots][2][128];  // (jlo, jhi) of every row of both query tiles
+    int2 band[C8 ? 1 : kItemSlots][C8 ? 1 : 2][128];  // (jlo, jhi) of every row of both query tiles (C8: a row's thread works them out)
     uint32_t tmem_base;
     int abort_flag;
     std::conditional_t<C8, Ring8<D, C::UNITS8>, char> bytes;  // C8: half tiles as the cache holds them
@@ -220,6 +223,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
         const uint32_t qbox = (uint32_t)(p.P * p.G) * 128u;
+        const int log_box = min(__ffs(a.box), 7) - 5;  // (16 to 64 rows)
         int n_q = 0;
         uint32_t units = 0;
         bool ok = true;
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
             if (end) break;
             if (u1 <= u0) continue;
-            Pages8 pages(a.cache8, p, table, a.num_pages, a.box, nk);
+            Pages8<KT> pages(a.cache8, p, table, a.num_pages, nk);
             pages.look(u0, u1);
             if (n_q > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty, (n_q - 1) & 1, ab)))) break;
             if (lane == 0) {
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 pages.take(j, u1, a.status);
 #pragma unroll 1
                 for (int x = 0; ok && x < 4; ++x)  // the halves of K, of V
-                    ok = s.bytes.load(units, pages, x & 1, x < 2 ? tmk : tmv, x < 2 ? a.cache8.k_scale : a.cache8.v_scale, g, ab);
+                    ok = s.bytes.load(units, pages, x & 1, log_box, x < 2 ? tmk : tmv, x < 2 ? a.cache8.k_scale : a.cache8.v_scale, g, ab);
             }
         }
         s.bytes.drain(units);
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 }
             }
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < (C8 ? 0 : 2); ++k) {
                 int lo_min = kNoRow, hi_max = -1;
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
@@ -637,6 +641,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 }
                 if constexpr (PG) {
                     it.nk = w.sv.nk;
+                    it.nq = w.sv.nq;
                     it.lo = w.band.lo(w.ti[0].s0);
                     it.hi = w.band.hi(min(w.ti[0].s0 + 2 * p.P, w.sv.nq) - 1);
                     it.part = part;
@@ -727,8 +732,20 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
         if (s.item[slot].end) break;
         tr.item(s.item[slot].idx);
         const int my_t0 = s.item[slot].t0[k], my_t1 = s.item[slot].t1[k];
-        const int2 rb = s.band[slot][k][r];
-        const int jlo = rb.x, jhi = rb.y;
+        int jlo, jhi;
+        if constexpr (C8) {
+            const ItemInfo& w = s.item[slot];
+            const int i = w.s0[k] + (int)((unsigned)r / (unsigned)p.G);
+            const Band bd{w.nk - w.nq, p.left, p.right, w.nk};
+            jlo = bd.lo(i);
+            jhi = bd.hi(i);
+            if (jhi < jlo) jlo = kNoKeys, jhi = -1;
+            if (r >= p.P * p.G || i >= w.nq) jlo = kNoRow, jhi = -1;
+        } else {
+            const int2 rb = s.band[slot][k][r];
+            jlo = rb.x;
+            jhi = rb.y;
+        }
         // the sink's logit, fetched now so that its latency hides behind the key loop
         float sink2 = 0.f;
         if (p.sinks && a.n_splits == 1 && jlo != kNoRow) sink2 = p.sinks[s.item[slot].g * p.G + r % p.G] * kLog2e;
@@ -791,7 +808,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                     tmem_st_32x32b_x32(tO + cb, orr);
                 }
             };
-            if (KT == 128 && __any_sync(0xffffffffu, rescale)) rescale_o();
+            if (KT == 128 && !C8 && __any_sync(0xffffffffu, rescale)) rescale_o();
             // P = exp2(S*c - m) as 16-bit pairs (the inputs' type), packed in place (slot cc/2 is already consumed).
             // On tiles without masked entries a fraction of the exponentials runs on the FMA
             // pipe (exp2_poly2) to share the load with the MUFU unit.
@@ -825,7 +842,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             if constexpr (KT == 128) tmem_st_32x32b_x64(tS, sr);
             else tmem_st_32x32b_x32(tS, sr);
             l += sum;
-            if (KT == 64 && __any_sync(0xffffffffu, rescale)) rescale_o();
+            if ((KT == 64 || C8) && __any_sync(0xffffffffu, rescale)) rescale_o();
             if (PG && !C8 && !poly_ok) {
                 // value rows outside every row's band (in a tile with masked entries, then): cleared by
                 // tile 0's group where it takes part (the P V of tile 1 is issued behind that of tile 0),
