@@ -409,7 +409,7 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     // where a token has more than 64.
     // (A cache in 8 bits: the few-row kernel's tiles are 8 to 32 rows.)
     const int most = !p.cache8 ? 64 : p.d <= 128 ? 32 : 16;
-    pl.many = rows > most && !(p.cache8 && p.d > 128);
+    pl.many = rows > most;
     const long tile = pl.many ? p.G : rows;
     pl.few_rows = p.cache8 && tile <= 8 ? 8 : tile <= 16 ? 16 : tile <= 32 ? 32 : 64;
     if (pl.few_rows > most) pl.few_rows = most;

@@ -20,14 +20,17 @@
 // the line of units of paged.cuh, one item after the other, its barriers set up anew for each (about
 // 2 us an item, a small part of the long ones it is there for); the producer warp loads
 // each key tile page by page, value rows that no query of the item sees are cleared before the
-// product, and a cut item's rows go to the partials un-normalised.
+// product, and a cut item's rows go to the partials un-normalised.  Over a cache in 8 bits (C8, 384
+// threads) it loads the bytes into a ring of their own, and warps 8..11 turn them into the 16-bit tiles
+// (cache8.cuh); the 16-bit ring is shorter by what that takes.
+#include "cache8.cuh"
 #include "common.cuh"
 #include "paged.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kThreads256 = 256;
+constexpr int kThreads256 = 256, kThreads256c8 = 384;
 constexpr int BN = 64;               // keys per KV tile
 constexpr int Q_CHUNK = 128 * 128;   // [128 rows][64 cols] 16-bit
 constexpr int KV_CHUNK = BN * 128;   // [64 rows][64 cols] 16-bit
@@ -35,12 +38,13 @@ constexpr uint32_t C_O = 0;
 constexpr uint32_t C_S = 256;        // S buffer b at columns 256 + 64 b
 constexpr uint32_t C_Q = 384;        // Q: column c holds elements 2c, 2c+1 of the row
 
-template <int D>
+template <int D, bool C8 = false>
 struct Cfg256 {
     static constexpr int KCH = D / 64;              // 64-column chunks
     static constexpr int KV_BYTES = KCH * KV_CHUNK; // one K or V tile (32 KB at d = 256)
     static constexpr int SLOT_BYTES = 2 * KV_BYTES; // ring slot: K then V; slot 0 first holds Q
-    static constexpr int STAGES = D == 256 ? 3 : 4;
+    static constexpr int STAGES = (D == 256 ? 3 : 4) - (C8 ? 1 : 0);
+    static constexpr int UNITS8 = C8 ? (D == 256 ? 5 : 6) : 1;  // tiles of bytes under way
     static_assert(KCH * Q_CHUNK == SLOT_BYTES, "the Q tile fills one ring slot");
     static_assert(C_Q + D / 2 <= 512 && C_O + D <= C_S, "tensor-memory columns overlap");
     // ring slot and use count of KV tile `it`: tiles 0 .. STAGES-2 take slots 1 .. STAGES-1,
@@ -49,15 +53,16 @@ struct Cfg256 {
     static __device__ __forceinline__ uint32_t use_parity(int it) { return (uint32_t)(it / STAGES) & 1u; }
 };
 
-template <int D>
+template <int D, bool C8 = false>
 struct __align__(1024) Smem256 {
-    uint8_t ring[Cfg256<D>::STAGES][Cfg256<D>::SLOT_BYTES];  // K at 0, V at KV_BYTES
+    using C = Cfg256<D, C8>;
+    uint8_t ring[C::STAGES][C::SLOT_BYTES];  // K at 0, V at KV_BYTES
     uint64_t q_full, q_tmem;
-    uint64_t k_full[Cfg256<D>::STAGES], k_empty[Cfg256<D>::STAGES], v_full[Cfg256<D>::STAGES],
-        v_empty[Cfg256<D>::STAGES];
+    uint64_t k_full[C::STAGES], k_empty[C::STAGES], v_full[C::STAGES], v_empty[C::STAGES];
     uint64_t s_full[2], p_full[2], pv_done, o_full, drain;
     uint32_t tmem_base;
     int abort_flag;
+    std::conditional_t<C8, Ring8<D, C::UNITS8>, char> bytes;
 };
 
 // One query tile against a range of key tiles.
@@ -72,14 +77,15 @@ struct WideItem {
 };
 
 // Barriers of one item (one thread; the caller synchronises).
-template <int D>
-__device__ __forceinline__ void wide_barriers(Smem256<D>& s) {
+template <int D, bool C8>
+__device__ __forceinline__ void wide_barriers(Smem256<D, C8>& s) {
+    using C = Cfg256<D, C8>;
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_tmem, 4);  // one arrive per softmax warp once its Q rows are in TMEM
-    for (int i = 0; i < Cfg256<D>::STAGES; ++i) {
-        mbar_init(&s.k_full[i], 1);
+    for (int i = 0; i < C::STAGES; ++i) {
+        mbar_init(&s.k_full[i], C8 ? 4 : 1);  // (C8: an arrival of each converting warp)
         mbar_init(&s.k_empty[i], 1);
-        mbar_init(&s.v_full[i], 1);
+        mbar_init(&s.v_full[i], C8 ? 4 : 1);
         mbar_init(&s.v_empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -92,12 +98,12 @@ __device__ __forceinline__ void wide_barriers(Smem256<D>& s) {
     fence_mbar_init();
 }
 
-template <int D>
-__device__ __forceinline__ void wide_invalidate(Smem256<D>& s) {
+template <int D, bool C8>
+__device__ __forceinline__ void wide_invalidate(Smem256<D, C8>& s) {
     auto inval = [](uint64_t* b) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory"); };
     inval(&s.q_full);
     inval(&s.q_tmem);
-    for (int i = 0; i < Cfg256<D>::STAGES; ++i) {
+    for (int i = 0; i < Cfg256<D, C8>::STAGES; ++i) {
         inval(&s.k_full[i]);
         inval(&s.k_empty[i]);
         inval(&s.v_full[i]);
@@ -112,10 +118,11 @@ __device__ __forceinline__ void wide_invalidate(Smem256<D>& s) {
     inval(&s.drain);
 }
 
-template <int D, bool F16, bool PG>
+// (units8: tiles of bytes loaded, or converted, so far; their ring's phases go on from item to item)
+template <int D, bool F16, bool PG, bool C8>
 __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                                          Smem256<D>& s, const WideItem& w, uint32_t tmem, const Abort& ab) {
-    using C = Cfg256<D>;
+                                          Smem256<D, C8>& s, const WideItem& w, uint32_t tmem, const Abort& ab, uint32_t& units8) {
+    using C = Cfg256<D, C8>;
     constexpr int KCH = C::KCH, KV_BYTES = C::KV_BYTES, SLOT_BYTES = C::SLOT_BYTES, STAGES = C::STAGES;
     const Problem& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,7 +130,49 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
     const Band& band = w.band;
     const int g = w.g, s0 = w.s0, t0 = w.t0, ntiles = w.ntiles, split = w.split;
     const bool tail = w.tail;
-    if (PG && warp == 0) {
+    if (C8 && warp == 0) {
+        // ================= TMA producer, paged cache in 8 bits (the whole warp) =================
+        if constexpr (C8) {
+            if (ntiles > 0) {
+                if (lane == 0) {
+                    mbar_expect_tx(&s.q_full, (uint32_t)(p.P * p.G) * 128u * KCH);
+                    for (int c = 0; c < KCH; ++c)
+                        tma_load_4d(&s.ring[0][c * Q_CHUNK], &tmq, &s.q_full, c * 64, g * p.G, sv.q0 + s0, 0);
+                }
+                const int log_box = __ffs(a.box) - 5;  // (16 to 64 rows)
+                Pages8<BN> pages(a.cache8, p, p.block_table + (long)sv.b * p.max_blocks, a.num_pages, sv.nk);
+                pages.look(t0, t0 + ntiles);
+                for (int t = t0, ok = 1; ok && t < t0 + ntiles; ++t) {
+                    pages.take(t, t0 + ntiles, a.status);
+                    ok = s.bytes.load(units8, pages, 0, log_box, tmk, a.cache8.k_scale, g, ab) &&
+                         s.bytes.load(units8, pages, 0, log_box, tmv, a.cache8.v_scale, g, ab);
+                }
+                s.bytes.drain(units8);  // (nothing to wait for, unless the call is being given up)
+                mbar_wait_quiet(&s.q_full, 0);
+            }
+        }
+    } else if (C8 && warp >= 8) {
+        // ================= C8: bytes to 16-bit tiles, a warp to 16 rows =================
+        if constexpr (C8) {
+            const int lo = band.lo(s0), hi = band.hi(min(s0 + p.P, sv.nq) - 1);
+            auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, ab)) != 0; };
+            for (int it = 0; it < ntiles; ++it) {
+                const int st = C::slot_of(it);
+                const uint32_t ph = C::use_parity(it) ^ 1;
+                if (it == STAGES - 1 && !wait(&s.q_tmem, 0)) break;
+                bool ok = true;
+#pragma unroll 1
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (!(ok = wait(x ? &s.v_empty[st] : &s.k_empty[st], ph))) break;
+                    if (!(ok = s.bytes.template widen<F16>(units8, warp - 8, s.ring[st] + x * KV_BYTES, KV_CHUNK, (t0 + it) * BN, lo, hi, ab))) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x ? &s.v_full[st] : &s.k_full[st]);
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (PG && warp == 0) {
         // ================= TMA producer, paged cache (the whole warp) =================
         if (ntiles > 0) {
             if (lane == 0) {
@@ -341,17 +390,22 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                 }
             }
             const float base = (m_used == -INFINITY) ? 0.f : m_used;
-            float sum = 0.f;
+            float sum = 0.f, cx = c;
+            if (C8 && __any_sync(0xffffffffu, fabsf(base) > 0x1p24f)) {  // (scores beyond 2^31: see the d <= 128 kernel)
+#pragma unroll
+                for (int cc = 0; cc < BN; ++cc) sr[cc] = __float_as_uint(__uint_as_float(sr[cc]) * c);
+                cx = 1.f;
+            }
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 2) {
-                const float p0 = ex2(fmaf(__uint_as_float(sr[cc]), c, -base));
-                const float p1 = ex2(fmaf(__uint_as_float(sr[cc + 1]), c, -base));
+                const float p0 = ex2(fmaf(__uint_as_float(sr[cc]), cx, -base));
+                const float p1 = ex2(fmaf(__uint_as_float(sr[cc + 1]), cx, -base));
                 sum += p0 + p1;
                 sr[cc / 2] = pack16<F16>(p0, p1);
             }
             l += sum;
             tmem_st_32x32b_x32(tS, sr);
-            if constexpr (PG) {
+            if constexpr (PG && !C8) {
                 // value rows outside every row's band: thread r clears key r % 64, half of its columns
                 const int lo = band.lo(s0), hi = band.hi(min(s0 + p.P, sv.nq) - 1), key = r & 63;
                 if (j0 < lo || j0 + BN - 1 > hi) {
@@ -518,7 +572,7 @@ __global__ void __launch_bounds__(kThreads256, 1)
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
     if (tid == 0) {
         s.abort_flag = 0;
-        wide_barriers<D>(s);
+        wide_barriers<D, false>(s);
     }
     if (p.P * p.G < 128) {
         for (int c = 0; c < KCH; ++c)
@@ -535,7 +589,8 @@ __global__ void __launch_bounds__(kThreads256, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
 
-    wide_item<D, F16, false>(a, tmq, tmk, tmv, s, WideItem{sv, band, g, s0, t0, ntiles, split, tail, -1}, tmem, ab);
+    uint32_t none = 0;
+    wide_item<D, F16, false, false>(a, tmq, tmk, tmv, s, WideItem{sv, band, g, s0, t0, ntiles, split, tail, -1}, tmem, ab, none);
 
     tc_fence_before();
     __syncthreads();
@@ -545,25 +600,33 @@ __global__ void __launch_bounds__(kThreads256, 1)
     }
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads256, 1)
+template <int D, bool F16, bool C8>
+__global__ void __launch_bounds__(C8 ? kThreads256c8 : kThreads256, 1)
     fwd256_paged_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
-    using C = Cfg256<D>;
+    using C = Cfg256<D, C8>;
     extern __shared__ uint8_t smem_raw[];
-    Smem256<D>& s = *reinterpret_cast<Smem256<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem256<D, C8>& s = *reinterpret_cast<Smem256<D, C8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ WideItem items[2];  // the current item and the next one
     __shared__ int more[2];
     const Problem& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     allow_next_kernel();
     wait_previous_kernel();
-    PagedWalk walk;
+    // (C8: the walk's state lies in shared memory, for the threads have no registers to spare for it)
+    __shared__ alignas(16) uint8_t walk_mem[C8 ? 32 * sizeof(PagedWalk) : 16];
+    PagedWalk walk_regs;
+    PagedWalk& walk = C8 ? reinterpret_cast<PagedWalk*>(walk_mem)[lane] : walk_regs;
+    if (C8 && warp == 3) walk = PagedWalk();
     if (warp == 3) walk.start(p, a.pre, a.line, cta);
     // without work, or in a call that already failed (one thread looks, so that all leave or none)
     if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
     Abort ab{&s.abort_flag, a.status, p.wait_ns};
-    if (tid == 0) s.abort_flag = 0;
+    if (tid == 0) {
+        s.abort_flag = 0;
+        if constexpr (C8) s.bytes.init();
+    }
+    uint32_t units8 = 0;
     if (warp == 2) {
         tmem_alloc(&s.tmem_base, 512);
         tmem_relinquish();
@@ -593,11 +656,11 @@ __global__ void __launch_bounds__(kThreads256, 1)
     };
     if (warp == 3) find(0);
     for (int x = 0;; x ^= 1) {
-        if (tid == 0) wide_barriers<D>(s);
+        if (tid == 0) wide_barriers<D, C8>(s);
         if (p.P * p.G < 128) {
             // rows past P*G of a Q tile are never written by TMA (the ring's other tiles were)
             for (int c = 0; c < C::KCH; ++c)
-                for (int y = p.P * p.G * 128 + tid * 16; y < 128 * 128; y += kThreads256 * 16)
+                for (int y = p.P * p.G * 128 + tid * 16; y < 128 * 128; y += (C8 ? kThreads256c8 : kThreads256) * 16)
                     *reinterpret_cast<uint4*>(&s.ring[0][c * Q_CHUNK + y]) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
         }
@@ -606,11 +669,11 @@ __global__ void __launch_bounds__(kThreads256, 1)
         tc_fence_after();
         if (!more[x]) break;
         if (warp == 3) find(x ^ 1);
-        wide_item<D, F16, true>(a, tmq, tmk, tmv, s, items[x], s.tmem_base, ab);
+        wide_item<D, F16, true, C8>(a, tmq, tmk, tmv, s, items[x], s.tmem_base, ab, units8);
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (tid == 0) wide_invalidate<D>(s);
+        if (tid == 0) wide_invalidate<D, C8>(s);
         if (s.abort_flag) break;  // (set before the barrier or not at all: every wait of the item has ended)
     }
     if (warp == 3 && lane == 0) a.cut[cta] = walk.cut;
@@ -624,21 +687,22 @@ __global__ void __launch_bounds__(kThreads256, 1)
 
 }  // namespace
 
-template <int D>
+template <int D, bool C8>
 static cudaError_t launch_fwd_wide_paged(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                          cudaStream_t st) {
-    const size_t smem = sizeof(Smem256<D>) + 1024;
-    auto kernel = a.p.dtype == FA_DTYPE_F16 ? fwd256_paged_kernel<D, true> : fwd256_paged_kernel<D, false>;
+    constexpr size_t smem = sizeof(Smem256<D, C8>) + 1024;
+    static_assert(smem + 1024 + (C8 ? 32 * sizeof(PagedWalk) : 0) <= 227 * 1024, "the wide forward's shared memory");
+    auto kernel = a.p.dtype == FA_DTYPE_F16 ? fwd256_paged_kernel<D, true, C8> : fwd256_paged_kernel<D, false, C8>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(a.n_ctas), kThreads256, smem, st, a, tq, tk, tv);
+    return launch_after(kernel, dim3(a.n_ctas), C8 ? kThreads256c8 : kThreads256, smem, st, a, tq, tk, tv);
 }
 
 cudaError_t launch_fwd256_paged(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t st) {
     switch (a.p.d) {
-        case 192: return launch_fwd_wide_paged<192>(a, tq, tk, tv, st);
-        case 256: return launch_fwd_wide_paged<256>(a, tq, tk, tv, st);
+        case 192: return a.p.cache8 ? launch_fwd_wide_paged<192, true>(a, tq, tk, tv, st) : launch_fwd_wide_paged<192, false>(a, tq, tk, tv, st);
+        case 256: return a.p.cache8 ? launch_fwd_wide_paged<256, true>(a, tq, tk, tv, st) : launch_fwd_wide_paged<256, false>(a, tq, tk, tv, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -260,3 +260,23 @@ def test_offsets_beyond_32_bits():
                           block_table=i32(table), s_kv=400, cache_scale=(big[1], big[3]))
     assert fa.device_status(ws) == 0
     assert torch.equal(o, want[0]) and torch.equal(z, want[1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+def test_a_wait_limit_ends_chunks_with_a_timeout(d):
+    """The chunks' kernels give up after 1 ns; the same call without the limit is right next (nothing was left behind).
+    The few-row kernel waits for its own copies only and has no limit to pass."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    c = case([300, 200], [3000, 700], h_q=8, h_kv=2, d=d, page=16)
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    kw = dict(causal=True, cu_q=i32(c["cu"]), seqused_k=i32(c["used"]), block_table=i32(c["table"]), s_kv=3000,
+              cache_scale=(i32(c["k"][1]), i32(c["v"][1])))
+    q, k, v = up(c["qb"], "bf16"), i32(c["k"][0]), i32(c["v"][0])
+    want, lse, ws = fa.forward(q, k, v, **kw)
+    assert fa.device_status(ws) == 0
+    for _ in range(2):
+        _, _, ws = fa.forward(q, k, v, **kw, wait_limit_ns=1)
+        assert fa.device_status(ws) == fa.FA_ERR_TIMEOUT
+        o, z, ws = fa.forward(q, k, v, **kw)
+        assert fa.device_status(ws) == 0 and torch.equal(o, want) and torch.equal(z, lse)
