@@ -469,7 +469,7 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     Cache8 kv{};
     if (p.cache8)
         kv = Cache8{reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(v), in.k_scale, in.v_scale, in.scale_block,
-                    p.page_size / in.scale_block};
+                    p.page_size / in.scale_block, divisor((uint32_t)p.page_size), divisor((uint32_t)in.scale_block)};
     CUtensorMap tk, tv;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     // a key's row is d * 2 bytes of h_kv times as many: fetched 256 bytes at a time, half of it would be

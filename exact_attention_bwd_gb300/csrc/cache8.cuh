@@ -22,10 +22,10 @@ struct Pages8 {
     __device__ __forceinline__ Pages8(const Cache8& c_, const Problem& p_, const int32_t* t, int pages, int nk_)
         : c(c_), p(p_), table(t), num_pages(pages), nk(nk_) {}
     __device__ __forceinline__ void look(int t, int end) {
-        const int lane = threadIdx.x & 31, key = t * TILE + 16 * lane, at = key / p.page_size;
+        const int lane = threadIdx.x & 31, key = t * TILE + 16 * lane, at = quotient(key, c.by_page);
         ahead_page = lane < GROUPS && t < end && key < nk ? table[at] : num_pages;
         ahead_row = key - at * p.page_size;
-        ahead_block = ahead_row / c.block;
+        ahead_block = quotient(ahead_row, c.by_block);
     }
     // Tile t is the one to load.  A lane's page is the pool's end, which reads as zeros, past the used keys and for
     // an entry outside the pool, which sets the status.

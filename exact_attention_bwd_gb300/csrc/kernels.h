@@ -35,11 +35,27 @@ struct Problem {
 // ------------------------------------------------------------------------------------------
 // forward (tensor-core path)
 // ------------------------------------------------------------------------------------------
+// Division of n in [0, 2^31) by a whole number d >= 2: with s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1
+// (32 bits, for d > 2^(s-1)), n m 2^-(31+s) exceeds n / d by less than 2^-s <= 1 / d.
+struct Divisor {
+    uint32_t m;
+    int s;
+};
+inline Divisor divisor(uint32_t d) {
+    int s = 1;
+    while ((1u << s) < d) ++s;
+    return Divisor{(uint32_t)((1ull << (31 + s)) / d + 1), s - 1};
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ int quotient(int n, const Divisor& d) { return (int)(__umulhi((uint32_t)n, d.m) >> d.s); }
+#endif
+
 // The 8-bit cache: pools of e4m3 bytes, scales [num_pages, blocks, h_kv] of `block` rows each.
 struct Cache8 {
     const uint8_t *k, *v;
     const float *k_scale, *v_scale;
     int block, blocks;
+    Divisor by_page, by_block;
 };
 struct FwdArgs {
     Problem p;

@@ -30,10 +30,8 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps8 = 8;
-constexpr int kThreads = 32 * kWarps8;
+constexpr int kGroups8 = 8;                   // 16-key groups of a tile: a warp each
 constexpr int kGroup = 16;                    // keys of a warp in a tile: they share a page and a scale
-constexpr int kMergeCols = 64;                // columns that the warps join at a time
 constexpr float kNoRef = -1e30f;              // reference of a row without a key so far
 constexpr float kNoUnit = 8.507059173e37f;    // u of a row without a value so far: 2^126
 constexpr float kTop = 512.f;                 // P and P vs u stay below
@@ -41,33 +39,40 @@ constexpr float kTop = 512.f;                 // P and P vs u stay below
 template <int D, int NT>
 struct Few8Cfg {
     static constexpr int NR = 8 * NT;
+    static constexpr int TILES = NT == 1 && D <= 128 ? 2 : 1;  // tiles side by side
+    static constexpr int WARPS = kGroups8 * TILES, THREADS = 32 * WARPS;
     static constexpr int CPR = D / 16;              // 16-byte chunks of a row
     static constexpr int GROUP_BYTES = kGroup * D;  // K (or V) rows of a warp's group
-    static constexpr int STAGES = D == 64 ? 10 : D == 128 ? 6 : D == 192 ? 4 : 3;
+    static constexpr int STAGES = (D == 64 ? 10 : D == 128 ? 6 : D == 192 ? 4 : 3) / TILES;
+    static constexpr int LINE = D % 128 ? 64 : 128;  // (d = 128: 262 us without the hint, 243 with it, 314 with 256 bytes)
     static constexpr int MT = D / 16;               // 16-row tiles of O^T
+    static constexpr int MERGE = 64 / TILES;        // columns that the warps join at a time
     static constexpr int Q_STRIDE = 2 * D + 16;     // bytes of a query row
     static constexpr bool Q_REGS = NT * D <= 256;   // query fragments held in registers
-    static constexpr int FIFO = STAGES + 2;         // pieces whose tiles are under way
 };
+
+constexpr int kPieces = 16, kLook = 8;  // places for pieces (a power of two), pieces looked ahead for
 
 struct Piece8 {
     int q0, off, nk, r0;     // first query row, nk - nq, keys, first row
     int rows, g, part, t0;   // rows, head, partial slot or -1, first tile
     int t1, in_lo, in_hi, lo;  // end; keys that every row sees; keys that any row sees
-    int hi, pad[3];
+    int hi, b, pad[2];       // sequence
 };
 
 template <int D, int NT>
 struct __align__(128) Few8Smem {
     using C = Few8Cfg<D, NT>;
-    uint8_t ring[kWarps8][C::STAGES][2][C::GROUP_BYTES];
+    uint8_t ring[C::WARPS][C::STAGES][2][C::GROUP_BYTES];
     uint8_t q[C::NR * C::Q_STRIDE];
-    float merge[kWarps8][8][kMergeCols];
-    float scale[kWarps8][C::STAGES][2];
+    float merge[C::WARPS][8][C::MERGE];
+    float scale[C::WARPS][C::STAGES][2];
     float qf[C::NR];                 // the power of two that a query row was divided by
-    float m[kWarps8][C::NR], l[kWarps8][C::NR], u[kWarps8][C::NR];  // the warps' states; u becomes the weight of its output
+    float m[C::WARPS][C::NR], l[C::WARPS][C::NR], u[C::WARPS][C::NR];  // the warps' states; u becomes the weight of its output
     float f[C::NR];                  // factor of a whole item's output
-    Piece8 fifo[kWarps8][C::FIFO];
+    Piece8 piece[kPieces];
+    int pieces[2];                   // found so far, as of each second meeting
+    PagedWalk walk[32];              // warp 0's walk over the CTA's stretch: a lane's state each
 };
 
 // Where chunk `col` of row `row` of a group lies: so that the lanes' reads of a fragment fall into different banks
@@ -106,110 +111,163 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 __device__ __forceinline__ float power_below(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs a, const Cache8 kv) {
+__global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(const PagedArgs a, const Cache8 kv) {
     using C = Few8Cfg<D, NT>;
-    constexpr int NR = C::NR, S = C::STAGES;
+    constexpr int NR = C::NR, S = C::STAGES, WARPS = C::WARPS, TILES = C::TILES;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Few8Smem<D, NT>& s = *reinterpret_cast<Few8Smem<D, NT>*>(smem_raw);
     const Problem& p = a.p;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    const int lg = lane >> 2, lt = lane & 3;  // a fragment's row (or column) and its pair
     const unsigned G = (unsigned)p.G;
     allow_next_kernel();
     wait_previous_kernel();
     // (one thread looks, so that all leave or none)
     if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
 
-    // ---- the warp's stream: pieces of the CTA's stretch, tile by tile, S tiles ahead of the arithmetic ----
-    PagedWalk walk;
-    const PagedLine line = *a.line;
-    walk.start(p, a.pre, a.line, cta);
-    int at_t = 0, end_t = 0;          // tiles of the piece that is being fetched
-    int b_lo = 0, b_hi = 0, b_g = 0;  // its keys that any row sees, its head
-    const int32_t* table = nullptr;
-    int issued = 0, pushed = 0;       // tiles, pieces
+    // ---- the pieces of the CTA's stretch, found by warp 0 (the walk's state lies in shared memory: it needs as many
+    // registers as an accumulator tile of 16 rows) ----
+    int found = 0;
     bool more = true;
-    auto fetch = [&]() {
-        if (more && at_t >= end_t) {
-            while ((more = walk.next(p, a.pre, line, cta, NR, a.no_split))) {
-                const PagedSeq& sq = walk.seq;
-                const int r0 = walk.x.rt * NR, rows = min(NR, sq.nq * p.G - r0), off = sq.nk - sq.nq;
-                const int part = walk.from_start && walk.to_end ? -1 : 2 * cta + (walk.from_start ? 1 : 0);
-                const Band bd{off, p.left, p.right, sq.nk};
-                at_t = walk.t0;
-                end_t = walk.t1;
-                b_g = walk.x.g;
-                b_lo = bd.lo((int)((unsigned)r0 / G));
-                b_hi = bd.hi((int)((unsigned)(r0 + rows - 1) / G));
-                table = p.block_table + (long)walk.b * p.max_blocks;
-                if (end_t > at_t) {
-                    if (lane == 0) {
-                        Piece8 x;
-                        x.q0 = sq.q0;
-                        x.off = off;
-                        x.nk = sq.nk;
-                        x.r0 = r0;
-                        x.rows = rows;
-                        x.g = b_g;
-                        x.part = part;
-                        x.t0 = at_t;
-                        x.t1 = end_t;
-                        x.lo = b_lo;
-                        x.hi = b_hi;
-                        x.in_lo = p.left >= 0 ? (int)((unsigned)(r0 + rows - 1) / G) + off - p.left : 0;
-                        x.in_hi = p.right >= 0 ? min(sq.nk - 1, (int)((unsigned)r0 / G) + off + p.right) : sq.nk - 1;
-                        s.fifo[warp][pushed % C::FIFO] = x;
-                    }
-                    ++pushed;
-                    break;
+    auto find = [&](int most) {
+        PagedWalk walk = s.walk[lane];
+        const PagedLine line = *a.line;
+        while (more && found < most) {
+            if (!(more = walk.next(p, a.pre, line, cta, NR, a.no_split))) break;
+            const PagedSeq& sq = walk.seq;
+            const int r0 = walk.x.rt * NR, rows = min(NR, sq.nq * p.G - r0), off = sq.nk - sq.nq;
+            const int i0 = (int)((unsigned)r0 / G), i1 = (int)((unsigned)(r0 + rows - 1) / G);
+            if (walk.t1 > walk.t0) {
+                if (lane == 0) {
+                    const Band bd{off, p.left, p.right, sq.nk};
+                    Piece8& x = s.piece[found % kPieces];
+                    x.q0 = sq.q0;
+                    x.off = off;
+                    x.nk = sq.nk;
+                    x.r0 = r0;
+                    x.rows = rows;
+                    x.g = walk.x.g;
+                    x.part = walk.from_start && walk.to_end ? -1 : 2 * cta + (walk.from_start ? 1 : 0);
+                    x.t0 = walk.t0;
+                    x.t1 = walk.t1;
+                    x.b = walk.b;
+                    x.lo = bd.lo(i0);
+                    x.hi = bd.hi(i1);
+                    x.in_lo = p.left >= 0 ? i1 + off - p.left : 0;
+                    x.in_hi = p.right >= 0 ? min(sq.nk - 1, i0 + off + p.right) : sq.nk - 1;
                 }
+                ++found;
+            } else {
                 // no key for any row (such a piece is whole): its rows are written here
-                for (int r = warp; r < rows; r += kWarps8) {
-                    const int i = (int)((unsigned)(r0 + r) / G), h = b_g * p.G + r0 + r - i * p.G;
+                for (int r = 0; r < rows; ++r) {
+                    const int i = (int)((unsigned)(r0 + r) / G), h = walk.x.g * p.G + r0 + r - i * p.G;
                     uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (((long)sq.q0 + i) * p.h_q + h) * D);
                     for (int x = lane; x < D / 2; x += 32) out[x] = 0u;
                     if (lane == 0 && a.lse) a.lse[(long)h * p.T_q + sq.q0 + i] = p.sinks ? p.sinks[h] : -INFINITY;
                 }
             }
         }
-        if (more) {
-            const int j0 = at_t * kKeyTile + kGroup * warp, st = issued % S;
-            if (j0 <= b_hi && j0 + kGroup > b_lo) {
-                const int page = table[j0 / p.page_size], row = j0 % p.page_size;
-                const bool there = (unsigned)page < (unsigned)a.num_pages;
-                if (!there && lane == 0) atomicCAS(a.status, 0, kStatusDeviceCheck);
-                const long first = there ? (((long)page * p.page_size + row) * p.h_kv + b_g) * D : 0;
-                const long step = (long)p.h_kv * D;
-#pragma unroll
-                for (int y = 0; y < C::CPR / 2; ++y) {
-                    const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR, j = j0 + r;
-                    const bool seen = there && j >= b_lo && j <= b_hi;  // (what lies behind a page's used keys may be anything)
-                    const long from = seen ? first + r * step + 16 * col : 0;
-                    copy16_async(&s.ring[warp][st][0][at_chunk<D, false>(r, col)], kv.k + from, seen);
-                    copy16_async(&s.ring[warp][st][1][at_chunk<D, true>(r, col)], kv.v + from, seen);
-                }
-                if (lane < 2)
-                    copy4_async(&s.scale[warp][st][lane], (lane ? kv.v_scale : kv.k_scale) +
-                                (there ? ((long)page * kv.blocks + row / kv.block) * p.h_kv + b_g : 0));
-            }
-            ++at_t;
-            ++issued;
-        }
-        copies_commit();  // (a group to each call, so that the groups count the tiles)
+        s.walk[lane] = walk;
+        if (!more && lane == 0) a.cut[cta] = walk.cut;
     };
-#pragma unroll 1
-    for (int x = 0; x < S; ++x) fetch();
+    if (warp == 0) {
+        PagedWalk walk;
+        walk.start(p, a.pre, a.line, cta);
+        s.walk[lane] = walk;
+        find(2);
+        if (lane == 0) s.pieces[0] = found;
+    }
 
-    int done = 0;  // tiles
+    // ---- a warp's 16 keys of every TILES-th tile ----
+    const int lg = lane >> 2, lt = lane & 3;  // a fragment's row (or column) and its pair
+    const int group = warp % kGroups8, side = warp / kGroups8;
+    // the warp's stream: tiles of one piece after another, S of them ahead of the arithmetic
+    int at_t = 0, end_t = 0;           // of the piece that is being fetched
+    int ahead = 0, known = 0;          // pieces begun to be fetched, found
+    int b_lo = 0, b_hi = 0, b_g = 0;   // its keys that any row sees, its head
+    const int32_t* table = nullptr;
+    int issued = 0;
+    // The lane's copies: chunk `col` of rows row0, row0 + RSTEP, ... (D = 192: of one chunk of 384 or of the next,
+    // three chunks on and so on)
+    constexpr int RSTEP = 32 / C::CPR;
+    const int row0 = lane / C::CPR, col0 = lane % C::CPR;
+    const long row_step = (long)p.h_kv * D;
+    int st_in = 0;  // stage to be filled
+    auto fetch = [&]() {
+        if (at_t >= end_t && ahead < known) {
+            const Piece8& x = s.piece[ahead++ % kPieces];
+            at_t = x.t0;
+            end_t = x.t1;
+            b_g = x.g;
+            b_lo = x.lo;
+            b_hi = x.hi;
+            table = p.block_table + (long)x.b * p.max_blocks;
+        }
+        if (at_t < end_t) {
+            const int j0 = (at_t + side) * kKeyTile + kGroup * group;
+            if (at_t + side < end_t && j0 <= b_hi && j0 + kGroup > b_lo) {
+                const int at = quotient(j0, kv.by_page), page = table[at], row = j0 - at * p.page_size;
+                const bool there = (unsigned)page < (unsigned)a.num_pages;
+                const long first = (((long)page * p.page_size + row) * p.h_kv + b_g) * D;
+                uint8_t *kd = s.ring[warp][st_in][0], *vd = s.ring[warp][st_in][1];
+                if (lane < 2)
+                    copy4_async(&s.scale[warp][st_in][lane], (lane ? kv.v_scale : kv.k_scale) +
+                                (there ? ((long)page * kv.blocks + quotient(row, kv.by_block)) * p.h_kv + b_g : 0));
+                if (there && j0 >= b_lo && j0 + kGroup - 1 <= b_hi) {
+                    const long from = first + row0 * row_step + 16 * col0;
+                    const uint8_t *ks = kv.k + from, *vs = kv.v + from;
+                    if constexpr (D == 192) {
+#pragma unroll
+                        for (int y = 0; y < C::CPR / 2; ++y) {
+                            const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR;
+                            const long more_ = (r - row0) * row_step + 16 * (col - col0);
+                            copy16_async<C::LINE>(kd + at_chunk<D, false>(r, col), ks + more_);
+                            copy16_async<C::LINE>(vd + at_chunk<D, true>(r, col), vs + more_);
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < C::CPR / 2; ++y) {
+                            copy16_async<C::LINE>(kd + at_chunk<D, false>(row0 + RSTEP * y, col0), ks);
+                            copy16_async<C::LINE>(vd + at_chunk<D, true>(row0 + RSTEP * y, col0), vs);
+                            ks += RSTEP * row_step;
+                            vs += RSTEP * row_step;
+                        }
+                    }
+                } else {
+                    // rows that no query sees become zeros (what lies behind a page's used keys may be anything)
+                    if (!there && lane == 0) atomicCAS(a.status, 0, kStatusDeviceCheck);
+#pragma unroll 1
+                    for (int y = 0; y < C::CPR / 2; ++y) {
+                        const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR, j = j0 + r;
+                        const bool seen = there && j >= b_lo && j <= b_hi;
+                        const long from = seen ? first + r * row_step + 16 * col : 0;
+                        copy16_async(kd + at_chunk<D, false>(r, col), kv.k + from, seen);
+                        copy16_async(vd + at_chunk<D, true>(r, col), kv.v + from, seen);
+                    }
+                }
+            }
+            st_in = st_in + 1 == S ? 0 : st_in + 1;
+            at_t += TILES;
+            ++issued;
+            copies_commit();  // (a group to each tile)
+        }
+    };
+
+    int done = 0, st = 0;  // tiles, stage of the next
 #pragma unroll 1
     for (int piece = 0;; ++piece) {
-        __syncwarp();
-        if (piece >= pushed) break;
-        const Piece8 w = s.fifo[warp][piece % C::FIFO];
+        __syncthreads();  // (the pieces found are there; the rows and states of the piece before have been read)
+        known = s.pieces[piece & 1];
+        if (piece >= known) break;
+        while (issued < done + S && (at_t < end_t || ahead < known)) fetch();
+        const Piece8 w = s.piece[piece % kPieces];
         // ---- the query rows, as fp16 ----
-        __syncthreads();  // (the rows and states of the piece before have been read)
-        for (int r = warp; r < NR; r += kWarps8) {
+        if (warp == 0) {  // (one or two pieces on, while the others fetch rows)
+            if (more) find(min(piece + kLook, found + 2));
+            if (lane == 0) s.pieces[(piece + 1) & 1] = found;
+        }
+        for (int r = warp - 1; r < NR; r += WARPS - 1) {
+            if (r < 0) break;
             uint32_t x[D / 64];
             float top = 0.f;
             if (r < w.rows) {
@@ -263,11 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
                 for (int e = 0; e < 4; ++e) acc[x][n][e] = 0.f;
         }
 #pragma unroll 1
-        for (int t = w.t0; t < w.t1; ++t, ++done) {
-            const int st = done % S, j0 = t * kKeyTile + kGroup * warp;
-            copies_wait_but<S - 1>();
+        for (int t = w.t0; t < w.t1; t += TILES, ++done, st = st + 1 == S ? 0 : st + 1) {
+            const int j0 = (t + side) * kKeyTile + kGroup * group;
+            if (issued - done >= S) copies_wait_but<S - 1>();
+            else copies_wait();  // (the ring is not full: no further piece is known)
             __syncwarp();
-            if (j0 <= w.hi && j0 + kGroup > w.lo) {
+            if (t + side < w.t1 && j0 <= w.hi && j0 + kGroup > w.lo) {
                 const uint8_t *k8 = s.ring[warp][st][0], *v8 = s.ring[warp][st][1];
                 const float ks = s.scale[warp][st][0], vs = s.scale[warp][st][1];
                 // ---- S^T = K Q^T ----
@@ -330,9 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pr[n][e] = ex2(sc[n][e] - m[n][e & 1]);
-                        over = fmaxf(over, pr[n][e] * fmaxf(1.f, vs * u[n][e & 1]));
+                    for (int e = 0; e < 2; ++e) {
+                        pr[n][e] = ex2(sc[n][e] - m[n][e]);
+                        pr[n][2 + e] = ex2(sc[n][2 + e] - m[n][e]);
+                        over = fmaxf(over, fmaxf(pr[n][e], pr[n][2 + e]) * fmaxf(1.f, vs * u[n][e]));
                     }
                 if (__any_sync(0xffffffffu, over > kTop)) {
                     // some row's reference or unit moves: to the maxima so far
@@ -429,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
         if (tid < NR) {
             float top = kNoRef, sum = 0.f;
 #pragma unroll
-            for (int x = 0; x < kWarps8; ++x) top = fmaxf(top, s.m[x][tid]);
+            for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.m[x][tid]);
 #pragma unroll
-            for (int x = 0; x < kWarps8; ++x) {
+            for (int x = 0; x < WARPS; ++x) {
                 const float keep = ex2(s.m[x][tid] - top);
                 sum += s.l[x][tid] * keep;
                 s.u[x][tid] = keep / s.u[x][tid];
@@ -456,24 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float w0 = s.u[warp][8 * n + 2 * lt], w1 = s.u[warp][8 * n + 2 * lt + 1];
-            // (64 columns at a time: of each lane's D / 8 columns eight)
+            // (MERGE columns at a time: of each lane's D / 8 columns MERGE / 8)
+            constexpr int EACH = C::MERGE / 8;
 #pragma unroll
-            for (int y = 0; y < D / kMergeCols; ++y) {
+            for (int y = 0; y < D / C::MERGE; ++y) {
                 if (n + y > 0) __syncthreads();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float* c = acc[4 * y + x][n];
-                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt][8 * lg + 2 * x]) = make_float2(c[0] * w0, c[2] * w0);
-                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt + 1][8 * lg + 2 * x]) = make_float2(c[1] * w1, c[3] * w1);
+                for (int x = 0; x < EACH / 2; ++x) {
+                    const float* c = acc[EACH / 2 * y + x][n];
+                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt][EACH * lg + 2 * x]) = make_float2(c[0] * w0, c[2] * w0);
+                    *reinterpret_cast<float2*>(&s.merge[warp][2 * lt + 1][EACH * lg + 2 * x]) = make_float2(c[1] * w1, c[3] * w1);
                 }
                 __syncthreads();
                 const int r = 8 * n + warp;  // a warp to a row
-                if (r < w.rows) {
+                if (warp < 8 && r < w.rows && 2 * lane < C::MERGE) {
                     float2 o = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int x = 0; x < kWarps8; ++x) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&s.merge[x][warp][2 * lane]));
+                    for (int x = 0; x < WARPS; ++x) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&s.merge[x][warp][2 * lane]));
                     const float f = s.f[r];
-                    const int col = (lane >> 2) * (D / 8) + 8 * y + 2 * (lane & 3);
+                    const int col = 2 * lane / EACH * (D / 8) + EACH * y + 2 * lane % EACH;
                     if (w.part >= 0) {
                         *reinterpret_cast<float2*>(&a.part_o[0][((long)w.part * NR + r) * D + col]) = o;
                     } else {
@@ -486,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_few_kernel(const PagedArgs
             }
         }
     }
-    if (tid == 0) a.cut[cta] = walk.cut;
 }
 
 template <int D, int NT>
@@ -495,7 +555,7 @@ cudaError_t launch_few8(const PagedArgs& a, const Cache8& kv, int ctas, cudaStre
     static_assert(smem <= 227 * 1024, "the few-row kernel's shared memory");
     cudaError_t e = cudaFuncSetAttribute(paged8_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(paged8_few_kernel<D, NT>, dim3(ctas), kThreads, smem, st, a, kv);
+    return launch_after(paged8_few_kernel<D, NT>, dim3(ctas), Few8Cfg<D, NT>::THREADS, smem, st, a, kv);
 }
 
 template <int D>
