@@ -125,16 +125,19 @@ cudaError_t timed(KernelId id, cudaStream_t st, F&& launch) {
     return e;
 }
 
-// 4-D tensor map over a paged pool of bytes [pages][rows][h][d], boxes of `box` whole rows of a head, not
-// swizzled.  Out-of-range pages read as zero.
-bool encode_pages8(CUtensorMap* m, const void* base, int d, int h, int rows, int pages, int box) {
+// 4-D tensor map over a paged pool of bytes [pages][rows][h][d], boxes of `box` rows of a head, of `bytes` bytes (0:
+// whole rows, not swizzled; 64 or 128: swizzled in as many).  Out-of-range pages read as zero.
+bool encode_pages8(CUtensorMap* m, const void* base, int d, int h, int rows, int pages, int box, int bytes) {
     auto fn = encoder();
     if (!fn) return false;
+    const bool whole = bytes == 0;
+    if (whole) bytes = d;
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)h, (cuuint64_t)rows, (cuuint64_t)pages};
     cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)h * d, (cuuint64_t)rows * h * d};
-    cuuint32_t bx[4] = {(cuuint32_t)d, 1, (cuuint32_t)box, 1}, es[4] = {1, 1, 1, 1};
+    cuuint32_t bx[4] = {(cuuint32_t)bytes, 1, (cuuint32_t)box, 1}, es[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swizzle = whole ? CU_TENSOR_MAP_SWIZZLE_NONE : bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              swizzle, d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -476,12 +479,16 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     // another head's where d * 2 is 128 or 384 (decode of 32 x 16000 keys, 4 heads: d = 64 111 us against
     // 126, d = 192 with 2 heads 132 against 146)
     const CUtensorMapL2promotion promotion = p.d % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    const int bytes8 = p.d % 128 ? 64 : 128;  // the few-row kernel's copies: 16 rows, of as many bytes
+    if (p.cache8 && pl.few_max > 0 && (!encode_pages8(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 16, bytes8) ||
+                                       !encode_pages8(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 16, bytes8)))
+        return FA_ERR_CUDA;
     if (!p.cache8 && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion) ||
                       !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, a.box, f16, promotion)))
         return FA_ERR_CUDA;
     cudaError_t e = timed(kPagedPrep, st, [&] { return launch_paged_prep(a, st); });
     if (e == cudaSuccess && pl.few_max > 0)
-        e = timed(kPagedFew, st, [&] { return p.cache8 ? launch_paged8_few(a, kv, pl.ctas, st) : launch_paged_few(a, tk, tv, pl.ctas, st); });
+        e = timed(kPagedFew, st, [&] { return p.cache8 ? launch_paged8_few(a, kv, tk, tv, pl.ctas, st) : launch_paged_few(a, tk, tv, pl.ctas, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     if (!pl.many) return cuda_status(timed(kPagedMerge, st, [&] { return launch_paged_merge(a, false, st); }));
     // sequences of more rows: the tensor-core kernels, 2 P G rows to an item (P G at d = 192 / 256,
@@ -504,7 +511,7 @@ fa_status paged_fwd(const Problem& p, const fa_params& in, const void* q, const 
     f.cache8 = kv;
     if (p.cache8) {
         const int rows8 = f.box < 64 ? f.box : 64;
-        if (!encode_pages8(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, rows8) || !encode_pages8(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, rows8))
+        if (!encode_pages8(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, rows8, 0) || !encode_pages8(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, rows8, 0))
             return FA_ERR_CUDA;
     } else if (f.box != a.box && (!encode_bhsd(&tk, k, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion) ||
                            !encode_bhsd(&tv, v, p.d, p.h_kv, p.page_size, in.num_pages, 1, f.box, f16, promotion)))

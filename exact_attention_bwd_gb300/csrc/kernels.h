@@ -243,7 +243,7 @@ cudaError_t launch_bwd_main(const BwdArgs& a, const CUtensorMap& tq, const CUten
 cudaError_t launch_bwd_post(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st);
 cudaError_t launch_paged_few(const PagedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
-cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st);
+cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs& a, bool many, cudaStream_t st);  // many: both kernels' items
 cudaError_t launch_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_append8(const RopeArgs& a, const Append8Args& c, cudaStream_t st);

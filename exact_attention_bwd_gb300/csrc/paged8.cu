@@ -41,12 +41,11 @@ struct Few8Cfg {
     static constexpr int NR = 8 * NT;
     static constexpr int TILES = NT == 1 && D <= 128 ? 2 : 1;  // tiles side by side
     static constexpr int WARPS = kGroups8 * TILES, THREADS = 32 * WARPS;
-    static constexpr int CPR = D / 16;              // 16-byte chunks of a row
     static constexpr int GROUP_BYTES = kGroup * D;  // K (or V) rows of a warp's group
-    static constexpr int STAGES = (D == 64 ? 10 : D == 128 ? 6 : D == 192 ? 4 : 3) / TILES;
-    static constexpr int LINE = D % 128 ? 64 : 128;  // (d = 128: 262 us without the hint, 243 with it, 314 with 256 bytes)
+    static constexpr int STAGES = D == 64 ? 8 / TILES : D == 128 ? (TILES == 2 ? 2 : 5) : D == 192 ? 4 : 3;
+    static constexpr int BOX = D % 128 ? 64 : 128, BOXES = D / BOX;  // bytes of a copy's rows (swizzled in as many), copies
     static constexpr int MT = D / 16;               // 16-row tiles of O^T
-    static constexpr int MERGE = 64 / TILES;        // columns that the warps join at a time
+    static constexpr int MERGE = D <= 128 ? D : NT == 2 ? 32 : 64;  // columns that the warps join at a time
     static constexpr int Q_STRIDE = 2 * D + 16;     // bytes of a query row
     static constexpr bool Q_REGS = NT * D <= 256;   // query fragments held in registers
 };
@@ -61,12 +60,15 @@ struct Piece8 {
 };
 
 template <int D, int NT>
-struct __align__(128) Few8Smem {
+struct __align__(1024) Few8Smem {
     using C = Few8Cfg<D, NT>;
     uint8_t ring[C::WARPS][C::STAGES][2][C::GROUP_BYTES];
-    uint8_t q[C::NR * C::Q_STRIDE];
+    uint8_t q[C::NR * C::Q_STRIDE];       // query rows as fp16
+    alignas(16) uint16_t raw[C::NR][D];  // those of the next piece as they come
     float merge[C::WARPS][8][C::MERGE];
     float scale[C::WARPS][C::STAGES][2];
+    uint64_t full[C::WARPS][C::STAGES];
+    int abort_flag;
     float qf[C::NR];                 // the power of two that a query row was divided by
     float m[C::WARPS][C::NR], l[C::WARPS][C::NR], u[C::WARPS][C::NR];  // the warps' states; u becomes the weight of its output
     float f[C::NR];                  // factor of a whole item's output
@@ -75,19 +77,17 @@ struct __align__(128) Few8Smem {
     PagedWalk walk[32];              // warp 0's walk over the CTA's stretch: a lane's state each
 };
 
-// Where chunk `col` of row `row` of a group lies: so that the lanes' reads of a fragment fall into different banks
-// (K: 16 bytes of two neighbouring rows at four neighbouring chunks; V: of four rows two apart at the chunks of two lanes).
-template <int D, bool V>
+// Where chunk `col` of row `row` of a group lies: boxes of 16 rows, 64- or 128-byte swizzled.
+template <int D>
 __device__ __forceinline__ int at_chunk(int row, int col) {
-    if constexpr (!V) {
-        return row * D + ((D == 128 || D == 256 ? col ^ ((row & 1) << 2) : col) << 4);
-    } else {
-        const int t = (row >> 1) & 3;
-        if constexpr (D == 64) return (row >> 1) * 128 + (((((row & 1) << 2) | col) ^ (t << 1)) << 4);
-        else if constexpr (D == 128) return row * D + ((col ^ (t << 1)) << 4);
-        else if constexpr (D == 192) return row * D + ((col ^ t) << 4);
-        else return row * D + ((col ^ ((t & 1) | ((t & 2) << 1))) << 4);
-    }
+    constexpr int BOX = Few8Cfg<D, 1>::BOX, PER = BOX / 16;
+    return col / PER * (kGroup * BOX) + row * BOX + ((col % PER ^ (BOX == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+// The key of row g of a fragment (and 8 on, of row g + 8).  The reads of K go two neighbouring rows and four
+// chunks at a time, which 128-byte rows then have in different banks.
+template <int D>
+__device__ __forceinline__ int key_of(int g) {
+    return Few8Cfg<D, 1>::BOX == 128 ? g ^ ((g & 1) << 2) : g;
 }
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -101,31 +101,32 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
     return r;
 }
-template <int N>
-__device__ __forceinline__ void copies_wait_but() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-
 // The power of two at or below x (x > 0 and normal).
 __device__ __forceinline__ float power_below(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(const PagedArgs a, const Cache8 kv) {
+__global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(const PagedArgs a, const Cache8 kv, const __grid_constant__ CUtensorMap tmk,
+                                                                               const __grid_constant__ CUtensorMap tmv) {
     using C = Few8Cfg<D, NT>;
     constexpr int NR = C::NR, S = C::STAGES, WARPS = C::WARPS, TILES = C::TILES;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    Few8Smem<D, NT>& s = *reinterpret_cast<Few8Smem<D, NT>*>(smem_raw);
+    Few8Smem<D, NT>& s = *reinterpret_cast<Few8Smem<D, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Problem& p = a.p;
     const bool f16 = p.dtype == FA_DTYPE_F16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     const unsigned G = (unsigned)p.G;
     allow_next_kernel();
+    Abort ab{&s.abort_flag, a.status, p.wait_ns};
+    if (tid == 0) s.abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&s.full[warp][i], 3);  // the rows' arrival, and two lanes' copies of scales
+        fence_mbar_init();
+    }
     wait_previous_kernel();
     // (one thread looks, so that all leave or none)
     if (__syncthreads_or(tid == 0 && (cta >= a.line->n || *reinterpret_cast<volatile int*>(a.status) != 0))) return;
 
-    // ---- the pieces of the CTA's stretch, found by warp 0 (the walk's state lies in shared memory: it needs as many
+    // ---- the pieces of the CTA's stretch, found by the last warp (the walk's state lies in shared memory: it needs as many
     // registers as an accumulator tile of 16 rows) ----
     int found = 0;
     bool more = true;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
         s.walk[lane] = walk;
         if (!more && lane == 0) a.cut[cta] = walk.cut;
     };
-    if (warp == 0) {
+    if (warp == WARPS - 1) {
         PagedWalk walk;
         walk.start(p, a.pre, a.line, cta);
         s.walk[lane] = walk;
@@ -187,12 +188,8 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
     int b_lo = 0, b_hi = 0, b_g = 0;   // its keys that any row sees, its head
     const int32_t* table = nullptr;
     int issued = 0;
-    // The lane's copies: chunk `col` of rows row0, row0 + RSTEP, ... (D = 192: of one chunk of 384 or of the next,
-    // three chunks on and so on)
-    constexpr int RSTEP = 32 / C::CPR;
-    const int row0 = lane / C::CPR, col0 = lane % C::CPR;
-    const long row_step = (long)p.h_kv * D;
-    int st_in = 0;  // stage to be filled
+    int st_in = 0;                       // stage to be filled
+    uint32_t filled = 0, phase = 0;      // stages with copies on their way or not yet read, parities that they complete
     auto fetch = [&]() {
         if (at_t >= end_t && ahead < known) {
             const Piece8& x = s.piece[ahead++ % kPieces];
@@ -208,81 +205,49 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
             if (at_t + side < end_t && j0 <= b_hi && j0 + kGroup > b_lo) {
                 const int at = quotient(j0, kv.by_page), page = table[at], row = j0 - at * p.page_size;
                 const bool there = (unsigned)page < (unsigned)a.num_pages;
-                const long first = (((long)page * p.page_size + row) * p.h_kv + b_g) * D;
-                uint8_t *kd = s.ring[warp][st_in][0], *vd = s.ring[warp][st_in][1];
-                if (lane < 2)
-                    copy4_async(&s.scale[warp][st_in][lane], (lane ? kv.v_scale : kv.k_scale) +
-                                (there ? ((long)page * kv.blocks + quotient(row, kv.by_block)) * p.h_kv + b_g : 0));
-                if (there && j0 >= b_lo && j0 + kGroup - 1 <= b_hi) {
-                    const long from = first + row0 * row_step + 16 * col0;
-                    const uint8_t *ks = kv.k + from, *vs = kv.v + from;
-                    if constexpr (D == 192) {
+                uint64_t* bar = &s.full[warp][st_in];
+                if (lane < 2) {
+                    if (there)
+                        copy4_async(&s.scale[warp][st_in][lane], (lane ? kv.v_scale : kv.k_scale) +
+                                    ((long)page * kv.blocks + quotient(row, kv.by_block)) * p.h_kv + b_g);
+                    mbar_arrive_copies(bar);
+                }
+                if (lane == 0) {
+                    if (!there) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    mbar_expect_tx(bar, 2 * C::GROUP_BYTES);
 #pragma unroll
-                        for (int y = 0; y < C::CPR / 2; ++y) {
-                            const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR;
-                            const long more_ = (r - row0) * row_step + 16 * (col - col0);
-                            copy16_async<C::LINE>(kd + at_chunk<D, false>(r, col), ks + more_);
-                            copy16_async<C::LINE>(vd + at_chunk<D, true>(r, col), vs + more_);
-                        }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < C::CPR / 2; ++y) {
-                            copy16_async<C::LINE>(kd + at_chunk<D, false>(row0 + RSTEP * y, col0), ks);
-                            copy16_async<C::LINE>(vd + at_chunk<D, true>(row0 + RSTEP * y, col0), vs);
-                            ks += RSTEP * row_step;
-                            vs += RSTEP * row_step;
-                        }
-                    }
-                } else {
-                    // rows that no query sees become zeros (what lies behind a page's used keys may be anything)
-                    if (!there && lane == 0) atomicCAS(a.status, 0, kStatusDeviceCheck);
-#pragma unroll 1
-                    for (int y = 0; y < C::CPR / 2; ++y) {
-                        const int x = lane + 32 * y, r = x / C::CPR, col = x % C::CPR, j = j0 + r;
-                        const bool seen = there && j >= b_lo && j <= b_hi;
-                        const long from = seen ? first + r * row_step + 16 * col : 0;
-                        copy16_async(kd + at_chunk<D, false>(r, col), kv.k + from, seen);
-                        copy16_async(vd + at_chunk<D, true>(r, col), kv.v + from, seen);
+                    for (int x = 0; x < C::BOXES; ++x) {  // (the pool's end reads as zeros)
+                        tma_load_4d(&s.ring[warp][st_in][0][x * kGroup * C::BOX], &tmk, bar, x * C::BOX, b_g, row, there ? page : a.num_pages);
+                        tma_load_4d(&s.ring[warp][st_in][1][x * kGroup * C::BOX], &tmv, bar, x * C::BOX, b_g, row, there ? page : a.num_pages);
                     }
                 }
+                filled |= 1u << st_in;
             }
             st_in = st_in + 1 == S ? 0 : st_in + 1;
             at_t += TILES;
             ++issued;
-            copies_commit();  // (a group to each tile)
         }
     };
 
-    int done = 0, st = 0;  // tiles, stage of the next
-#pragma unroll 1
-    for (int piece = 0;; ++piece) {
-        __syncthreads();  // (the pieces found are there; the rows and states of the piece before have been read)
-        known = s.pieces[piece & 1];
-        if (piece >= known) break;
-        while (issued < done + S && (at_t < end_t || ahead < known)) fetch();
-        const Piece8 w = s.piece[piece % kPieces];
-        // ---- the query rows, as fp16 ----
-        if (warp == 0) {  // (one or two pieces on, while the others fetch rows)
-            if (more) find(min(piece + kLook, found + 2));
-            if (lane == 0) s.pieces[(piece + 1) & 1] = found;
+    // The query rows of a piece: asked for a piece ahead, turned to fp16 where the piece before ends (a warp its own).
+    auto ask = [&](const Piece8& x) {
+        for (int r = warp; r < NR; r += WARPS) {
+            const int i = (int)((unsigned)(x.r0 + r) / G), h = x.g * p.G + x.r0 + r - i * p.G;
+            const uint16_t* src = r < x.rows ? a.q + (((long)x.q0 + i) * p.h_q + h) * D : a.q;
+            if (lane < D / 8) copy16_async(&s.raw[r][8 * lane], src + 8 * lane, r < x.rows);
         }
-        for (int r = warp - 1; r < NR; r += WARPS - 1) {
-            if (r < 0) break;
-            uint32_t x[D / 64];
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    auto take = [&]() {
+        asm volatile("cp.async.wait_group 0;\n" ::: "memory");  // (not for the scales' copies since, which are in no group)
+        __syncwarp();
+        for (int r = warp; r < NR; r += WARPS) {
             float top = 0.f;
-            if (r < w.rows) {
-                const int i = (int)((unsigned)(w.r0 + r) / G), h = w.g * p.G + w.r0 + r - i * p.G;
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (((long)w.q0 + i) * p.h_q + h) * D);
-#pragma unroll
-                for (int e = 0; e < D / 64; ++e) x[e] = src[lane + 32 * e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < D / 64; ++e) x[e] = 0u;
-            }
             float2 v[D / 64];
 #pragma unroll
             for (int e = 0; e < D / 64; ++e) {
-                v[e] = f16 ? make_float2(lo16<true>(x[e]), hi16<true>(x[e])) : make_float2(lo16<false>(x[e]), hi16<false>(x[e]));
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(&s.raw[r][2 * (lane + 32 * e)]);
+                v[e] = f16 ? make_float2(lo16<true>(x), hi16<true>(x)) : make_float2(lo16<false>(x), hi16<false>(x));
                 top = fmaxf(top, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
             }
             top = warp_max(top);
@@ -293,7 +258,27 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 *reinterpret_cast<uint32_t*>(&s.q[r * C::Q_STRIDE + 4 * (lane + 32 * e)]) = pack16<true>(v[e].x * inv, v[e].y * inv);
             if (lane == 0) s.qf[r] = unit * p.scale_log2;
         }
-        __syncthreads();
+        __syncwarp();
+    };
+
+    int done = 0, st = 0;  // tiles, stage of the next
+    bool ok = true;
+    __syncthreads();
+    known = s.pieces[0];
+    if (known > 0) {
+        ask(s.piece[0]);
+        while (issued < S && (at_t < end_t || ahead < known)) fetch();
+        take();
+    }
+#pragma unroll 1
+    for (int piece = 0;; ++piece) {
+        // (the pieces found are there; the rows and states of the piece before have been read; one warp that gave up ends all)
+        if (__syncthreads_or(!ok)) break;
+        known = s.pieces[piece & 1];
+        if (piece >= known) break;
+        while (issued < done + S && (at_t < end_t || ahead < known)) fetch();
+        const Piece8 w = s.piece[piece % kPieces];
+        if (piece + 1 < known) ask(s.piece[(piece + 1) % kPieces]);
         // ---- state: rows 8 n + 2 lt and 8 n + 2 lt + 1 ----
         float m[NT][2], u[NT][2], l[NT][2], qf[NT][2], acc[C::MT][NT][4];
         uint4 qr[C::Q_REGS ? NT : 1][D / 64][2];
@@ -323,10 +308,10 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
 #pragma unroll 1
         for (int t = w.t0; t < w.t1; t += TILES, ++done, st = st + 1 == S ? 0 : st + 1) {
             const int j0 = (t + side) * kKeyTile + kGroup * group;
-            if (issued - done >= S) copies_wait_but<S - 1>();
-            else copies_wait();  // (the ring is not full: no further piece is known)
-            __syncwarp();
             if (t + side < w.t1 && j0 <= w.hi && j0 + kGroup > w.lo) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][st], (phase >> st) & 1, ab)))) break;
+                phase ^= 1u << st;
+                filled &= ~(1u << st);
                 const uint8_t *k8 = s.ring[warp][st][0], *v8 = s.ring[warp][st][1];
                 const float ks = s.scale[warp][st][0], vs = s.scale[warp][st][1];
                 // ---- S^T = K Q^T ----
@@ -337,8 +322,8 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                     for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    const uint4 ka = *reinterpret_cast<const uint4*>(k8 + at_chunk<D, false>(lg, lt + 4 * i));
-                    const uint4 kb = *reinterpret_cast<const uint4*>(k8 + at_chunk<D, false>(lg + 8, lt + 4 * i));
+                    const uint4 ka = *reinterpret_cast<const uint4*>(k8 + at_chunk<D>(key_of<D>(lg), lt + 4 * i));
+                    const uint4 kb = *reinterpret_cast<const uint4*>(k8 + at_chunk<D>(key_of<D>(lg) + 8, lt + 4 * i));
                     uint4 q0[NT], q1[NT];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -356,7 +341,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                         }
                     }
                 }
-                // ---- scores in log2 units; keys j0 + lg and j0 + lg + 8 ----
+                // ---- scores in log2 units; keys j0 + key_of(lg) and 8 on ----
                 const bool edge = j0 < w.in_lo || j0 + kGroup - 1 > w.in_hi;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -369,7 +354,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 if (edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int j = j0 + lg + 8 * h;
+                        const int j = j0 + key_of<D>(lg) + 8 * h;
                         // rows [ra, rb] see key j: positions j - off - right <= i <= j - off + left
                         int ra = 0, rb = NR - 1;
                         if (p.right >= 0) ra = (int)max(min(((long)j - w.off - p.right) * p.G - w.r0, (long)NR), 0l);
@@ -437,11 +422,11 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 uint32_t vw[4][WORDS];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int r = 2 * lt + (y & 1) + 8 * (y >> 1);
+                    const int r = key_of<D>(2 * lt + (y & 1)) + 8 * (y >> 1);
                     if constexpr (D >= 128 && D != 192) {
 #pragma unroll
                         for (int z = 0; z < WORDS / 4; ++z) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(v8 + at_chunk<D, true>(r, lg * (WORDS / 4) + z));
+                            const uint4 x = *reinterpret_cast<const uint4*>(v8 + at_chunk<D>(r, lg * (WORDS / 4) + z));
                             vw[y][4 * z] = x.x;
                             vw[y][4 * z + 1] = x.y;
                             vw[y][4 * z + 2] = x.z;
@@ -451,10 +436,20 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
 #pragma unroll
                         for (int z = 0; z < WORDS / 2; ++z) {
                             const int byte = lg * (D / 8) + 8 * z;
-                            const uint2 x = *reinterpret_cast<const uint2*>(v8 + at_chunk<D, true>(r, byte >> 4) + (byte & 8));
+                            const uint2 x = *reinterpret_cast<const uint2*>(v8 + at_chunk<D>(r, byte >> 4) + (byte & 8));
                             vw[y][2 * z] = x.x;
                             vw[y][2 * z + 1] = x.y;
                         }
+                    }
+                }
+                if (edge) {
+                    // (values that no query sees may be anything, and 0 * NaN is NaN)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int j = j0 + key_of<D>(2 * lt + (y & 1)) + 8 * (y >> 1);
+                        if (j < w.lo || j > w.hi)
+#pragma unroll
+                            for (int z = 0; z < WORDS; ++z) vw[y][z] = 0u;
                     }
                 }
 #pragma unroll
@@ -472,6 +467,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
             fetch();
         }
         // ---- the warps' states join ----
+        // (the next piece's rows, asked for ahead of the tiles, have long been there: each warp's wait covers its own)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -486,6 +482,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 }
             }
         __syncthreads();
+        if (piece + 1 < known) take();
         if (tid < NR) {
             float top = kNoRef, sum = 0.f;
 #pragma unroll
@@ -528,13 +525,16 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                     *reinterpret_cast<float2*>(&s.merge[warp][2 * lt + 1][EACH * lg + 2 * x]) = make_float2(c[1] * w1, c[3] * w1);
                 }
                 __syncthreads();
-                const int r = 8 * n + warp;  // a warp to a row
-                if (warp < 8 && r < w.rows && 2 * lane < C::MERGE) {
+                // a warp to a row and 64 columns
+#pragma unroll
+                for (int z = warp; z < 8 * ((C::MERGE + 63) / 64); z += WARPS) {
+                    const int rr = z & 7, r = 8 * n + rr, at = 64 * (z >> 3) + 2 * lane;
+                    if (r >= w.rows || at >= C::MERGE) continue;
                     float2 o = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int x = 0; x < WARPS; ++x) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&s.merge[x][warp][2 * lane]));
+                    for (int x = 0; x < WARPS; ++x) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&s.merge[x][rr][at]));
                     const float f = s.f[r];
-                    const int col = 2 * lane / EACH * (D / 8) + EACH * y + 2 * lane % EACH;
+                    const int col = at / EACH * (D / 8) + EACH * y + at % EACH;
                     if (w.part >= 0) {
                         *reinterpret_cast<float2*>(&a.part_o[0][((long)w.part * NR + r) * D + col]) = o;
                     } else {
@@ -546,37 +546,44 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 }
             }
         }
+        if (warp == WARPS - 1) {  // one or two pieces on
+            if (more) find(min(piece + kLook, found + 2));
+            if (lane == 0) s.pieces[(piece + 1) & 1] = found;
+        }
     }
+    // (given up: every copy still in flight lands before the CTA may exit)
+    for (int i = 0; i < S; ++i)
+        if ((filled >> i) & 1) mbar_wait_quiet(&s.full[warp][i], (phase >> i) & 1);
 }
 
 template <int D, int NT>
-cudaError_t launch_few8(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
-    constexpr size_t smem = sizeof(Few8Smem<D, NT>);
+cudaError_t launch_few8(const PagedArgs& a, const Cache8& kv, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
+    constexpr size_t smem = sizeof(Few8Smem<D, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "the few-row kernel's shared memory");
     cudaError_t e = cudaFuncSetAttribute(paged8_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(paged8_few_kernel<D, NT>, dim3(ctas), Few8Cfg<D, NT>::THREADS, smem, st, a, kv);
+    return launch_after(paged8_few_kernel<D, NT>, dim3(ctas), Few8Cfg<D, NT>::THREADS, smem, st, a, kv, tk, tv);
 }
 
 template <int D>
-cudaError_t launch_few8_d(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
+cudaError_t launch_few8_d(const PagedArgs& a, const Cache8& kv, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
     switch (a.few_rows) {
-        case 8: return launch_few8<D, 1>(a, kv, ctas, st);
-        case 16: return launch_few8<D, 2>(a, kv, ctas, st);
+        case 8: return launch_few8<D, 1>(a, kv, tk, tv, ctas, st);
+        case 16: return launch_few8<D, 2>(a, kv, tk, tv, ctas, st);
         case 32:
-            if constexpr (D <= 128) return launch_few8<D, 4>(a, kv, ctas, st);
+            if constexpr (D <= 128) return launch_few8<D, 4>(a, kv, tk, tv, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, int ctas, cudaStream_t st) {
+cudaError_t launch_paged8_few(const PagedArgs& a, const Cache8& kv, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t st) {
     switch (a.p.d) {
-        case 64: return launch_few8_d<64>(a, kv, ctas, st);
-        case 128: return launch_few8_d<128>(a, kv, ctas, st);
-        case 192: return launch_few8_d<192>(a, kv, ctas, st);
-        case 256: return launch_few8_d<256>(a, kv, ctas, st);
+        case 64: return launch_few8_d<64>(a, kv, tk, tv, ctas, st);
+        case 128: return launch_few8_d<128>(a, kv, tk, tv, ctas, st);
+        case 192: return launch_few8_d<192>(a, kv, tk, tv, ctas, st);
+        case 256: return launch_few8_d<256>(a, kv, tk, tv, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -166,12 +166,6 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ void copy16_async(void* to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
-// (LINE: bytes that the L2 fetches together, the rest of a row that other lanes ask for)
-template <int LINE>
-__device__ __forceinline__ void copy16_async(void* to, const void* from) {
-    if constexpr (LINE == 128) asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
-    else asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
 // The same for 4 bytes, and the thread's arrival on a barrier once all that it has started has landed (the
 // barrier counts it among its arrivals).
 __device__ __forceinline__ void copy4_async(void* to, const void* from) {
