@@ -34,6 +34,7 @@ constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 // of 262144 tokens, four heads a group, by one thread: 273 us)
 constexpr int kPrepAlone = 32;
 
+template <int FEW, int MANY>  // the leads
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArgs a) {
     __shared__ long long warp_sum[2][kPrepWarps];
     __shared__ unsigned long long units_of[kPrepThreads];
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
 #pragma unroll 1
                     for (int r = 0; r < (int)rows; r += step) {
                         int t0, t1;
-                        w += paged_tiles(p, s, r, step, t0, t1);
+                        w += few ? paged_tiles<FEW>(p, s, r, step, t0, t1) : paged_tiles<MANY>(p, s, r, step, t0, t1);
                     }
                 }
                 (few ? w0 : w1) = w;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
 #pragma unroll 1
             for (long r = (long)tid * step; r < rows; r += (long)kPrepThreads * step) {
                 int t0, t1;
-                w += paged_tiles(p, s, (int)r, step, t0, t1);
+                w += rows <= a.few_max ? paged_tiles<FEW>(p, s, (int)r, step, t0, t1) : paged_tiles<MANY>(p, s, (int)r, step, t0, t1);
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -131,9 +132,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const PagedArg
         a.pre[0] = 0;
         a.pre[p.B + 1] = 0;
         *a.status = bad_any ? kStatusDeviceCheck : kStatusOk;
-        a.line[0] = paged_line(run0 * p.h_kv, a.few_ctas);
+        a.line[0] = paged_line<FEW>(run0 * p.h_kv, a.few_ctas);
     } else if (tid == 32) {
-        a.line[1] = paged_line(run1 * p.h_kv, a.many_ctas);
+        a.line[1] = paged_line<MANY>(run1 * p.h_kv, a.many_ctas);
     }
 }
 
@@ -1076,7 +1077,8 @@ cudaError_t launch_merge_d(const PagedArgs& a, const dim3& grid, int few_groups,
 }  // namespace
 
 cudaError_t launch_paged_prep(const PagedArgs& a, cudaStream_t st) {
-    paged_prep_kernel<<<1, kPrepThreads, 0, st>>>(a);
+    if (a.p.cache8) paged_prep_kernel<kLeadFew8, kLead><<<1, kPrepThreads, 0, st>>>(a);
+    else paged_prep_kernel<kLead, kLead><<<1, kPrepThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

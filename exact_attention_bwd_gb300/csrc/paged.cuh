@@ -34,15 +34,20 @@ __device__ __forceinline__ PagedSeq paged_seq(const Problem& p, int b) {
 // The lead of an item in tiles: flat from 1 to 4 for both kernels (8 chunks of 1024 tokens 707 / 703 /
 // 705 / 707 us, a mixed batch at d = 64 65 / 65 / 64 / 66).
 constexpr int kLead = 2;
+// Few rows over a cache in 8 bits: a tile takes half of the time, and an item's ends join 8 or 16 warps.
+// (Decode of 64 requests over 2k to 32k keys with a lead of 2 / 4 / 6 / 10: 254 / 241 / 235 / 239 us; the chunks' kernels
+// prefer 2 there as well.)
+constexpr int kLeadFew8 = 6;
 
 // Key tiles [t0, t1) of the rows [r0, r0 + rows) (numbered position * G + head of the group; r0 is
 // one of them, nq * G fits 32 bits), and the units of the item.
+template <int LEAD = kLead>
 __device__ __forceinline__ int paged_tiles(const Problem& p, const PagedSeq& s, int r0, int rows, int& t0, int& t1) {
     const Band bd{s.nk - s.nq, p.left, p.right, s.nk};
     const unsigned G = (unsigned)p.G;
     const int i0 = (int)((unsigned)r0 / G), i1 = min(s.nq - 1, (int)((unsigned)(r0 + rows - 1) / G));
     kv_tile_range(bd, i0, i1, kKeyTile, t0, t1);
-    return kLead + max(t1 - t0, 1);
+    return LEAD + max(t1 - t0, 1);
 }
 
 // The line of one kernel's units as the preparation leaves it: n CTAs take part, CTA c's stretch
@@ -58,12 +63,13 @@ struct PagedLine {
         return u < head ? (int)(u / (each + 1)) : more + (int)((u - head) / each);
     }
 };
-// With more than one CTA a stretch has kLead units at least (4 units: two of 2).  One that ends among
+// With more than one CTA a stretch has LEAD units at least (4 units: two of 2).  One that ends among
 // the lead of the item that it starts passes the item on, so a CTA may be left without a tile.
+template <int LEAD = kLead>
 __device__ __forceinline__ PagedLine paged_line(long long units, int n_ctas) {
     PagedLine x;
     x.units = units;
-    x.n = (int)min((long long)n_ctas, (units + kLead) / (kLead + 1));
+    x.n = (int)min((long long)n_ctas, (units + LEAD) / (LEAD + 1));
     x.each = x.n > 0 ? units / x.n : 0;
     x.more = x.n > 0 ? (int)(units % x.n) : 0;
     return x;
@@ -95,6 +101,7 @@ struct PagedLook {
     int g = -1, base = 0;  // head, first of the 32 row tiles
     long long units = 0;   // of the head ahead of them
 };
+template <int LEAD = kLead>
 __device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq& s, int rows, long long rem, long long per_head,
                                                 PagedLook& look) {
     const int lane = threadIdx.x & 31;
@@ -107,7 +114,7 @@ __device__ __forceinline__ PagedUnit paged_unit(const Problem& p, const PagedSeq
 #pragma unroll 1
     for (;; base += 32) {
         t0 = t1 = cost = 0;
-        if (base + lane < tiles) cost = paged_tiles(p, s, (base + lane) * rows, rows, t0, t1);
+        if (base + lane < tiles) cost = paged_tiles<LEAD>(p, s, (base + lane) * rows, rows, t0, t1);
         sum = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -140,7 +147,8 @@ struct PagedCut {
 // The walk of one warp over its CTA's stretch, piece by piece.  Up to 32 sequences are held a lane
 // each from the start, when line, units, offsets and lengths are read side by side; more are looked up one
 // after another (decode of 32 sequences over 4000 keys 56.2 us, 57.2 with lookups).
-struct PagedWalk {
+template <int LEAD>
+struct PagedWalkOf {
     long long u = 0, end = 0;  // next unit, end of the stretch
     bool held = false;
     long long my_pre = 0, my_units = 0;  // held: the units of a head ahead of the lane's sequence and its own
@@ -182,17 +190,17 @@ struct PagedWalk {
                 after = before + per_head * p.h_kv;
                 look.g = -1;
             }
-            x = paged_unit(p, seq, rows, u - before, per_head, look);
-            if (no_split && x.k > kLead) {  // the item is the CTA's that holds its start
+            x = paged_unit<LEAD>(p, seq, rows, u - before, per_head, look);
+            if (no_split && x.k > LEAD) {  // the item is the CTA's that holds its start
                 u += x.cost - x.k;
                 continue;
             }
             const long long start = u - x.k;
-            if (end - start <= kLead) break;  // the item's start counts for the next CTA
-            from_start = x.k <= kLead;
+            if (end - start <= LEAD) break;  // the item's start counts for the next CTA
+            from_start = x.k <= LEAD;
             to_end = no_split || end - start >= x.cost;
-            t0 = x.t0 + (from_start ? 0 : x.k - kLead);
-            t1 = to_end ? x.t1 : x.t0 + (int)(end - start) - kLead;
+            t0 = x.t0 + (from_start ? 0 : x.k - LEAD);
+            t1 = to_end ? x.t1 : x.t0 + (int)(end - start) - LEAD;
             u = to_end ? start + x.cost : end;
             if (from_start && !to_end) {
                 const int r0 = x.rt * rows;
@@ -203,6 +211,9 @@ struct PagedWalk {
         return false;
     }
 };
+
+using PagedWalk = PagedWalkOf<kLead>;
+using PagedWalkFew8 = PagedWalkOf<kLeadFew8>;
 
 // A warp's own copy of a value that all its lanes hold.  Where the warp groups split the registers
 // between them, the walk needs more than its group has, and what other roles share with it would be

@@ -74,7 +74,7 @@ struct __align__(1024) Few8Smem {
     float f[C::NR];                  // factor of a whole item's output
     Piece8 piece[kPieces];
     int pieces[2];                   // found so far, as of each second meeting
-    PagedWalk walk[32];              // warp 0's walk over the CTA's stretch: a lane's state each
+    PagedWalkFew8 walk[32];             // the last warp's walk over the CTA's stretch: a lane's state each
 };
 
 // Where chunk `col` of row `row` of a group lies: boxes of 16 rows, 64- or 128-byte swizzled.
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
     int found = 0;
     bool more = true;
     auto find = [&](int most) {
-        PagedWalk walk = s.walk[lane];
+        PagedWalkFew8 walk = s.walk[lane];
         const PagedLine line = *a.line;
         while (more && found < most) {
             if (!(more = walk.next(p, a.pre, line, cta, NR, a.no_split))) break;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
         if (!more && lane == 0) a.cut[cta] = walk.cut;
     };
     if (warp == WARPS - 1) {
-        PagedWalk walk;
+        PagedWalkFew8 walk;
         walk.start(p, a.pre, a.line, cta);
         s.walk[lane] = walk;
         find(2);
@@ -190,7 +190,10 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
     int issued = 0;
     int st_in = 0;                       // stage to be filled
     uint32_t filled = 0, phase = 0;      // stages with copies on their way or not yet read, parities that they complete
-    auto fetch = [&]() {
+    // looks at the next tile: the warp's keys' entry of the table is on its way until the tile's copies are started
+    bool looked = false, mine = false;
+    int entry = 0, row = 0;
+    auto look = [&]() {
         if (at_t >= end_t && ahead < known) {
             const Piece8& x = s.piece[ahead++ % kPieces];
             at_t = x.t0;
@@ -200,10 +203,22 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
             b_hi = x.hi;
             table = p.block_table + (long)x.b * p.max_blocks;
         }
-        if (at_t < end_t) {
+        looked = at_t < end_t;
+        if (looked) {
             const int j0 = (at_t + side) * kKeyTile + kGroup * group;
-            if (at_t + side < end_t && j0 <= b_hi && j0 + kGroup > b_lo) {
-                const int at = quotient(j0, kv.by_page), page = table[at], row = j0 - at * p.page_size;
+            mine = at_t + side < end_t && j0 <= b_hi && j0 + kGroup > b_lo;
+            if (mine) {
+                const int at = quotient(j0, kv.by_page);
+                entry = table[at];
+                row = j0 - at * p.page_size;
+            }
+        }
+    };
+    auto fetch = [&]() {
+        if (!looked) look();
+        if (looked) {
+            if (mine) {
+                const int page = entry;
                 const bool there = (unsigned)page < (unsigned)a.num_pages;
                 uint64_t* bar = &s.full[warp][st_in];
                 if (lane < 2) {
@@ -226,6 +241,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
             st_in = st_in + 1 == S ? 0 : st_in + 1;
             at_t += TILES;
             ++issued;
+            look();
         }
     };
 
