@@ -988,6 +988,8 @@ fa_status fa_qk_norm_rope(const fa_rope_params* in, const void* q, const void* k
     a.v_cache = reinterpret_cast<uint16_t*>(v_cache);
     a.slots = in->slots;
     a.num_slots = (long)in->num_slots;
+    a.dq_stride = wq;
+    a.dk_stride = wk;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
 }
@@ -1039,11 +1041,13 @@ fa_status fa_qk_norm_rope_append8(const fa_rope_params* in, const fa_cache8_para
     const Append8Args c{x.B, a.T, x.scale_block, x.page_size, x.max_blocks_per_seq, x.num_pages, x.cu_seqlens_q, x.seqused_k,
                         x.block_table, reinterpret_cast<uint8_t*>(k_cache), reinterpret_cast<uint8_t*>(v_cache), k_scale, v_scale};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (timed(kAppend8, st, [&] { return launch_append8(a, c, st); }) != cudaSuccess) return FA_ERR_CUDA;
-    a.k = a.v = nullptr;  // the queries
-    a.h_kv = 0;
-    a.after = x.B > 0;
-    return cuda_status(timed(kNormRope, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
+    RopeArgs b = a;  // the queries
+    b.k = b.v = nullptr;
+    b.h_kv = 0;
+    b.dq_stride = wq;
+    b.beside = x.B > 0;
+    if (timed(kNormRope, st, [&] { return launch_norm_rope(b, sm_count(), st); }) != cudaSuccess) return FA_ERR_CUDA;
+    return cuda_status(timed(kAppend8, st, [&] { return launch_append8(a, c, st); }));
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* in) {
@@ -1109,6 +1113,17 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* in, const void* q, const voi
     a.dwk = dk_weight;
     a.dw_part = reinterpret_cast<float*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (a.no_norm) {  // dx = dy turned back
+        if (a.T == 0) return FA_OK;
+        a.q = a.dq_out;
+        a.k = a.dk_out;
+        a.q_stride = wq;
+        a.k_stride = wk;
+        a.q_out = a.dq;
+        a.k_out = a.dk;
+        a.back = 1;
+        return cuda_status(timed(kNormRopeBwd, st, [&] { return launch_norm_rope(a, sm_count(), st); }));
+    }
     return cuda_status(timed(kNormRopeBwd, st, [&] { return launch_norm_rope_bwd(a, sm_count(), st); }));
 }
 

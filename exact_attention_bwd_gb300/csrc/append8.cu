@@ -13,7 +13,8 @@
 // block's keys are turned twice, the second time from rows that the L1 holds; its values are read
 // twice as well.  One CTA to a block and head, half of its warps on the keys and half on the values: what
 // a decode step costs is one chain of loads (lengths, table, row), and a chunk has as many CTAs as blocks
-// and heads.  The queries' rotation is the kernel of rope.cu, which runs beside this one.
+// and heads.  The queries' rotation is the kernel of rope.cu, launched ahead: a stream of one CTA to an SM that
+// leaves threads and latency to this one's chains beside it.
 #include "rope.cuh"
 
 namespace fa {
@@ -80,14 +81,12 @@ __device__ __forceinline__ void load_angles(const RopeArgs& a, const int* pos, i
 }
 
 template <int D, bool F16, bool ADJ>
-__global__ void __launch_bounds__(kThreads8) append8_kernel(const RopeArgs a, const Append8Args c) {
+__device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Args& c, float* amax_of) {
     using C = RowCfg<D>;
     constexpr int LANES = C::LANES, ROWS = C::ROWS;
-    __shared__ float amax_of[2 * kSideWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LANES, lr = lane / LANES;
     const bool on = li < C::PAIRS;
     const int side = warp / kSideWarps, w = warp % kSideWarps, head = blockIdx.y;  // side 0: keys, 1: values
-    allow_next_kernel();
     // ---- the block: rows [r0, r1) of page `page` are new, r1 - r0 tokens from t0 on ----
     int first;
     const int u = blockIdx.x, b = unit_sequence(c, u, first);
@@ -211,11 +210,16 @@ __global__ void __launch_bounds__(kThreads8) append8_kernel(const RopeArgs a, co
     }
 }
 
+template <int D, bool F16, bool ADJ>
+__global__ void __launch_bounds__(kThreads8) append8_kernel(const RopeArgs a, const Append8Args c) {
+    __shared__ float amax_of[2 * kSideWarps];
+    append8_block<D, F16, ADJ>(a, c, amax_of);
+    wait_previous_kernel();  // (what comes next in the stream waits for both)
+}
+
 template <int D, bool F16>
 cudaError_t launch_df(const RopeArgs& a, const Append8Args& c, const dim3& grid, cudaStream_t st) {
-    if (a.adjacent) append8_kernel<D, F16, true><<<grid, kThreads8, 0, st>>>(a, c);
-    else append8_kernel<D, F16, false><<<grid, kThreads8, 0, st>>>(a, c);
-    return cudaGetLastError();
+    return launch_after(a.adjacent ? append8_kernel<D, F16, true> : append8_kernel<D, F16, false>, grid, kThreads8, 0, st, a, c);
 }
 template <int D>
 cudaError_t launch_d(const RopeArgs& a, const Append8Args& c, const dim3& grid, cudaStream_t st) {

@@ -204,7 +204,8 @@ struct RopeArgs {
     unsigned long long wait_ns;  // bound on each wait
     int axes, no_norm;         // position axes (0 or 1: one, positions [T]; else [axes][T]), y = x turned
     uint8_t pair_axis[FA_ROPE_MAX_PAIRS];
-    int after;                 // the launch runs beside the kernel ahead of it and ends behind it
+    int beside;                // the next kernel of the stream may run beside this one (and ends behind it)
+    int back;                  // y = x turned by minus the angles (the gradient without the norm)
     int unit_rows, kv_rows, warps;  // rows a warp takes at a time (of k and v together), warps that walk over them
 };
 

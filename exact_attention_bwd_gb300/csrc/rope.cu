@@ -23,7 +23,8 @@
 // The EXT instantiations take several position axes and leave the norm out on demand.  A token's
 // angles are then no row of the tables: pair j's come from the row of its own axis's position, so
 // the warp gathers them, four bytes a lane, by asynchronous copies that arrive on the unit's barrier
-// like its rows.  Without the norm y is x turned, and dx is dy turned back: x is not read.
+// like its rows.  Without the norm y is x turned, and dx is dy turned back, which the forward kernel does as
+// well: x is not read.
 #include "rope.cuh"
 
 namespace fa {
@@ -52,14 +53,16 @@ struct WarpSmem {
     RowMeta meta[kBufs];
 };
 
-// The position of axis x of token t, or -1: padding, or outside the tables, which sets the status.
-// (`on`: lane x < axes has one; the others return 0.)
-__device__ __forceinline__ int position_of_axis(const RopeArgs& a, long t, int x, bool on) {
-    if (!on) return 0;
-    const int pos = a.positions ? a.positions[x * (long)a.T + t] : (int)((unsigned)t % (unsigned)a.seq_len);
-    if (pos >= 0 && pos < a.max_pos) return pos;
-    if (pos != -1 && a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
-    return -1;
+// The position of axis x of token t as it stands (lanes x < axes; `on`; 0 in the others), and, when it is
+// there, in every lane whether the token has a row of the tables on each axis: padding (-1 on some axis)
+// and positions outside the tables, which set the status, have none.
+__device__ __forceinline__ int axis_position(const RopeArgs& a, long t, int x, bool on) {
+    return !on ? 0 : a.positions ? a.positions[x * (long)a.T + t] : (int)((unsigned)t % (unsigned)a.seq_len);
+}
+__device__ __forceinline__ bool on_every_axis(const RopeArgs& a, int pos, bool on) {
+    const bool bad = on && (pos < 0 || pos >= a.max_pos);
+    if (bad && pos != -1 && a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
+    return !__any_sync(0xffffffffu, bad);
 }
 
 // The axes of the pairs lane, lane + 32, ... (a byte each).
@@ -149,12 +152,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     int next_pos = -1, next_slot = -1;  // of the unit `ahead` (lane 0; EXT: next_pos of axis `lane`)
     uint32_t flight = 0;                // buffers with copies on their way (lane 0)
     const uint32_t axes = EXT ? lane_axes(a, lane) : 0;
+    const bool has_axis = lane < max(a.axes, 1);
     auto look = [&]() {
         if constexpr (EXT) {
-            if (ahead.t < a.T) {
-                next_pos = position_of_axis(a, ahead.t, lane, lane < max(a.axes, 1));
-                if (__any_sync(0xffffffffu, next_pos < 0)) next_pos = -1;
-            }
+            if (ahead.t < a.T) next_pos = axis_position(a, ahead.t, lane, has_axis);
             if (lane == 0 && ahead.t < a.T && a.slots && ahead.x >= gq) {
                 next_slot = a.slots[ahead.t];
                 if (next_slot >= a.num_slots || next_slot < -1) {
@@ -177,7 +178,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     };
     // starts the copies of the unit `ahead` into buffer b and moves on
     auto issue = [&](int b) {
-        if (EXT && ahead.t < a.T && next_pos >= 0) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
+        if (EXT && ahead.t < a.T) {
+            if (on_every_axis(a, next_pos, has_axis)) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
+            else next_pos = -1;
+        }
         if (lane == 0 && ahead.t < a.T) {
             s.meta[b] = RowMeta{next_pos, next_slot};
             if (next_pos >= 0) {
@@ -206,6 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
     __syncwarp();
     look();
     for (int b = 0; b < kBufs; ++b) issue(b);
+    if (EXT && a.beside) allow_next_kernel();
     int u0, u1;
     lane_units<D, ADJ>(on ? li : 0, a.rot, u0, u1);
     float2 wq[8], wk[8];
@@ -217,11 +222,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         const RowMeta meta = s.meta[b];
         int kind, r0, rows;
         unit(now.x, kind, r0, rows);
-        uint16_t* out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
+        uint16_t* out0;
+        if constexpr (EXT)
+            out0 = kind == 0 ? a.q_out + now.t * a.dq_stride + (long)r0 * D : a.k_out ? a.k_out + now.t * a.dk_stride + (long)r0 * D : nullptr;
+        else out0 = kind == 0 ? a.q_out + (now.t * a.h_q + r0) * D : a.k_out ? a.k_out + (now.t * a.h_kv + r0) * D : nullptr;
         if (meta.pos >= 0) {
             if (!__all_sync(0xffffffffu, mbar_wait_within(&s.full[b], (phase >> b) & 1, a.wait_ns))) {
                 give_up(s, flight, phase, a.status);
-                if (EXT && a.after) wait_previous_kernel();
                 return;
             }
             phase ^= 1u << b;
@@ -236,6 +243,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
             if (out0 || out1) {
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
+                if (EXT && a.back) ang.turn_round();
                 // (two row batches at a time, so that one's sums and roots hide behind the other's)
 #pragma unroll 2
                 for (int r = lr; r < rows + lr; r += ROWS) {
@@ -279,8 +287,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_kernel(const RopeArg
         issue(b);
         __syncwarp();
     }
-    // (a launch beside the kernel ahead of it: what comes next in the stream waits for both)
-    if (EXT && a.after) wait_previous_kernel();
 }
 
 // Gradient: the same walk, over the query rows and then over the key rows, with dy beside x in
@@ -307,8 +313,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
     const unsigned n_warps = (unsigned)a.warps, me = blockIdx.x * kWarps + warp;
     uint32_t phase = 0, flight = 0;
     bool failed = false;
-    const bool norm = !EXT || !a.no_norm;  // without it a unit holds dy alone
     const uint32_t axes = EXT ? lane_axes(a, lane) : 0;
+    const bool has_axis = lane < max(a.axes, 1);
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         const int heads = kind ? a.h_kv : a.h_q;
@@ -325,25 +331,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
         int next_pos = -1;
         auto look = [&]() {
             if constexpr (EXT) {
-                if (ahead.t < a.T) {
-                    next_pos = position_of_axis(a, ahead.t, lane, lane < max(a.axes, 1));
-                    if (__any_sync(0xffffffffu, next_pos < 0)) next_pos = -1;
-                }
+                if (ahead.t < a.T) next_pos = axis_position(a, ahead.t, lane, has_axis);
             } else {
                 if (lane == 0 && ahead.t < a.T) next_pos = position_of(a, ahead.t);
             }
         };
         auto issue = [&](int b) {
-            if (EXT && ahead.t < a.T && next_pos >= 0) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
+            if (EXT && ahead.t < a.T) {
+                if (on_every_axis(a, next_pos, has_axis)) gather_angles(a, axes, next_pos, s.buf[b].cos, s.buf[b].sin, &s.full[b]);
+                else next_pos = -1;
+            }
             if (lane == 0 && ahead.t < a.T) {
                 s.meta[b] = RowMeta{next_pos, 0};
                 if (next_pos >= 0) {
                     const int r0 = ahead.x * a.unit_rows, rows = min(a.unit_rows, heads - r0);
                     const uint32_t bytes = (uint32_t)rows * D * 2, angle = EXT ? 0u : (uint32_t)a.rot * 2;
                     flight |= 1u << b;
-                    mbar_expect_tx(&s.full[b], (norm ? 2 : 1) * bytes + 2 * angle);
-                    if (norm) bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
-                    bulk_load(s.buf[b].rows + (norm ? kUnitBytes / 2 : 0), gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
+                    mbar_expect_tx(&s.full[b], 2 * bytes + 2 * angle);
+                    bulk_load(s.buf[b].rows, xs + ahead.t * xstride + (long)r0 * D, bytes, &s.full[b]);
+                    bulk_load(s.buf[b].rows + kUnitBytes / 2, gs + (ahead.t * heads + r0) * D, bytes, &s.full[b]);
                     if (angle) {
                         bulk_load(s.buf[b].cos, a.cos + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
                         bulk_load(s.buf[b].sin, a.sin + (long)next_pos * (a.rot / 2), angle, &s.full[b]);
@@ -369,21 +375,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
                 }
                 phase ^= 1u << b;
                 flight &= ~(1u << b);
-                const uint8_t *px = s.buf[b].rows, *pg = px + (norm ? kUnitBytes / 2 : 0);
+                const uint8_t *px = s.buf[b].rows, *pg = px + kUnitBytes / 2;
                 Angles<ADJ> ang;
                 ang.load(s.buf[b].cos, s.buf[b].sin, u0, u1, a.rot);
-                if (EXT && !norm) {
-#pragma unroll 2
-                    for (int r = lr; r < rows; r += ROWS) {
-                        if (!on) continue;
-                        float2 y[8];
-                        widen8<F16>(*reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u0), y);
-                        widen8<F16>(*reinterpret_cast<const uint4*>(pg + r * (D * 2) + 16 * u1), y + 4);
-                        ang.template turn<true, true>(y, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
-                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u0) = narrow8<F16>(y);
-                        *reinterpret_cast<uint4*>(pd + r * D + 8 * u1) = narrow8<F16>(y + 4);
-                    }
-                } else
 #pragma unroll 2
                 for (int r = lr; r < rows + lr; r += ROWS) {
                     const bool live = on && r < rows;
@@ -435,7 +429,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) norm_rope_bwd_kernel(const Rop
             issue(b);
             __syncwarp();
         }
-        if (EXT && !norm) continue;  // (no weights)
         // the warp's lanes with the same values, then the CTA's warps, in order (in the first buffer,
         // which no copy is under way into)
         float* part = reinterpret_cast<float*>(reinterpret_cast<WarpSmem<D>*>(smem_raw)[warp].buf[0].rows);
@@ -497,14 +490,12 @@ cudaError_t launch_fwd_dfae(const RopeArgs& a, int ctas, cudaStream_t st) {
     constexpr int smem = sizeof(WarpSmem<D>) * kWarps;
     cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<D, F16, ADJ, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    if constexpr (EXT)
-        if (a.after) return launch_after(norm_rope_kernel<D, F16, ADJ, EXT>, dim3(ctas), 32 * kWarps, smem, st, a);
     norm_rope_kernel<D, F16, ADJ, EXT><<<ctas, 32 * kWarps, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 // Whether a call takes the instantiations with several axes, without the norm, or beside another kernel.
-bool extended(const RopeArgs& a) { return a.axes > 1 || a.no_norm || a.after; }
+bool extended(const RopeArgs& a) { return a.axes > 1 || a.no_norm || a.beside || a.back; }
 
 template <int D, bool F16, bool ADJ>
 cudaError_t launch_fwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
@@ -529,7 +520,7 @@ cudaError_t launch_bwd_dfae(const RopeArgs& a, int ctas, cudaStream_t st) {
 template <int D, bool F16, bool ADJ>
 cudaError_t launch_bwd_dfa(const RopeArgs& a, int ctas, cudaStream_t st) {
     const cudaError_t e = extended(a) ? launch_bwd_dfae<D, F16, ADJ, true>(a, ctas, st) : launch_bwd_dfae<D, F16, ADJ, false>(a, ctas, st);
-    if (e != cudaSuccess || a.no_norm) return e;
+    if (e != cudaSuccess) return e;
     norm_rope_dw_kernel<<<2 * (D / 32), 1024, 0, st>>>(a, ctas);
     return cudaGetLastError();
 }
@@ -582,13 +573,13 @@ cudaError_t launch_norm_rope(const RopeArgs& args, int sms, cudaStream_t st) {
 }
 
 int norm_rope_bwd_ctas(const RopeArgs& a, int sms) {
-    const int rows = unit_rows_of(a.d, (long)a.T * a.h_q, !a.no_norm, sms);
+    const int rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
     return ctas_for((long)a.T * cdiv(a.h_q, rows), sms);
 }
 
 cudaError_t launch_norm_rope_bwd(const RopeArgs& args, int sms, cudaStream_t st) {
     RopeArgs a = args;
-    a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, !a.no_norm, sms);
+    a.unit_rows = unit_rows_of(a.d, (long)a.T * a.h_q, true, sms);
     const int ctas = norm_rope_bwd_ctas(a, sms);
     a.warps = ctas * kWarps;
     switch (a.d) {

@@ -58,6 +58,11 @@ struct Angles {
             }
         }
     }
+    // The angles of the inverse.
+    __device__ __forceinline__ void turn_round() {
+#pragma unroll
+        for (int e = 0; e < (ADJ ? 8 : 4); ++e) s[e] = make_float2(-s[e].x, -s[e].y);
+    }
     // Turns the lane's 16 values (unit 0 in v[0..3], unit 1 in v[4..7]); BACK: by minus the angle.  Values
     // behind the rotated part are turned by the angle 0, or with STRICT left alone (an infinity
     // times sin 0 would be NaN in its neighbour): unit 0 is rotated if r0, unit 1 if r1.
