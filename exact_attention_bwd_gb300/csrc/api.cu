@@ -1039,7 +1039,8 @@ fa_status fa_qk_norm_rope_append8(const fa_rope_params* in, const fa_cache8_para
     a.v_stride = (long)in->v_stride;
     a.q_out = reinterpret_cast<uint16_t*>(q_out);
     const Append8Args c{x.B, a.T, x.scale_block, x.page_size, x.max_blocks_per_seq, x.num_pages, x.cu_seqlens_q, x.seqused_k,
-                        x.block_table, reinterpret_cast<uint8_t*>(k_cache), reinterpret_cast<uint8_t*>(v_cache), k_scale, v_scale};
+                        x.block_table, reinterpret_cast<uint8_t*>(k_cache), reinterpret_cast<uint8_t*>(v_cache), k_scale, v_scale,
+                        divisor((uint32_t)x.scale_block), divisor((uint32_t)x.page_size)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     RopeArgs b = a;  // the queries
     b.k = b.v = nullptr;

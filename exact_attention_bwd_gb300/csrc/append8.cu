@@ -9,9 +9,8 @@
 // an older one again only where it falls below e4m3's normal range (scales of another kind that the
 // caller put there are kept while they suffice).
 //
-// x is rotated in fp32 and its block's maximum is known only behind the last of its rows, so a
-// block's keys are turned twice, the second time from rows that the L1 holds; its values are read
-// twice as well.  One CTA to a block and head, half of its warps on the keys and half on the values: what
+// x is rotated in fp32 and its block's maximum is known only behind the last of its rows, so a warp keeps
+// its first kKeep batches of rows in registers; what larger blocks have beyond is read, and turned, a second time.  One CTA to a block and head, half of its warps on the keys and half on the values: what
 // a decode step costs is one chain of loads (lengths, table, row), and a chunk has as many CTAs as blocks
 // and heads.  The queries' rotation is the kernel of rope.cu, launched ahead: a stream of one CTA to an SM that
 // leaves threads and latency to this one's chains beside it.
@@ -22,13 +21,14 @@ namespace {
 
 constexpr int kSideWarps = 4;  // warps on a block's keys, and on its values
 constexpr int kThreads8 = 2 * 32 * kSideWarps;
+constexpr int kKeep = 2;
 
 // The sequence of unit u, and the unit's number in it: sequence b has the units from cu[b] / block + 2 b
 // on, of which those behind its last block are idle (n tokens touch n / block + 2 blocks at most, and
 // each sequence has as many units).  Warp-wide.
 __device__ __forceinline__ int unit_sequence(const Append8Args& a, int u, int& first) {
     const int lane = threadIdx.x & 31;
-    auto start = [&](int b) { return min(max(a.cu[b], 0), a.T) / a.block + 2 * b; };
+    auto start = [&](int b) { return quotient(min(max(a.cu[b], 0), a.T), a.by_block) + 2 * b; };
     int lo = 0, hi = a.B - 1;
 #pragma unroll 1
     while (hi > lo) {
@@ -51,8 +51,13 @@ __device__ __forceinline__ float block_scale(float amax) {
 template <bool ADJ>
 __device__ __forceinline__ void load_angles(const RopeArgs& a, const int* pos, int u0, int u1, Angles<ADJ>& ang) {
     const int half = a.rot / 2;
+    if (a.axes <= 1) {  // a row of the tables
+        const long row = (long)pos[0] * half;
+        ang.load(a.cos + row, a.sin + row, u0, u1, a.rot);
+        return;
+    }
     auto at = [&](int j, float& c, float& s) {
-        const int x = a.axes > 1 ? a.pair_axis[j] : 0;
+        const int x = a.pair_axis[j];
         const int p = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
         c = a.cos[(long)p * half + j];
         s = a.sin[(long)p * half + j];
@@ -95,20 +100,20 @@ __device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Ar
     const int limit = c.max_blocks * c.page_size, from = max(start, 0), to = min(total, limit);
     if (n > 0 && (start < 0 || total > limit) && u == first && threadIdx.x == 0 && head == 0 && a.status)
         atomicCAS(a.status, 0, kStatusDeviceCheck);
-    const long at_block = (long)(from / c.block) + (u - first);
+    const long at_block = (long)quotient(from, c.by_block) + (u - first);
     if (n <= 0 || at_block * c.block >= to) return;
     const int place = (int)at_block * c.block;  // of the block's first row
-    const int page = c.table[(long)b * c.max_blocks + place / c.page_size];
+    const int nth = quotient(place, c.by_page), page = c.table[(long)b * c.max_blocks + nth];
     if ((unsigned)page >= (unsigned)c.num_pages) {
         if (threadIdx.x == 0 && head == 0 && a.status) atomicCAS(a.status, 0, kStatusDeviceCheck);
         return;
     }
-    const int in_page = place % c.page_size;
+    const int in_page = place - nth * c.page_size;
     const int r0 = max(from - place, 0), r1 = min(to - place, c.block);  // new rows of the block
     const int t0 = q0 + place - start;                                    // the token of the block's row 0
     uint8_t* rows8 = (side ? c.v_cache : c.k_cache) + (((long)page * c.page_size + in_page) * a.h_kv + head) * D;
     const long row_step = (long)a.h_kv * D;
-    float* scale_at = (side ? c.v_scale : c.k_scale) + ((long)page * (c.page_size / c.block) + in_page / c.block) * a.h_kv + head;
+    float* scale_at = (side ? c.v_scale : c.k_scale) + ((long)page * quotient(c.page_size, c.by_block) + quotient(in_page, c.by_block)) * a.h_kv + head;
     const uint16_t* src = (side ? a.v : a.k) + (long)head * D;
     const long src_step = side ? a.v_stride : a.k_stride;
     int u0, u1;
@@ -139,37 +144,62 @@ __device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Ar
         widen8<F16>(x0, v);
         widen8<F16>(x1, v + 4);
         if (side == 0) {
-            float2 ss = __fmul2_rn(v[0], v[0]);
+            float rs = 1.f;
+            if (!a.no_norm) {
+                float2 ss = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-            for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
-            const float rs = a.no_norm ? 1.f : rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
-            if (there) {
-                Angles<ADJ> ang;
-                load_angles<ADJ>(a, pos, u0, u1, ang);
+                for (int e = 1; e < 8; ++e) ss = __ffma2_rn(v[e], v[e], ss);
+                rs = rsqrtf(row_sum<LANES>(ss.x + ss.y) * (1.f / D) + a.eps);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], weight[e]);
-                ang.template turn<false, true>(v, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
-                const float2 rs2 = make_float2(rs, rs);
+            }
+            if (there) {
+                if ((ADJ ? 8 : 16) * u0 < a.rot || (ADJ && 8 * u1 < a.rot)) {
+                    Angles<ADJ> ang;
+                    load_angles<ADJ>(a, pos, u0, u1, ang);
+                    ang.template turn<false, true>(v, (ADJ ? 8 : 16) * u0 < a.rot, 8 * u1 < a.rot);
+                }
+                if (!a.no_norm) {
+                    const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], rs2);
+                    for (int e = 0; e < 8; ++e) v[e] = __fmul2_rn(v[e], rs2);
+                }
             }
         }
         return there;
     };
-    // ---- the largest finite value (infinities are stored as the block's largest, NaN as NaN) ----
+    // ---- the largest finite value (infinities are stored as the block's largest, NaN, which a maximum passes over, as NaN) ----
     float amax = -1.f;  // (no row)
-#pragma unroll 1
-    for (int r = r0 + w * ROWS + lr; r < r1 + lr; r += kSideWarps * ROWS) {
-        float2 v[8];
-        if (row_of(r, v) && on) {
-            amax = fmaxf(amax, 0.f);
+    auto most_of = [&](bool there, const float2* v) {
+        if (there && on) {
+            float top = 0.f, x[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = fabsf(v[e].x), y = fabsf(v[e].y);
-                if (x < INFINITY) amax = fmaxf(amax, x);
-                if (y < INFINITY) amax = fmaxf(amax, y);
+            for (int e = 0; e < 16; ++e) x[e] = fabsf(e & 1 ? v[e / 2].y : v[e / 2].x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e]);
+            if (top == INFINITY) {
+                top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (x[e] < INFINITY) top = fmaxf(top, x[e]);
             }
+            amax = fmaxf(amax, top);
         }
+    };
+    constexpr int STEP = kSideWarps * ROWS;
+    const int mine = r0 + w * ROWS + lr;  // the lane's first row
+    float2 kept[kKeep][8];
+    bool there[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        there[k] = mine - lr + k * STEP < r1 && row_of(mine + k * STEP, kept[k]);
+        most_of(there[k], kept[k]);
+    }
+#pragma unroll 1
+    for (int r = mine + kKeep * STEP; r < r1 + lr; r += STEP) {
+        float2 v[8];
+        const bool y = row_of(r, v);
+        most_of(y, v);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -194,19 +224,23 @@ __device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Ar
         }
     }
     // ---- the new rows ----
-#pragma unroll 1
-    for (int r = r0 + w * ROWS + lr; r < r1 + lr; r += kSideWarps * ROWS) {
-        float2 v[8];
-        if (row_of(r, v) && on) {
-            uint8_t* out = rows8 + r * row_step;
+    auto store = [&](int r, const float2* v) {
+        uint8_t* out = rows8 + r * row_step;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float2* x = v + 4 * h;
-                *reinterpret_cast<uint2*>(out + 8 * (h ? u1 : u0)) =
-                    make_uint2(pack_e4m3x4(x[0].x * inv, x[0].y * inv, x[1].x * inv, x[1].y * inv),
-                               pack_e4m3x4(x[2].x * inv, x[2].y * inv, x[3].x * inv, x[3].y * inv));
-            }
+        for (int h = 0; h < 2; ++h) {
+            const float2* x = v + 4 * h;
+            *reinterpret_cast<uint2*>(out + 8 * (h ? u1 : u0)) =
+                make_uint2(pack_e4m3x4(x[0].x * inv, x[0].y * inv, x[1].x * inv, x[1].y * inv),
+                           pack_e4m3x4(x[2].x * inv, x[2].y * inv, x[3].x * inv, x[3].y * inv));
         }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+        if (there[k] && on) store(mine + k * STEP, kept[k]);
+#pragma unroll 1
+    for (int r = mine + kKeep * STEP; r < r1 + lr; r += STEP) {
+        float2 v[8];
+        if (row_of(r, v) && on) store(r, v);
     }
 }
 

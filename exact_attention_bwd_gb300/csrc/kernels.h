@@ -32,9 +32,6 @@ struct Problem {
     unsigned long long wait_ns;  // bound on each pipeline wait (ns) before a CTA gives up
 };
 
-// ------------------------------------------------------------------------------------------
-// forward (tensor-core path)
-// ------------------------------------------------------------------------------------------
 // Division of n in [0, 2^31) by a whole number d >= 2: with s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1
 // (32 bits, for d > 2^(s-1)), n m 2^-(31+s) exceeds n / d by less than 2^-s <= 1 / d.
 struct Divisor {
@@ -50,6 +47,9 @@ inline Divisor divisor(uint32_t d) {
 __device__ __forceinline__ int quotient(int n, const Divisor& d) { return (int)(__umulhi((uint32_t)n, d.m) >> d.s); }
 #endif
 
+// ------------------------------------------------------------------------------------------
+// forward (tensor-core path)
+// ------------------------------------------------------------------------------------------
 // The 8-bit cache: pools of e4m3 bytes, scales [num_pages, blocks, h_kv] of `block` rows each.
 struct Cache8 {
     const uint8_t *k, *v;
@@ -215,6 +215,7 @@ struct Append8Args {
     const int32_t *cu, *used, *table;
     uint8_t *k_cache, *v_cache;  // [num_pages, page_size, h_kv, d]
     float *k_scale, *v_scale;    // [num_pages, page_size / block, h_kv]
+    Divisor by_block, by_page;
 };
 
 struct PagePlanArgs {
