@@ -39,10 +39,10 @@ constexpr float kTop = 512.f;                 // P and P vs u stay below
 template <int D, int NT>
 struct Few8Cfg {
     static constexpr int NR = 8 * NT;
-    static constexpr int TILES = NT == 1 && D <= 128 ? 2 : 1;  // tiles side by side
+    static constexpr int TILES = NT == 1 && D == 128 ? 2 : 1;  // tiles side by side
     static constexpr int WARPS = kGroups8 * TILES, THREADS = 32 * WARPS;
     static constexpr int GROUP_BYTES = kGroup * D;  // K (or V) rows of a warp's group
-    static constexpr int STAGES = D == 64 ? 8 / TILES : D == 128 ? (TILES == 2 ? 2 : 5) : D == 192 ? 4 : 3;
+    static constexpr int STAGES = D == 64 ? 8 : D == 128 ? (TILES == 2 ? 2 : 5) : D == 192 ? 4 : 3;
     static constexpr int BOX = D % 128 ? 64 : 128, BOXES = D / BOX;  // bytes of a copy's rows (swizzled in as many), copies
     static constexpr int MT = D / 16;               // 16-row tiles of O^T
     static constexpr int MERGE = D <= 128 ? D : NT == 2 ? 32 : 64;  // columns that the warps join at a time
