@@ -90,4 +90,4 @@ def check_append(name, before, after, rows, slack, stored, cu, used, table):
             assert np.all(err <= np.where(f == 1, 0, np.maximum(2.0 ** -4 * np.abs(was * f), 2.0 ** -10) * (1 + 2.0 ** -20))), name
             seen8[page, first:first + lo] = True
     assert np.array_equal(b8[~seen8], a8[~seen8]), f"{name}: rows that the call has not to touch"
-    assert np.array_equal(bs[~seens], as_[~seens]), f"{name}: scales that the call has not to touch"
+    assert np.array_equal(bs[~seens], as_[~seens], equal_nan=True), f"{name}: scales that the call has not to touch"
