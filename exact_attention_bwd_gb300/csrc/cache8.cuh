@@ -100,35 +100,45 @@ struct Ring8 {
     }
     // Rows 16 w and on of the next unit, keys j0 + 16 w and on, to rows of a tile (zeros outside the keys [lo, hi] that
     // any query sees: what lies there may be anything).  A lane turns 16 bytes into two 16-byte units, four times over
-    // with their loads ahead; every other group of four chunks takes its second half first, so that the
-    // stores of a phase fall into different banks.
+    // with their loads ahead; every other group of four chunks takes its second half first (swap_of), so that the
+    // stores of a phase, and the loads where a row is a power of two, fall into different banks.  What no query sees
+    // is cleared as bytes, in a branch of its own: conversions share the issue slots with the softmax, and a second copy
+    // of them for edges costs more in instruction fetches than it saves (8 chunks of 1024 tokens at d = 128 793 to 814 us, 885
+    // with it; 32 x 5 tokens at d = 256 72, 77 with outputs selected, 80 two chunks at a time and 92 eight).
     template <bool F16>
     __device__ __forceinline__ bool widen(uint32_t& n, int w, uint8_t* tile, int chunk_bytes, int j0, int lo, int hi, const Abort& ab) {
         constexpr int ALL = CPR / 2, BATCH = ALL % 4 == 0 ? 4 : ALL < 4 ? ALL : 3;  // chunks of a lane
         const int lane = threadIdx.x & 31, st = n % UNITS;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / UNITS) & 1, ab))) return false;
-        const float f = scale[st][w];
+        // (a group that no query sees may have any scale)
+        const float f = j0 + 16 * w <= hi && j0 + 16 * w + 15 >= lo ? scale[st][w] : 0.f;
         const uint8_t* from = &rows[st][16 * w * D];
         const bool inside = j0 + 16 * w >= lo && j0 + 16 * w + 15 <= hi;
+        auto swap_of = [](int x) { return (D == 64 ? x >> 3 : D == 192 ? (x % CPR) >> 2 : (x >> 2) ^ (x >> 3)) & 1; };
 #pragma unroll 1
         for (int y0 = 0; y0 < ALL; y0 += BATCH) {
             uint2 b[BATCH][2];
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
-                const int x = lane + 32 * (y0 + y), swap = ((x % CPR) >> 2) & 1;
+                const int x = lane + 32 * (y0 + y), swap = swap_of(x);
                 b[y][0] = *reinterpret_cast<const uint2*>(from + 16 * x + 8 * swap);
                 b[y][1] = *reinterpret_cast<const uint2*>(from + 16 * x + 8 - 8 * swap);
             }
+            if (!inside) {
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                    const int j = j0 + 16 * w + (lane + 32 * (y0 + y)) / CPR;
+                    if (j < lo || j > hi) b[y][0] = b[y][1] = make_uint2(0, 0);
+                }
+            }
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
-                const int x = lane + 32 * (y0 + y), r = 16 * w + x / CPR, c = x % CPR, u = 2 * (c & 3), swap = (c >> 2) & 1;
+                const int x = lane + 32 * (y0 + y), r = 16 * w + x / CPR, c = x % CPR, u = 2 * (c & 3), swap = swap_of(x);
                 uint8_t* to = tile + (c >> 2) * chunk_bytes + r * 128;
-                const bool seen = inside || (j0 + r >= lo && j0 + r <= hi);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint4 o = make_uint4(scaled_e4m3x2<F16, false>(b[y][h].x, f), scaled_e4m3x2<F16, true>(b[y][h].x, f),
                                          scaled_e4m3x2<F16, false>(b[y][h].y, f), scaled_e4m3x2<F16, true>(b[y][h].y, f));
-                    if (!seen) o = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(to + (((u + (swap ^ h)) ^ (r & 7)) << 4)) = o;
                 }
             }
