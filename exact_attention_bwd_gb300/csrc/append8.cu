@@ -10,10 +10,15 @@
 // caller put there are kept while they suffice).
 //
 // x is rotated in fp32 and its block's maximum is known only behind the last of its rows, so a warp keeps
-// its first kKeep batches of rows in registers; what larger blocks have beyond is read, and turned, a second time.  One CTA to a block and head, half of its warps on the keys and half on the values: what
+// its first kKeep batches of rows in registers; what larger blocks have beyond is read, and turned, a second time.
+// One CTA to a block and head, half of its warps on the keys and half on the values: what
 // a decode step costs is one chain of loads (lengths, table, row), and a chunk has as many CTAs as blocks
-// and heads.  The queries' rotation is the kernel of rope.cu, launched ahead: a stream of one CTA to an SM that
-// leaves threads and latency to this one's chains beside it.
+// and heads.  The queries' rotation is the kernel of rope.cu, launched ahead; this one's CTAs start where that one's
+// leave registers, most of them behind it.
+//
+// Measured, 8192 tokens in chunks, 16 / 2 heads of 256, blocks of 64 rows: 43 us with the queries' rotation (24 at
+// the copy rate), 18 of them this kernel.  It is bound by its chains (issue slots 44 %, DRAM 10 %).  One batch kept 45.9,
+// four 57.8 (registers).  A decode step of 32 tokens: 14 us on the device.
 #include "rope.cuh"
 
 namespace fa {

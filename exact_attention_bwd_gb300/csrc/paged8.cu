@@ -9,8 +9,8 @@
 // is rounded to fp16 (2^-11, where the 16-bit cache's kernels round P to the inputs' type).
 //
 // A decode step reads each byte of the cache once and does little with it: what counts is that the
-// bytes keep coming.  Each warp streams its own 16 keys of every 128-key tile through a private ring
-// of asynchronous copies and keeps its own online softmax, so the warps wait for each other only where
+// bytes keep coming.  Each warp streams its own 16 keys of every 128-key tile by TMA copies through a private ring
+// and keeps its own online softmax, so the warps wait for each other only where
 // an item ends and their states are joined.  With the cache on the long side of the products
 // (mma.sync, S^T = K Q^T: 16 keys x 8 rows, O^T = V^T P^T: 16 of d x 8 rows) a tile of 8 rows wastes
 // nothing; converted to fp16 in registers, a byte passes shared memory once, where the
@@ -18,12 +18,17 @@
 // traffic for each of the cache's, more than the memory's rate leaves.
 //
 // The contraction's order is free, so the fragments need no transposition on the way from shared memory: a lane
-// takes 16 consecutive bytes of a key's row for four k-steps of S^T, and for O^T 2, 4 or 8
+// takes 16 consecutive bytes of a key's row for four k-steps of S^T, and for O^T d / 8
 // consecutive columns' bytes of its four keys, which byte permutes pair up.
 //
 // Rounding: per row a running reference m of the scores (moved where some score passes it by 2^9) and a
 // power of two u with P' = P vs u <= 2^9, so that neither blocks of tiny nor of huge values leave fp16's range:
 // what a row's product loses is relative to its own largest term.
+//
+// Measured, decode of 64 requests over 2k to 32k keys, 32 / 8 heads of 128 (1.3 GB, 195 us at the copy rate): 227 to 235 us,
+// 5.6 to 5.8 TB/s.  Bound by the memory's path and the ends of items; the arithmetic issues in half of the cycles.
+// One warp to a group of keys (8 warps) with 16-byte asynchronous copies 302, two tiles side by side (16 warps) 262,
+// their bytes by TMA 256, the table's entry asked for a tile ahead and a lead of 6 units for an item 235.
 #include "cache8.cuh"
 #include "paged.cuh"
 
@@ -39,7 +44,9 @@ constexpr float kTop = 512.f;                 // P and P vs u stay below
 template <int D, int NT>
 struct Few8Cfg {
     static constexpr int NR = 8 * NT;
-    static constexpr int TILES = NT == 1 && D == 128 ? 2 : 1;  // tiles side by side
+    // tiles side by side (d = 128: above; at d = 64 a mixed batch of short items takes 82 us with two, 76 with one, and
+    // beyond that registers or shared memory do not hold 16 warps' states)
+    static constexpr int TILES = NT == 1 && D == 128 ? 2 : 1;
     static constexpr int WARPS = kGroups8 * TILES, THREADS = 32 * WARPS;
     static constexpr int GROUP_BYTES = kGroup * D;  // K (or V) rows of a warp's group
     static constexpr int STAGES = D == 64 ? 8 : D == 128 ? (TILES == 2 ? 2 : 5) : D == 192 ? 4 : 3;
@@ -74,7 +81,7 @@ struct __align__(1024) Few8Smem {
     float f[C::NR];                  // factor of a whole item's output
     Piece8 piece[kPieces];
     int pieces[2];                   // found so far, as of each second meeting
-    PagedWalkFew8 walk[32];             // the last warp's walk over the CTA's stretch: a lane's state each
+    PagedWalkFew8 walk[32];          // the last warp's walk over the CTA's stretch: a lane's state each
 };
 
 // Where chunk `col` of row `row` of a group lies: boxes of 16 rows, 64- or 128-byte swizzled.

@@ -24,7 +24,8 @@
 // angles are then no row of the tables: pair j's come from the row of its own axis's position, so
 // the warp gathers them, four bytes a lane, by asynchronous copies that arrive on the unit's barrier
 // like its rows.  Without the norm y is x turned, and dx is dy turned back, which the forward kernel does as
-// well: x is not read.
+// well: x is not read.  (16384 tokens, 32 / 8 heads of 128, three axes: with the norm 60.6 us, gradient without it
+// 59.7, 50.3 at the copy rate; angles gathered without their positions asked for a unit ahead 64.2 / 64.0.)
 #include "rope.cuh"
 
 namespace fa {

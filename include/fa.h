@@ -108,8 +108,9 @@
  *    output's, bf16 or fp16; every head dimension): k and v are pools of e4m3 bytes and the true keys and
  *    values are byte * scale, with one scale for scale_block rows of a page and a head: k_scale,
  *    v_scale [num_pages, page_size / scale_block, h_kv] (fp32, not negative).  scale_block is a positive multiple
- *    of 16 that divides page_size.  fa_qk_norm_rope_append8 fills such a cache.  All else is as above;
- *    bytes and scales of rows behind a sequence's used keys have no effect.
+ *    of 16 that divides page_size, the scales are finite.  fa_qk_norm_rope_append8 fills such a cache.  All else is
+ *    as above; bytes of rows behind a sequence's used keys, and scales of blocks behind them, have no effect.  (A NaN among
+ *    the bytes of a value that some query of a sequence sees may reach outputs of that sequence's other queries.)
  *
  * FP8 forward (vllm-project/flash-attention README, "FlashAttention-3 beta release":
  * "FP8 forward"): with dtype = FA_DTYPE_E4M3, q, k and v hold e4m3 bytes (1 byte per
@@ -253,7 +254,8 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * axis's position, pos = positions[pair_axis[j]][t].  The axes share the tables.  A token with -1 on
  * some axis is padding; one with another position outside [0, max_pos) on some axis sets *status.
  * Without the norm (no_norm; the weights must be NULL): y = x.  The gradient then reads neither q nor k,
- * which may be NULL, and has no weights' gradients (dq_weight and dk_weight must be NULL).
+ * which may be NULL, and has no weights' gradients (dq_weight and dk_weight must be NULL); the workspace is
+ * given all the same.
  * A wait that passes wait_limit_ns ends the call's work early and sets *status to FA_ERR_TIMEOUT
  * (the outputs are then unspecified); without a status word the caller does not learn of it.
  * bf16 and fp16; d in {64, 128, 192, 256}; rot_dim a multiple of 16 up to d; strides multiples
@@ -355,7 +357,8 @@ const char *fa_status_string(fa_status s);
 /* Per-kernel timing: when enabled, every launch the library makes is bracketed by
  * CUDA events on its stream.  fa_profile_read synchronises on the last launch of
  * the named kernel ("fwd", "decode", "combine", "bwd_pre", "bwd_main", "bwd_post",
- * "paged_prep", "paged_few", "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan")
+ * "paged_prep", "paged_few", "paged_merge", "norm_rope", "norm_rope_bwd", "page_plan",
+ * "append8")
  * and writes its duration in milliseconds; returns FA_ERR_INVALID_ARG for an
  * unknown name or a kernel not launched since profiling was enabled. */
 fa_status fa_profile_enable(int on);
