@@ -52,14 +52,15 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w) {
 }
 
 // Two e4m3 bytes times a scale, in the 16-bit type.  (fp16: kept within its range, so that a finite
-// value does not become infinite where the scale was rounded up.)
+// value does not become infinite where the scale was rounded up; NaN stays NaN.)
 template <bool F16, bool HI>
 __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t w, float scale) {
     const uint32_t h = widen_e4m3x2<HI>(w);
-    float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(scale, scale));
+    const float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(scale, scale));
     if constexpr (F16) {
-        x.x = x.x > 65504.f ? 65504.f : x.x < -65504.f ? -65504.f : x.x;  // (NaN stays)
-        x.y = x.y > 65504.f ? 65504.f : x.y < -65504.f ? -65504.f : x.y;
+        uint32_t r;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+        return r;
     }
     return pack16<F16>(x.x, x.y);
 }

@@ -195,6 +195,31 @@ def test_what_lies_behind_the_used_keys(d, chunk):
     assert np.array_equal(from_dev(first[0]), from_dev(again[0])) and np.array_equal(first[1].cpu().numpy(), again[1].cpu().numpy())
 
 
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+def test_chunks_of_fp16_beyond_its_largest_value(d):
+    """A byte times its scale that fp16 rounds to infinity becomes fp16's largest value in the 16-bit tiles of a chunk (a scale that is a
+    power of two lies up to twice above what its block needs), and NaN stays NaN.  Each query sees one key, so P is 1
+    but for the rounding of its exponent, 65504 (1 + 2^-20) rounds to 65504, and what is NaN is known."""
+    n, sign = 200, np.where(np.arange(d) % 3 == 0, -1.0, 1.0)
+    c = case([n], [n], h_q=4, h_kv=2, d=d, page=32, kind="f16")
+    page, row = c["table"][0, np.arange(n) // 32], np.arange(n) % 32
+    pool, scale = c["v"]
+    pool[...] = np.where(sign < 0, 0xF8, 0x78)  # 256
+    scale[...] = 256.0
+    c["k"][0][page[130], row[130], 0, 5] = 0x7F
+    pool[page[70], row[70], 1, 7] = 0xFF
+    o, z, status = gpu(c, window=(0, 0))
+    out = from_dev(o)
+    assert status == 0
+    assert np.isnan(out[130, :2]).all() and np.isnan(out[70, 2:, 7]).all()
+    out[130, :2] = out[70, 2:, 7] = np.nan
+    near = np.isnan(out)  # (a value's NaN may reach the same sequence's other queries, at its head and column)
+    near[130, :2] = near[:, 2:, 7] = False
+    assert not near.any()
+    want = np.broadcast_to(65504.0 * sign, out.shape)
+    assert np.array_equal(np.where(np.isnan(out), want, out), want)
+
+
 def test_large_and_small_queries():
     """Rows of queries from 2^-40 to 2^60 (bf16), zeros among them: they are brought into fp16's range by their own power."""
     from exact_attention_bwd_gb300 import inputs
