@@ -592,7 +592,7 @@ def _set_axes(p, positions, pair_axis, norm):
         pairs = bytes(pair_axis)
     except (TypeError, ValueError):
         pairs = b"\xff"
-    if pairs and max(pairs) >= axes:
+    if pairs.translate(None, b"\0\1\2\3"[:axes]):  # (what is left when the axes are taken out)
         raise ValueError(f"pair_axis must hold axes (0 to {axes - 1})")
     ctypes.memmove(p.pair_axis, pairs, len(pairs))
 
@@ -628,10 +628,10 @@ def _rope_params(dev, q, k, q_weight, k_weight, cos, sin, positions, seq_len, ep
     if seq_len is None:
         seq_len = max(1, q.shape[1] if q.dim() == 4 else T)
     p = FaRopeParams(T, h_q, h_kv, d, 2 * half, 1 if interleaved else 0, seq_len, max_pos, eps, code, 1 if wtype is not kind else 0,
-                        q_stride, k_stride, h_kv * d, h_q * d, h_kv * d, None if positions is None else positions.data_ptr(),
-                        None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
-                        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-                        None, 0, None if status is None else status.data_ptr())
+                     q_stride, k_stride, h_kv * d, h_q * d, h_kv * d, None if positions is None else positions.data_ptr(),
+                     None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
+                     None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                     None, 0, None if status is None else status.data_ptr())
     if not norm or pair_axis is not None:
         _set_axes(p, positions, pair_axis, norm)
     return p

@@ -89,13 +89,14 @@ struct FwdCfg {
     // registers per thread after setmaxnreg: producer / MMA / TMEM owner / scheduler group,
     // and the two softmax groups; 128 REG_LOW + 256 REG_HIGH stays within what the CTA is
     // launched with (checked before every launch)
-    // (C8: 128 x 80 for the converting warps as well, 65536 in all.  8 chunks of 1024 tokens with 208 / 48, 200 / 64,
-    // 192 / 80 and 184 / 88 registers for softmax and conversion: 982 / 893 / 829 / 838 us; eight converting warps
-    // at 168 / 48: 887.  O follows a moved reference behind P, when the scores are out of the registers.)
+    // (C8: 128 REG_CONV for the converting warps as well, 65536 in all.  8 chunks of 1024 tokens at d = 128 with 200 / 64,
+    // 192 / 80, 184 / 96 and 176 / 112 registers for softmax and conversion: 864 / 806 / 790 / 806 us, a mixed batch
+    // at d = 64 71.7 / 72 / 73.5 / 72.5; eight converting warps at 168 / 48 cost 7 % more than four.  O follows a moved
+    // reference behind P, when the scores are out of the registers.)
     static constexpr int REG_LOW = KT == 128 && !C8 ? 56 : 48;
-    static constexpr int REG_HIGH = C8 ? 192 : KT == 128 ? 224 : 96;
-    static constexpr int REG_CONV = 80;
-    // C8: half tiles of bytes under way (d = 128: three 864 us, four 829)
+    static constexpr int REG_HIGH = C8 ? (D == 128 ? 184 : 192) : KT == 128 ? 224 : 96;
+    static constexpr int REG_CONV = D == 128 ? 96 : 80;
+    // C8: half tiles of bytes under way (d = 128: three cost 4 % more than four)
     static constexpr int UNITS8 = D == 64 ? 6 : 4;
 };
 
