@@ -28,9 +28,10 @@ constexpr int kSideWarps = 4;  // warps on a block's keys, and on its values
 constexpr int kThreads8 = 2 * 32 * kSideWarps;
 constexpr int kKeep = 2;
 
-// The sequence of unit u, and the unit's number in it: sequence b has the units from cu[b] / block + 2 b
+// The sequence of unit u and its first unit: sequence b has the units from cu[b] / block + 2 b
 // on, of which those behind its last block are idle (n tokens touch n / block + 2 blocks at most, and
-// each sequence has as many units).  Warp-wide.
+// each sequence has as many units).  Units ahead of all sequences' (rows of no sequence come first) are given
+// to sequence 0 with first > u, and are idle too; offsets that decrease can do the same.  Warp-wide.
 __device__ __forceinline__ int unit_sequence(const Append8Args& a, int u, int& first) {
     const int lane = threadIdx.x & 31;
     auto start = [&](int b) { return quotient(min(max(a.cu[b], 0), a.T), a.by_block) + 2 * b; };
@@ -100,6 +101,7 @@ __device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Ar
     // ---- the block: rows [r0, r1) of page `page` are new, r1 - r0 tokens from t0 on ----
     int first;
     const int u = blockIdx.x, b = unit_sequence(c, u, first);
+    if (u < first) return;
     const int q0 = min(max(c.cu[b], 0), c.T), n = min(max(c.cu[b + 1], q0), c.T) - q0;
     const int total = c.used[b], start = total - n;  // places [start, total) in the sequence
     const int limit = c.max_blocks * c.page_size, from = max(start, 0), to = min(total, limit);
@@ -253,6 +255,11 @@ template <int D, bool F16, bool ADJ>
 __global__ void __launch_bounds__(kThreads8) append8_kernel(const RopeArgs a, const Append8Args c) {
     __shared__ float amax_of[2 * kSideWarps];
     append8_block<D, F16, ADJ>(a, c, amax_of);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && a.status) {  // (where offsets decrease the search may miss a sequence)
+        bool bad = false;
+        for (int b = threadIdx.x; b < c.B; b += kThreads8) bad |= min(max(c.cu[b + 1], 0), c.T) < min(max(c.cu[b], 0), c.T);
+        if (bad) atomicCAS(a.status, 0, kStatusDeviceCheck);
+    }
     wait_previous_kernel();  // (what comes next in the stream waits for both)
 }
 

@@ -296,7 +296,9 @@ fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k,
  * [num_pages, page_size / scale_block, h_kv]: a byte stands for its e4m3 value times its block's scale.
  * The new tokens of sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 and the last of its
  * seqused_k[b] keys (as fa_page_plan leaves them and fa_fwd takes them); key j is row j % page_size of
- * page block_table[b * max_blocks_per_seq + j / page_size].  For each block that gets new rows
+ * page block_table[b * max_blocks_per_seq + j / page_size].  Offsets are kept within [0, T] and may begin at any row (rows ahead
+ * of the first one, as those behind the last, belong to no sequence); where they decrease, *status is set and tokens
+ * of the sequences concerned may not be stored.  For each block that gets new rows
  *   s = max(old scale, smallest power of two with (largest finite |x| of its new rows) <= 448 s),
  * (at least 2^-126; the old scale counts as 0 where the block's first row is a new one and where it is no
  * positive finite number), new rows become e4m3(x / s), rounded once from fp32 (infinities: the largest
