@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                             // the largest term so far, at 1 / u in units of the old reference, and of these keys
                             const float most = fmaxf(keep / u[n][e], ex2(top - mn) * vs);
                             const float un = most > 0x1p-126f && most < INFINITY ? 1.f / power_below(most) : kNoUnit;
-                            const float f = keep * (un / u[n][e]);
+                            // (un / u alone may pass fp32's range, and 0 * inf would be NaN; keep / u is one of the terms of `most`)
+                            const float by = un / u[n][e], f = by < INFINITY ? keep * by : keep / u[n][e] * un;
                             m[n][e] = mn;
                             l[n][e] *= keep;
                             u[n][e] = un;

@@ -3,7 +3,11 @@ definition.  Bounds are those of test_gpu_append8.py and test_gpu_paged8.py."""
 import numpy as np
 import pytest
 
+import cache8_helpers as c8
+import step_helpers as ref
 import test_gpu_append8 as ap
+import test_gpu_paged8 as at
+from gpu_helpers import from_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +50,47 @@ def test_append_with_offsets_that_decrease():
         mine[c["table"][b][c["table"][b] >= 0]] = True
     for (pool, scale), (pool2, scale2) in zip(c["cache"], after):
         assert np.array_equal(pool[~mine], pool2[~mine]) and np.array_equal(scale[~mine], scale2[~mine])
+
+
+def groups_case(new, groups, d, seed=0):
+    """One sequence over 528 keys in pages of 16.  Its queries are ones and groups[g] = (e, b, s): the keys of group g
+    have the byte b and the scale 2^e, which is a score of 2^e E4M3[b] at softmax scale 1 / d, their values random bytes and the
+    scale s (groups that are not named: score 0, value scale 0).  Groups 0, 8, 16, ... lie in one warp's stream."""
+    from exact_attention_bwd_gb300 import inputs
+    c = at.case([new], [528], h_q=4, h_kv=2, d=d, page=16, seed=seed)
+    q = np.ones(c["q"].shape, np.float32)
+    c["qb"], c["q"] = inputs.bf16_bits(q), q.astype(np.float64)
+    c["k"][0][...], c["k"][1][...], c["v"][1][...] = 0, 1.0, 0.0
+    for g, (e, b, s) in groups.items():
+        page = c["table"][0, g]
+        c["k"][0][page], c["k"][1][page], c["v"][1][page] = b, 2.0 ** e, s
+    return c
+
+
+def far_scores(c, d, new):
+    """Bounds of test_gpu_paged8.py for scores of up to 2^8 units, which are off by 2^-13 at most (five roundings of 2^-24), and the
+    probabilities below fp32's normal range, which are 0 on the GPU: 2^-126 sum_j vs_j |byte_j| at most."""
+    o, z, status = at.gpu(c, causal=False, scale=1.0 / d, hint=new)
+    assert status == 0
+    v = c8.true_values(*c["v"])
+    args = (c["cu"], c["used"], c["table"])
+    want, lse, spread = ref.attention(c["q"], c8.true_values(*c["k"]), v, *args, causal=False, scale=1.0 / d)
+    unit = c8.true_values(np.full_like(c["v"][0], 0x38), c["v"][1])
+    units, _, _ = ref.attention(c["q"], c8.true_values(*c["k"]), unit, *args, causal=False, scale=1.0 / d)
+    sizes = np.repeat(np.abs(c8.E4M3[ref.gather(c["v"][0], c["table"], c["used"])]).sum(0), 2, 0)  # (two query heads to a group)
+    gone = 2.0 ** -126 * np.repeat(np.abs(ref.gather(v, c["table"], c["used"])).sum(0), 2, 0)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * spread + 2.0 ** -25 * units * sizes + gone
+    err = np.abs(from_dev(o) - want)
+    assert np.all(err <= bound), (float(err.max()), float((err - bound).max()), np.argwhere(~(err <= bound))[:4])
+    assert np.abs(z.cpu().numpy() - lse).max() <= 2.0 ** -13
+
+
+HIGHEST = [(6, 0x3D)]  # a score of 104: 150 in powers of two
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 5, 200])
+@pytest.mark.parametrize("first,last", [(8.0, 0.0), (8.0, 2.0 ** -126), (2.0 ** 40, 0.0), (2.0 ** 100, 2.0 ** -126), (1.0, 2.0 ** -60)])
+def test_scores_that_leave_all_before_them_behind(d, new, first, last):
+    """Keys whose scores pass those before them by 2^150 and whose values are 0, or nearly: the output is theirs, not NaN."""
+    far_scores(groups_case(new, {0: (0, 0, first), 8: (0, 0, first), 16: (*HIGHEST[0], last), 32: (*HIGHEST[0], last)}, d), d, new)
