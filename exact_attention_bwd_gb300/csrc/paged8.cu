@@ -434,10 +434,18 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                 for (int n = 0; n < NT; ++n) {
                     l[n][0] += pr[n][0] + pr[n][2];
                     l[n][1] += pr[n][1] + pr[n][3];
-                    // (a row without a value so far has u = 2^126 and P = 0: 0 * inf would be NaN)
+                    // (vs u may pass fp32's range where P is small, or 0 in a row without a value so far: P vs first, then)
                     float f0 = vs * u[n][0], f1 = vs * u[n][1];
-                    f0 = f0 > 0x1p100f ? 0x1p100f : f0;
-                    f1 = f1 > 0x1p100f ? 0x1p100f : f1;
+                    if (f0 > 0x1p100f) {
+                        pr[n][0] *= vs;
+                        pr[n][2] *= vs;
+                        f0 = u[n][0];
+                    }
+                    if (f1 > 0x1p100f) {
+                        pr[n][1] *= vs;
+                        pr[n][3] *= vs;
+                        f1 = u[n][1];
+                    }
                     pb[n][0] = transpose8x8(pack16<true>(pr[n][0] * f0, pr[n][1] * f1));
                     pb[n][1] = transpose8x8(pack16<true>(pr[n][2] * f0, pr[n][3] * f1));
                 }

@@ -94,3 +94,11 @@ HIGHEST = [(6, 0x3D)]  # a score of 104: 150 in powers of two
 def test_scores_that_leave_all_before_them_behind(d, new, first, last):
     """Keys whose scores pass those before them by 2^150 and whose values are 0, or nearly: the output is theirs, not NaN."""
     far_scores(groups_case(new, {0: (0, 0, first), 8: (0, 0, first), 16: (*HIGHEST[0], last), 32: (*HIGHEST[0], last)}, d), d, new)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 5, 200])
+@pytest.mark.parametrize("first,last", [(2.0 ** -50, 2.0 ** 60), (2.0 ** -50, 2.0 ** 65), (2.0 ** -57, 2.0 ** 52), (2.0 ** -100, 2.0 ** 16)])
+def test_large_values_of_small_probabilities(d, new, first, last):
+    """Keys far below the highest score whose values are as much larger: both count (2^-115 last is about first)."""
+    far_scores(groups_case(new, {0: (6, 0x3A, first), 16: (0, 0, last), 32: (0, 0, last)}, d), d, new)
