@@ -10,6 +10,7 @@ library is missing or cannot be built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -589,7 +590,8 @@ def _set_axes(p, positions, pair_axis, norm):
     if len(pair_axis) != p.rot_dim // 2:
         raise ValueError(f"pair_axis must have {p.rot_dim // 2} entries, one for each pair; it has {len(pair_axis)}")
     try:
-        pairs = bytes(pair_axis)
+        # (bytes() of an array would be its memory, not its entries)
+        pairs = bytes(pair_axis if isinstance(pair_axis, (tuple, list)) else list(map(operator.index, pair_axis)))
     except (TypeError, ValueError):
         pairs = b"\xff"
     if pairs.translate(None, b"\0\1\2\3"[:axes]):  # (what is left when the axes are taken out)
