@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
         for (int t = w.t0; t < w.t1; t += TILES, ++done, st = st + 1 == S ? 0 : st + 1) {
             const int j0 = (t + side) * kKeyTile + kGroup * group;
             if (t + side < w.t1 && j0 <= w.hi && j0 + kGroup > w.lo) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.full[warp][st], (phase >> st) & 1, ab)))) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait_copy(&s.full[warp][st], (phase >> st) & 1, ab)))) break;
                 phase ^= 1u << st;
                 filled &= ~(1u << st);
                 const uint8_t *k8 = s.ring[warp][st][0], *v8 = s.ring[warp][st][1];

@@ -195,9 +195,9 @@ typedef struct fa_params {
      * MMAs that should have landed); 0 selects 2 s.  A wait that runs past it makes the CTA
      * give up: it records FA_ERR_TIMEOUT in the status word, lets its own copies and MMAs
      * land, frees its tensor memory and returns, and the call's later kernels do nothing.
-     * A limit below the kernels' own latencies (a few microseconds) turns every call into
-     * such a failure, which is how the failure path is exercised; outputs of a failed call
-     * are unspecified. */
+     * A limit below the kernels' own latencies (a few microseconds) turns every call in which something
+     * is waited for into such a failure, which is how the failure path is exercised; outputs of a
+     * failed call are unspecified. */
     unsigned long long wait_limit_ns;
     /* A cache in 8 bits (packed queries over a paged cache only; see above) */
     int cache_dtype;        /* 0: k and v have the queries' type; FA_DTYPE_E4M3 */

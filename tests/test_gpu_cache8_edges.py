@@ -102,3 +102,41 @@ def test_scores_that_leave_all_before_them_behind(d, new, first, last):
 def test_large_values_of_small_probabilities(d, new, first, last):
     """Keys far below the highest score whose values are as much larger: both count (2^-115 last is about first)."""
     far_scores(groups_case(new, {0: (6, 0x3A, first), 16: (0, 0, last), 32: (0, 0, last)}, d), d, new)
+
+
+@pytest.mark.parametrize("d,G,new", [(64, 4, 1), (64, 4, 4), (64, 4, 8), (128, 4, 1), (128, 4, 4), (128, 4, 8), (192, 4, 2), (192, 4, 4),
+                                     (256, 4, 2), (256, 4, 4)])
+@pytest.mark.parametrize("long", [False, True])
+def test_a_wait_limit_ends_the_few_row_kernel_with_a_timeout(d, G, new, long):
+    """Each tile of the few-row kernel: a limit of 1 ns ends it with a timeout, and the same call without the limit is right next (no
+    copy landed late, nothing was left behind).  Short caches: a CTA has one tile, which comes from memory, where the queries
+    come from L2.  Long ones: dozens of tiles, whose arithmetic or whose bytes may be behind."""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    g = torch.Generator(device="cuda").manual_seed(d)
+    B, page = (25, 32) if long else (100, 128)
+    used, i32 = (40000 - 777 * np.arange(B) if long else 128 - np.arange(B)), lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()
+    blocks = -(-used // page)
+    table = np.zeros((B, blocks.max()), np.int32)
+    for b in range(B):
+        table[b, :blocks[b]] = blocks[:b].sum() + np.arange(blocks[b])
+    k, v = (torch.randint(0, 0x70, (int(blocks.sum()), page, 1, d), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2))
+    scales = tuple(torch.full((k.shape[0], 1, 1), 2.0 ** -6, device="cuda") for _ in range(2))
+    q = torch.randn(B * new, G, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    kw = dict(causal=True, cu_q=i32(new * np.arange(B + 1)), seqused_k=i32(used), block_table=i32(table), s_kv=int(used.max()),
+              max_seqlen_q=new, cache_scale=scales)
+    want, lse, ws = fa.forward(q, k, v, **kw)
+    assert fa.device_status(ws) == 0 and torch.isfinite(lse).all()
+    flush, ended = torch.empty(64 << 20, device="cuda"), 0  # 256 MB, twice the L2
+    for _ in range(6):
+        flush.fill_(1.0)
+        q.mul_(1.0)
+        o, z, ws = fa.forward(q, k, v, **kw, wait_limit_ns=1)
+        status = fa.device_status(ws)
+        assert status in (0, fa.FA_ERR_TIMEOUT)
+        ended += status != 0
+        if status != 0:
+            o, z, ws = fa.forward(q, k, v, **kw)
+            assert fa.device_status(ws) == 0
+        assert torch.equal(o, want) and torch.equal(z, lse)
+    assert long or ended
