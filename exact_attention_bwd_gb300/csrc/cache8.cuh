@@ -15,26 +15,27 @@ struct Pages8 {
     const Cache8& c;
     const Problem& p;
     const int32_t* table;
-    int num_pages, nk;
+    int num_pages, lo, hi;  // keys that any query of the item sees
     int ahead_page = 0, ahead_row = 0, ahead_block = 0;  // of the next tile
     int page = 0, row = 0;                               // page of the lane's rows, first row in it
     long scale = 0;                                      // place of their scale, head 0 (-1: none)
-    __device__ __forceinline__ Pages8(const Cache8& c_, const Problem& p_, const int32_t* t, int pages, int nk_)
-        : c(c_), p(p_), table(t), num_pages(pages), nk(nk_) {}
+    __device__ __forceinline__ Pages8(const Cache8& c_, const Problem& p_, const int32_t* t, int pages, int lo_, int hi_)
+        : c(c_), p(p_), table(t), num_pages(pages), lo(lo_), hi(hi_) {}
     __device__ __forceinline__ void look(int t, int end) {
         const int lane = threadIdx.x & 31, key = t * TILE + 16 * lane, at = quotient(key, c.by_page);
-        ahead_page = lane < GROUPS && t < end && key < nk ? table[at] : num_pages;
+        ahead_page = lane < GROUPS && t < end && key <= hi ? table[at] : num_pages;
         ahead_row = key - at * p.page_size;
         ahead_block = quotient(ahead_row, c.by_block);
     }
-    // Tile t is the one to load.  A lane's page is the pool's end, which reads as zeros, past the used keys and for
-    // an entry outside the pool, which sets the status.
+    // Tile t is the one to load.  A lane's page is the pool's end, which reads as zeros, past the keys that are seen and for
+    // an entry outside the pool, which sets the status if any of the lane's keys is seen.
     __device__ __forceinline__ void take(int t, int end, int* status) {
         const int lane = threadIdx.x & 31;
         page = ahead_page;
         row = ahead_row;
         if (lane < GROUPS && (unsigned)page >= (unsigned)num_pages) {
-            if (t * TILE + 16 * lane < nk) atomicCAS(status, 0, kStatusDeviceCheck);
+            const int key = t * TILE + 16 * lane;
+            if (key <= hi && key + 16 > lo) atomicCAS(status, 0, kStatusDeviceCheck);
             page = num_pages;
         }
         scale = page < num_pages ? ((long)page * c.blocks + ahead_block) * p.h_kv : -1;

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             const int slot = n % kItemSlots;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
             const ItemInfo& it = s.item[slot];
-            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, nk = it.nk;
+            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, lo = it.lo, hi = it.hi;
             const int32_t* table = p.block_table + (long)it.b * p.max_blocks;
             const int qr0 = it.q0 + it.s0[0], qr1 = it.q0 + it.s0[1];
             const bool on0 = it.t1[0] > it.t0[0], on1 = it.t1[1] > it.t0[1];
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
             if (end) break;
             if (u1 <= u0) continue;
-            Pages8<KT> pages(a.cache8, p, table, a.num_pages, nk);
+            Pages8<KT> pages(a.cache8, p, table, a.num_pages, lo, hi);
             pages.look(u0, u1);
             if (n_q > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty, (n_q - 1) & 1, ab)))) break;
             if (lane == 0) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             const int slot = n % kItemSlots;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
             const ItemInfo& it = s.item[slot];
-            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, nk = it.nk;
+            const int end = it.end, g = it.g, u0 = it.u0, u1 = it.u1, lo = it.lo, hi = it.hi;
             const int32_t* table = p.block_table + (long)it.b * p.max_blocks;
             const int qr0 = it.q0 + it.s0[0], qr1 = it.q0 + it.s0[1];
             const bool on0 = it.t1[0] > it.t0[0], on1 = it.t1[1] > it.t0[1];
@@ -287,11 +287,12 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             if (end) break;
             if (u1 <= u0) continue;
             tr.item(n);
-            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used keys
-            // or for a table entry outside the pool; the next tile's entry is fetched ahead
+            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the keys that any row sees
+            // or for a table entry outside the pool, which is an error where some row sees a key of the
+            // box; the next tile's entry is fetched ahead
             auto entry = [&](int t) {
                 const int j = t * kKeyTile + lane * a.box;
-                return lane < boxes && t < u1 && j < nk ? table[j / p.page_size] : a.num_pages;
+                return lane < boxes && t < u1 && j <= hi ? table[j / p.page_size] : a.num_pages;
             };
             int next = entry(u0);
             if (n_q > 0 && !(ok = wait(kBQEmpty, &s.q_empty, (n_q - 1) & 1))) break;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 next = entry(j + 1);
                 const int key = j * kKeyTile + lane * a.box, row = key % p.page_size;
                 if (lane < boxes && (unsigned)page >= (unsigned)a.num_pages) {
-                    if (key < nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    if (key <= hi && key + a.box > lo) atomicCAS(a.status, 0, kStatusDeviceCheck);
                     page = a.num_pages;
                 }
                 if (!(ok = wait(kBKEmpty, &s.k_empty[st], ph ^ 1))) break;

@@ -140,7 +140,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                         tma_load_4d(&s.ring[0][c * Q_CHUNK], &tmq, &s.q_full, c * 64, g * p.G, sv.q0 + s0, 0);
                 }
                 const int log_box = __ffs(a.box) - 5;  // (16 to 64 rows)
-                Pages8<BN> pages(a.cache8, p, p.block_table + (long)sv.b * p.max_blocks, a.num_pages, sv.nk);
+                Pages8<BN> pages(a.cache8, p, p.block_table + (long)sv.b * p.max_blocks, a.num_pages, band.lo(s0), band.hi(min(s0 + p.P, sv.nq) - 1));
                 pages.look(t0, t0 + ntiles);
                 for (int t = t0, ok = 1; ok && t < t0 + ntiles; ++t) {
                     pages.take(t, t0 + ntiles, a.status);
@@ -181,12 +181,14 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                     tma_load_4d(&s.ring[0][c * Q_CHUNK], &tmq, &s.q_full, c * 64, g * p.G, sv.q0 + s0, 0);
             }
             const int boxes = BN / a.box, end = t0 + ntiles;
+            const int lo = band.lo(s0), hi = band.hi(min(s0 + p.P, sv.nq) - 1);  // keys that any row sees
             const int32_t* table = p.block_table + (long)sv.b * p.max_blocks;
-            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used keys
-            // or for a table entry outside the pool; the next tile's entry is fetched ahead
+            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the keys that any row sees
+            // or for a table entry outside the pool, which is an error where some row sees a key of the
+            // box; the next tile's entry is fetched ahead
             auto entry = [&](int t) {
                 const int j = t * BN + lane * a.box;
-                return lane < boxes && t < end && j < sv.nk ? table[j / p.page_size] : a.num_pages;
+                return lane < boxes && t < end && j <= hi ? table[j / p.page_size] : a.num_pages;
             };
             auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, ab)) != 0; };
             int next = entry(t0), k_issued = 0, v_issued = 0;
@@ -197,7 +199,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                 next = entry(t0 + it + 1);
                 const int key = (t0 + it) * BN + lane * a.box, row = key % p.page_size;
                 if (lane < boxes && (unsigned)page >= (unsigned)a.num_pages) {
-                    if (key < sv.nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    if (key <= hi && key + a.box > lo) atomicCAS(a.status, 0, kStatusDeviceCheck);
                     page = a.num_pages;
                 }
                 if (it == STAGES - 1 && !wait(&s.q_tmem, 0)) break;

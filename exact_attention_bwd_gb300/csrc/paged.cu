@@ -324,18 +324,18 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         for (int it = 0; ok; ++it) {
             const int slot = it % kItems;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (it / kItems) & 1, ab)))) break;
-            const int end = s.item[slot].end, b = s.item[slot].b, nk = s.item[slot].nk, g = s.item[slot].g;
+            const int end = s.item[slot].end, b = s.item[slot].b, lo = s.item[slot].lo, hi = s.item[slot].hi, g = s.item[slot].g;
             const int t0 = s.item[slot].t0, t1 = s.item[slot].t1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
             if (end) break;
             const int32_t* table = p.block_table + (long)b * p.max_blocks;
-            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the used
-            // keys or for a table entry outside the pool.  The entry of the next tile is on its way
-            // while this one waits for its slots.
+            // lane x takes box x of a tile: its page, or the pool's end (zero fill) past the keys that any
+            // row sees or for a table entry outside the pool, which is an error where some row sees a key of
+            // the box.  The entry of the next tile is on its way while this one waits for its slots.
             auto entry = [&](int t) {
                 const int j = t * kKeyTile + lane * a.box;
-                return lane < boxes && t < t1 && j < nk ? table[j / p.page_size] : a.num_pages;
+                return lane < boxes && t < t1 && j <= hi ? table[j / p.page_size] : a.num_pages;
             };
             int next = entry(t0);
             for (int t = t0; ok && t < t1; ++t) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                 next = entry(t + 1);
                 const int j = t * kKeyTile + lane * a.box, row = j % p.page_size;
                 if (lane < boxes && (unsigned)page >= (unsigned)a.num_pages) {
-                    if (j < nk) atomicCAS(a.status, 0, kStatusDeviceCheck);
+                    if (j <= hi && j + a.box > lo) atomicCAS(a.status, 0, kStatusDeviceCheck);
                     page = a.num_pages;
                 }
 #pragma unroll
