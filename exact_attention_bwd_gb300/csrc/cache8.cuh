@@ -52,18 +52,25 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w) {
     return r;
 }
 
+// A pair of an output's values in the 16-bit type.  fp16: kept within its range (NaN stays NaN), for a value near its
+// largest may stand in the cache as the next e4m3 value above, which fp16 rounds to infinity.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_out8(float x, float y) {
+    if constexpr (F16) {
+        uint32_t r;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+        return r;
+    }
+    return pack16<F16>(x, y);
+}
+
 // Two e4m3 bytes times a scale, in the 16-bit type.  (fp16: kept within its range, so that a finite
 // value does not become infinite where the scale was rounded up; NaN stays NaN.)
 template <bool F16, bool HI>
 __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t w, float scale) {
     const uint32_t h = widen_e4m3x2<HI>(w);
     const float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(scale, scale));
-    if constexpr (F16) {
-        uint32_t r;
-        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
-        return r;
-    }
-    return pack16<F16>(x.x, x.y);
+    return pack_out8<F16>(x.x, x.y);
 }
 
 template <int D, int UNITS>

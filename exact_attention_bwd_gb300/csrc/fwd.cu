@@ -922,6 +922,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             }
         }
         if (has_o && ok) {
+            auto pack = [](float x, float y) { return C8 ? pack_out8<F16>(x, y) : pack16<F16>(x, y); };
             // the whole O row into registers (warp-collective TMEM reads), then O_k is free for
             // the next item's P V while the row is scaled and stored; only valid rows store
             uint32_t orr[D];
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                             uint32_t wv[8];
 #pragma unroll
                             for (int u = 0; u < 8; ++u)
-                                wv[u] = pack16<F16>(__uint_as_float(orr[16 * t + 2 * u]) * oscale,
+                                wv[u] = pack(__uint_as_float(orr[16 * t + 2 * u]) * oscale,
                                                     __uint_as_float(orr[16 * t + 2 * u + 1]) * oscale);
                             st_global_v8(orow + 16 * t, wv);
                         }
@@ -948,10 +949,10 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
 #pragma unroll
                         for (int t = 0; t < D / 8; ++t) {
                             uint4 wv;
-                            wv.x = pack16<F16>(__uint_as_float(orr[8 * t + 0]) * oscale, __uint_as_float(orr[8 * t + 1]) * oscale);
-                            wv.y = pack16<F16>(__uint_as_float(orr[8 * t + 2]) * oscale, __uint_as_float(orr[8 * t + 3]) * oscale);
-                            wv.z = pack16<F16>(__uint_as_float(orr[8 * t + 4]) * oscale, __uint_as_float(orr[8 * t + 5]) * oscale);
-                            wv.w = pack16<F16>(__uint_as_float(orr[8 * t + 6]) * oscale, __uint_as_float(orr[8 * t + 7]) * oscale);
+                            wv.x = pack(__uint_as_float(orr[8 * t + 0]) * oscale, __uint_as_float(orr[8 * t + 1]) * oscale);
+                            wv.y = pack(__uint_as_float(orr[8 * t + 2]) * oscale, __uint_as_float(orr[8 * t + 3]) * oscale);
+                            wv.z = pack(__uint_as_float(orr[8 * t + 4]) * oscale, __uint_as_float(orr[8 * t + 5]) * oscale);
+                            wv.w = pack(__uint_as_float(orr[8 * t + 6]) * oscale, __uint_as_float(orr[8 * t + 7]) * oscale);
                             reinterpret_cast<uint4*>(orow)[t] = wv;
                         }
                     }

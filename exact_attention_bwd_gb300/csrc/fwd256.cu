@@ -466,6 +466,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                 a.lse_part[(long)split * nrows + prow] = lse;
             }
         }
+        auto pack = [](float x, float y) { return C8 ? pack_out8<F16>(x, y) : pack16<F16>(x, y); };
         for (int cb = 0; cb < D; cb += 32) {
             uint32_t orr[32];
             if (has_o && ok) {
@@ -483,7 +484,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                     uint32_t wv[8];
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        wv[u] = pack16<F16>(__uint_as_float(orr[16 * t + 2 * u]) * oscale,
+                        wv[u] = pack(__uint_as_float(orr[16 * t + 2 * u]) * oscale,
                                             __uint_as_float(orr[16 * t + 2 * u + 1]) * oscale);
                     st_global_v8(orow + 16 * t, wv);
                 }
@@ -492,10 +493,10 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     uint4 wv;
-                    wv.x = pack16<F16>(__uint_as_float(orr[8 * t + 0]) * oscale, __uint_as_float(orr[8 * t + 1]) * oscale);
-                    wv.y = pack16<F16>(__uint_as_float(orr[8 * t + 2]) * oscale, __uint_as_float(orr[8 * t + 3]) * oscale);
-                    wv.z = pack16<F16>(__uint_as_float(orr[8 * t + 4]) * oscale, __uint_as_float(orr[8 * t + 5]) * oscale);
-                    wv.w = pack16<F16>(__uint_as_float(orr[8 * t + 6]) * oscale, __uint_as_float(orr[8 * t + 7]) * oscale);
+                    wv.x = pack(__uint_as_float(orr[8 * t + 0]) * oscale, __uint_as_float(orr[8 * t + 1]) * oscale);
+                    wv.y = pack(__uint_as_float(orr[8 * t + 2]) * oscale, __uint_as_float(orr[8 * t + 3]) * oscale);
+                    wv.z = pack(__uint_as_float(orr[8 * t + 4]) * oscale, __uint_as_float(orr[8 * t + 5]) * oscale);
+                    wv.w = pack(__uint_as_float(orr[8 * t + 6]) * oscale, __uint_as_float(orr[8 * t + 7]) * oscale);
                     reinterpret_cast<uint4*>(orow)[t] = wv;
                 }
             } else {

@@ -21,6 +21,7 @@
 //   warps 4..7   softmax (thread = key) and epilogue (thread = column of O, then warp = row)
 //   warps 8..11  with two groups: the softmax of the odd tiles of the CTA's stream (warps 4..7 then
 //                have the even ones) and the epilogue of the second half of the rows
+#include "cache8.cuh"
 #include "paged.cuh"
 
 namespace fa {
@@ -1017,7 +1018,10 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, const PagedCut& c
         if (a.lse && lane == 0) a.lse[(long)h * p.T_q + cut.q0 + i] = lt != 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
         uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (((long)cut.q0 + i) * p.h_q + h) * D + VW * lane);
 #pragma unroll
-        for (int e = 0; e < VW; e += 2) out[e / 2] = f == 0.f ? 0u : pack16<F16>(acc[z][e] * f, acc[z][e + 1] * f);
+        for (int e = 0; e < VW; e += 2) {
+            const float x = acc[z][e] * f, y = acc[z][e + 1] * f;
+            out[e / 2] = f == 0.f ? 0u : F16 && p.cache8 ? pack_out8<F16>(x, y) : pack16<F16>(x, y);
+        }
     }
 }
 

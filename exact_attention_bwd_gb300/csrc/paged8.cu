@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Few8Cfg<D, NT>::THREADS, 1) paged8_few_kernel(
                         const int i = (int)((unsigned)(w.r0 + r) / G), h = w.g * p.G + w.r0 + r - i * p.G;
                         const float ox = f == 0.f ? 0.f : o.x * f, oy = f == 0.f ? 0.f : o.y * f;
                         *reinterpret_cast<uint32_t*>(&a.o[(((long)w.q0 + i) * p.h_q + h) * D + col]) =
-                            f16 ? pack16<true>(ox, oy) : pack16<false>(ox, oy);
+                            f16 ? pack_out8<true>(ox, oy) : pack_out8<false>(ox, oy);
                     }
                 }
             }

@@ -112,6 +112,7 @@
  *    of 16 that divides page_size, the scales are finite.  fa_qk_norm_rope_append8 fills such a cache.  All else is
  *    as above; bytes of rows behind a sequence's used keys, and scales of blocks behind them, have no effect.  (A NaN among
  *    the bytes of a value that some query of a sequence sees may reach outputs of that sequence's other queries.)
+ *    fp16 outputs are kept within fp16's range (a value near its largest, appended, stands for the next e4m3 value).
  *
  * FP8 forward (vllm-project/flash-attention README, "FlashAttention-3 beta release":
  * "FP8 forward"): with dtype = FA_DTYPE_E4M3, q, k and v hold e4m3 bytes (1 byte per

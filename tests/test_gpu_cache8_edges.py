@@ -140,3 +140,27 @@ def test_a_wait_limit_ends_the_few_row_kernel_with_a_timeout(d, G, new, long):
             assert fa.device_status(ws) == 0
         assert torch.equal(o, want) and torch.equal(z, lse)
     assert ended or not (long and (d, new) in ((128, 1), (256, 2), (256, 4)))
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", at.HEADS)
+@pytest.mark.parametrize("new", [1, 5, 200])
+def test_fp16_outputs_stay_finite(d, h_q, h_kv, new):
+    """Values of 65504, fp16's largest, are appended as 65536 (e4m3 has no nearer one): the output of every kernel, of items
+    that are cut as well, is 65504 again.  (All values of a head's column are alike, so its exact output is 65536.)"""
+    import torch
+    from exact_attention_bwd_gb300 import binding as fa
+    T = 3000
+    sign = torch.where(torch.arange(d, device="cuda") % 3 == 0, -1.0, 1.0).half()
+    x = torch.randn(T, h_q, d, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).half()
+    k, v = torch.randn(T, h_kv, d, device="cuda").half(), (65504.0 * sign).expand(T, h_kv, d).contiguous()
+    i32 = lambda *y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    pools = [torch.zeros(-(-T // 64), 64, h_kv, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(-(-T // 64), 2, h_kv, device="cuda") for _ in range(2)]
+    table = torch.arange(-(-T // 64), dtype=torch.int32, device="cuda")[None].contiguous()
+    fa.qk_norm_rope_append8(x, k, v, None, None, None, None, k_cache=pools[0], v_cache=pools[1], k_scale=scales[0], v_scale=scales[1],
+                            cu_q=i32(0, T), seqused_k=i32(T), block_table=table, positions=torch.zeros(T, dtype=torch.int32, device="cuda"), norm=False)
+    assert (scales[1] == 256).all()
+    for used in (T, 40 + new):
+        o, _, ws = fa.forward(x[:new], pools[0], pools[1], causal=True, cu_q=i32(0, new), seqused_k=i32(used), block_table=table, s_kv=T,
+                              cache_scale=tuple(scales), max_seqlen_q=new)
+        assert fa.device_status(ws) == 0 and torch.equal(o, (65504.0 * sign).expand_as(o))
