@@ -43,6 +43,36 @@ struct Pages8 {
     }
 };
 
+// Powers of two that bring the largest scales of an item's keys and of their values to at most 2^7 (and more than 2^6), so that
+// every e4m3 value times its scale fits fp16 wherever the cache's values lie: (keys, values).  What is 2^-22 of
+// the item's largest scale and more is exact where the scales are powers of two, and what is less loses the bits below 2^-31 of it.
+// [lo, hi] are the keys that any row of the item sees (a whole warp; four looks at the table and the scales in flight).
+struct Fit8 {
+    float key, value;
+    static __device__ __forceinline__ float power(float most) {
+        const uint32_t x = __float_as_uint(most), e = (x >> 23) + ((x & 0x7fffffu) ? 1 : 0);  // most <= 2^(e - 127)
+        return most > 0.f ? __uint_as_float(min(261u - e, 223u) << 23) : 1.f;                 // 2^-121 to 2^96
+    }
+    static __device__ __forceinline__ float inverse(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
+    __device__ __forceinline__ void look(const Cache8& c, const Problem& p, const int32_t* table, int num_pages, int g, int lo, int hi) {
+        float k = 0.f, v = 0.f;
+        if (lo <= hi) {
+            const int last = quotient(hi, c.by_block);
+#pragma unroll 4
+            for (int b = quotient(lo, c.by_block) + (threadIdx.x & 31); b <= last; b += 32) {
+                const int at = quotient(b * c.block, c.by_page), page = table[at];
+                if ((unsigned)page < (unsigned)num_pages) {
+                    const long x = ((long)page * c.blocks + quotient(b * c.block - at * p.page_size, c.by_block)) * p.h_kv + g;
+                    k = fmaxf(k, c.k_scale[x]);
+                    v = fmaxf(v, c.v_scale[x]);
+                }
+            }
+        }
+        key = power(warp_max(k));
+        value = power(warp_max(v));
+    }
+};
+
 // Two e4m3 bytes (the low or the high half of a word) as an fp16 pair, the lower byte low.
 template <bool HI>
 __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w) {
@@ -64,13 +94,12 @@ __device__ __forceinline__ uint32_t pack_out8(float x, float y) {
     return pack16<F16>(x, y);
 }
 
-// Two e4m3 bytes times a scale, in the 16-bit type.  (fp16: kept within its range, so that a finite
-// value does not become infinite where the scale was rounded up; NaN stays NaN.)
+// Two e4m3 bytes times a scale, in the 16-bit type.
 template <bool F16, bool HI>
 __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t w, float scale) {
     const uint32_t h = widen_e4m3x2<HI>(w);
     const float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(scale, scale));
-    return pack_out8<F16>(x.x, x.y);
+    return pack16<F16>(x.x, x.y);
 }
 
 template <int D, int UNITS>
@@ -114,13 +143,15 @@ struct Ring8 {
     // is cleared as bytes, in a branch of its own: conversions share the issue slots with the softmax, and a second copy
     // of them for edges costs more in instruction fetches than it saves (8 chunks of 1024 tokens at d = 128 793 to 814 us, 885
     // with it; 32 x 5 tokens at d = 256 72, 77 with outputs selected, 80 two chunks at a time and 92 eight).
+    // fp16: scales times `by` (Fit8).
     template <bool F16>
-    __device__ __forceinline__ bool widen(uint32_t& n, int w, uint8_t* tile, int chunk_bytes, int j0, int lo, int hi, const Abort& ab) {
+    __device__ __forceinline__ bool widen(uint32_t& n, int w, uint8_t* tile, int chunk_bytes, int j0, int lo, int hi, float by,
+                                          const Abort& ab) {
         constexpr int ALL = CPR / 2, BATCH = ALL % 4 == 0 ? 4 : ALL < 4 ? ALL : 3;  // chunks of a lane
         const int lane = threadIdx.x & 31, st = n % UNITS;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / UNITS) & 1, ab))) return false;
         // (a group that no query sees may have any scale)
-        const float f = j0 + 16 * w <= hi && j0 + 16 * w + 15 >= lo ? scale[st][w] : 0.f;
+        const float f = j0 + 16 * w <= hi && j0 + 16 * w + 15 >= lo ? (F16 ? scale[st][w] * by : scale[st][w]) : 0.f;
         const uint8_t* from = &rows[st][16 * w * D];
         const bool inside = j0 + 16 * w >= lo && j0 + 16 * w + 15 <= hi;
         auto swap_of = [](int x) { return (D == 64 ? x >> 3 : D == 192 ? (x % CPR) >> 2 : (x >> 2) ^ (x >> 3)) & 1; };

@@ -50,7 +50,9 @@
 // The C8 instantiation is that over a cache in 8 bits (512 threads): the producer warp loads half tiles
 // of e4m3 bytes and their blocks' scales into a ring of their own, and warps 12..15 turn them into the
 // 16-bit tiles that the products read, byte * scale in the queries' type: exact for scales that are powers of
-// two (an e4m3 value has four significant bits), else rounded once, as a 16-bit cache would hold it.
+// two (an e4m3 value has four significant bits), else rounded once, as a 16-bit cache would hold it.  For fp16 the scheduler
+// warp looks up an item's largest scales ahead and the tiles hold the products times a power of two that the
+// softmax's factor and the output's take back (Fit8), for they may lie outside fp16's range.
 #include "cache8.cuh"
 #include "fwd_items.cuh"
 #include "paged.cuh"
@@ -135,6 +137,7 @@ struct __align__(1024) FwdSmem {
     uint32_t tmem_base;
     int abort_flag;
     std::conditional_t<C8, Ring8<D, C::UNITS8>, char> bytes;  // C8: half tiles as the cache holds them
+    Fit8 fit[C8 ? kItemSlots : 1];  // C8 with fp16 queries: of each item
 };
 
 template <int D, bool F16, int KT, bool PG, bool C8>
@@ -143,6 +146,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                const __grid_constant__ CUtensorMap tmv) {
     using C = FwdCfg<D, KT, C8>;
     static_assert(!C8 || PG, "a cache in 8 bits is paged");
+    constexpr bool FIT = C8 && F16;  // keys and values are brought into fp16's range, item by item (Fit8)
     extern __shared__ uint8_t smem_raw[];
     FwdSmem<D, KT, C8>& smem =
         *reinterpret_cast<FwdSmem<D, KT, C8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -582,6 +586,10 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 w = fwd_item(a, idx, KT);
             }
             if (!w.live) continue;
+            Fit8 fit{1.f, 1.f};
+            if constexpr (FIT)
+                fit.look(a.cache8, p, p.block_table + (long)w.sv.b * p.max_blocks, a.num_pages, w.g, max(w.band.lo(w.ti[0].s0), w.u0 * KT),
+                         min(w.band.hi(min(w.ti[0].s0 + 2 * p.P, w.sv.nq) - 1), w.u1 * KT - 1));
             const int slot = n % kItemSlots;
             if (n >= kItemSlots) {
                 const bool wt = mbar_wait(&s.item_empty[slot], ((n / kItemSlots) - 1) & 1, ab);
@@ -644,6 +652,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                 if constexpr (PG) {
                     it.nk = w.sv.nk;
                     it.nq = w.sv.nq;
+                    if constexpr (FIT) s.fit[slot] = fit;
                     it.lo = w.band.lo(w.ti[0].s0);
                     it.hi = w.band.hi(min(w.ti[0].s0 + 2 * p.P, w.sv.nq) - 1);
                     it.part = part;
@@ -681,6 +690,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s.item_full[slot], (n / kItemSlots) & 1, ab)))) break;
             const ItemInfo& it = s.item[slot];
             const int end = it.end, u0 = it.u0, u1 = it.u1, lo = it.lo, hi = it.hi;
+            const Fit8 fit = FIT ? s.fit[slot] : Fit8{1.f, 1.f};
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[slot]);
             if (end) break;
@@ -694,7 +704,8 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
                     uint8_t* tile = x ? s.v[st] : s.k[st];
 #pragma unroll 1
                     for (int h = 0; ok && h < 2; ++h)
-                        ok = s.bytes.template widen<F16>(units, warp - 12, tile + 64 * h * 128, C::KV_CHUNK, j * KT + 64 * h, lo, hi, ab);
+                        ok = s.bytes.template widen<F16>(units, warp - 12, tile + 64 * h * 128, C::KV_CHUNK, j * KT + 64 * h, lo, hi,
+                                                         x ? fit.value : fit.key, ab);
                     if (!ok) break;
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -714,7 +725,6 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
         const uint32_t lane_base = (uint32_t)((warp & 3) << 5) << 16;
         const uint32_t tS = tmem + lane_base + C::s_col(k);
         const uint32_t tO = tmem + lane_base + C::o_col(k);
-        const float c = p.scale_log2;
         uint32_t scount = 0, ocount = 0;  // S tiles and O tiles received (carried across items)
         bool ok = true;
         Tracer tr;
@@ -751,6 +761,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
         // the sink's logit, fetched now so that its latency hides behind the key loop
         float sink2 = 0.f;
         if (p.sinks && a.n_splits == 1 && jlo != kNoRow) sink2 = p.sinks[s.item[slot].g * p.G + r % p.G] * kLog2e;
+        const float c = FIT ? p.scale_log2 * Fit8::inverse(s.fit[slot].key) : p.scale_log2;
         float m_used = -INFINITY, l = 0.f;
         for (int j = my_t0; j < my_t1; ++j) {
             const bool w = twait(tr, kBSFull, &s.s_full[k], scount & 1, ab);
@@ -912,6 +923,7 @@ __global__ void __launch_bounds__(FwdCfg<D, KT, C8>::THREADS, FwdCfg<D, KT>::CTA
         // PG: rows of a partial slot are those of the item, tile by tile; O stays un-normalised
         const long pg_row = (long)part * (2 * p.P * p.G) + k * p.P * p.G + r;
         if (PG && split_mode) oscale = 1.f;
+        if constexpr (FIT) oscale *= Fit8::inverse(s.fit[slot].value);
         if (row_valid) {
             if (!split_mode) {
                 if (a.lse) a.lse[lse_index(p, sv, i, h)] = lse;

@@ -74,6 +74,7 @@ struct WideItem {
     int split;
     bool tail;
     int part;         // paged: partial slot, or -1
+    Fit8 fit;         // C8 with fp16 queries
 };
 
 // Barriers of one item (one thread; the caller synchronises).
@@ -124,6 +125,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
                                           Smem256<D, C8>& s, const WideItem& w, uint32_t tmem, const Abort& ab, uint32_t& units8) {
     using C = Cfg256<D, C8>;
     constexpr int KCH = C::KCH, KV_BYTES = C::KV_BYTES, SLOT_BYTES = C::SLOT_BYTES, STAGES = C::STAGES;
+    constexpr bool FIT = C8 && F16;  // keys and values are brought into fp16's range, item by item (Fit8)
     const Problem& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SeqView& sv = w.sv;
@@ -164,7 +166,8 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
 #pragma unroll 1
                 for (int x = 0; ok && x < 2; ++x) {
                     if (!(ok = wait(x ? &s.v_empty[st] : &s.k_empty[st], ph))) break;
-                    if (!(ok = s.bytes.template widen<F16>(units8, warp - 8, s.ring[st] + x * KV_BYTES, KV_CHUNK, (t0 + it) * BN, lo, hi, ab))) break;
+                    if (!(ok = s.bytes.template widen<F16>(units8, warp - 8, s.ring[st] + x * KV_BYTES, KV_CHUNK, (t0 + it) * BN, lo, hi,
+                                                           x ? w.fit.value : w.fit.key, ab))) break;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(x ? &s.v_full[st] : &s.k_full[st]);
@@ -316,7 +319,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
         const bool row_valid = (r < p.P * p.G) && i < sv.nq;
         const int jlo = row_valid ? band.lo(i) : 1;
         const int jhi = row_valid ? band.hi(i) : 0;
-        const float c = p.scale_log2;
+        const float c = FIT ? p.scale_log2 * Fit8::inverse(w.fit.key) : p.scale_log2;
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         if (ntiles > 0) {
@@ -457,6 +460,7 @@ __device__ __forceinline__ void wide_item(const FwdArgs& a, const CUtensorMap& t
         // paged: rows of a partial slot are those of the item; O stays un-normalised
         const long pg_row = (long)w.part * (p.P * p.G) + r;
         if (PG && split_mode) oscale = 1.f;
+        if constexpr (FIT) oscale *= Fit8::inverse(w.fit.value);
         if (row_valid) {
             if (!split_mode) {
                 if (a.lse) a.lse[lse_index(p, sv, i, h)] = lse;
@@ -638,6 +642,16 @@ __global__ void __launch_bounds__(C8 ? kThreads256c8 : kThreads256, 1)
     // warp 3 finds the next item while the others work on the current one
     auto find = [&](int x) {
         const bool y = walk.next(p, a.pre, line, cta, p.P * p.G, a.no_split);
+        Fit8 fit{1.f, 1.f};
+        if constexpr (C8 && F16) {
+            if (y) {
+                const PagedSeq& q = walk.seq;
+                const Band band{q.nk - q.nq, p.left, p.right, q.nk};
+                const int s0 = walk.x.rt * p.P;
+                fit.look(a.cache8, p, p.block_table + (long)walk.b * p.max_blocks, a.num_pages, walk.x.g, max(band.lo(s0), walk.t0 * kKeyTile),
+                         min(band.hi(min(s0 + p.P, q.nq) - 1), walk.t1 * kKeyTile - 1));
+            }
+        }
         if (lane == 0) {
             more[x] = y;
             if (y) {
@@ -647,6 +661,7 @@ __global__ void __launch_bounds__(C8 ? kThreads256c8 : kThreads256, 1)
                 w.band = Band{q.nk - q.nq, p.left, p.right, q.nk};
                 w.g = walk.x.g;
                 w.s0 = walk.x.rt * p.P;
+                w.fit = fit;
                 int t0, t1;  // 64-key tiles of the rows' band within the piece's 128-key tiles
                 kv_tile_range(w.band, w.s0, min(w.s0 + p.P, q.nq) - 1, BN, t0, t1);
                 w.t0 = max(t0, walk.t0 * (kKeyTile / BN));

@@ -102,7 +102,8 @@
  *    FA_ERR_DEVICE_CHECK in the status word (the outputs are then unspecified); one that no query needs, of a
  *    page freed behind a sliding window, may be anything.  FA_FLAG_VALIDATE_CU checks cu_seqlens_q (from 0, not decreasing, at most
  *    T_q) and seqused_k.  max_seqlen_q is used when given (the most query rows of a sequence;
- *    it picks the kernel's tile, and a wrong one costs time, not correctness).  Results do not
+ *    it picks the kernel's tile, and a wrong one costs time, not correctness: outputs stay within the
+ *    types' roundings).  Results do not
  *    depend on how other work is scheduled: the same call gives the same bits.
  *
  *  - the same form over a cache in 8 bits (cache_dtype = FA_DTYPE_E4M3; dtype is the queries' and the
@@ -112,6 +113,11 @@
  *    of 16 that divides page_size, the scales are finite.  fa_qk_norm_rope_append8 fills such a cache.  All else is
  *    as above; bytes of rows behind a sequence's used keys, and scales of blocks behind them, have no effect.  (A NaN among
  *    the bytes of a value that some query of a sequence sees may reach outputs of that sequence's other queries.)
+ *    Two kernels share the work: one for sequences of few rows (8 to 32 of a key/value head's), which leaves the scales outside
+ *    its products, and one for more, which takes keys and values times their scales in the queries' type: exactly where
+ *    the scales are powers of two, as fa_qk_norm_rope_append8 makes them (fp16: wherever they lie, down to 2^-22 of the largest
+ *    among the keys that a work item of up to 256 rows sees), else rounded once more, as a 16-bit cache would hold them.  max_seqlen_q
+ *    decides which one takes short sequences, so a hint can change an output by such a rounding.
  *    fp16 outputs are kept within fp16's range (a value near its largest, appended, stands for the next e4m3 value).
  *
  * FP8 forward (vllm-project/flash-attention README, "FlashAttention-3 beta release":

@@ -164,3 +164,76 @@ def test_fp16_outputs_stay_finite(d, h_q, h_kv, new):
         o, _, ws = fa.forward(x[:new], pools[0], pools[1], causal=True, cu_q=i32(0, new), seqused_k=i32(used), block_table=table, s_kv=T,
                               cache_scale=tuple(scales), max_seqlen_q=new)
         assert fa.device_status(ws) == 0 and torch.equal(o, (65504.0 * sign).expand_as(o))
+
+
+def f16_queries(c, factor):
+    """The case with queries times a power of two."""
+    from exact_attention_bwd_gb300 import inputs
+    c["qb"] = inputs.f16_bits((c["q"] * factor).astype(np.float32))
+    c["q"] = inputs.f16_to_f64(c["qb"])
+    return c
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", at.HEADS)
+@pytest.mark.parametrize("new", [1, 4, 200])
+@pytest.mark.parametrize("power", [12, 3, -20, -26])
+def test_keys_outside_the_range_of_fp16(d, h_q, h_kv, new, power):
+    """fp16 queries: keys beyond 65504 (up to 448 x 2^14), and keys below fp16's smallest step, count as what they are in
+    every kernel.  (Queries are as much smaller or larger.)"""
+    c = f16_queries(at.case([new, new], [900, 250], h_q=h_q, h_kv=h_kv, d=d, page=64, block=16, kind="f16"), 2.0 ** -min(power + 4, 14) if power > 0 else 2.0 ** 10)
+    c["k"][1][...] = 2.0 ** power * 2.0 ** np.random.default_rng(d).integers(-2, 3, c["k"][1].shape)
+    at.compare(c, hint=new)
+    at.compare(c, hint=new, window=(70, -1))
+
+
+def compare_f16(c, *, causal=True, window=(-1, -1), hint=0):
+    """The bound of test_gpu_paged8.py for fp16, element by element, but that a probability that is rounded below fp16's normal
+    range is off by 2^-25 at most, where the row's largest is 1 and more before their sum divides them (a chunk's kernel moves its
+    reference when a score passes it, and does not bring values into the probabilities, as the few-row kernel does):
+    2^-25 sum_j |v_j| in all.  What lies outside fp16's range is limited to it on both sides."""
+    o, z, status = at.gpu(c, causal=causal, window=window, hint=hint)
+    assert status == 0
+    k, v = c8.true_values(*c["k"]), c8.true_values(*c["v"])
+    scale, args = c["d"] ** -0.5, (c["cu"], c["used"], c["table"])
+    want, lse, spread = ref.attention(c["q"], k, v, *args, causal=causal, window=window, scale=scale,
+                                      sinks=None if c["sinks"] is None else c["sinks"].astype(np.float64))
+    most = np.abs(ref.gather(k, c["table"], c["used"])).sum(-1).max() * np.abs(c["q"]).max()
+    score = min(most * scale * c["d"] * 2.0 ** -24, 2.0 ** -9) + 2.0 ** -18
+    sizes = np.zeros_like(want)
+    for b in range(len(c["used"])):
+        x = np.abs(ref.gather(v, c["table"][b:b + 1], c["used"][b:b + 1])).sum(0)
+        sizes[c["cu"][b]:c["cu"][b + 1]] = np.repeat(x, c["h_q"] // c["h_kv"], 0)
+    want = np.clip(want, -65504, 65504)
+    err = np.abs(from_dev(o) - want)
+    bound = 2.0 ** -11 * np.abs(want) + (2.0 ** -11 + 2 * score) * spread + 2.0 ** -25 * sizes + 2.0 ** -24
+    assert np.all(err <= bound), (float(err.max()), float((err - bound).max()), np.argwhere(~(err <= bound))[:4])
+    assert np.abs(z.cpu().numpy() - lse).max() <= score + 2.0 ** -22 * np.abs(lse).max()
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", at.HEADS)
+@pytest.mark.parametrize("new", [1, 4, 200])
+@pytest.mark.parametrize("power", [9, -16, -30])
+def test_values_outside_the_range_of_fp16(d, h_q, h_kv, new, power):
+    """fp16 outputs from values beyond 65504 (up to 448 x 2^11, of both signs, whose means may pass it as well), and from values
+    of fp16's smallest steps and less."""
+    c = at.case([new, new], [900, 250], h_q=h_q, h_kv=h_kv, d=d, page=64, block=16, kind="f16")
+    c["v"][1][...] = 2.0 ** power * 2.0 ** np.random.default_rng(d).integers(-2, 3, c["v"][1].shape)
+    compare_f16(c, hint=new)
+    compare_f16(dict(c, sinks=np.linspace(-1, 2, h_q).astype(np.float32)), hint=0, causal=False)
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", at.HEADS)
+def test_blocks_of_unlike_size_in_one_item(d, h_q, h_kv):
+    """fp16: scales of keys and of values over 2^-16 .. 2^3 within an item's reach, some 0, entries of pages behind a window anything."""
+    c = at.case([300, 1, 150], [1900, 77, 400], h_q=h_q, h_kv=h_kv, d=d, page=32, block=16, kind="f16")
+    rng = np.random.default_rng(d)
+    for pool in (c["k"], c["v"]):
+        pool[1][...] = 2.0 ** rng.integers(-16, 4, pool[1].shape) * (rng.random(pool[1].shape) < 0.9)
+    f16_queries(c, 2.0 ** -8)
+    compare_f16(c)
+    table = c["table"].copy()
+    table[0, :(1900 - 300 - 500) // 32] = -1
+    compare_f16(c, window=(500, -1))
+    want = at.gpu(c, window=(500, -1))
+    got = at.gpu(dict(c, table=table), window=(500, -1))
+    assert got[2] == 0 and np.array_equal(from_dev(got[0]), from_dev(want[0]))
