@@ -400,7 +400,8 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     pl = PagedPlan();
     if (!supported_d(p.d)) return FA_ERR_UNSUPPORTED;
     if (p.B == 0 || p.T_q == 0) return FA_OK;
-    // a sequence's rows are counted in 32 bits
+    // keys, with a right window added and rounded up to whole tiles, are counted in 32 bits, and so are a sequence's rows
+    if ((long)p.s_kv + std::max(p.right, 0) > 0x7fffffffL - 256) return FA_ERR_UNSUPPORTED;
     if ((long)p.T_q * p.G > 0x7fffffffL - 256) return FA_ERR_UNSUPPORTED;
     pl.empty = false;
     pl.ctas = sm_count();

@@ -7,6 +7,8 @@ import numpy as np
 import pytest
 
 from exact_attention_bwd_gb300 import binding as fa
+from test_cache8_host import over_cache8
+from test_step_host import A, B, C, D, E, paged
 
 
 @pytest.mark.parametrize("half", [8, 64, 128])
@@ -36,3 +38,16 @@ def test_axes_that_are_refused(bad):
     p.rot_dim = 16
     with pytest.raises(ValueError, match="pair_axis must hold axes"):
         fa._set_axes(p, torch.zeros(3, 5, dtype=torch.int32), bad, True)
+
+
+@pytest.mark.parametrize("form", [paged, over_cache8])
+@pytest.mark.parametrize("s_kv,right,taken", [
+    (2 ** 31 - 1, 0, False), (2 ** 31 - 256, 0, False), (2 ** 31 - 257, 0, True), (2 ** 31 - 257, -1, True),
+    (2 ** 31 - 5000, 4000, True), (2 ** 31 - 5000, 5000, False), (2 ** 31 - 2 ** 22, 2 ** 31 - 1, False), (2 ** 30, 2 ** 31 - 1, True),
+])
+def test_keys_are_counted_in_32_bits(form, s_kv, right, taken):
+    """The last key tile of a longest cache, and the last key of a right window, would pass 2^31 and be taken for negative."""
+    p = form(s_kv=s_kv, page_size=1024, max_blocks_per_seq=1 << 21, window_right=right, causal=0)
+    assert (fa.fa_fwd_workspace_size(p) > 0) == taken
+    if not taken:
+        assert fa.fa_fwd(p, A, B, C, D, None, E, 1 << 40, None) == fa.FA_ERR_UNSUPPORTED
