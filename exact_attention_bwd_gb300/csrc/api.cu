@@ -145,6 +145,7 @@ bool encode_pages8(CUtensorMap* m, const void* base, int d, int h, int rows, int
 // argument normalisation
 // ------------------------------------------------------------------------------------------
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Default bound on each pipeline wait of a kernel (2 s; fa_params.wait_limit_ns = 0).
 constexpr unsigned long long kWaitLimitNsDefault = 2000000000ull;
@@ -198,7 +199,7 @@ fa_status normalise(const fa_params* in, Problem& p) {
     if (a.cache_dtype != 0 && a.cache_dtype != FA_DTYPE_E4M3) return FA_ERR_INVALID_ARG;
     if (a.cache_dtype == FA_DTYPE_E4M3) {
         if (!a.block_table || !a.cu_seqlens_q || a.cu_seqlens_k) return FA_ERR_UNSUPPORTED;
-        if (!a.k_scale || !a.v_scale || a.scale_block <= 0 || a.scale_block % 16 || a.page_size <= 0 || a.page_size % a.scale_block)
+        if (!a.k_scale || !a.v_scale || !aligned4(a.k_scale) || !aligned4(a.v_scale) || a.scale_block <= 0 || a.scale_block % 16 || a.page_size <= 0 || a.page_size % a.scale_block)
             return FA_ERR_INVALID_ARG;
         p.cache8 = 1;
     }
@@ -1014,7 +1015,8 @@ fa_status fa_qk_norm_rope_append8(const fa_rope_params* in, const fa_cache8_para
     if (in->v_stride < (long long)a.h_kv * a.d || in->v_stride % 8) return FA_ERR_INVALID_ARG;
     if (!a.positions || !q || !k || !v || !q_out || !k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
     if (x.B > 0 && (!x.cu_seqlens_q || !x.seqused_k || !x.block_table)) return FA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) ||
+        !aligned4(v_scale))
         return FA_ERR_INVALID_ARG;
     // q_out may be q, in the same layout; nothing else that the call writes shares a byte with anything else of it
     const long wq = (long)a.h_q * a.d, wk = (long)a.h_kv * a.d;

@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 
 from exact_attention_bwd_gb300 import binding as fa
-from test_cache8_host import over_cache8
-from test_step_host import A, B, C, D, E, paged
+from test_cache8_host import append, call, over_cache8
+from test_step_host import A, B, C, D, E, paged, rope
 
 
 @pytest.mark.parametrize("half", [8, 64, 128])
@@ -51,3 +51,13 @@ def test_keys_are_counted_in_32_bits(form, s_kv, right, taken):
     assert (fa.fa_fwd_workspace_size(p) > 0) == taken
     if not taken:
         assert fa.fa_fwd(p, A, B, C, D, None, E, 1 << 40, None) == fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_scales_that_are_not_aligned_are_refused(off):
+    """They are copied four bytes at a time."""
+    for name in ("k_scale", "v_scale"):
+        p = over_cache8(**{name: 0x6000 + off})
+        assert fa.fa_fwd_workspace_size(p) == 0 and fa.fa_fwd(p, A, B, C, D, None, E, 1 << 40, None) == fa.FA_ERR_INVALID_ARG
+    for name in ("ks", "vs"):
+        assert call(rope(positions=0x3000), append(), **{name: ctypes.c_void_p((11 << 32) + off)}) == fa.FA_ERR_INVALID_ARG
