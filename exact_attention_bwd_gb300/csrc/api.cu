@@ -412,7 +412,10 @@ fa_status plan_paged(const Problem& p, const fa_params& in, PagedPlan& pl) {
     // few tokens, its tile and limit the smallest that holds a token's heads (a tile of 64 rows costs
     // a decode step 33 us where one of 16 takes 20: 20 sequences of 5 heads a group, d = 64), and none
     // where a token has more than 64.
-    // (A cache in 8 bits: the few-row kernel's tiles are 8 to 32 rows.)
+    // (A cache in 8 bits: the few-row kernel's tiles are 8 to 32 rows, 16 at d > 128, which is what its registers hold.  It against the
+    // chunks' kernel, 32 sequences over 2k to 8k keys: d = 64, 8 heads, 16 / 32 rows 91 / 120 us against 146 / 143; d = 128, 8 heads, 16 / 20 / 32 rows
+    // 105 / 156 / 159 against 167 / 167 / 164; d = 192 and 256, 2 heads, 16 rows 51 and 55 against 85 and 90.  8 sequences over 512 to 2k keys:
+    // 21 / 27, 23 / 31 / 32 and 27 and 30 against 27 / 26, 29 and 26 and 28.)
     const int most = !p.cache8 ? 64 : p.d <= 128 ? 32 : 16;
     pl.many = rows > most;
     const long tile = pl.many ? p.G : rows;

@@ -6,8 +6,8 @@
 //   s = max(s_old, need)  (s_old = 0 where the block's first row is a new one),
 //   new rows: e4m3(x / s),  rows ahead of them where s grew: e4m3(byte s_old / s).
 // The scale is a power of two so that neither division rounds: a new row is rounded once, to e4m3, and
-// an older one again only where it falls below e4m3's normal range (scales of another kind that the
-// caller put there are kept while they suffice).
+// an older one again only where it falls below e4m3's normal range.  (Scales of another kind that the
+// caller put there are kept while they suffice; x / s is then x times the reciprocal, within 2^-23, ahead of the rounding.)
 //
 // x is rotated in fp32 and its block's maximum is known only behind the last of its rows, so a warp keeps
 // its first kKeep batches of rows in registers; what larger blocks have beyond is read, and turned, a second time.
@@ -16,9 +16,9 @@
 // and heads.  The queries' rotation is the kernel of rope.cu, launched ahead; this one's CTAs start where that one's
 // leave registers, most of them behind it.
 //
-// Measured, 8192 tokens in chunks, 16 / 2 heads of 256, blocks of 64 rows: 43 us with the queries' rotation (24 at
-// the copy rate), 18 of them this kernel.  It is bound by its chains (issue slots 44 %, DRAM 10 %).  One batch kept 45.9,
-// four 57.8 (registers).  A decode step of 32 tokens: 14 us on the device.
+// Measured, 8192 tokens in chunks, 16 / 2 heads of 256, blocks of 16 rows: 43 us with the queries' rotation (24 at
+// the copy rate), 17 of them this kernel.  It is bound by its chains (issue slots 28 %, DRAM 11 %).  One batch kept 45.9,
+// four 57.8 (registers).  A decode step of 32 tokens: 10.5 us on the device, with the queries' kernel.
 #include "rope.cuh"
 
 namespace fa {

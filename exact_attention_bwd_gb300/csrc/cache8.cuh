@@ -141,7 +141,7 @@ struct Ring8 {
     // with their loads ahead; every other group of four chunks takes its second half first (swap_of), so that the
     // stores of a phase, and the loads where a row is a power of two, fall into different banks.  What no query sees
     // is cleared as bytes, in a branch of its own: conversions share the issue slots with the softmax, and a second copy
-    // of them for edges costs more in instruction fetches than it saves (8 chunks of 1024 tokens at d = 128 793 to 814 us, 885
+    // of them for edges costs more in instruction fetches than it saves (8 chunks of 1024 tokens at d = 128, 785 us, took 885
     // with it; 32 x 5 tokens at d = 256 72, 77 with outputs selected, 80 two chunks at a time and 92 eight).
     // fp16: scales times `by` (Fit8).
     template <bool F16>

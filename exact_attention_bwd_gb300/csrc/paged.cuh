@@ -63,8 +63,9 @@ struct PagedLine {
         return u < head ? (int)(u / (each + 1)) : more + (int)((u - head) / each);
     }
 };
-// With more than one CTA a stretch has LEAD units at least (4 units: two of 2).  One that ends among
-// the lead of the item that it starts passes the item on, so a CTA may be left without a tile.
+// With more than one CTA a stretch has LEAD / 2 + 1 units at least (two CTAs; at a lead of 2 4 units are two of 2, at one
+// of 6 8 units two of 4).  One that ends among the lead of an item passes the item on, to the CTA that
+// holds the lead's end, so a CTA may be left without a tile.
 template <int LEAD = kLead>
 __device__ __forceinline__ PagedLine paged_line(long long units, int n_ctas) {
     PagedLine x;

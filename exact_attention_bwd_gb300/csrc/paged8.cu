@@ -29,6 +29,8 @@
 // 5.6 to 5.8 TB/s.  Bound by the memory's path and the ends of items; the arithmetic issues in half of the cycles.
 // One warp to a group of keys (8 warps) with 16-byte asynchronous copies 302, two tiles side by side (16 warps) 262,
 // their bytes by TMA 256, the table's entry asked for a tile ahead and a lead of 6 units for an item 235.
+// Up to 32 rows at d <= 128 and 16 above are this kernel's where the chunks' kernel would be slower over long caches; both sides at the rule
+// in api.cu.  (16 and 24 bytes of the widest states are spilled there: <128, 4>, <256, 2>.)
 #include "cache8.cuh"
 #include "paged.cuh"
 

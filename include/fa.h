@@ -310,12 +310,14 @@ fa_status fa_qk_norm_rope(const fa_rope_params *p, const void *q, const void *k,
  *   s = max(old scale, smallest power of two with (largest finite |x| of its new rows) <= 448 s),
  * (at least 2^-126; the old scale counts as 0 where the block's first row is a new one and where it is no
  * positive finite number), new rows become e4m3(x / s), rounded once from fp32 (infinities: the largest
- * value, NaN: NaN), the block's rows ahead of them are rescaled where s has grown
- * (e4m3(byte * old / s)), rows behind them are left as they were.  A block that gets new rows must be the
+ * value, NaN: NaN; with an old scale that is no power of two x / s is itself off by up to 2^-23 of it), the block's
+ * rows ahead of them are rescaled where s has grown (e4m3(byte * old / s)), rows behind them are left as they were.  A block that gets new rows must be the
  * writing sequence's alone.  positions must be given (they drive the rotation; the table and the
  * lengths say where a token goes); slots must be NULL, zero_skipped and q_out are as in fa_qk_norm_rope, q_out may be q
  * (contiguous).  A token that fa_qk_norm_rope would skip is not stored; nor is one of no sequence, and one whose
- * place is negative or behind the table or whose page is outside the pool, which sets *status.
+ * place is negative or behind the table or whose page is outside the pool, which sets *status.  A block of which a call
+ * stores nothing is left alone, its scale too: where a sequence's first tokens in a block are all skipped, set the
+ * scale to 0 before the next ones are appended, or what an earlier owner of the page left there counts as old.
  * page_size a positive multiple of 16, scale_block a positive multiple of 16 that divides it. */
 typedef struct fa_cache8_params {
     int B;                        /* sequences */

@@ -237,3 +237,24 @@ def test_blocks_of_unlike_size_in_one_item(d, h_q, h_kv):
     want = at.gpu(c, window=(500, -1))
     got = at.gpu(dict(c, table=table), window=(500, -1))
     assert got[2] == 0 and np.array_equal(from_dev(got[0]), from_dev(want[0]))
+
+
+@pytest.mark.parametrize("reset", [False, True])
+def test_a_block_whose_first_tokens_were_skipped(reset):
+    """A call leaves alone a block of which it stores nothing; the next tokens take the scale that is there for old, or
+    none where the caller has set it to 0."""
+    c = ap.append_case([0], [5], 4, 2, 64, 64, 16, 16, seed=7)
+    page = c["table"][0, 0]
+    for _, scale in c["cache"]:
+        scale[page] = 2.0 ** 20  # of an earlier owner of the page
+    c["pos"][:] = -1
+    _, after = ap.run(c)
+    for (a, b), (x, y) in zip(c["cache"], after):
+        assert np.array_equal(a, x) and np.array_equal(b, y)
+    c = dict(ap.append_case([5], [6], 4, 2, 64, 64, 16, 16, seed=8), table=c["table"], cache=after)
+    if reset:
+        for _, scale in c["cache"]:
+            scale[page] = 0
+    q, after = ap.run(c)
+    ap.verify(c, q, after)
+    assert all(((y[page] < 1) == reset).all() for _, y in after)
