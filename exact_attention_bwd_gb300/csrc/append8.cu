@@ -18,7 +18,7 @@
 //
 // Measured, 8192 tokens in chunks, 16 / 2 heads of 256, blocks of 16 rows: 43 us with the queries' rotation (24 at
 // the copy rate), 17 of them this kernel.  It is bound by its chains (issue slots 28 %, DRAM 11 %).  One batch kept 45.9,
-// four 57.8 (registers).  A decode step of 32 tokens: 10.5 us on the device, with the queries' kernel.
+// four 57.8 (registers).  A decode step of 32 tokens: 10.3 us on the device, with the queries' kernel.
 #include "rope.cuh"
 
 namespace fa {
@@ -101,14 +101,13 @@ __device__ __forceinline__ void append8_block(const RopeArgs& a, const Append8Ar
     // ---- the block: rows [r0, r1) of page `page` are new, r1 - r0 tokens from t0 on ----
     int first;
     const int u = blockIdx.x, b = unit_sequence(c, u, first);
-    if (u < first) return;
     const int q0 = min(max(c.cu[b], 0), c.T), n = min(max(c.cu[b + 1], q0), c.T) - q0;
     const int total = c.used[b], start = total - n;  // places [start, total) in the sequence
     const int limit = c.max_blocks * c.page_size, from = max(start, 0), to = min(total, limit);
     if (n > 0 && (start < 0 || total > limit) && u == first && threadIdx.x == 0 && head == 0 && a.status)
         atomicCAS(a.status, 0, kStatusDeviceCheck);
     const long at_block = (long)quotient(from, c.by_block) + (u - first);
-    if (n <= 0 || at_block * c.block >= to) return;
+    if (u < first || n <= 0 || at_block * c.block >= to) return;  // (the one branch on all that was loaded)
     const int place = (int)at_block * c.block;  // of the block's first row
     const int nth = quotient(place, c.by_page), page = c.table[(long)b * c.max_blocks + nth];
     if ((unsigned)page >= (unsigned)c.num_pages) {
